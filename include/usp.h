@@ -432,6 +432,184 @@ size_t usp_attn_decode_workspace_size(int B, int Tq, int S, int Hq, int Hkv,
                                       int D, int cp_size, int splits_per_shard);
 
 /*
+ * The 4-bit KV cache.
+ *
+ * A serving cache of B sequences with room for `capacity` tokens each, held
+ * as 4-bit integers with one 8-bit scale per 32 channels: D (1 + 1/16) bytes
+ * per token and KV head for K and V together, where bf16 takes 4 D. The pages
+ * have no counterpart; it stands beside usp_attn_decode, whose cache is bf16
+ * and of one length, as "flash decoding is ring attention at inference time"
+ * ("Long Context Attention" notes, "Ring Attention") over a quarter of the
+ * bytes.
+ *
+ * Values. With y = x * (1 / descale) (the reciprocal and the product rounded
+ * to fp32, a NaN taken as 0), a block of 32 channels has the scale
+ *     s = e4m3(max |y| / 7)        nearest, ties to even, at most 448
+ * and the codes
+ *     c = clamp(round_half_even(y / s), -7, 7),   0 where s = 0
+ * (quotients in fp32, correctly rounded). It stands for c * s * descale. An
+ * infinity is stored as the largest value, +-7 * 448 * descale. The code is
+ * kept as the nibble c + 8; the channels 2i and 2i+1 are the low and the high
+ * nibble of byte i of the token's row. The block's scale is its E4M3 byte.
+ * The cache is trusted: a scale byte of 0x7F or 0xFF (never stored) reads as
+ * NaN, a nibble 0 as -8.
+ *
+ * The arrays are head-major, so that one head's tokens are contiguous:
+ *     k_codes, v_codes    [B][Hkv][capacity][D/2]   bytes
+ *     k_scales, v_scales  [B][Hkv][capacity][D/32]  bytes
+ *     key_weight          [B][Hkv][capacity] fp32, the attention weight that
+ *                         each cached key has collected (may be NULL where a
+ *                         call does not need it)
+ *     seq_lens            [B] int32, the cached tokens of every sequence. On
+ *                         the device: no call reads it on the host, so calls
+ *                         can be captured into graphs and replayed as the
+ *                         sequences grow. Values below 0 count as 0, above
+ *                         capacity as capacity.
+ * The struct is host memory, read during the call. Requirements, checked by
+ * every call: B >= 0, Hkv >= 1 (both at most 65535), D 64 or 128
+ * (USP_ERR_UNSUPPORTED), capacity >= 0 and a multiple of 16, descales finite,
+ * > 0 and with a finite reciprocal, the code, scale and weight arrays 16-byte
+ * aligned, seq_lens 4-byte aligned. Rows behind a sequence's length are never
+ * read as keys, and are left as they were.
+ */
+typedef struct {
+  void *k_codes;
+  void *k_scales;
+  void *v_codes;
+  void *v_scales;
+  float *key_weight;
+  int32_t *seq_lens;
+  int B, capacity, Hkv, D;
+  float k_descale, v_descale;
+} usp_kv4_cache_t;
+
+/*
+ * usp_kv4_append - store new tokens' keys and values in the cache.
+ *
+ * k, v  [B, T, Hkv, D] in natural order, bf16 or fp32 (dtype); with
+ *      cu_seqlens [B + 1] (int32, device, trusted as in usp_attn_fwd) a
+ *      packed batch [T, Hkv, D] of T tokens in all. T >= 0.
+ * Token t of sequence b goes to row seq_lens[b] + t of the sequence's rows;
+ *      tokens that find no room are dropped.
+ * new_weight  NULL, or the new keys' attention weights so far, fp32
+ *      [B, Hkv, T] (packed [Hkv, T]), as usp_attn_key_weights gives them.
+ *      Where the cache has a key_weight, the new rows get these, or 0.
+ * seq_lens_out  [B] int32 or NULL: min(capacity, seq_lens[b] + the sequence's
+ *      new tokens) is written. May be the cache's seq_lens itself.
+ * Two appends to one cache must not overlap on the GPU.
+ * Errors: USP_ERR_INVALID_ARG, USP_ERR_UNSUPPORTED, USP_ERR_ALIGNMENT,
+ *      USP_ERR_CUDA.
+ */
+usp_status_t usp_kv4_append(const usp_kv4_cache_t *cache, const void *k, const void *v,
+                            const float *new_weight, const int32_t *cu_seqlens, int T,
+                            usp_dtype_t dtype, int32_t *seq_lens_out, usp_stream_t stream);
+
+/*
+ * usp_kv4_read - the values the cache stands for.
+ *
+ * Writes rows start[b] .. start[b] + T - 1 (start NULL: 0 ..) of every
+ * sequence as k, v [B, T, Hkv, D] in dtype (c * s in fp32, times descale,
+ * rounded once more to bf16), what usp_attn_fwd takes: a prefix of the cache
+ * for the next chunk of a prompt. Rows before 0 or behind the sequence's
+ * length are written as zeros. start: int32 [B], device, 4-byte aligned.
+ * Errors: USP_ERR_INVALID_ARG, USP_ERR_UNSUPPORTED, USP_ERR_ALIGNMENT,
+ *      USP_ERR_CUDA.
+ */
+usp_status_t usp_kv4_read(const usp_kv4_cache_t *cache, const int32_t *start, int T,
+                          void *k, void *v, usp_dtype_t dtype, usp_stream_t stream);
+
+/*
+ * usp_attn_decode_kv4 - one decoding step against the 4-bit cache.
+ *
+ * The newest Tq tokens of every sequence, the last Tq of its seq_lens[b]
+ * cached ones, attend to the cached keys: with L = seq_lens[b], token t sits
+ * at i = L - Tq + t and sees key j < L iff the library's mask says so
+ * (causal, window, sink_tokens, with the positions counted in the cache). A
+ * token with i < 0, or that sees no key, gets O = 0 and LSE = -inf.
+ *
+ * q    [B, Tq, Hq, D] bf16; out likewise, written; lse [B, Tq, Hq] fp32,
+ *      written (natural log of the scaled scores' sum; with it the partial of
+ *      this cache can be merged with others by usp_merge_partials).
+ * accumulate  != 0: the attention weight that every cached key gets from this
+ *      step, summed over the Tq tokens and the query heads that share its KV
+ *      head, is added to the cache's key_weight (which must not be NULL).
+ * The work is divided on the device by the lengths that it finds there: every
+ * CTA takes an equal run of 32-key steps, over the ends of heads and
+ * sequences, and the partials of a head are merged in key order. The result
+ * does not vary from run to run.
+ * Hq % Hkv == 0; any number of query rows per KV head. dtype USP_BF16.
+ * workspace: at least usp_attn_decode_kv4_workspace_size(...) bytes, 256-byte
+ *      aligned, contents on entry irrelevant; calls that overlap on the GPU
+ *      need one each.
+ * Errors: USP_ERR_INVALID_ARG, USP_ERR_UNSUPPORTED (D; dtype USP_FP32),
+ *      USP_ERR_ALIGNMENT, USP_ERR_WORKSPACE, USP_ERR_CUDA.
+ */
+usp_status_t usp_attn_decode_kv4(const usp_kv4_cache_t *cache, const void *q, void *out,
+                                 float *lse, int Tq, int Hq, float softmax_scale,
+                                 int causal, int window, int sink_tokens, int accumulate,
+                                 usp_dtype_t dtype, void *workspace,
+                                 size_t workspace_bytes, usp_stream_t stream);
+
+/* Bytes of scratch usp_attn_decode_kv4 needs; 0 for invalid sizes. */
+size_t usp_attn_decode_kv4_workspace_size(int B, int Tq, int capacity, int Hq, int Hkv,
+                                          int D, int accumulate);
+
+/*
+ * usp_attn_key_weights - how much each key of a prompt was attended.
+ *
+ * From the forward's q, k and lse (arguments as given to and by usp_attn_fwd:
+ * rank-major order, masks, cu_seqlens, ring layout),
+ *     weight[b][g][j] = sum over observed queries i that see key j and query
+ *                       heads h of KV head g of exp(s_ij - LSE_i),
+ * the column sums of the attention matrix ("Long Context Attention" notes,
+ * "Motivation": LSE is what is kept of the forward). `observe` <= 0 observes
+ * every query; observe = n the last n of each sequence.
+ * weight [B, Hkv, S] fp32 (packed [Hkv, S]), rank-major, written; 16-byte
+ *      aligned like the others. lse: a query with LSE = -inf adds nothing.
+ * flags: USP_FLAG_FORCE_SIMT or none (else USP_ERR_UNSUPPORTED).
+ * workspace: at least usp_attn_key_weights_workspace_size(...) bytes (B: the
+ *      tensors' batch rows, 1 for packed sequences), 16-byte aligned, may be
+ *      NULL when that is 0; contents on entry irrelevant; calls that overlap
+ *      on the GPU need one each.
+ * Errors: as usp_attn_fwd.
+ */
+usp_status_t usp_attn_key_weights(const void *q, const void *k, const float *lse,
+                                  float *weight, int B, int S, int Hq, int Hkv, int D,
+                                  float softmax_scale, int causal, int window,
+                                  int sink_tokens, const int32_t *cu_seqlens, int cp_size,
+                                  usp_layout_t layout, int observe, usp_dtype_t dtype,
+                                  unsigned flags, void *workspace,
+                                  size_t workspace_bytes, usp_stream_t stream);
+
+/* Bytes of scratch usp_attn_key_weights needs; 0 for invalid sizes. */
+size_t usp_attn_key_weights_workspace_size(int B, int S, int Hq, int Hkv, int observe,
+                                           usp_dtype_t dtype, unsigned flags);
+
+/*
+ * usp_kv4_evict - keep the `keep` keys of every (sequence, KV head) that
+ * matter, in order.
+ *
+ * A sequence of L = seq_lens[b] > keep cached tokens keeps, in each KV head:
+ * its first sink_tokens, its last `recent`, and of the others the
+ * keep - sink_tokens - recent with the largest key_weight (a NaN counts above
+ * every number; of equal ones the first). A shorter one keeps all. The kept
+ * rows' codes, scales and weights move to rows 0 .. of dst in their order.
+ * dst  another cache with src's B, Hkv, D and capacity >= keep, that shares
+ *      no memory with src, or src itself (every pointer the same): in place.
+ *      key_weight may be NULL in dst. dst's seq_lens are written
+ *      (min(L, keep)) and not read; its descales are not looked at (the caller
+ *      gives dst src's).
+ * kept [B, Hkv, keep] int32, written: the source row of each row of dst,
+ *      ascending, -1 behind the last.
+ * 0 <= sink_tokens, 0 <= recent, sink_tokens + recent <= keep, keep >= 1.
+ * Errors: USP_ERR_INVALID_ARG, USP_ERR_UNSUPPORTED, USP_ERR_ALIGNMENT,
+ *      USP_ERR_CUDA.
+ */
+usp_status_t usp_kv4_evict(const usp_kv4_cache_t *src, const usp_kv4_cache_t *dst,
+                           int32_t *kept, int keep, int recent, int sink_tokens,
+                           usp_stream_t stream);
+
+/*
  * usp_permute - sequence layouts and the Ulysses all-to-all, bit-exact.
  *
  * EXTRACT / RESTORE (the YunChang README's EXTRACT_FUNC_DICT /

@@ -16,10 +16,12 @@ Modules
              and the per-shard partials that a tree merge combines
   fp8        E4M3 codes (encode / decode / per-tensor quantization) and the
              attention of e4m3 q, k, v with per-tensor descales
+  kv4        the 4-bit KV cache: its codes, a decode step over it, the
+             attention weight of each key, eviction by that weight
 
 Every function is pinned by `-m "not gpu"` tests against something other than
 itself (brute force, a library routine, finite differences, closed forms and
 the worked examples printed on the pages). No function here is "parity
 unpinned".
 """
-from . import attention, decode, fp8, layouts, merge, ring  # noqa: F401
+from . import attention, decode, fp8, kv4, layouts, merge, ring  # noqa: F401

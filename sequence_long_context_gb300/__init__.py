@@ -6,12 +6,13 @@ Every step of the computation runs in the CUDA library libusp.so; there is
 no Python or CPU fallback, and a missing library raises.
 
 The helpers below them (attn_forward, attn_backward, permute,
-merge_partials) allocate outputs and workspaces with PyTorch and call the
-same entry points.
+merge_partials, the kv4_* calls of the 4-bit KV cache) allocate outputs and
+workspaces with PyTorch and call the same entry points.
 """
 from __future__ import annotations
 
-from typing import Optional, Tuple
+import ctypes
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -155,6 +156,53 @@ def usp_attn_decode_workspace_size(B, Tq, S, Hq, Hkv, D, cp_size,
         B, Tq, S, Hq, Hkv, D, cp_size, splits_per_shard))
 
 
+def usp_kv4_append(cache, k, v, new_weight, cu_seqlens, T, dtype, seq_lens_out,
+                   stream=None) -> None:
+    """cache: a _lib.Kv4CacheStruct (as in the other usp_kv4 calls)."""
+    _check(_lib.load().usp_kv4_append(
+        ctypes.addressof(cache), _p(k), _p(v), _p(new_weight), _p(cu_seqlens), int(T),
+        _enum(DTYPE, dtype), _p(seq_lens_out), _stream(stream)))
+
+
+def usp_kv4_read(cache, start, T, k, v, dtype, stream=None) -> None:
+    _check(_lib.load().usp_kv4_read(ctypes.addressof(cache), _p(start), int(T), _p(k), _p(v),
+                                    _enum(DTYPE, dtype), _stream(stream)))
+
+
+def usp_attn_decode_kv4(cache, q, out, lse, Tq, Hq, softmax_scale, causal, window,
+                        sink_tokens, accumulate, dtype, workspace=None,
+                        workspace_bytes=0, stream=None) -> None:
+    _check(_lib.load().usp_attn_decode_kv4(
+        ctypes.addressof(cache), _p(q), _p(out), _p(lse), Tq, Hq, float(softmax_scale),
+        int(causal), int(window), int(sink_tokens), int(accumulate), _enum(DTYPE, dtype),
+        _p(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def usp_attn_decode_kv4_workspace_size(B, Tq, capacity, Hq, Hkv, D, accumulate) -> int:
+    return int(_lib.load().usp_attn_decode_kv4_workspace_size(B, Tq, capacity, Hq, Hkv, D,
+                                                              int(accumulate)))
+
+
+def usp_attn_key_weights(q, k, lse, weight, B, S, Hq, Hkv, D, softmax_scale, causal, window,
+                         sink_tokens, cu_seqlens, cp_size, layout, observe, dtype, flags=0,
+                         workspace=None, workspace_bytes=0, stream=None) -> None:
+    _check(_lib.load().usp_attn_key_weights(
+        _p(q), _p(k), _p(lse), _p(weight), B, S, Hq, Hkv, D, float(softmax_scale), int(causal),
+        int(window), int(sink_tokens), _p(cu_seqlens), cp_size, _enum(LAYOUT, layout),
+        int(observe), _enum(DTYPE, dtype), flags, _p(workspace), int(workspace_bytes),
+        _stream(stream)))
+
+
+def usp_attn_key_weights_workspace_size(B, S, Hq, Hkv, observe, dtype, flags=0) -> int:
+    return int(_lib.load().usp_attn_key_weights_workspace_size(
+        B, S, Hq, Hkv, int(observe), _enum(DTYPE, dtype), flags))
+
+
+def usp_kv4_evict(src, dst, kept, keep, recent, sink_tokens, stream=None) -> None:
+    _check(_lib.load().usp_kv4_evict(ctypes.addressof(src), ctypes.addressof(dst), _p(kept),
+                                     int(keep), int(recent), int(sink_tokens), _stream(stream)))
+
+
 def usp_permute(src, dst, kind, layout, B, S, H, D, cp_size, ulysses_degree,
                 elem_bytes, stream=None) -> None:
     _check(_lib.load().usp_permute(
@@ -286,6 +334,11 @@ def attn_decode(q, k, v, *, causal=True, cp=1, splits=1, tree_order=True,
     return out, lse
 
 
+def _on(device):
+    """The tensors' device as the current one (launches go to its stream)."""
+    return torch.cuda.device(device)
+
+
 def _use_workspace(workspace, need, device):
     """The caller's uint8 workspace (checked for size), else a fresh one."""
     if workspace is None:
@@ -414,3 +467,182 @@ def merge_partials(o_parts: torch.Tensor, lse_parts: torch.Tensor,
     usp_merge_partials(o_parts, lse_parts, n, rows, D, tree_order, o,
                        out_dtype, lse, stream)
     return o, lse
+
+
+# --- the 4-bit KV cache --------------------------------------------------------
+
+class KV4Cache(NamedTuple):
+    """A KV cache in 4 bits (usp_kv4_cache_t in include/usp.h, which gives the
+    number format): codes uint8 [B, Hkv, capacity, D/2], E4M3 scales uint8
+    [B, Hkv, capacity, D/32], cached tokens int32 [B], and (or None) the
+    attention weight each key has collected, fp32 [B, Hkv, capacity]. All on
+    one device and contiguous; capacity a multiple of 16."""
+    k: torch.Tensor
+    k_scale: torch.Tensor
+    v: torch.Tensor
+    v_scale: torch.Tensor
+    seq_lens: torch.Tensor
+    key_weight: Optional[torch.Tensor] = None
+    k_descale: float = 1.0
+    v_descale: float = 1.0
+
+
+def kv4_cache(B: int, capacity: int, Hkv: int, D: int, *, device="cuda", key_weight=False,
+              k_descale: float = 1.0, v_descale: float = 1.0) -> KV4Cache:
+    """An empty cache; the capacity is rounded up to a multiple of 16.
+    descales: what a stored value is multiplied with. 1 suits keys and values
+    whose blocks of 32 have maxima between 0.1 and 3136 (the scales' range)."""
+    C = -(-int(capacity) // 16) * 16
+    z = dict(dtype=torch.uint8, device=device)
+    return KV4Cache(
+        torch.zeros((B, Hkv, C, D // 2), **z), torch.zeros((B, Hkv, C, D // 32), **z),
+        torch.zeros((B, Hkv, C, D // 2), **z), torch.zeros((B, Hkv, C, D // 32), **z),
+        torch.zeros((B,), dtype=torch.int32, device=device),
+        torch.zeros((B, Hkv, C), dtype=torch.float32, device=device) if key_weight else None,
+        float(k_descale), float(v_descale))
+
+
+def _need(x, name, dtype, shape, device) -> None:
+    if x.dtype != dtype or tuple(x.shape) != tuple(shape) or x.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {x.dtype} {tuple(x.shape)} on {x.device}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _kv4_struct(c: KV4Cache) -> "_lib.Kv4CacheStruct":
+    """The C struct of a cache whose tensors fit together, else ValueError."""
+    B, H, C, half = c.k.shape
+    dev = c.k.device
+    D = 2 * half
+    u8 = torch.uint8
+    _need(c.k, "cache.k", u8, (B, H, C, half), dev)
+    _need(c.v, "cache.v", u8, (B, H, C, half), dev)
+    _need(c.k_scale, "cache.k_scale", u8, (B, H, C, D // 32), dev)
+    _need(c.v_scale, "cache.v_scale", u8, (B, H, C, D // 32), dev)
+    _need(c.seq_lens, "cache.seq_lens", torch.int32, (B,), dev)
+    w = None
+    if c.key_weight is not None:
+        _need(c.key_weight, "cache.key_weight", torch.float32, (B, H, C), dev)
+        w = _p(c.key_weight)
+    return _lib.Kv4CacheStruct(_p(c.k), _p(c.k_scale), _p(c.v), _p(c.v_scale), w,
+                               _p(c.seq_lens), B, C, H, D, c.k_descale, c.v_descale)
+
+
+def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, *, key_weight=None,
+               cu_seqlens=None, seq_lens_out=None, stream=None) -> torch.Tensor:
+    """Store new tokens' keys and values (bf16 or fp32, natural order) behind
+    each sequence's cached ones: k, v [B,T,Hkv,D], or packed [T,Hkv,D] with
+    cu_seqlens. key_weight: their attention weights so far ([B,Hkv,T], packed
+    [Hkv,T]; attn_key_weights), else 0. Returns the new lengths, written to
+    seq_lens_out (default: the cache's own seq_lens, in place). Tokens that
+    find no room are dropped."""
+    s = _kv4_struct(cache)
+    dev = cache.k.device
+    packed = cu_seqlens is not None
+    T = k.shape[0] if packed else k.shape[1]
+    shape = (T, s.Hkv, s.D) if packed else (s.B, T, s.Hkv, s.D)
+    if k.dtype not in DTYPE:
+        raise ValueError("keys and values must be bf16 or fp32")
+    _need(k, "k", k.dtype, shape, dev)
+    _need(v, "v", k.dtype, shape, dev)
+    if packed:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (s.B + 1,), dev)
+    if key_weight is not None:
+        if cache.key_weight is None:
+            raise ValueError("the cache has no key_weight to store the weights in")
+        _need(key_weight, "key_weight", torch.float32, 
+              (s.Hkv, T) if packed else (s.B, s.Hkv, T), dev)
+    lens = cache.seq_lens if seq_lens_out is None else seq_lens_out
+    _need(lens, "seq_lens_out", torch.int32, (s.B,), dev)
+    with _on(dev):
+        usp_kv4_append(s, k, v, key_weight, cu_seqlens, T, k.dtype, lens, stream)
+    return lens
+
+
+def kv4_read(cache: KV4Cache, tokens: int, *, starts=None, dtype=torch.bfloat16, stream=None
+             ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(k, v) [B, tokens, Hkv, D]: the values of rows starts[b] (default 0) ..
+    of every sequence; zeros behind its length."""
+    s = _kv4_struct(cache)
+    dev = cache.k.device
+    if starts is not None:
+        _need(starts, "starts", torch.int32, (s.B,), dev)
+    k = torch.empty((s.B, tokens, s.Hkv, s.D), dtype=dtype, device=dev)
+    v = torch.empty_like(k)
+    with _on(dev):
+        usp_kv4_read(s, starts, tokens, k, v, dtype, stream)
+    return k, v
+
+
+def attn_decode_kv4(q: torch.Tensor, cache: KV4Cache, *, causal=True, window=0, sink_tokens=0,
+                    accumulate=False, softmax_scale=0.0, workspace=None, stream=None
+                    ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(out [B,Tq,Hq,D], lse [B,Tq,Hq]) of the newest Tq tokens q [B,Tq,Hq,D]
+    (already in the cache) against the cached keys; accumulate adds each key's
+    attention weight of this step to cache.key_weight."""
+    s = _kv4_struct(cache)
+    dev = cache.k.device
+    B, Tq, Hq, D = q.shape
+    _need(q, "q", torch.bfloat16, (s.B, Tq, Hq, s.D), dev)
+    if accumulate and cache.key_weight is None:
+        raise ValueError("accumulate needs a cache with key_weight")
+    out = torch.empty_like(q)
+    lse = torch.empty((B, Tq, Hq), dtype=torch.float32, device=dev)
+    ws, ws_n = _use_workspace(
+        workspace,
+        usp_attn_decode_kv4_workspace_size(B, Tq, s.capacity, Hq, s.Hkv, D, accumulate), dev)
+    with _on(dev):
+        usp_attn_decode_kv4(s, q, out, lse, Tq, Hq, softmax_scale, causal, window, sink_tokens,
+                            accumulate, q.dtype, ws, ws_n, stream)
+    return out, lse
+
+
+def attn_key_weights(q, k, lse, *, causal=True, window=0, sink_tokens=0, cu_seqlens=None, cp=1,
+                     layout="contiguous", observe=0, softmax_scale=0.0, flags=0, workspace=None,
+                     stream=None) -> torch.Tensor:
+    """[B,Hkv,S] fp32 (packed [Hkv,T]): the attention weight that each key
+    collected from the observed queries (observe = n: the last n of each
+    sequence; 0: all) and the query heads sharing its KV head, from the
+    forward's q, k (rank-major) and lse."""
+    B, S, Hq, Hkv, D, Bl = _dims(q, k, cu_seqlens)
+    dev = q.device
+    lead = () if cu_seqlens is not None else (Bl,)
+    _need(q, "q", q.dtype, q.shape, dev)
+    _need(k, "k", q.dtype, lead + (S, Hkv, D), dev)
+    _need(lse, "lse", torch.float32, lead + (Hq, S), dev)
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    weight = torch.empty(lead + (Hkv, S), dtype=torch.float32, device=dev)
+    ws, ws_n = _use_workspace(
+        workspace, usp_attn_key_weights_workspace_size(Bl, S, Hq, Hkv, observe, q.dtype, flags),
+        dev)
+    with _on(dev):
+        usp_attn_key_weights(q, k, lse, weight, B, S, Hq, Hkv, D, softmax_scale, causal, window,
+                             sink_tokens, cu_seqlens, cp, layout, observe, q.dtype, flags, ws,
+                             ws_n, stream)
+    return weight
+
+
+def kv4_evict(cache: KV4Cache, keep: int, *, recent=0, sink_tokens=0, out=None, stream=None
+              ) -> Tuple[KV4Cache, torch.Tensor]:
+    """(cache, kept [B,Hkv,keep] int32): every sequence longer than `keep`
+    keeps, in each KV head, its first sink_tokens, its last `recent` and the
+    keys with the largest key_weight, in order; kept gives their old rows (-1
+    behind the last). out: another cache that takes them (default: in place)."""
+    dst = cache if out is None else out
+    if cache.key_weight is None:
+        raise ValueError("eviction needs a cache with key_weight")
+    s = _kv4_struct(cache)
+    d = s if out is None else _kv4_struct(out)
+    dev = cache.k.device
+    if dst.k.device != dev:
+        raise ValueError("both caches must be on one device")
+    if (s.k_descale, s.v_descale) != (d.k_descale, d.v_descale):
+        raise ValueError("both caches must have the same descales")
+    if keep < 1:
+        raise ValueError("keep must be at least 1")
+    kept = torch.empty((s.B, s.Hkv, keep), dtype=torch.int32, device=dev)
+    with _on(dev):
+        usp_kv4_evict(s, d, kept, keep, recent, sink_tokens, stream)
+    return dst, kept

@@ -35,6 +35,15 @@ SIGNATURES = {
                               _i, _i, _i, _vp, _i, _i, _i, _u, _vp, _sz, _vp]),
     "usp_attn_fwd_fp8_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "usp_quantize_e4m3": (_i, [_vp, _vp, _i64, _f, _vp]),
+    "usp_kv4_append": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp]),
+    "usp_kv4_read": (_i, [_vp, _vp, _i, _vp, _vp, _i, _vp]),
+    "usp_attn_decode_kv4": (_i, [_vp, _vp, _vp, _vp, _i, _i, _f, _i, _i, _i, _i, _i, _vp, _sz,
+                                 _vp]),
+    "usp_attn_decode_kv4_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "usp_attn_key_weights": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _i, _i, _vp,
+                                  _i, _i, _i, _i, _u, _vp, _sz, _vp]),
+    "usp_attn_key_weights_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _u]),
+    "usp_kv4_evict": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp]),
     "usp_permute": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
     "usp_status_string": (_c.c_char_p, [_i]),
     "usp_launch_count": (_u64, []),
@@ -49,6 +58,14 @@ SIGNATURES = {
 class KernelStat(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_uint64),
                 ("total_ms", ctypes.c_double)]
+
+
+class Kv4CacheStruct(ctypes.Structure):
+    """usp_kv4_cache_t."""
+    _fields_ = [("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp),
+                ("key_weight", _vp), ("seq_lens", _vp), ("B", _i), ("capacity", _i),
+                ("Hkv", _i), ("D", _i), ("k_descale", _f), ("v_descale", _f)]
+
 
 _lib = None
 

@@ -27,7 +27,8 @@ NVCC_FLAGS = ARCH + [
 ]
 SOURCES = ["api.cu", "permute.cu", "merge.cu", "attn_simt.cu", "decode.cu",
            "attn_fwd_tc.cu", "attn_bwd_tc.cu", "attn_fwd_fp8.cu", "noalloc.cu",
-           "selftest.cu"]
+           "selftest.cu", "kv4_api.cu", "kv4_cache.cu", "kv4_evict.cu", "decode_kv4.cu",
+           "key_weights.cu"]
 
 
 def _nvcc() -> str:

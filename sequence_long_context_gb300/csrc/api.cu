@@ -335,9 +335,10 @@ const char* usp_last_error_detail(void) { return g_detail; }
 
 usp_status_t usp_device_status(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return USP_ERR_CUDA;
-  const int words[5] = {read_clear_fwd_tc_status(), read_clear_bwd_tc_status(),
+  const int words[7] = {read_clear_fwd_tc_status(), read_clear_bwd_tc_status(),
                         read_clear_decode_status(), read_clear_selftest_status(),
-                        read_clear_fwd_fp8_status()};
+                        read_clear_fwd_fp8_status(), read_clear_decode_kv4_status(),
+                        read_clear_key_weights_status()};
   for (int w : words)
     if (w < 0) return USP_ERR_CUDA;
   for (int w : words)
@@ -756,6 +757,43 @@ usp_status_t usp_quantize_e4m3(const void* x, void* out, int64_t n, float inv_sc
   if (n > 0 && (!x || !out)) return USP_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(out)) return USP_ERR_ALIGNMENT;
   return launch_quantize_e4m3(x, out, n, inv_scale, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t usp_attn_key_weights_workspace_size(int B, int S, int Hq, int Hkv, int observe,
+                                           usp_dtype_t dtype, unsigned flags) {
+  if (B < 0 || S < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
+  if (dtype != USP_BF16 || (flags & USP_FLAG_FORCE_SIMT)) return 0;
+  return key_weights_workspace(B, S, Hq, Hkv, observe > 0 ? observe : 0);
+}
+
+usp_status_t usp_attn_key_weights(const void* q, const void* k, const float* lse, float* weight,
+                                  int B, int S, int Hq, int Hkv, int D, float softmax_scale,
+                                  int causal, int window, int sink_tokens,
+                                  const int32_t* cu_seqlens, int cp_size, usp_layout_t layout,
+                                  int observe, usp_dtype_t dtype, unsigned flags,
+                                  void* workspace, size_t workspace_bytes,
+                                  usp_stream_t stream) {
+  Shape s = shape_of(B, S, Hq, Hkv, D, cp_size, 1, layout, dtype, cu_seqlens != nullptr);
+  usp_status_t r = validate(s, window, sink_tokens);
+  if (r != USP_OK) return r;
+  if (flags & ~USP_FLAG_FORCE_SIMT) return USP_ERR_UNSUPPORTED;
+  if (S > 0 && s.B_eff() > 0 && (!q || !k || !lse || !weight)) return USP_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, lse, weight, workspace};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return USP_ERR_ALIGNMENT;
+  if (s.B_eff() == 0 || S == 0) return USP_OK;
+  const size_t need =
+      usp_attn_key_weights_workspace_size(s.B_eff(), S, Hq, Hkv, observe, dtype, flags);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return USP_ERR_WORKSPACE;
+  AttnParams P = make_params(s, softmax_scale, causal, window, sink_tokens, cu_seqlens);
+  P.q = q;
+  P.k = k;
+  P.lse = const_cast<float*>(lse);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int obs = observe > 0 ? observe : 0;
+  if (dtype == USP_BF16 && !(flags & USP_FLAG_FORCE_SIMT))
+    return launch_key_weights_tc(P, weight, obs, workspace, st);
+  return launch_key_weights_simt(P, weight, obs, dtype == USP_BF16, st);
 }
 
 usp_status_t usp_merge_partials(const float* o_parts, const float* lse_parts,

@@ -1,0 +1,812 @@
+// Decode-step attention over the 4-bit KV cache.
+//
+// "Long Context Attention" notes, "Ring Attention" (flash decoding is ring
+// attention at inference time) and "Tree Attention" (log-sum-exp partials
+// combine in any order): the newest Tq tokens of every sequence attend to its
+// cached keys, D (1 + 1/16) bytes per key and KV head.
+//
+// Division of the work. A unit is one (sequence, KV head, block of up to 8 NT
+// query rows); a step is 32 of its keys. All steps of all units, in unit
+// order, are one line of T steps that the CTAs share in equal runs, whatever
+// the lengths (read on the device). CTA c takes steps [T c / N, T (c+1) / N)
+// of N = min(grid, T / 8) CTAs; a run may cover the end of one unit and the
+// start of others. It leaves one partial (m, l, O) per unit it meets, in slot
+// c + unit: between two consecutive partials either c or the unit grows, so
+// the slots differ, and a unit's partials are consecutive. The merge kernel
+// finds them from the same arithmetic.
+//
+// One CTA. Eight warps take the steps of a run in turn. Each warp has its own
+// ring of stages (codes and scales of 32 keys, four untiled bulk copies) and
+// its own online softmax; warps meet only at the end of a unit. The keys and
+// channels are the M side of the matrix products and the query rows the N
+// side (8 rows per product, where 16 would be padding for most head groups):
+//   S^T [keys x rows]  = K [keys x D] Q^T      (bf16 m16n8k16, K exact)
+//   O^T [D x rows]    += V^T [D x keys] P^T    (fp16 m16n8k16, V exact)
+// The K index of a product may be any permutation of the channels (keys) that
+// both operands share. Thread (g, t) = (lane / 4, lane % 4) owns channels
+// [t D/4, ..) of key rows g and g + 8 for K, and channels [g D/8, ..) of keys
+// 2t, 2t+1, 2t+8, 2t+9 for V: vector loads, and one scale per key (D/4 and
+// D/8 divide a block of 32 or are one).
+//
+// 4 bits to 16: the nibble u = c + 8 is placed in the mantissa of a constant
+// power of two B whose step makes it B + u; one packed FMA by (s, -(B + 8) s)
+// gives c s. (B + 8) s must be exact: B = 16 in bf16 (24 s, 6 bits), B = 64 in
+// fp16 (72 s, 8 bits). K uses bf16 because q is bf16 (exact products), V fp16
+// because P in fp16 has a rounding of 2^-11 where bf16 has 2^-8.
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "kv4.cuh"
+#include "kv4_host.h"
+#include "tc_ptx.cuh"
+
+namespace usp {
+namespace {
+
+using namespace kv4;
+using namespace tc;
+
+__device__ int g_decode_kv4_status = 0;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStep = 32;                 // keys per step
+constexpr int kGridMax = 304;             // 152 SMs x 2 resident CTAs
+constexpr float kLazy = 8.f;              // the max moves when it grows by 2^8
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Params {
+  Cache c;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* lse;
+  float* o_part;    // [slots][8 NT][D], columns in the kernel's order
+  float2* ml_part;  // [slots][8 NT]: (m, l) in log2 units
+  float* scores;    // accumulate: [B][H][C][Rs] log2-scaled scores, else nullptr
+  float2* ml;       // accumulate: [B][H][Rs] merged (m, 1 / l)
+  int Tq, Hq, G, R, Rs, nrb;  // R = G Tq rows per KV head, nrb blocks of them
+  int grid;
+  float score_mul;            // softmax scale * log2(e) * k_descale
+  float v_descale;
+  int causal, window, sink;
+};
+
+// What a sequence of L cached tokens has to visit: steps [0, sinks) and
+// [first, ..), `n` in all.
+struct SeqSteps {
+  int n, sinks, skip;  // step s is key step s (s < sinks) or s + skip
+};
+__device__ __forceinline__ SeqSteps seq_steps(const Params& P, int L) {
+  SeqSteps r{0, 0, 0};
+  if (L <= 0) return r;
+  const int all = (L + kStep - 1) / kStep;
+  if (P.window > 0) {
+    const int i0 = max(0, L - P.Tq);                 // first query position
+    const int first = max(0, i0 - P.window + 1) / kStep;
+    r.sinks = min((min(P.sink, L) + kStep - 1) / kStep, first);
+    r.skip = first - r.sinks;
+  }
+  r.n = all - r.skip;
+  return r;
+}
+__device__ __forceinline__ int seq_len(const Params& P, int b) {
+  return clamp_len(__ldg(P.c.lens + b), P.c.C);
+}
+
+// Steps of all sequences, per (KV head, row block), by one warp.
+__device__ __forceinline__ long long total_steps_warp(const Params& P) {
+  long long n = 0;
+  for (int b = threadIdx.x & 31; b < P.c.B; b += 32) n += seq_steps(P, seq_len(P, b)).n;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+__device__ __forceinline__ long long active_ctas(const Params& P, long long T) {
+  const long long want = (T + kWarps - 1) / kWarps;
+  return want < P.grid ? want : P.grid;
+}
+
+// A walk over the steps of a CTA's run: the current unit's steps [s, end).
+struct Walk {
+  int b, hr;        // sequence, KV head * nrb + row block
+  int s, end;       // of the unit
+  long long left;   // steps of the run behind this unit
+};
+__device__ __forceinline__ bool next_unit(const Params& P, Walk& w) {
+  if (w.left <= 0) return false;
+  int n = 0;
+  if (++w.hr == P.c.H * P.nrb) {
+    w.hr = 0;
+    do {
+      ++w.b;
+      n = w.b < P.c.B ? seq_steps(P, seq_len(P, w.b)).n : -1;
+    } while (n == 0);
+    if (n < 0) return false;
+  } else {
+    n = seq_steps(P, seq_len(P, w.b)).n;
+  }
+  w.s = 0;
+  w.end = (int)min((long long)n, w.left);
+  w.left -= w.end;
+  return true;
+}
+
+template <int D>
+struct Stage {
+  static constexpr int kCodes = kStep * D / 2;
+  static constexpr int kScales = kStep * D / kBlock;
+  static constexpr int kKC = 0, kVC = kCodes, kKS = 2 * kCodes, kVS = 2 * kCodes + kScales;
+  static constexpr int kBytes = 2 * kCodes + 2 * kScales;
+};
+// Two resident CTAs (8 rows) have 113 KB each, which leaves two stages per
+// warp at D = 128; one CTA (16 rows, by registers) has room for four.
+template <int D, int NT>
+struct Smem {
+  static constexpr int kStages = (D == 128 && NT == 1) ? 2 : 4;
+  static constexpr int kStage = 0;  // [kWarps][kStages]
+  static constexpr int kRedStride = D + 4;
+  static constexpr int kRed = kStage + kWarps * kStages * Stage<D>::kBytes;  // [kWarps][8][D + 4]
+  static constexpr int kML = kRed + kWarps * 8 * kRedStride * 4;             // [kWarps][8] float2
+  static constexpr int kBar = kML + kWarps * 8 * 8;
+  static constexpr int kMisc = kBar + kWarps * kStages * 8;  // abort, run
+  static constexpr int kBytes = kMisc + 64;
+  static_assert(kBytes <= (NT == 1 ? 113 : 227) * 1024, "residency");
+  static_assert(kRed % 16 == 0 && kML % 16 == 0 && kBar % 8 == 0 && kMisc % 16 == 0, "alignment");
+};
+
+__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// (x & mask) | base
+template <uint32_t kMask, uint32_t kBase>
+__device__ __forceinline__ uint32_t and_or(uint32_t x) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "n"(kMask), "n"(kBase));
+  return d;
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+// Row of a 16-key tile that stands at index i (0..15) of the products' M (K)
+// or K (V) side: neighbouring rows go to indices whose threads read together,
+// so that a quarter (V: half) of a warp spreads over both halves of the banks.
+__device__ __forceinline__ int tile_key(int i) { return i ^ ((i >> 1) & 1); }
+
+// Starts the copies of one step into a stage.
+template <int D>
+__device__ __forceinline__ void load_step(const Params& P, const Walk& w, uint32_t stage,
+                                          uint32_t bar) {
+  const int L = seq_len(P, w.b);
+  const SeqSteps q = seq_steps(P, L);
+  const int key0 = (w.s < q.sinks ? w.s : w.s + q.skip) * kStep;
+  // whole 16-row groups that hold cached keys (the capacity is a multiple of 16)
+  const int rows = min(kStep, (L - key0 + kRowAlign - 1) / kRowAlign * kRowAlign);
+  const long long row = head_row(P.c, w.b, w.hr / P.nrb) + key0;
+  const uint32_t cb = rows * (D / 2), sb = rows * (D / kBlock);
+  mbar_expect_tx(bar, 2 * (cb + sb));
+  bulk_load(stage + Stage<D>::kKC, P.c.kc + row * (D / 2), cb, bar);
+  bulk_load(stage + Stage<D>::kKS, P.c.ks + row * (D / kBlock), sb, bar);
+  bulk_load(stage + Stage<D>::kVC, P.c.vc + row * (D / 2), cb, bar);
+  bulk_load(stage + Stage<D>::kVS, P.c.vs + row * (D / kBlock), sb, bar);
+}
+
+template <int D, int NT, bool SC>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(const Params P) {
+  using L = Smem<D, NT>;
+  constexpr int kStages = L::kStages;
+  using St = Stage<D>;
+  constexpr int kRows = 8 * NT;
+  constexpr int kWK = D / 32;      // 32-bit words of codes a thread has per K row
+  constexpr int kWV = D / 64;      // and per V row
+  constexpr int kMT = D / 16;      // 16-channel tiles of O^T
+  extern __shared__ __align__(128) uint8_t sm[];
+  const uint32_t sbase = smem_u32(sm);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kMisc);
+  long long* run = reinterpret_cast<long long*>(sm + L::kMisc + 16);  // first step, count, ..
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t my_stage = sbase + L::kStage + warp * kStages * St::kBytes;
+  uint8_t* my_stage_p = sm + L::kStage + warp * kStages * St::kBytes;
+  const uint32_t my_bar = sbase + L::kBar + warp * kStages * 8;
+
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(my_bar + 8 * s, 1);
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    const int per_seq = P.c.H * P.nrb;
+    const long long T = total_steps_warp(P) * per_seq;
+    const long long N = active_ctas(P, T);
+    long long first = 0, count = 0;
+    if (blockIdx.x < N) {
+      first = T * blockIdx.x / N;
+      count = T * (blockIdx.x + 1) / N - first;
+    }
+    // the sequence that holds step `first`: sums over 32 sequences at a time
+    int b0 = 0;
+    long long before = 0;
+    if (count > 0) {
+      for (;; b0 += 32) {
+        const int b = b0 + lane;
+        long long n = b < P.c.B ? (long long)seq_steps(P, seq_len(P, b)).n * per_seq : 0;
+        long long inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += x;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, before + inc > first);
+        if (over) {
+          const int src = __ffs(over) - 1;
+          before += __shfl_sync(0xffffffffu, inc - n, src);
+          b0 += src;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+        if (b0 + 32 >= P.c.B) {  // not reached: first < T
+          count = 0;
+          break;
+        }
+      }
+    }
+    if (lane == 0) {
+      run[0] = first - before;  // within sequence b0
+      run[1] = count;
+      run[2] = b0;
+      *abort_flag = 0;
+    }
+  }
+  __syncthreads();
+  if (run[1] == 0) return;
+  Walk cur;
+  {
+    cur.b = (int)run[2];
+    const int n = seq_steps(P, seq_len(P, cur.b)).n;
+    cur.hr = (int)(run[0] / n);
+    cur.s = (int)(run[0] - (long long)cur.hr * n);
+    cur.end = (int)min((long long)n, cur.s + run[1]);
+    cur.left = run[1] - (cur.end - cur.s);
+  }
+  // this warp's copies run ahead of its computation, over the ends of units
+  Walk pre = cur;
+  pre.s += warp;
+  bool more = true;
+  auto settle = [&]() {  // to the warp's next step, maybe in a later unit
+    while (more && pre.s >= pre.end) {
+      more = next_unit(P, pre);
+      pre.s += warp;
+    }
+  };
+  settle();
+  int issued = 0, used = 0;
+  auto issue = [&]() {
+    if (!more) return;
+    if (lane == 0)
+      load_step<D>(P, pre, my_stage + (issued % kStages) * St::kBytes,
+                   my_bar + 8 * (issued % kStages));
+    ++issued;
+    pre.s += kWarps;
+    settle();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) issue();
+
+  bool ok = true;
+  for (;;) {
+    // ---------------------------------------------------------------- a unit
+    const int b = cur.b, h = cur.hr / P.nrb, rb = cur.hr - h * P.nrb;
+    const int len = seq_len(P, b);
+    const SeqSteps steps = seq_steps(P, len);
+    // Q^T fragments: product kk = 2w + jj takes channels (8w + 2jj, + 4) and
+    // (8w + 2jj + 1, + 4) of the thread's run of D/4
+    uint32_t qf[NT][2 * kWK][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = rb * kRows + nt * 8 + g;
+      const __nv_bfloat16* src = nullptr;
+      if (r < P.R) {
+        const int hh = r / P.Tq, tok = r - hh * P.Tq;
+        src = P.q + (((long long)b * P.Tq + tok) * P.Hq + h * P.G + hh) * D + t * (D / 4);
+      }
+#pragma unroll
+      for (int w = 0; w < kWK; ++w) {
+        const uint4 x = src ? __ldg(reinterpret_cast<const uint4*>(src) + w) : make_uint4(0, 0, 0, 0);
+        qf[nt][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);
+        qf[nt][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);
+        qf[nt][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
+        qf[nt][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
+      }
+    }
+    float o[NT][kMT][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    const int i_first = len - P.Tq;  // position of token 0
+    for (int s = cur.s + warp; s < cur.end; s += kWarps) {
+      const int st = used % kStages;
+      if (!mbar_wait(my_bar + 8 * st, (used / kStages) & 1, abort_flag, &g_decode_kv4_status))
+        ok = false;
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      ++used;
+      const uint8_t* stp = my_stage_p + st * St::kBytes;
+      const int key0 = (s < steps.sinks ? s : s + steps.skip) * kStep;
+      // does the mask (or the sequence's end) hide any of the step's keys?
+      const int last = key0 + kStep - 1;
+      const bool masked = last >= len || i_first < 0 || (P.causal && last > i_first) ||
+                          (P.window > 0 && len - 1 - key0 >= P.window);
+      // ------------------------------------------------------------ scores
+      float sc[NT][2][4];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r0 = 16 * half + tile_key(g), r1 = r0 + 8;
+        uint32_t k0[kWK], k1[kWK];
+        const uint8_t* kc = stp + St::kKC + t * (D / 8);
+        if constexpr (D == 128) {
+          const uint4 a = *reinterpret_cast<const uint4*>(kc + r0 * (D / 2));
+          const uint4 c = *reinterpret_cast<const uint4*>(kc + r1 * (D / 2));
+          k0[0] = a.x; k0[1] = a.y; k0[2] = a.z; k0[3] = a.w;
+          k1[0] = c.x; k1[1] = c.y; k1[2] = c.z; k1[3] = c.w;
+        } else {
+          const uint2 a = *reinterpret_cast<const uint2*>(kc + r0 * (D / 2));
+          const uint2 c = *reinterpret_cast<const uint2*>(kc + r1 * (D / 2));
+          k0[0] = a.x; k0[1] = a.y;
+          k1[0] = c.x; k1[1] = c.y;
+        }
+        const uint8_t* ks = stp + St::kKS + (t * (D / 4)) / kBlock;
+        const float2 ss = __half22float2(
+            e4m3x2_to_half2(ks[r0 * (D / kBlock)] | (ks[r1 * (D / kBlock)] << 8)));
+        const uint32_t s0 = pack_bf16(ss.x, ss.x), s1 = pack_bf16(ss.y, ss.y);
+        const uint32_t z0 = pack_bf16(-24.f * ss.x, -24.f * ss.x);
+        const uint32_t z1 = pack_bf16(-24.f * ss.y, -24.f * ss.y);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[nt][half][e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWK; ++w) {
+          // nibbles j and j + 4 of a word: channels 8w + j, 8w + 4 + j
+          auto pair = [](uint32_t x, int j) {
+            const uint32_t y = j == 0 ? x << 3 : j == 1 ? x >> 1 : j == 2 ? x >> 5 : x >> 9;
+            return and_or<0x00780078u, 0x41804180u>(y);
+          };
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const uint32_t a[4] = {bf2_fma(pair(k0[w], 2 * jj), s0, z0),
+                                   bf2_fma(pair(k1[w], 2 * jj), s1, z1),
+                                   bf2_fma(pair(k0[w], 2 * jj + 1), s0, z0),
+                                   bf2_fma(pair(k1[w], 2 * jj + 1), s1, z1)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_bf16(sc[nt][half], a, qf[nt][2 * w + jj][0], qf[nt][2 * w + jj][1]);
+          }
+        }
+      }
+      // ----------------------------------------------------------- softmax
+      bool grow = false;
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = sc[nt][half][e] * P.score_mul;
+            if (masked) {
+              const int j = key0 + 16 * half + tile_key(g) + 8 * (e >> 1);
+              const int tok = (rb * kRows + nt * 8 + 2 * t + (e & 1)) % P.Tq;
+              const int i = i_first + tok;
+              const bool see = j < len && i >= 0 && (!P.causal || j <= i) &&
+                               (P.window <= 0 || i - j < P.window || j < P.sink);
+              if (!see) x = -INFINITY;
+            }
+            sc[nt][half][e] = x;
+          }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[nt][e] = fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][e + 2]),
+                            fmaxf(sc[nt][1][e], sc[nt][1][e + 2]));
+          grow |= mx[nt][e] > m[nt][e] + kLazy;
+        }
+      }
+      if constexpr (SC) {
+        // the weights need every score once the whole row's sum is known
+        float* dst = P.scores + head_row(P.c, b, h) * P.Rs;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = rb * kRows + nt * 8 + 2 * t;
+          if (r >= P.Rs) continue;
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const int j = key0 + 16 * half + tile_key(g) + 8 * (e >> 1);
+              if (j < len)
+                *reinterpret_cast<float2*>(dst + (long long)j * P.Rs + r) =
+                    make_float2(sc[nt][half][e], sc[nt][half][e + 1]);
+            }
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float a[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = mx[nt][e];
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+            x = fmaxf(x, m[nt][e]);
+            a[e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - x);
+            m[nt][e] = x;
+            l[nt][e] *= a[e];
+          }
+#pragma unroll
+          for (int i = 0; i < kMT; ++i) {
+            o[nt][i][0] *= a[0];
+            o[nt][i][1] *= a[1];
+            o[nt][i][2] *= a[0];
+            o[nt][i][3] *= a[1];
+          }
+        }
+      }
+      uint32_t pf[NT][2][2];  // P^T fragments: [half][keys 0-7, 8-15]
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = ex2(sc[nt][half][e] - ((e & 1) ? m1 : m0));
+          l[nt][0] += p[0] + p[2];
+          l[nt][1] += p[1] + p[3];
+          pf[nt][half][0] = movmatrix_t(half2_bits(__floats2half2_rn(p[0], p[1])));
+          pf[nt][half][1] = movmatrix_t(half2_bits(__floats2half2_rn(p[2], p[3])));
+        }
+      }
+      // -------------------------------------------------------------- P V
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int ka = 16 * half + tile_key(2 * t), kb = 16 * half + tile_key(2 * t + 1);
+        const int keys[4] = {ka, kb, ka + 8, kb + 8};
+        uint32_t vw[4][kWV], sb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* vc = stp + St::kVC + keys[i] * (D / 2) + g * (D / 16);
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(vc);
+            vw[i][0] = x.x;
+            vw[i][1] = x.y;
+          } else {
+            vw[i][0] = *reinterpret_cast<const uint32_t*>(vc);
+          }
+          sb[i] = stp[St::kVS + keys[i] * (D / kBlock) + (g * (D / 8)) / kBlock];
+          // rows behind the sequence hold anything: 0, so that 0 * it is 0
+          if (masked && key0 + keys[i] >= len) sb[i] = 0;
+        }
+        const __half2 sab = e4m3x2_to_half2(sb[0] | (sb[1] << 8));
+        const __half2 scd = e4m3x2_to_half2(sb[2] | (sb[3] << 8));
+        const __half2 m72 = __float2half2_rn(-72.f);
+        const uint32_t s0 = half2_bits(sab), z0 = half2_bits(__hmul2(sab, m72));
+        const uint32_t s1 = half2_bits(scd), z1 = half2_bits(__hmul2(scd, m72));
+        auto pair = [](uint32_t x, int j) {
+          const uint32_t y = j == 0 ? x << 4 : j == 1 ? x : j == 2 ? x >> 4 : x >> 8;
+          return and_or<0x00F000F0u, 0x54005400u>(y);
+        };
+#pragma unroll
+        for (int w = 0; w < kWV; ++w) {
+          // channels 8w + 0..3 (low halves) and 8w + 4..7 of both keys
+          const uint32_t xl = __byte_perm(vw[0][w], vw[1][w], 0x5410);
+          const uint32_t xh = __byte_perm(vw[0][w], vw[1][w], 0x7632);
+          const uint32_t yl = __byte_perm(vw[2][w], vw[3][w], 0x5410);
+          const uint32_t yh = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a[4] = {h2_fma(pair(xl, j), s0, z0), h2_fma(pair(xh, j), s0, z0),
+                                   h2_fma(pair(yl, j), s1, z1), h2_fma(pair(yh, j), s1, z1)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(o[nt][4 * w + j], a, pf[nt][half][0], pf[nt][half][1]);
+          }
+        }
+      }
+      __syncwarp();  // the stage has been read
+      issue();
+    }
+    // ------------------------------------------------- the unit's partial
+    // O in the order (tile i, half, g): element 16 i + 8 half + g of a row is
+    // channel g D/8 + 8 (i / 4) + i % 4 + 4 half
+    const long long slot = (long long)blockIdx.x + (long long)b * P.c.H * P.nrb + cur.hr;
+    float* red = reinterpret_cast<float*>(sm + L::kRed);
+    float2* ml = reinterpret_cast<float2*>(sm + L::kML);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[nt][e];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        if (g == 0) ml[warp * 8 + 2 * t + e] = make_float2(m[nt][e], x);
+      }
+      float* mine = red + (warp * 8 + 2 * t) * L::kRedStride + g;
+#pragma unroll
+      for (int i = 0; i < kMT; ++i) {
+        mine[16 * i] = o[nt][i][0];
+        mine[L::kRedStride + 16 * i] = o[nt][i][1];
+        mine[16 * i + 8] = o[nt][i][2];
+        mine[L::kRedStride + 16 * i + 8] = o[nt][i][3];
+      }
+      __syncthreads();
+      for (int x = threadIdx.x; x < 8 * D; x += kThreads) {
+        const int r = x / D, d = x - r * D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * 8 + r].x);
+        float os = 0.f, ls = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 a = ml[w * 8 + r];
+          const float f = a.x == -INFINITY ? 0.f : ex2(a.x - M);
+          ls += a.y * f;
+          os += red[(w * 8 + r) * L::kRedStride + d] * f;
+        }
+        P.o_part[(slot * kRows + nt * 8 + r) * D + d] = os;
+        if (d == 0) P.ml_part[slot * kRows + nt * 8 + r] = make_float2(M, ls);
+      }
+      __syncthreads();
+    }
+    if (*abort_flag) break;
+    if (!next_unit(P, cur)) break;
+  }
+  // an aborted warp lets its copies in flight land before the CTA ends
+  if (lane == 0 && *abort_flag)
+    for (; used < issued; ++used) mbar_wait_drain(my_bar + 8 * (used % kStages), (used / kStages) & 1);
+}
+
+// One block per (unit, 8 NT rows): the unit's partials, which are consecutive
+// slots, are merged in key order by blocks of D threads per part.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) merge_kv4_kernel(const Params P) {
+  constexpr int kRows = 8 * NT;
+  constexpr int kParts = 256 / D;
+  __shared__ float s_o[kParts][D];
+  __shared__ float2 s_ml[kParts];
+  __shared__ long long s_n[2];
+  const int unit = blockIdx.x, r = blockIdx.y;  // r: row within the block
+  const int per_seq = P.c.H * P.nrb;
+  const int b = unit / per_seq, hr = unit - b * per_seq;
+  const int h = hr / P.nrb, rb = hr - h * P.nrb;
+  const int row = rb * kRows + r;
+  if (row >= P.R) return;
+  if (threadIdx.x < 32) {
+    // steps of all sequences, and of those before b
+    long long all = 0, before = 0;
+    for (int i = threadIdx.x; i < P.c.B; i += 32) {
+      const long long n = seq_steps(P, seq_len(P, i)).n;
+      all += n;
+      if (i < b) before += n;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    if (threadIdx.x == 0) {
+      const long long T = all * per_seq, N = active_ctas(P, T);
+      const long long n = seq_steps(P, seq_len(P, b)).n;
+      const long long a = before * per_seq + n * hr;
+      // CTA c holds step x iff c = ((x + 1) N - 1) / T
+      s_n[0] = n > 0 ? ((a + 1) * N - 1) / T : 0;
+      s_n[1] = n > 0 ? ((a + n) * N - 1) / T : -1;
+    }
+  }
+  __syncthreads();
+  const long long c0 = s_n[0] + unit, c1 = s_n[1] + unit;  // slots
+  const int part = threadIdx.x / D, d = threadIdx.x - part * D;
+  float M = -INFINITY, ls = 0.f, os = 0.f;
+  for (long long s = c0 + part; s <= c1; s += kParts) {
+    const float2 a = P.ml_part[s * kRows + r];
+    const float x = P.o_part[(s * kRows + r) * D + d];
+    const float Mn = fmaxf(M, a.x);
+    const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn);
+    const float f1 = a.x == -INFINITY ? 0.f : ex2(a.x - Mn);
+    os = os * f0 + x * f1;
+    ls = ls * f0 + a.y * f1;
+    M = Mn;
+  }
+  s_o[part][d] = os;
+  if (d == 0) s_ml[part] = make_float2(M, ls);
+  __syncthreads();
+  if (part != 0) return;
+  float Mt = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) Mt = fmaxf(Mt, s_ml[i].x);
+  float lt = 0.f, ot = 0.f;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    const float f = s_ml[i].x == -INFINITY ? 0.f : ex2(s_ml[i].x - Mt);
+    lt += s_ml[i].y * f;
+    ot += s_o[i][d] * f;
+  }
+  const int hh = row / P.Tq, tok = row - hh * P.Tq;
+  const long long o_row = ((long long)b * P.Tq + tok) * P.Hq + h * P.G + hh;
+  const bool none = lt == 0.f;  // no visible key (a NaN score makes lt NaN)
+  const float inv = none ? 0.f : 1.f / lt;
+  const int i = d >> 4, half = (d >> 3) & 1, g = d & 7;
+  const int ch = g * (D / 8) + 8 * (i >> 2) + (i & 3) + 4 * half;
+  P.out[o_row * D + ch] = __float2bfloat16_rn(none ? 0.f : ot * inv * P.v_descale);
+  if (d == 0) {
+    P.lse[o_row] = none ? -INFINITY : (Mt + log2f(lt)) * kLn2;
+    if (P.ml) P.ml[((long long)b * P.c.H + h) * P.Rs + row] = make_float2(none ? 0.f : Mt, inv);
+  }
+}
+
+// key_weight[j] += sum over the rows of 2^(score - m) / l.
+__global__ void __launch_bounds__(256) weight_kv4_kernel(const Params P) {
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int len = seq_len(P, b);
+  const SeqSteps q = seq_steps(P, len);
+  const long long head = head_row(P.c, b, h);
+  const float2* ml = P.ml + ((long long)b * P.c.H + h) * P.Rs;
+  for (long long x = blockIdx.x * 256ll + threadIdx.x; x < (long long)q.n * kStep;
+       x += (long long)gridDim.x * 256) {
+    const int s = (int)(x / kStep);
+    const int j = (s < q.sinks ? s : s + q.skip) * kStep + (int)(x % kStep);
+    if (j >= len) continue;
+    const float* sc = P.scores + (head + j) * P.Rs;
+    float w = 0.f;
+    for (int r = 0; r < P.R; ++r) {
+      const float2 a = __ldg(ml + r);
+      w += ex2(sc[r] - a.x) * a.y;
+    }
+    P.c.w[head + j] += w;
+  }
+}
+
+// ------------------------------------------------------------------- host
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Ws {
+  size_t o, ml, scores, merged, total;
+};
+int tiles_for(int R) { return R <= 8 ? 1 : 2; }
+
+Ws layout(int B, int Tq, int C, int Hq, int Hkv, int D, int accumulate) {
+  const long long R = (long long)(Hq / Hkv) * Tq;
+  const int rows = 8 * tiles_for((int)(R < 16 ? R : 16));
+  const long long nrb = (R + rows - 1) / rows;
+  const long long slots = (long long)B * Hkv * nrb + kGridMax;
+  const long long Rs = (R + 1) / 2 * 2;
+  Ws w{};
+  size_t at = 0;
+  w.o = at;
+  at += up256((size_t)slots * rows * D * 4);
+  w.ml = at;
+  at += up256((size_t)slots * rows * 8);
+  if (accumulate) {
+    w.scores = at;
+    at += up256((size_t)B * Hkv * C * Rs * 4);
+    w.merged = at;
+    at += up256((size_t)B * Hkv * Rs * 8);
+  }
+  w.total = at;
+  return w;
+}
+
+template <int D, int NT, bool SC>
+usp_status_t launch_t(const Params& P, cudaStream_t st) {
+  const int smem = Smem<D, NT>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(decode_kv4_kernel<D, NT, SC>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
+  {
+    ProfScope ps(st, "attn_decode_kv4");
+    decode_kv4_kernel<D, NT, SC><<<P.grid, kThreads, smem, st>>>(P);
+  }
+  note_launch();
+  usp_status_t r = check_launch();
+  if (r != USP_OK) return r;
+  {
+    ProfScope ps(st, "attn_decode_kv4_merge");
+    merge_kv4_kernel<D, NT><<<dim3(P.c.B * P.c.H * P.nrb, 8 * NT), 256, 0, st>>>(P);
+  }
+  note_launch();
+  if ((r = check_launch()) != USP_OK) return r;
+  if constexpr (SC) {
+    int bx = (P.c.C + 255) / 256;
+    const int cap = 152 * 16 / (P.c.B * P.c.H) + 1;
+    {
+      ProfScope ps(st, "attn_decode_kv4_weight");
+      weight_kv4_kernel<<<dim3(bx < cap ? bx : cap, P.c.H, P.c.B), 256, 0, st>>>(P);
+    }
+    note_launch();
+    r = check_launch();
+  }
+  return r;
+}
+
+template <int D>
+usp_status_t launch_d(const Params& P, int nt, cudaStream_t st) {
+  if (P.scores) return nt == 1 ? launch_t<D, 1, true>(P, st) : launch_t<D, 2, true>(P, st);
+  return nt == 1 ? launch_t<D, 1, false>(P, st) : launch_t<D, 2, false>(P, st);
+}
+
+}  // namespace
+
+size_t decode_kv4_workspace(int B, int Tq, int C, int Hq, int Hkv, int D, int accumulate) {
+  return layout(B, Tq, C, Hq, Hkv, D, accumulate).total;
+}
+
+usp_status_t launch_decode_kv4(const DecodeKv4Args& a, void* workspace, cudaStream_t st) {
+  const Ws w = layout(a.c.B, a.Tq, a.c.C, a.Hq, a.c.H, a.D, a.accumulate);
+  char* base = static_cast<char*>(workspace);
+  Params P{};
+  P.c = a.c;
+  P.q = static_cast<const __nv_bfloat16*>(a.q);
+  P.out = static_cast<__nv_bfloat16*>(a.out);
+  P.lse = a.lse;
+  P.o_part = reinterpret_cast<float*>(base + w.o);
+  P.ml_part = reinterpret_cast<float2*>(base + w.ml);
+  if (a.accumulate) {
+    P.scores = reinterpret_cast<float*>(base + w.scores);
+    P.ml = reinterpret_cast<float2*>(base + w.merged);
+  }
+  P.Tq = a.Tq;
+  P.Hq = a.Hq;
+  P.G = a.Hq / a.c.H;
+  P.R = P.G * a.Tq;
+  P.Rs = (P.R + 1) / 2 * 2;
+  const int nt = tiles_for(P.R);
+  P.nrb = (P.R + 8 * nt - 1) / (8 * nt);
+  P.grid = nt == 1 ? kGridMax : kGridMax / 2;
+  P.score_mul = a.scale * kLog2e * a.k_descale;
+  P.v_descale = a.v_descale;
+  P.causal = a.causal;
+  P.window = a.window;
+  P.sink = a.sink;
+  return a.D == 128 ? launch_d<128>(P, nt, st) : launch_d<64>(P, nt, st);
+}
+
+int read_clear_decode_kv4_status() {
+  int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_decode_kv4_status, sizeof(int)) != cudaSuccess) return -1;
+  if (v != 0) cudaMemcpyToSymbol(g_decode_kv4_status, &z, sizeof(int));
+  return v;
+}
+
+}  // namespace usp

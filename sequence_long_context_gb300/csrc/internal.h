@@ -85,6 +85,18 @@ int read_clear_selftest_status();  // -1 on a CUDA error
 int decode_max_rows();
 int decode_keys_per_tile();
 
+int read_clear_decode_kv4_status();  // decode_kv4.cu; -1 on a CUDA error
+
+// key_weights.cu. P: the problem (q, k, lse and the masks); weight [Bt][Hkv][S]
+// fp32; observe 0: every query, else the last `observe` of each sequence. The
+// tensor-core kernel (bf16) takes any shape and needs the workspace's bytes.
+size_t key_weights_workspace(int B, int S, int Hq, int Hkv, int observe);
+usp_status_t launch_key_weights_tc(const AttnParams& P, float* weight, int observe,
+                                   void* workspace, cudaStream_t st);
+usp_status_t launch_key_weights_simt(const AttnParams& P, float* weight, int observe, int bf16,
+                                     cudaStream_t st);
+int read_clear_key_weights_status();  // -1 on a CUDA error
+
 bool bwd_tc_supported(const AttnParams& P);
 usp_status_t launch_bwd_tc(const AttnParams& P, cudaStream_t st);
 int read_clear_bwd_tc_status();  // -1 on a CUDA error

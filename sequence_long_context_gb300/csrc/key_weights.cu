@@ -1,0 +1,656 @@
+// How much each key of a prompt was attended: column sums of the attention
+// matrix, from the forward's q, k and LSE.
+//
+//     weight[g][j] = sum over query heads h of group g and observed queries i
+//                    that see key j of exp(scale <q_i,h, k_j> - LSE_i,h)
+// ("Long Context Attention" notes, "Motivation": the LSE is what the forward
+// keeps; with it a probability needs no second pass over its row.)
+//
+// Tensor-core kernel (bf16). One CTA owns 256 keys (two tiles of 128) of one
+// KV head and takes the query tiles of 64 that may see them, for some of the
+// group's query heads and a segment of the queries: S^T = K Q^T, keys on the
+// 128 TMEM lanes, so that a softmax thread owns a key and the column sum is a
+// register. Nothing is normalised or rescaled, and nothing goes back to the
+// tensor core. 256 keys share each query tile: 16 KB of Q per 2 x 128 x 64
+// scores keeps the L2 traffic at a quarter of what one tile of 64 would need.
+// Roles (320 threads, two CTAs per SM):
+//   warps 0-7  softmax: warp w owns keys [32 w, 32 w + 32) of the 256
+//   warp 8     producer: finds the query tiles that can see the keys (32 at a
+//              time, one per lane), loads Q (two slots) and, with all lanes,
+//              the tile's LSE and natural positions (a ring of eight)
+//   warp 9     MMA issuer, owner of tensor memory: S^T of key tile a, buffer c
+//              in columns [128 a + 64 c, + 64)
+// Positions are read per query from shared memory, so a tile may cross chunk
+// and shard boundaries: any layout and any length has this kernel.
+//
+// The partial sums of several heads or segments go to the workspace and are
+// added in a fixed order by a second kernel.
+//
+// CUDA-core kernel (fp32 inputs, and as a cross-check): 64 x 64 tiles.
+#include <cudaTypedefs.h>
+
+#include <cstdio>
+
+#include "internal.h"
+#include "tc_ptx.cuh"
+#include "tile_sched.cuh"
+
+namespace usp {
+namespace {
+
+using namespace tc;
+
+__device__ int g_key_weights_status = 0;
+
+constexpr int kQT = 64;             // queries per tile
+constexpr int kKeys = 2 * kTile;    // keys per CTA
+constexpr int kSoftWarps = 8;
+constexpr int kProducerWarp = kSoftWarps;
+constexpr int kMmaWarp = kProducerWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kRing = 8;            // entries of query statistics
+constexpr int kEnd = -1;
+constexpr int kNowhere = -(1 << 30);  // position of a row that is not observed
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct WeightParams {
+  AttnParams P;
+  float* part;   // [parts][Bt][Hkv][S]
+  int observe;   // 0: all
+  int hpi;       // query heads per CTA
+  int nseg;      // segments of query tiles
+  int tps;       // query tiles per segment
+  int nkb;       // key blocks
+  int ntiles;    // query tiles
+};
+
+template <int D>
+struct WSmem {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kKHalf = kTile * 128;            // 64 channels of one key tile
+  static constexpr int kKTile = kKHalf * kHalves;
+  static constexpr int kQHalf = kQT * 128;
+  static constexpr int kQTile = kQHalf * kHalves;
+  static constexpr int kK = 0;
+  static constexpr int kQ = kK + 2 * kKTile;            // 2 slots
+  static constexpr int kStat = kQ + 2 * kQTile;         // kRing x (lse2[64], pos[64])
+  static constexpr int kStatBytes = 2 * kQT * 4;
+  static constexpr int kSched = kStat + kRing * kStatBytes;  // kRing ints
+  static constexpr int kBar = kSched + kRing * 4;
+  static constexpr int kKFull = 0, kQFull = 1, kQFree = 3, kSFull = 5, kSFree = 9, kStatFull = 13,
+                       kMmaDone = kStatFull + kRing, kNumBars = kMmaDone + 1;
+  static constexpr int kMisc = (kBar + 8 * kNumBars + 15) / 16 * 16;
+  static constexpr int kBytes = kMisc + 16;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 113 * 1024, "two CTAs per SM");
+  static_assert(kBar % 8 == 0 && kStat % 16 == 0, "alignment");
+};
+
+// The queries that see the key at natural position j, as positions [lo, hi].
+struct Seen {
+  int lo, hi;
+};
+__device__ __forceinline__ Seen seen_by(const AttnParams& P, int j) {
+  int s = 0, e = P.S;
+  if (P.cu != nullptr) {
+    const int n = seg_of(P.cu, P.nseq, j);
+    s = __ldg(P.cu + n);
+    e = __ldg(P.cu + n + 1);
+  }
+  Seen r;
+  r.lo = P.causal ? j : s;
+  r.hi = e - 1;
+  if (P.window > 0 && j - s >= P.sink) r.hi = min(r.hi, j + P.window - 1);
+  return r;
+}
+
+// Natural position of the query at rank-major row p if it is observed.
+__device__ __forceinline__ int observed_pos(const WeightParams& W, int p) {
+  const AttnParams& P = W.P;
+  if (p >= P.S) return kNowhere;
+  const int i = nat_pos(P, p);
+  if (W.observe > 0) {
+    int e = P.S;
+    if (P.cu != nullptr) e = __ldg(P.cu + seg_of(P.cu, P.nseq, i) + 1);
+    if (i < e - W.observe) return kNowhere;
+  }
+  return i;
+}
+
+// Bounds of the natural positions of rank-major rows [p0, p0 + n) (clipped to
+// S); exact where the rows are one run of a chunk, else row by row.
+__device__ __forceinline__ PosRange row_bounds(const AttnParams& P, int p0, int n) {
+  PosRange r{1, 0};
+  const int p1 = min(p0 + n, P.S) - 1;
+  if (p1 < p0) return r;
+  const int run = P.layout == kZigzag ? P.chunk : P.shard;
+  if (p0 / run == p1 / run) {
+    r.lo = nat_pos(P, p0);
+    r.hi = nat_pos(P, p1);
+    return r;
+  }
+  if (P.layout == kContiguous) {
+    r.lo = p0;
+    r.hi = p1;
+    return r;
+  }
+  r.lo = P.S;
+  r.hi = -1;
+  for (int p = p0; p <= p1; ++p) {
+    const int i = nat_pos(P, p);
+    r.lo = min(r.lo, i);
+    r.hi = max(r.hi, i);
+  }
+  return r;
+}
+
+struct KeyBlock {
+  PosRange k;     // natural positions of the keys
+  PosRange q;     // of the queries that may see one of them
+  int seg0, seg1; // packed sequences of the first and last key
+};
+__device__ __forceinline__ KeyBlock key_block(const AttnParams& P, int key0) {
+  KeyBlock b;
+  b.k = row_bounds(P, key0, kKeys);
+  int s0 = 0, e1 = P.S;
+  b.seg0 = b.seg1 = 0;
+  if (P.cu != nullptr) {
+    b.seg0 = seg_of(P.cu, P.nseq, b.k.lo);
+    b.seg1 = seg_of(P.cu, P.nseq, b.k.hi);
+    s0 = __ldg(P.cu + b.seg0);
+    e1 = __ldg(P.cu + b.seg1 + 1);
+  }
+  const bool sinks = P.sink > 0 && (b.seg0 != b.seg1 || b.k.lo < s0 + P.sink);
+  b.q.lo = P.causal ? b.k.lo : s0;
+  b.q.hi = (P.window > 0 && !sinks) ? min(e1 - 1, b.k.hi + P.window - 1) : e1 - 1;
+  return b;
+}
+
+// empty / full / masked for the queries of tile qt against the key block.
+__device__ __forceinline__ int classify_tile(const WeightParams& W, int qt, const KeyBlock& b) {
+  const AttnParams& P = W.P;
+  const PosRange q = row_bounds(P, qt * kQT, kQT);
+  if (q.lo > q.hi || q.hi < b.q.lo || q.lo > b.q.hi) return kClsEmpty;
+  bool all = qt * kQT + kQT <= P.S;
+  if (W.observe > 0) {
+    if (P.cu == nullptr) {
+      if (q.hi < P.S - W.observe) return kClsEmpty;
+      all = all && q.lo >= P.S - W.observe;
+    } else {
+      // the last `observe` of some sequence between q.lo's and q.hi's
+      const int n = seg_of(P.cu, P.nseq, q.lo);
+      const int e = __ldg(P.cu + n + 1);
+      if (q.hi < e - W.observe) return kClsEmpty;
+      all = all && q.lo >= e - W.observe;
+    }
+  }
+  if (P.cu != nullptr) {
+    const int s0 = seg_of(P.cu, P.nseq, q.lo), s1 = seg_of(P.cu, P.nseq, q.hi);
+    if (s0 != s1 || b.seg0 != b.seg1 || s0 != b.seg0) return kClsMasked;
+  }
+  if (P.causal && b.k.hi > q.lo) all = false;
+  if (P.window > 0 && q.hi - b.k.lo >= P.window) all = false;
+  return all ? kClsFull : kClsMasked;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_k) {
+  using L = WSmem<D>;
+  const AttnParams& P = W.P;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(sm);
+  auto bar = [&](int i) { return sbase + L::kBar + 8 * i; };
+  volatile int* sched = reinterpret_cast<volatile int*>(sm + L::kSched);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
+  int* status = &g_key_weights_status;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // key blocks outermost: with a causal mask the heaviest (first) start first
+  const int groups = P.G / W.hpi;  // CTAs per KV head and segment
+  int idx = blockIdx.x;
+  const int part = idx % (groups * W.nseg);
+  idx /= groups * W.nseg;
+  const int g = idx % P.Hkv;
+  idx /= P.Hkv;
+  const int bt = idx % P.Bt, kb = idx / P.Bt;
+  const int seg = part / groups, h0 = g * P.G + (part % groups) * W.hpi;
+  const int key0 = kb * kKeys;
+
+  if (warp == kProducerWarp && lane == 0) {
+    mbar_init(bar(L::kKFull), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(L::kQFull + s), 1);
+      mbar_init(bar(L::kQFree + s), 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(bar(L::kSFull + s), 1);
+      mbar_init(bar(L::kSFree + s), 4);  // the four warps of a key tile
+    }
+    for (int s = 0; s < kRing; ++s) mbar_init(bar(L::kStatFull + s), 1);
+    mbar_init(bar(L::kMmaDone), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch(&tm_q);
+    mbar_expect_tx(bar(L::kKFull), 2 * L::kKTile);
+    for (int a = 0; a < 2; ++a)
+      for (int hf = 0; hf < L::kHalves; ++hf)
+        tma_load_4d(sbase + L::kK + a * L::kKTile + hf * L::kKHalf, &tm_k, bar(L::kKFull), hf * 64,
+                    g, key0 + a * kTile, bt);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(sbase + L::kMisc, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ producer
+    const KeyBlock blk = key_block(P, key0);
+    int n = 0;
+    bool ok = true;
+    int first = seg * W.tps, last = min(W.ntiles, first + W.tps);
+    if (P.layout == kContiguous) {  // rank-major order is natural order
+      first = max(first, blk.q.lo / kQT);
+      last = min(last, blk.q.hi / kQT + 1);
+      if (W.observe > 0 && P.cu == nullptr) first = max(first, max(0, P.S - W.observe) / kQT);
+    }
+    for (int base = first; base < last && ok; base += 32) {
+      const int mine = base + lane < last ? classify_tile(W, base + lane, blk) : kClsEmpty;
+      unsigned todo = __ballot_sync(0xffffffffu, mine != kClsEmpty);
+      while (todo && ok) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int qt = base + src;
+        const int cls = __shfl_sync(0xffffffffu, mine, src);
+        int pos[2];
+        for (int e = 0; e < 2; ++e) pos[e] = observed_pos(W, qt * kQT + lane + 32 * e);
+        for (int hh = 0; hh < W.hpi && ok; ++hh) {
+          const int h = h0 + hh, slot = n & 1, ring = n & (kRing - 1);
+          float lse[2];
+          for (int e = 0; e < 2; ++e) {
+            const int p = qt * kQT + lane + 32 * e;
+            lse[e] = pos[e] >= 0 ? __ldg(P.lse + lse_index(P, bt, h, p)) : 0.f;
+          }
+          if (n >= 2)  // the slot's previous tile has been multiplied
+            ok = mbar_wait(bar(L::kQFree + slot), ((n >> 1) - 1) & 1, abort_flag, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          // The ring entry is free: the products of tile n - 2 are done, so
+          // the softmax has read the scores of tile n - 4 and is past the
+          // statistics of tile n - 8.
+          float* st = reinterpret_cast<float*>(sm + L::kStat + ring * L::kStatBytes);
+          for (int e = 0; e < 2; ++e) {
+            const float x = lse[e] * kLog2e;
+            // a row that sees nothing adds nothing
+            const bool none = pos[e] < 0 || x == -INFINITY;
+            st[lane + 32 * e] = none ? INFINITY : x;
+            reinterpret_cast<int*>(st)[kQT + lane + 32 * e] = pos[e];
+          }
+          if (lane == 0) sched[ring] = cls;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(L::kStatFull + ring));
+            mbar_expect_tx(bar(L::kQFull + slot), L::kQTile);
+            for (int hf = 0; hf < L::kHalves; ++hf)
+              tma_load_4d(sbase + L::kQ + slot * L::kQTile + hf * L::kQHalf, &tm_q,
+                          bar(L::kQFull + slot), hf * 64, h, qt * kQT, bt);
+          }
+          ++n;
+        }
+      }
+    }
+    if (lane == 0) {
+      if (ok) {
+        const int ring = n & (kRing - 1);
+        // as above: the entry is free once the products of tile n - 2 are done
+        if (n < 2 || mbar_wait(bar(L::kQFree + (n & 1)), ((n >> 1) - 1) & 1, abort_flag, status)) {
+          sched[ring] = kEnd;
+          mbar_arrive(bar(L::kStatFull + ring));
+        }
+      }
+      // copies in flight land before the CTA ends, aborted or without a tile
+      mbar_wait_drain(bar(L::kKFull), 0);
+      if (*abort_flag)
+        for (int i = n >= 2 ? n - 2 : 0; i < n; ++i)
+          mbar_wait_drain(bar(L::kQFull + (i & 1)), (i >> 1) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kId = idesc_bf16_f32(kTile, kQT, 0, 0);
+      const uint64_t dk = sdesc_sw128(sbase + L::kK, 16, 1024);
+      const uint64_t dq = sdesc_sw128(sbase + L::kQ, 16, 1024);
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const int slot = n & 1, ring = n & (kRing - 1);
+        if (!(ok = mbar_wait(bar(L::kStatFull + ring), (n / kRing) & 1, abort_flag, status))) break;
+        if (sched[ring] == kEnd) break;
+        if (n == 0 && !(ok = mbar_wait(bar(L::kKFull), 0, abort_flag, status))) break;
+        if (!(ok = mbar_wait(bar(L::kQFull + slot), (n >> 1) & 1, abort_flag, status))) break;
+        for (int a = 0; a < 2; ++a) {
+          // the buffer's previous scores (tile n - 2) have been read
+          if (n >= 2 && !(ok = mbar_wait(bar(L::kSFree + 2 * a + slot), ((n >> 1) - 1) & 1,
+                                         abort_flag, status)))
+            break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + 128 * a + 64 * slot,
+                   sdesc_add(dk, a * L::kKTile + (kk >> 2) * L::kKHalf + (kk & 3) * 32),
+                   sdesc_add(dq, slot * L::kQTile + (kk >> 2) * L::kQHalf + (kk & 3) * 32), kId,
+                   kk > 0 ? 1u : 0u);
+          mma_commit(bar(L::kSFull + 2 * a + slot));
+        }
+        if (!ok) break;
+        mma_commit(bar(L::kQFree + slot));
+      }
+      mma_commit(bar(L::kMmaDone));
+      mbar_wait_drain(bar(L::kMmaDone), 0);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int a = warp >> 2;  // key tile
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int kp = key0 + warp * 32 + lane;
+    Seen vis{1, 0};
+    if (kp < P.S) vis = seen_by(P, nat_pos(P, kp));
+    const uint64_t sc2 = f2_pack(P.scale_log2, P.scale_log2);
+    uint64_t sum[2] = {0ull, 0ull};
+    bool ok = true;
+    for (int n = 0;; ++n) {
+      const int slot = n & 1, ring = n & (kRing - 1);
+      ok = mbar_wait(bar(L::kStatFull + ring), (n / kRing) & 1, abort_flag, status);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const int cls = sched[ring];
+      if (cls == kEnd) break;
+      ok = mbar_wait(bar(L::kSFull + 2 * a + slot), (n >> 1) & 1, abort_flag, status);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      tc_fence_after();
+      uint32_t v[2][32];
+      tmem_ld32(tmem + lane_off + 128 * a + 64 * slot, v[0]);
+      tmem_ld32(tmem + lane_off + 128 * a + 64 * slot + 32, v[1]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kSFree + 2 * a + slot));
+      const float4* lse2 = reinterpret_cast<const float4*>(sm + L::kStat + ring * L::kStatBytes);
+      const int4* pos = reinterpret_cast<const int4*>(lse2 + kQT / 4);
+      if (cls == kClsFull) {
+#pragma unroll
+        for (int k = 0; k < kQT / 4; ++k) {
+          const float4 l = lse2[k];
+          const uint32_t* s = &v[k >> 3][4 * (k & 7)];
+          const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2,
+                                    f2_pack(-l.x, -l.y));
+          const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3])), sc2,
+                                    f2_pack(-l.z, -l.w));
+          float x0, x1, y0, y1;
+          f2_unpack(x, x0, x1);
+          f2_unpack(y, y0, y1);
+          sum[0] = f2_add(sum[0], f2_pack(ex2(x0), ex2(x1)));
+          sum[1] = f2_add(sum[1], f2_pack(ex2(y0), ex2(y1)));
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kQT / 4; ++k) {
+          const float4 l = lse2[k];
+          const int4 i = pos[k];
+          const uint32_t* s = &v[k >> 3][4 * (k & 7)];
+          auto one = [&](uint32_t sv, float lv, int iv) {
+            const float p = ex2(fmaf(__uint_as_float(sv), P.scale_log2, -lv));
+            return iv >= vis.lo && iv <= vis.hi ? p : 0.f;
+          };
+          sum[0] = f2_add(sum[0], f2_pack(one(s[0], l.x, i.x), one(s[1], l.y, i.y)));
+          sum[1] = f2_add(sum[1], f2_pack(one(s[2], l.z, i.z), one(s[3], l.w, i.w)));
+        }
+      }
+    }
+    if (ok && kp < P.S) {
+      float x, y;
+      f2_unpack(f2_add(sum[0], sum[1]), x, y);
+      W.part[(((long long)part * P.Bt + bt) * P.Hkv + g) * P.S + kp] = x + y;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 256);
+}
+
+// weight[i] = the parts' sum, in order.
+__global__ void __launch_bounds__(256)
+key_weights_sum_kernel(const float* __restrict__ part, float* __restrict__ weight, long long n,
+                       int parts) {
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    float s = 0.f;
+    for (int p = 0; p < parts; ++p) s += __ldg(part + p * n + i);
+    weight[i] = s;
+  }
+}
+
+// CUDA cores: 64 keys per block, query tiles of 64 in 32-channel slices;
+// thread (ty, tx) of 16 x 16 owns 4 keys x 4 queries.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) key_weights_simt_kernel(const WeightParams W, float* weight) {
+  constexpr int kT = 64, kC = 32;
+  __shared__ float ks[kC][kT + 4], qs[kC][kT + 4];
+  __shared__ float red[16][kT + 1];
+  const AttnParams& P = W.P;
+  const int g = blockIdx.y, bt = blockIdx.z, key0 = blockIdx.x * kT;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const T* k = static_cast<const T*>(P.k) + ((long long)bt * P.S * P.Hkv + g) * D;
+  Seen vis[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int kp = key0 + 4 * ty + a;
+    vis[a] = kp < P.S ? seen_by(P, nat_pos(P, kp)) : Seen{1, 0};
+  }
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int q0 = 0; q0 < P.S; q0 += kT) {
+    int pos[4];
+    bool any = false;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      pos[c] = observed_pos(W, q0 + 4 * tx + c);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) any |= pos[c] >= vis[a].lo && pos[c] <= vis[a].hi;
+    }
+    if (!__syncthreads_or(any)) continue;
+    for (int h = g * P.G; h < (g + 1) * P.G; ++h) {
+      const T* q = static_cast<const T*>(P.q) + ((long long)bt * P.S * P.Hq + h) * D;
+      float acc[4][4] = {};
+      for (int d0 = 0; d0 < D; d0 += kC) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < kT * kC / 4; i += 256) {
+          const int r = i / (kC / 4), c = (i % (kC / 4)) * 4;
+          float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+          if (key0 + r < P.S) load_row<T, 4>(k + (long long)(key0 + r) * P.Hkv * D + d0 + c, x);
+          if (q0 + r < P.S) load_row<T, 4>(q + (long long)(q0 + r) * P.Hq * D + d0 + c, y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ks[c + e][r] = x[e];
+            qs[c + e][r] = y[e];
+          }
+        }
+        __syncthreads();
+#pragma unroll 8
+        for (int d = 0; d < kC; ++d) {
+          const float4 x = *reinterpret_cast<const float4*>(&ks[d][4 * ty]);
+          const float4 y = *reinterpret_cast<const float4*>(&qs[d][4 * tx]);
+          const float xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[a][c] = fmaf(xa[a], ya[c], acc[a][c]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (pos[c] < 0) continue;
+        const float lse = __ldg(P.lse + lse_index(P, bt, h, q0 + 4 * tx + c));
+        if (lse == -INFINITY) continue;
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+          if (pos[c] >= vis[a].lo && pos[c] <= vis[a].hi)
+            sum[a] += exp2f((acc[a][c] * P.scale - lse) * kLog2e);
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int a = 0; a < 4; ++a) red[tx][4 * ty + a] = sum[a];
+  __syncthreads();
+  if (threadIdx.x < kT && key0 + threadIdx.x < P.S) {
+    float s = 0.f;
+    for (int i = 0; i < 16; ++i) s += red[i][threadIdx.x];
+    weight[((long long)bt * P.Hkv + g) * P.S + key0 + threadIdx.x] = s;
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (fn == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                         cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  return fn;
+}
+
+// [Bt][S][H][D] bf16 -> 4-D map (D, H, S, Bt), box (64, 1, rows, 1), 128-byte
+// swizzle; rows behind S read as zeros.
+bool make_map(CUtensorMap* m, const void* base, int Bt, int S, int H, int D, int rows) {
+  auto fn = encode_fn();
+  if (!fn) {
+    fail_cuda_msg("cuTensorMapEncodeTiled", "driver entry point not found");
+    return false;
+  }
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)S, (cuuint64_t)Bt};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2, (cuuint64_t)S * H * D * 2};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+                  box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char msg[64];
+    std::snprintf(msg, sizeof(msg), "CUresult %d", (int)r);
+    fail_cuda_msg("cuTensorMapEncodeTiled", msg);
+    return false;
+  }
+  return true;
+}
+
+// How the problem is cut (host side, from the shapes alone).
+struct Cut {
+  int hpi, nseg, tps, nkb, ntiles, parts;
+};
+Cut cut_of(int B, int S, int Hq, int Hkv, int observe) {
+  Cut c{};
+  const int G = Hq / Hkv;
+  c.nkb = (S + kKeys - 1) / kKeys;
+  c.ntiles = (S + kQT - 1) / kQT;
+  c.hpi = G;
+  c.nseg = 1;
+  const long long blocks = (long long)c.nkb * Hkv * B;
+  const long long want = 8LL * 304;  // eight CTAs per resident slot even out the masks
+  // few observed queries: a CTA has only a few tiles, all heads in one
+  const int tiles = observe > 0 ? (observe + kQT - 1) / kQT + 1 : c.ntiles;
+  if (blocks < want && tiles > 2) {
+    c.hpi = 1;
+    const long long have = blocks * G;
+    if (have < want) {
+      long long n = (want + have - 1) / have;
+      const long long most = (tiles + 7) / 8;  // at least eight tiles each
+      if (n > most) n = most;
+      if (n > 16) n = 16;
+      // with few observed queries they sit in the last segments
+      c.nseg = observe > 0 ? 1 : (int)n;
+    }
+  }
+  c.tps = (c.ntiles + c.nseg - 1) / c.nseg;
+  c.parts = (G / c.hpi) * c.nseg;
+  return c;
+}
+
+template <int D>
+usp_status_t launch_tc(const WeightParams& W, cudaStream_t st) {
+  const AttnParams& P = W.P;
+  CUtensorMap mq, mk;
+  if (!make_map(&mq, P.q, P.Bt, P.S, P.Hq, D, kQT) || !make_map(&mk, P.k, P.Bt, P.S, P.Hkv, D, kTile))
+    return USP_ERR_CUDA;
+  const int smem = WSmem<D>::kAlloc;
+  cudaError_t e = cudaFuncSetAttribute(key_weights_tc_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
+  const long long blocks = (long long)W.nkb * P.Bt * P.Hkv * (P.G / W.hpi) * W.nseg;
+  if (blocks > 0x7fffffffLL) return USP_ERR_UNSUPPORTED;
+  {
+    ProfScope ps(st, "attn_key_weights");
+    key_weights_tc_kernel<D><<<(unsigned)blocks, kThreads, smem, st>>>(W, mq, mk);
+  }
+  note_launch();
+  return check_launch();
+}
+
+}  // namespace
+
+size_t key_weights_workspace(int B, int S, int Hq, int Hkv, int observe) {
+  const Cut c = cut_of(B, S, Hq, Hkv, observe);
+  return c.parts > 1 ? (size_t)c.parts * B * Hkv * S * 4 : 0;
+}
+
+usp_status_t launch_key_weights_tc(const AttnParams& P, float* weight, int observe,
+                                   void* workspace, cudaStream_t st) {
+  const Cut c = cut_of(P.Bt, P.S, P.Hq, P.Hkv, observe);
+  WeightParams W{P, c.parts > 1 ? static_cast<float*>(workspace) : weight, observe, c.hpi, c.nseg,
+                 c.tps, c.nkb, c.ntiles};
+  usp_status_t r = P.D == 128 ? launch_tc<128>(W, st) : launch_tc<64>(W, st);
+  if (r != USP_OK || c.parts == 1) return r;
+  const long long n = (long long)P.Bt * P.Hkv * P.S;
+  const long long blocks = (n + 255) / 256;
+  {
+    ProfScope ps(st, "attn_key_weights_sum");
+    key_weights_sum_kernel<<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), 256, 0, st>>>(
+        W.part, weight, n, c.parts);
+  }
+  note_launch();
+  return check_launch();
+}
+
+usp_status_t launch_key_weights_simt(const AttnParams& P, float* weight, int observe, int bf16,
+                                     cudaStream_t st) {
+  WeightParams W{P, nullptr, observe, P.G, 1, 0, 0, 0};
+  const dim3 grid((P.S + 63) / 64, P.Hkv, P.Bt);
+  {
+    ProfScope ps(st, "attn_key_weights_simt");
+    if (bf16) {
+      if (P.D == 128) key_weights_simt_kernel<__nv_bfloat16, 128><<<grid, 256, 0, st>>>(W, weight);
+      else key_weights_simt_kernel<__nv_bfloat16, 64><<<grid, 256, 0, st>>>(W, weight);
+    } else {
+      if (P.D == 128) key_weights_simt_kernel<float, 128><<<grid, 256, 0, st>>>(W, weight);
+      else key_weights_simt_kernel<float, 64><<<grid, 256, 0, st>>>(W, weight);
+    }
+  }
+  note_launch();
+  return check_launch();
+}
+
+int read_clear_key_weights_status() {
+  int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_key_weights_status, sizeof(int)) != cudaSuccess) return -1;
+  if (v != 0) cudaMemcpyToSymbol(g_key_weights_status, &z, sizeof(int));
+  return v;
+}
+
+}  // namespace usp
