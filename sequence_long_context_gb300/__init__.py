@@ -334,11 +334,6 @@ def attn_decode(q, k, v, *, causal=True, cp=1, splits=1, tree_order=True,
     return out, lse
 
 
-def _on(device):
-    """The tensors' device as the current one (launches go to its stream)."""
-    return torch.cuda.device(device)
-
-
 def _use_workspace(workspace, need, device):
     """The caller's uint8 workspace (checked for size), else a fresh one."""
     if workspace is None:
@@ -510,23 +505,59 @@ def _need(x, name, dtype, shape, device) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
-def _kv4_struct(c: KV4Cache) -> "_lib.Kv4CacheStruct":
-    """The C struct of a cache whose tensors fit together, else ValueError."""
-    B, H, C, half = c.k.shape
-    dev = c.k.device
-    D = 2 * half
-    u8 = torch.uint8
-    _need(c.k, "cache.k", u8, (B, H, C, half), dev)
-    _need(c.v, "cache.v", u8, (B, H, C, half), dev)
-    _need(c.k_scale, "cache.k_scale", u8, (B, H, C, D // 32), dev)
-    _need(c.v_scale, "cache.v_scale", u8, (B, H, C, D // 32), dev)
-    _need(c.seq_lens, "cache.seq_lens", torch.int32, (B,), dev)
-    w = None
-    if c.key_weight is not None:
-        _need(c.key_weight, "cache.key_weight", torch.float32, (B, H, C), dev)
-        w = _p(c.key_weight)
-    return _lib.Kv4CacheStruct(_p(c.k), _p(c.k_scale), _p(c.v), _p(c.v_scale), w,
-                               _p(c.seq_lens), B, C, H, D, c.k_descale, c.v_descale)
+def _fits(x, dtype, shape, index) -> bool:
+    return (x.dtype is dtype and x.shape == shape and x.get_device() == index
+            and x.is_contiguous())
+
+
+def _require(x, name, dtype, shape, index, like) -> None:
+    """_need, with the common case (it fits) in as few calls as possible: a
+    decoding step's helpers run for a few microseconds on the GPU."""
+    if not _fits(x, dtype, shape, index):
+        _need(x, name, dtype, shape, like.device)
+
+
+def _call(fn, index, stream, *args) -> None:
+    """fn(*args, stream) on the tensors' device and (default) its current
+    stream; raises what it returns."""
+    if index < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, raw)
+    if st:
+        _check(st)
+
+
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
+
+
+def _kv4_struct(cache: KV4Cache):
+    """(C struct, device index) of a cache whose tensors fit together, else
+    ValueError."""
+    k, ks, v, vs, lens, w, kd, vd = cache
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError("cache.k must be [B, Hkv, capacity, D/2]")
+    B, H, C, half = shape
+    at = k.get_device()
+    sshape = (B, H, C, half // 16)
+    if not (_fits(k, _U8, shape, at) and _fits(ks, _U8, sshape, at) and _fits(v, _U8, shape, at)
+            and _fits(vs, _U8, sshape, at) and _fits(lens, _I32, (B,), at)
+            and (w is None or _fits(w, _F32, (B, H, C), at))):
+        _need(k, "cache.k", _U8, shape, k.device)
+        _need(v, "cache.v", _U8, shape, k.device)
+        _need(ks, "cache.k_scale", _U8, sshape, k.device)
+        _need(vs, "cache.v_scale", _U8, sshape, k.device)
+        _need(lens, "cache.seq_lens", _I32, (B,), k.device)
+        if w is not None:
+            _need(w, "cache.key_weight", _F32, (B, H, C), k.device)
+    return _lib.Kv4CacheStruct(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(),
+                               None if w is None else w.data_ptr(), lens.data_ptr(), B, C, H,
+                               2 * half, kd, vd), at
 
 
 def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, *, key_weight=None,
@@ -537,26 +568,29 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, *, key_weight=
     [Hkv,T]; attn_key_weights), else 0. Returns the new lengths, written to
     seq_lens_out (default: the cache's own seq_lens, in place). Tokens that
     find no room are dropped."""
-    s = _kv4_struct(cache)
-    dev = cache.k.device
+    s, at = _kv4_struct(cache)
     packed = cu_seqlens is not None
+    dt = k.dtype
+    if dt not in DTYPE:
+        raise ValueError("keys and values must be bf16 or fp32")
     T = k.shape[0] if packed else k.shape[1]
     shape = (T, s.Hkv, s.D) if packed else (s.B, T, s.Hkv, s.D)
-    if k.dtype not in DTYPE:
-        raise ValueError("keys and values must be bf16 or fp32")
-    _need(k, "k", k.dtype, shape, dev)
-    _need(v, "v", k.dtype, shape, dev)
+    _require(k, "k", dt, shape, at, cache.k)
+    _require(v, "v", dt, shape, at, cache.k)
     if packed:
-        _need(cu_seqlens, "cu_seqlens", torch.int32, (s.B + 1,), dev)
+        _require(cu_seqlens, "cu_seqlens", _I32, (s.B + 1,), at, cache.k)
     if key_weight is not None:
         if cache.key_weight is None:
             raise ValueError("the cache has no key_weight to store the weights in")
-        _need(key_weight, "key_weight", torch.float32, 
-              (s.Hkv, T) if packed else (s.B, s.Hkv, T), dev)
-    lens = cache.seq_lens if seq_lens_out is None else seq_lens_out
-    _need(lens, "seq_lens_out", torch.int32, (s.B,), dev)
-    with _on(dev):
-        usp_kv4_append(s, k, v, key_weight, cu_seqlens, T, k.dtype, lens, stream)
+        _require(key_weight, "key_weight", _F32, (s.Hkv, T) if packed else (s.B, s.Hkv, T), at,
+                 cache.k)
+    lens = cache.seq_lens
+    if seq_lens_out is not None:
+        lens = seq_lens_out
+        _require(lens, "seq_lens_out", _I32, (s.B,), at, cache.k)
+    _call(_lib.load().usp_kv4_append, at, stream, ctypes.addressof(s), k.data_ptr(), v.data_ptr(),
+          None if key_weight is None else key_weight.data_ptr(),
+          cu_seqlens.data_ptr() if packed else None, T, DTYPE[dt], lens.data_ptr())
     return lens
 
 
@@ -564,14 +598,16 @@ def kv4_read(cache: KV4Cache, tokens: int, *, starts=None, dtype=torch.bfloat16,
              ) -> Tuple[torch.Tensor, torch.Tensor]:
     """(k, v) [B, tokens, Hkv, D]: the values of rows starts[b] (default 0) ..
     of every sequence; zeros behind its length."""
-    s = _kv4_struct(cache)
-    dev = cache.k.device
+    s, at = _kv4_struct(cache)
+    if dtype not in DTYPE:
+        raise ValueError("keys and values are read as bf16 or fp32")
     if starts is not None:
-        _need(starts, "starts", torch.int32, (s.B,), dev)
-    k = torch.empty((s.B, tokens, s.Hkv, s.D), dtype=dtype, device=dev)
+        _require(starts, "starts", _I32, (s.B,), at, cache.k)
+    k = torch.empty((s.B, tokens, s.Hkv, s.D), dtype=dtype, device=cache.k.device)
     v = torch.empty_like(k)
-    with _on(dev):
-        usp_kv4_read(s, starts, tokens, k, v, dtype, stream)
+    _call(_lib.load().usp_kv4_read, at, stream, ctypes.addressof(s),
+          None if starts is None else starts.data_ptr(), tokens, k.data_ptr(), v.data_ptr(),
+          DTYPE[dtype])
     return k, v
 
 
@@ -581,20 +617,21 @@ def attn_decode_kv4(q: torch.Tensor, cache: KV4Cache, *, causal=True, window=0, 
     """(out [B,Tq,Hq,D], lse [B,Tq,Hq]) of the newest Tq tokens q [B,Tq,Hq,D]
     (already in the cache) against the cached keys; accumulate adds each key's
     attention weight of this step to cache.key_weight."""
-    s = _kv4_struct(cache)
-    dev = cache.k.device
+    s, at = _kv4_struct(cache)
     B, Tq, Hq, D = q.shape
-    _need(q, "q", torch.bfloat16, (s.B, Tq, Hq, s.D), dev)
+    _require(q, "q", torch.bfloat16, (s.B, Tq, Hq, s.D), at, cache.k)
     if accumulate and cache.key_weight is None:
         raise ValueError("accumulate needs a cache with key_weight")
+    lib = _lib.load()
     out = torch.empty_like(q)
-    lse = torch.empty((B, Tq, Hq), dtype=torch.float32, device=dev)
-    ws, ws_n = _use_workspace(
-        workspace,
-        usp_attn_decode_kv4_workspace_size(B, Tq, s.capacity, Hq, s.Hkv, D, accumulate), dev)
-    with _on(dev):
-        usp_attn_decode_kv4(s, q, out, lse, Tq, Hq, softmax_scale, causal, window, sink_tokens,
-                            accumulate, q.dtype, ws, ws_n, stream)
+    lse = q.new_empty((B, Tq, Hq), dtype=_F32)
+    need = lib.usp_attn_decode_kv4_workspace_size(B, Tq, s.capacity, Hq, s.Hkv, D,
+                                                  1 if accumulate else 0)
+    ws = q.new_empty(need, dtype=_U8) if workspace is None else \
+        _use_workspace(workspace, need, q.device)[0]
+    _call(lib.usp_attn_decode_kv4, at, stream, ctypes.addressof(s), q.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), Tq, Hq, softmax_scale, 1 if causal else 0, window, sink_tokens,
+          1 if accumulate else 0, 0, ws.data_ptr(), ws.numel())
     return out, lse
 
 
@@ -606,21 +643,29 @@ def attn_key_weights(q, k, lse, *, causal=True, window=0, sink_tokens=0, cu_seql
     sequence; 0: all) and the query heads sharing its KV head, from the
     forward's q, k (rank-major) and lse."""
     B, S, Hq, Hkv, D, Bl = _dims(q, k, cu_seqlens)
-    dev = q.device
-    lead = () if cu_seqlens is not None else (Bl,)
-    _need(q, "q", q.dtype, q.shape, dev)
-    _need(k, "k", q.dtype, lead + (S, Hkv, D), dev)
-    _need(lse, "lse", torch.float32, lead + (Hq, S), dev)
+    at = q.get_device()
+    dt = q.dtype
+    if dt not in DTYPE:
+        raise ValueError("q and k must be bf16 or fp32")
+    lead = (Bl,) if cu_seqlens is None else ()
+    _require(q, "q", dt, lead + (S, Hq, D), at, q)
+    _require(k, "k", dt, lead + (S, Hkv, D), at, q)
+    _require(lse, "lse", _F32, lead + (Hq, S), at, q)
     if cu_seqlens is not None:
-        _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
-    weight = torch.empty(lead + (Hkv, S), dtype=torch.float32, device=dev)
-    ws, ws_n = _use_workspace(
-        workspace, usp_attn_key_weights_workspace_size(Bl, S, Hq, Hkv, observe, q.dtype, flags),
-        dev)
-    with _on(dev):
-        usp_attn_key_weights(q, k, lse, weight, B, S, Hq, Hkv, D, softmax_scale, causal, window,
-                             sink_tokens, cu_seqlens, cp, layout, observe, q.dtype, flags, ws,
-                             ws_n, stream)
+        _require(cu_seqlens, "cu_seqlens", _I32, (B + 1,), at, q)
+    lib = _lib.load()
+    weight = q.new_empty(lead + (Hkv, S), dtype=_F32)
+    need = lib.usp_attn_key_weights_workspace_size(Bl, S, Hq, Hkv, observe, DTYPE[dt], flags)
+    ws = workspace
+    if ws is not None:
+        ws = _use_workspace(ws, need, q.device)[0]
+    elif need:
+        ws = q.new_empty(need, dtype=_U8)
+    _call(lib.usp_attn_key_weights, at, stream, q.data_ptr(), k.data_ptr(), lse.data_ptr(),
+          weight.data_ptr(), B, S, Hq, Hkv, D, softmax_scale, 1 if causal else 0, window,
+          sink_tokens, None if cu_seqlens is None else cu_seqlens.data_ptr(), cp,
+          _enum(LAYOUT, layout), observe, DTYPE[dt], flags,
+          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return weight
 
 
@@ -630,19 +675,20 @@ def kv4_evict(cache: KV4Cache, keep: int, *, recent=0, sink_tokens=0, out=None, 
     keeps, in each KV head, its first sink_tokens, its last `recent` and the
     keys with the largest key_weight, in order; kept gives their old rows (-1
     behind the last). out: another cache that takes them (default: in place)."""
-    dst = cache if out is None else out
     if cache.key_weight is None:
         raise ValueError("eviction needs a cache with key_weight")
-    s = _kv4_struct(cache)
-    d = s if out is None else _kv4_struct(out)
-    dev = cache.k.device
-    if dst.k.device != dev:
-        raise ValueError("both caches must be on one device")
-    if (s.k_descale, s.v_descale) != (d.k_descale, d.v_descale):
-        raise ValueError("both caches must have the same descales")
     if keep < 1:
         raise ValueError("keep must be at least 1")
-    kept = torch.empty((s.B, s.Hkv, keep), dtype=torch.int32, device=dev)
-    with _on(dev):
-        usp_kv4_evict(s, d, kept, keep, recent, sink_tokens, stream)
+    s, at = _kv4_struct(cache)
+    d, dst = s, cache
+    if out is not None:
+        dst = out
+        d, at2 = _kv4_struct(out)
+        if at2 != at:
+            raise ValueError("both caches must be on one device")
+        if (s.k_descale, s.v_descale) != (d.k_descale, d.v_descale):
+            raise ValueError("both caches must have the same descales")
+    kept = cache.seq_lens.new_empty((s.B, s.Hkv, keep))
+    _call(_lib.load().usp_kv4_evict, at, stream, ctypes.addressof(s), ctypes.addressof(d),
+          kept.data_ptr(), keep, recent, sink_tokens)
     return dst, kept

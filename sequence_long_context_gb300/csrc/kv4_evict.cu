@@ -1,19 +1,38 @@
 // Eviction from the 4-bit KV cache by accumulated attention weight.
 //
-// Select: one block per (sequence, KV head) finds the rank-th largest weight
-// of the keys between the sinks and the recent ones by four 8-bit radix
-// passes over order-preserving 32-bit keys, then writes the kept rows'
-// indices in ascending order. Move: the kept rows are copied to their places.
+// A cluster of CTAs owns one (sequence, KV head). Every CTA takes an equal,
+// contiguous part of the head's weights, brings it into shared memory once as
+// order-preserving 32-bit keys, and the cluster finds the n-th largest key by
+// three radix passes (11, 11 and 10 bits): each CTA counts its part into its
+// own histogram, and after one cluster barrier every CTA adds up the
+// cluster's histograms through distributed shared memory and scans them, so
+// that all reach the same bin with no further exchange. One more barrier
+// gives every CTA how many keys are kept before its part, and it writes their
+// rows in ascending order; after another the cluster copies the kept rows'
+// codes, scales and weights.
+//
+// Bound by HBM for long caches (the weights once, the kept rows twice), by the
+// five barriers for short ones. Rows only move towards the front, so in place
+// the copy goes in rounds: every row of a round is in registers before a
+// barrier, and written after it; later rounds read behind every row that
+// earlier ones write.
 #include "internal.h"
 #include "kv4.cuh"
 #include "kv4_host.h"
+#include "tc_ptx.cuh"
 
 namespace usp {
 namespace {
 
 using namespace kv4;
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+// keys of a CTA's part that fit beside the histograms with two CTAs per SM;
+// longer parts (beyond 8 x 20K tokens) are read again from L2 in each pass
+constexpr int kKeysInSmem = 20480;
 
 // Larger float <=> larger key; +0 and -0 alike; a NaN above everything.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -23,170 +42,332 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The 32-bit word at this CTA's shared address `p`, of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t peer_load(const uint32_t* p, uint32_t rank) {
+  uint32_t a, v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
 struct EvictParams {
   Cache src, dst;
   int* kept;
   int keep, recent, sink;
+  int in_place;
+  int cluster;  // CTAs per (sequence, KV head)
 };
 
-__global__ void __launch_bounds__(kThreads) select_kernel(const EvictParams P) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_prefix, s_need;
-  __shared__ uint32_t warp_tie[32], warp_keep[32];
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int L = clamp_len(P.src.lens[b], P.src.C);
-  int* kept = P.kept + ((long long)b * P.src.H + h) * P.keep;
-  if (L <= P.keep) {
-    for (int i = threadIdx.x; i < P.keep; i += kThreads) kept[i] = i < L ? i : -1;
-    return;
-  }
-  const float* w = P.src.w + head_row(P.src, b, h);
-  const int lo = P.sink, hi = L - P.recent;  // candidates [lo, hi)
-  uint32_t need = (uint32_t)(P.keep - P.sink - P.recent);
-  uint32_t prefix = 0;  // the threshold's bits found so far
-  if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kThreads) hist[i] = 0;
-      __syncthreads();
-      const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      for (int j = lo + threadIdx.x; j < hi; j += kThreads) {
-        const uint32_t key = order_key(w[j]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        uint32_t left = need;
-        int bin = 255;
-        while (bin > 0 && hist[bin] < left) left -= hist[bin--];
-        s_prefix = prefix | ((uint32_t)bin << shift);
-        s_need = left;
-      }
-      __syncthreads();
-      prefix = s_prefix;
-      need = s_need;
-    }
-  }
-  // keys above `prefix` are kept, and the first `need` equal to it
+struct __align__(16) EvictSmem {
+  uint32_t hist[3][kBins];
+  uint32_t scan[kWarps];
+  uint32_t above[kWarps], tie[kWarps];  // of each warp's part
+  uint32_t total[2];                    // kept for sure and ties of this CTA
+  uint32_t bin, left;
+};
+
+// Adds the cluster's histograms, and finds the bin (from the top) in which the
+// need-th key lies and how many of the bin are needed: s.bin, s.left.
+__device__ __forceinline__ void find_bin(EvictSmem& s, int pass, int cluster, uint32_t need) {
+  // thread t owns the kOwn bins from kBins - 1 - kOwn t downwards
+  constexpr int kOwn = kBins / kThreads;
+  const int b0 = kBins - 1 - kOwn * threadIdx.x;
+  uint32_t n[kOwn] = {}, mine = 0;
+  for (int r = 0; r < cluster; ++r)
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) n[i] += peer_load(&s.hist[pass][b0 - i], r);
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) mine += n[i];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool any = P.keep - P.sink - P.recent > 0;
-  uint32_t ties = 0, out = 0;  // so far, the same in every thread
-  for (int base = 0; base < L; base += kThreads) {
-    const int j = base + threadIdx.x;
-    bool above = false, tie = false;
-    if (j < L) {
-      if (j < lo || j >= hi) {
-        above = true;
-      } else if (any) {
-        const uint32_t key = order_key(w[j]);
-        above = key > prefix;
-        tie = key == prefix;
-      }
-    }
-    const uint32_t tb = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) warp_tie[warp] = __popc(tb);
-    __syncthreads();
-    uint32_t before = ties, all = ties;
-    for (int i = 0; i < 32; ++i) {
-      if (i < warp) before += warp_tie[i];
-      all += warp_tie[i];
-    }
-    before += __popc(tb & ((1u << lane) - 1u));
-    const bool take = above || (tie && before < need);
-    const uint32_t kb = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) warp_keep[warp] = __popc(kb);
-    __syncthreads();
-    uint32_t at = out, total = out;
-    for (int i = 0; i < 32; ++i) {
-      if (i < warp) at += warp_keep[i];
-      total += warp_keep[i];
-    }
-    at += __popc(kb & ((1u << lane) - 1u));
-    if (take && at < (uint32_t)P.keep) kept[at] = j;
-    ties = all;
-    out = total;
-    __syncthreads();
+  uint32_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
   }
+  if (lane == 31) s.scan[warp] = inc;
+  __syncthreads();
+  uint32_t before = 0;
+  {
+    const uint32_t x = lane < kWarps ? s.scan[lane] : 0u;
+    uint32_t y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    before = __shfl_sync(0xffffffffu, y - x, warp);
+  }
+  uint32_t above = before + inc - mine;  // keys in higher bins than b0
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    if (above < need && need <= above + n[i]) {
+      s.bin = b0 - i;
+      s.left = need - above;
+    }
+    above += n[i];
+  }
+  __syncthreads();
 }
 
-// One block per (sequence, KV head), in rounds of kRows rows: every row of a
-// round is in registers before any is written, and rows only move towards
-// the front, so dst may be src.
-constexpr int kRows = 256;
-
 template <int D>
-__global__ void __launch_bounds__(kThreads) move_kernel(const EvictParams P) {
-  constexpr int kChunks = D / 32;               // 16-byte pieces of one tensor's row
-  constexpr int kPieces = kRows * 2 * kChunks;  // of a round
-  constexpr int kPer = (kPieces + kThreads - 1) / kThreads;
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int* kept = P.kept + ((long long)b * P.src.H + h) * P.keep;
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  EvictSmem& s = *reinterpret_cast<EvictSmem*>(smem_raw);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem_raw + sizeof(EvictSmem));
+  const int rank = (int)cluster_rank();
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int L = clamp_len(P.src.lens[b], P.src.C);
+  const int n_out = min(L, P.keep);
+  int* kept = P.kept + ((long long)b * P.src.H + h) * P.keep;
   const long long s0 = head_row(P.src, b, h), d0 = head_row(P.dst, b, h);
-  for (int r0 = 0; r0 < P.keep; r0 += kRows) {
+  const float* w = P.src.w + s0;
+
+  if (L <= P.keep) {
+    for (int i = rank * kThreads + threadIdx.x; i < P.keep; i += P.cluster * kThreads)
+      kept[i] = i < L ? i : -1;
+    if (P.in_place) return;  // (the whole cluster)
+  } else {
+    const int lo = P.sink, hi = L - P.recent;  // candidates [lo, hi)
+    uint32_t need = (uint32_t)(P.keep - P.sink - P.recent);
+    // this warp's part: `per` keys from `first` on
+    const int per = ((L + P.cluster * kWarps - 1) / (P.cluster * kWarps) + 127) / 128 * 128;
+    const long long first = (long long)(rank * kWarps + warp) * per;
+    const int n = (int)max(0LL, min((long long)per, L - first));
+    const bool in_smem = per * kWarps <= kKeysInSmem;
+    uint32_t* mine = keys + warp * per;
+    for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) s.hist[0][i] = 0;
+    if (in_smem) {
+      // 16 bytes per lane (the rows before a head are a multiple of 16); a
+      // read behind L stays inside the capacity
+#pragma unroll 4
+      for (int i = 4 * lane; i < n; i += 128) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(w + first + i));
+        *reinterpret_cast<uint4*>(mine + i) =
+            make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
+      }
+    }
+    __syncthreads();
+    auto key_at = [&](int i) { return in_smem ? mine[i] : order_key(__ldg(w + first + i)); };
+    uint32_t prefix = 0;  // the n-th largest key's bits found so far
+    if (need > 0) {
+      constexpr int kShift[3] = {21, 10, 0};
+      constexpr uint32_t kMask[3] = {0u, 0xffe00000u, 0xfffffc00u};
+#pragma unroll
+      for (int pass = 0; pass < 3; ++pass) {
+        for (int i0 = 0; i0 < n; i0 += 32) {
+          const int i = i0 + lane;
+          const long long j = first + i;
+          bool in = i < n && j >= lo && j < hi;
+          uint32_t key = 0;
+          if (in) {
+            key = key_at(i);
+            in = (key & kMask[pass]) == prefix;
+          }
+          const uint32_t bin = (key >> kShift[pass]) & (pass == 2 ? 1023u : 2047u);
+          // one addition where a whole warp agrees (runs of equal weights)
+          int same;
+          __match_all_sync(0xffffffffu, in ? bin : 0xffffffffu, &same);
+          if (same) {
+            if (in && lane == 0) atomicAdd(&s.hist[pass][bin], 32u);
+          } else if (in) {
+            atomicAdd(&s.hist[pass][bin], 1u);
+          }
+        }
+        cluster_sync();
+        find_bin(s, pass, P.cluster, need);
+        prefix |= s.bin << kShift[pass];
+        need = s.left;
+      }
+    }
+    const bool any = P.keep - P.sink - P.recent > 0;
+    // kept for sure (sinks, recent, above the n-th largest), and equal to it
+    uint32_t above = 0, tie = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      const long long j = first + i;
+      bool a = false, t = false;
+      if (i < n) {
+        const bool fixed = j < lo || j >= hi;
+        const uint32_t key = !fixed && any ? key_at(i) : 0u;
+        a = fixed || (any && key > prefix);
+        t = !fixed && any && key == prefix;
+      }
+      above += __popc(__ballot_sync(0xffffffffu, a));
+      tie += __popc(__ballot_sync(0xffffffffu, t));
+    }
+    if (lane == 0) {
+      s.above[warp] = above;
+      s.tie[warp] = tie;
+    }
+    __syncthreads();
+    uint32_t a_before = 0, t_before = 0;
+    {
+      const uint32_t x = lane < kWarps ? s.above[lane] : 0u, y = lane < kWarps ? s.tie[lane] : 0u;
+      uint32_t xi = x, yi = y;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t xo = __shfl_up_sync(0xffffffffu, xi, o);
+        const uint32_t yo = __shfl_up_sync(0xffffffffu, yi, o);
+        if (lane >= o) {
+          xi += xo;
+          yi += yo;
+        }
+      }
+      a_before = __shfl_sync(0xffffffffu, xi - x, warp);
+      t_before = __shfl_sync(0xffffffffu, yi - y, warp);
+      if (warp == 0 && lane == 31) {
+        s.total[0] = xi;
+        s.total[1] = yi;
+      }
+    }
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      a_before += peer_load(&s.total[0], r);
+      t_before += peer_load(&s.total[1], r);
+    }
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      const long long j = first + i;
+      bool a = false, t = false;
+      if (i < n) {
+        const bool fixed = j < lo || j >= hi;
+        const uint32_t key = !fixed && any ? key_at(i) : 0u;
+        a = fixed || (any && key > prefix);
+        t = !fixed && any && key == prefix;
+      }
+      const uint32_t below = (1u << lane) - 1u;
+      const uint32_t ab = __ballot_sync(0xffffffffu, a), tb = __ballot_sync(0xffffffffu, t);
+      // the first `need` ties are kept
+      const uint32_t t_at = t_before + __popc(tb & below);
+      const uint32_t at = a_before + __popc(ab & below) + min(t_at, need);
+      if ((a || (t && t_at < need)) && at < (uint32_t)P.keep) kept[at] = (int)j;
+      a_before += __popc(ab);
+      t_before += __popc(tb);
+    }
+  }
+  cluster_sync();  // the list is complete; no CTA needs another's memory any more
+
+  // ------------------------------------------------------------------ move
+  constexpr int kChunks = D / 16;  // 16-byte pieces of a row's K and V codes
+  constexpr int kPer = 4;          // pieces in a thread's registers
+  constexpr int kRows = kThreads * kPer / kChunks;  // rows per CTA and round
+  const int c = threadIdx.x % kChunks;
+  const uint8_t* from_codes = (c < kChunks / 2 ? P.src.kc : P.src.vc) + (c % (kChunks / 2)) * 16;
+  uint8_t* to_codes = (c < kChunks / 2 ? P.dst.kc : P.dst.vc) + (c % (kChunks / 2)) * 16;
+  for (int r0 = rank * kRows; r0 - rank * kRows < n_out; r0 += P.cluster * kRows) {
     uint4 buf[kPer];
-    uint32_t sc = 0;
-    float w = 0.f;
     int from[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int p = threadIdx.x + i * kThreads;
-      const int r = r0 + p / (2 * kChunks), c = p % (2 * kChunks);
-      from[i] = (p < kPieces && r < P.keep) ? kept[r] : -1;
-      if (from[i] >= 0) {
-        const uint8_t* t = c < kChunks ? P.src.kc : P.src.vc;
-        buf[i] = *reinterpret_cast<const uint4*>(t + (s0 + from[i]) * (D / 2) + (c % kChunks) * 16);
-      }
+      const int r = r0 + threadIdx.x / kChunks + i * (kThreads / kChunks);
+      from[i] = r < n_out ? kept[r] : -1;
     }
-    // threads 0 .. kRows-1: K scales and weights; kRows .. 2 kRows - 1: V scales
-    const int sr = r0 + (threadIdx.x % kRows), st = threadIdx.x / kRows;
-    const int sfrom = (st < 2 && sr < P.keep) ? kept[sr] : -1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (from[i] >= 0)
+        buf[i] = *reinterpret_cast<const uint4*>(from_codes + (s0 + from[i]) * (D / 2));
+    // scales and weights: a thread per row
+    const int sr = r0 + threadIdx.x;
+    const int sfrom = threadIdx.x < kRows && sr < n_out ? kept[sr] : -1;
+    uint32_t sk = 0, sv = 0;
+    float sw = 0.f;
     if (sfrom >= 0) {
-      const uint8_t* t = (st ? P.src.vs : P.src.ks) + (s0 + sfrom) * (D / 32);
-      sc = D == 128 ? *reinterpret_cast<const uint32_t*>(t) : *reinterpret_cast<const uint16_t*>(t);
-      if (st == 0) w = P.src.w[s0 + sfrom];
+      const uint8_t* ks = P.src.ks + (s0 + sfrom) * (D / kBlock);
+      const uint8_t* vs = P.src.vs + (s0 + sfrom) * (D / kBlock);
+      if constexpr (D == 128) {
+        sk = *reinterpret_cast<const uint32_t*>(ks);
+        sv = *reinterpret_cast<const uint32_t*>(vs);
+      } else {
+        sk = *reinterpret_cast<const uint16_t*>(ks);
+        sv = *reinterpret_cast<const uint16_t*>(vs);
+      }
+      sw = w[sfrom];
     }
-    __syncthreads();
+    if (P.in_place) cluster_sync();
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int p = threadIdx.x + i * kThreads;
-      const int r = r0 + p / (2 * kChunks), c = p % (2 * kChunks);
-      if (from[i] >= 0) {
-        uint8_t* t = c < kChunks ? P.dst.kc : P.dst.vc;
-        *reinterpret_cast<uint4*>(t + (d0 + r) * (D / 2) + (c % kChunks) * 16) = buf[i];
-      }
+      const int r = r0 + threadIdx.x / kChunks + i * (kThreads / kChunks);
+      if (from[i] >= 0) *reinterpret_cast<uint4*>(to_codes + (d0 + r) * (D / 2)) = buf[i];
     }
     if (sfrom >= 0) {
-      uint8_t* t = (st ? P.dst.vs : P.dst.ks) + (d0 + sr) * (D / 32);
-      if (D == 128) *reinterpret_cast<uint32_t*>(t) = sc;
-      else *reinterpret_cast<uint16_t*>(t) = (uint16_t)sc;
-      if (st == 0) {
-        if (P.dst.w) P.dst.w[d0 + sr] = w;
-        // the last kept row tells the new length
-        if (h == 0 && (sr + 1 == P.keep || kept[sr + 1] < 0)) P.dst.lens[b] = sr + 1;
+      uint8_t* ks = P.dst.ks + (d0 + sr) * (D / kBlock);
+      uint8_t* vs = P.dst.vs + (d0 + sr) * (D / kBlock);
+      if constexpr (D == 128) {
+        *reinterpret_cast<uint32_t*>(ks) = sk;
+        *reinterpret_cast<uint32_t*>(vs) = sv;
+      } else {
+        *reinterpret_cast<uint16_t*>(ks) = (uint16_t)sk;
+        *reinterpret_cast<uint16_t*>(vs) = (uint16_t)sv;
       }
+      if (P.dst.w) P.dst.w[d0 + sr] = sw;
     }
-    __syncthreads();
   }
-  if (h == 0 && threadIdx.x == 0 && kept[0] < 0) P.dst.lens[b] = 0;
+  // In place, other clusters may still have to read the old length: a launch
+  // behind this one writes the new one.
+  if (!P.in_place && h == 0 && rank == 0 && threadIdx.x == 0) P.dst.lens[b] = n_out;
+}
+
+__global__ void evict_lens_kernel(const EvictParams P) {
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b < P.src.B) P.dst.lens[b] = min(clamp_len(P.src.lens[b], P.src.C), P.keep);
+}
+
+template <int D>
+usp_status_t launch_d(const EvictParams& P, cudaStream_t st) {
+  const int per = ((P.src.C + P.cluster * kWarps - 1) / (P.cluster * kWarps) + 127) / 128 * 128;
+  const int n = per * kWarps <= kKeysInSmem ? per * kWarps : kKeysInSmem;
+  const size_t smem = sizeof(EvictSmem) + (size_t)n * 4;
+  cudaError_t e = cudaFuncSetAttribute(evict_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(sizeof(EvictSmem) + kKeysInSmem * 4));
+  if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(P.cluster, P.src.H, P.src.B);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = P.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  {
+    ProfScope ps(st, "kv4_evict");
+    e = cudaLaunchKernelEx(&cfg, evict_kernel<D>, P);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail_cuda("kernel launch", e);
+  }
+  note_launch();
+  return USP_OK;
 }
 
 }  // namespace
 
 usp_status_t launch_kv4_evict(const Cache& src, const Cache& dst, int D, int* kept, int keep,
                               int recent, int sink, cudaStream_t st) {
-  EvictParams P{src, dst, kept, keep, recent, sink};
+  EvictParams P{src, dst, kept, keep, recent, sink, src.kc == dst.kc && src.C > 0, 1};
+  // a CTA per 4K tokens (one radix pass takes a warp 128 keys), at most eight
+  while (P.cluster < kMaxCluster && (long long)P.cluster * 4096 < src.C) P.cluster *= 2;
+  usp_status_t r = D == 128 ? launch_d<128>(P, st) : launch_d<64>(P, st);
+  if (r != USP_OK || !P.in_place) return r;
   {
-    ProfScope ps(st, "kv4_evict_select");
-    select_kernel<<<dim3(src.H, src.B), kThreads, 0, st>>>(P);
-  }
-  note_launch();
-  usp_status_t r = check_launch();
-  if (r != USP_OK) return r;
-  {
-    ProfScope ps(st, "kv4_evict_move");
-    if (D == 128)
-      move_kernel<128><<<dim3(src.H, src.B), kThreads, 0, st>>>(P);
-    else
-      move_kernel<64><<<dim3(src.H, src.B), kThreads, 0, st>>>(P);
+    ProfScope ps(st, "kv4_evict_lens");
+    evict_lens_kernel<<<(src.B + 255) / 256, 256, 0, st>>>(P);
   }
   note_launch();
   return check_launch();
