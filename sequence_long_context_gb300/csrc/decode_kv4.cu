@@ -20,19 +20,31 @@
 // its own online softmax; warps meet only at the end of a unit. The keys and
 // channels are the M side of the matrix products and the query rows the N
 // side (8 rows per product, where 16 would be padding for most head groups):
-//   S^T [keys x rows]  = K [keys x D] Q^T      (bf16 m16n8k16, K exact)
-//   O^T [D x rows]    += V^T [D x keys] P^T    (fp16 m16n8k16, V exact)
+//   S^T [keys x rows]  = K [keys x D] Q^T      (fp16 m16n8k16, fp32 sums)
+//   O^T [D x rows]    += V^T [D x keys] P^T
 // The K index of a product may be any permutation of the channels (keys) that
 // both operands share. Thread (g, t) = (lane / 4, lane % 4) owns channels
 // [t D/4, ..) of key rows g and g + 8 for K, and channels [g D/8, ..) of keys
 // 2t, 2t+1, 2t+8, 2t+9 for V: vector loads, and one scale per key (D/4 and
 // D/8 divide a block of 32 or are one).
 //
-// 4 bits to 16: the nibble u = c + 8 is placed in the mantissa of a constant
-// power of two B whose step makes it B + u; one packed FMA by (s, -(B + 8) s)
-// gives c s. (B + 8) s must be exact: B = 16 in bf16 (24 s, 6 bits), B = 64 in
-// fp16 (72 s, 8 bits). K uses bf16 because q is bf16 (exact products), V fp16
-// because P in fp16 has a rounding of 2^-11 where bf16 has 2^-8.
+// 4 bits to 16. The products take u s with the nibble u = c + 8 >= 0, and the
+// bias 8 s is taken off by one more product per 16 keys:
+//   S^T: sum_d q_d (u_d - 8) s_d = sum_d q_d u_d s_d + sum_blocks s_blk (-8 sum_{d in blk} q_d)
+//   O^T: sum_j p_j (u_j - 8) s_j = sum_j p_j u_j s_j - 8 sum_j p_j s_j
+// u s has at most 8 significant bits, so it is exact in fp16, and costs half an
+// instruction per element and half a multiply-add: a nibble in bits [3:0] of an
+// fp16 whose constant is 1024 stands for 1024 + u, in bits [7:4] under 64 for
+// 64 + u, and (B + u) s - B s needs B s to be exact only, which a power of two
+// always is. Two of a word's four nibble pairs are in place, the other two
+// after one shift. (With the bias inside, (B + 8) s must be exact, which takes
+// smaller constants and a shift for every pair: 425 instructions per 16 keys
+// instead of 330, and the integer pipe at its limit.) The scale is 2^-4 s, so
+// that 1024 s stays in range. q is scaled by a power of two per row, exactly,
+// to a largest element of 64 .. 128 (elements below 2^-23 of it lose bits),
+// and -8 sum q is given as three fp16 parts. The rounding of p to fp16
+// (2^-11; bf16 would have 2^-8) is the only one of the products, and is the
+// same in both of O's sums.
 #include <cuda_fp16.h>
 
 #include "internal.h"
@@ -111,23 +123,27 @@ __device__ __forceinline__ long long active_ctas(const Params& P, long long T) {
 struct Walk {
   int b, hr;        // sequence, KV head * nrb + row block
   int s, end;       // of the unit
+  int len;          // of the sequence
+  SeqSteps q;
+  long long row;    // before the head's first
   long long left;   // steps of the run behind this unit
 };
+__device__ __forceinline__ void enter_seq(const Params& P, Walk& w) {
+  w.len = seq_len(P, w.b);
+  w.q = seq_steps(P, w.len);
+}
 __device__ __forceinline__ bool next_unit(const Params& P, Walk& w) {
   if (w.left <= 0) return false;
-  int n = 0;
   if (++w.hr == P.c.H * P.nrb) {
     w.hr = 0;
     do {
-      ++w.b;
-      n = w.b < P.c.B ? seq_steps(P, seq_len(P, w.b)).n : -1;
-    } while (n == 0);
-    if (n < 0) return false;
-  } else {
-    n = seq_steps(P, seq_len(P, w.b)).n;
+      if (++w.b >= P.c.B) return false;
+      enter_seq(P, w);
+    } while (w.q.n == 0);
   }
+  w.row = head_row(P.c, w.b, w.hr / P.nrb);
   w.s = 0;
-  w.end = (int)min((long long)n, w.left);
+  w.end = (int)min((long long)w.q.n, w.left);
   w.left -= w.end;
   return true;
 }
@@ -155,11 +171,6 @@ struct Smem {
   static_assert(kRed % 16 == 0 && kML % 16 == 0 && kBar % 8 == 0 && kMisc % 16 == 0, "alignment");
 };
 
-__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
 __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -171,13 +182,6 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x) {
   uint32_t d;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "n"(kMask), "n"(kBase));
   return d;
-}
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
@@ -198,16 +202,25 @@ __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_
 // so that a quarter (V: half) of a warp spreads over both halves of the banks.
 __device__ __forceinline__ int tile_key(int i) { return i ^ ((i >> 1) & 1); }
 
+// The four pairs (nibbles j and j + 4, j = 0..3) of a word of codes times a pair
+// of scales: a[j] = u s. zb = -1024 s, zs = -64 s.
+__device__ __forceinline__ void expand(uint32_t x, uint32_t s, uint32_t zb, uint32_t zs,
+                                       uint32_t (&a)[4]) {
+  const uint32_t y = x >> 8;
+  a[0] = h2_fma(and_or<0x000F000Fu, 0x64006400u>(x), s, zb);
+  a[1] = h2_fma(and_or<0x00F000F0u, 0x54005400u>(x), s, zs);
+  a[2] = h2_fma(and_or<0x000F000Fu, 0x64006400u>(y), s, zb);
+  a[3] = h2_fma(and_or<0x00F000F0u, 0x54005400u>(y), s, zs);
+}
+
 // Starts the copies of one step into a stage.
 template <int D>
 __device__ __forceinline__ void load_step(const Params& P, const Walk& w, uint32_t stage,
                                           uint32_t bar) {
-  const int L = seq_len(P, w.b);
-  const SeqSteps q = seq_steps(P, L);
-  const int key0 = (w.s < q.sinks ? w.s : w.s + q.skip) * kStep;
+  const int key0 = (w.s < w.q.sinks ? w.s : w.s + w.q.skip) * kStep;
   // whole 16-row groups that hold cached keys (the capacity is a multiple of 16)
-  const int rows = min(kStep, (L - key0 + kRowAlign - 1) / kRowAlign * kRowAlign);
-  const long long row = head_row(P.c, w.b, w.hr / P.nrb) + key0;
+  const int rows = w.len - key0 > kRowAlign ? kStep : kRowAlign;
+  const long long row = w.row + key0;
   const uint32_t cb = rows * (D / 2), sb = rows * (D / kBlock);
   mbar_expect_tx(bar, 2 * (cb + sb));
   bulk_load(stage + Stage<D>::kKC, P.c.kc + row * (D / 2), cb, bar);
@@ -287,8 +300,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
   Walk cur;
   {
     cur.b = (int)run[2];
-    const int n = seq_steps(P, seq_len(P, cur.b)).n;
+    enter_seq(P, cur);
+    const int n = cur.q.n;
     cur.hr = (int)(run[0] / n);
+    cur.row = head_row(P.c, cur.b, cur.hr / P.nrb);
     cur.s = (int)(run[0] - (long long)cur.hr * n);
     cur.end = (int)min((long long)n, cur.s + run[1]);
     cur.left = run[1] - (cur.end - cur.s);
@@ -317,15 +332,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
 #pragma unroll
   for (int s = 0; s < kStages; ++s) issue();
 
+  const __half2 k2m4 = __float2half2_rn(0.0625f);
+  const __half2 m1024 = __float2half2_rn(-1024.f), m64 = __float2half2_rn(-64.f);
   bool ok = true;
   for (;;) {
     // ---------------------------------------------------------------- a unit
     const int b = cur.b, h = cur.hr / P.nrb, rb = cur.hr - h * P.nrb;
-    const int len = seq_len(P, b);
-    const SeqSteps steps = seq_steps(P, len);
+    const int len = cur.len;
+    const SeqSteps steps = cur.q;
     // Q^T fragments: product kk = 2w + jj takes channels (8w + 2jj, + 4) and
-    // (8w + 2jj + 1, + 4) of the thread's run of D/4
-    uint32_t qf[NT][2 * kWK][2];
+    // (8w + 2jj + 1, + 4) of the thread's run of D/4; qb: -8 times the run's
+    // (its block's part's) sum in three parts
+    uint32_t qf[NT][2 * kWK][2], qb[NT][2];
+    float mul[NT][2];  // of rows 2t, 2t + 1: scores to log2 units
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = rb * kRows + nt * 8 + g;
@@ -334,16 +353,55 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
         const int hh = r / P.Tq, tok = r - hh * P.Tq;
         src = P.q + (((long long)b * P.Tq + tok) * P.Hq + h * P.G + hh) * D + t * (D / 4);
       }
+      uint4 x[kWK];
+      float big = 0.f;
 #pragma unroll
       for (int w = 0; w < kWK; ++w) {
-        const uint4 x = src ? __ldg(reinterpret_cast<const uint4*>(src) + w) : make_uint4(0, 0, 0, 0);
-        qf[nt][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);
-        qf[nt][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);
-        qf[nt][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
-        qf[nt][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
+        x[w] = src ? __ldg(reinterpret_cast<const uint4*>(src) + w) : make_uint4(0, 0, 0, 0);
+        const uint32_t e[4] = {x[w].x, x[w].y, x[w].z, x[w].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          big = fmaxf(big, fmaxf(fabsf(__uint_as_float(e[i] << 16)),
+                                 fabsf(__uint_as_float(e[i] & 0xffff0000u))));
       }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // 2^ex times a largest element in [1, 2) is brought to [64, 128)
+      const int ex = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100), 127);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 6 - ex) << 23);
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWK; ++w) {
+        const uint32_t e[4] = {x[w].x, x[w].y, x[w].z, x[w].w};
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = __uint_as_float(e[i] << 16) * up;
+          f[2 * i + 1] = __uint_as_float(e[i] & 0xffff0000u) * up;
+        }
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const __half2 p = __floats2half2_rn(f[2 * jj + i], f[2 * jj + i + 4]);
+            qf[nt][2 * w + jj][i] = half2_bits(p);
+            const float2 back = __half22float2(p);
+            sum += back.x + back.y;
+          }
+      }
+      sum *= -8.f;
+      const __half hi = __float2half_rn(sum);
+      const float rest = sum - __half2float(hi);
+      const __half mid = __float2half_rn(rest);
+      qb[nt][0] = half2_bits(__halves2half2(hi, mid));
+      qb[nt][1] = half2_bits(__floats2half2_rn(rest - __half2float(mid), 0.f));
+      // 16 for the scale's 2^-4
+      const float row_mul = ldexpf(P.score_mul * 16.f, ex - 6);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        mul[nt][e] = __shfl_sync(0xffffffffu, row_mul, 4 * (2 * t + e));
     }
-    float o[NT][kMT][4];
+    float o[NT][kMT][4], ob[NT][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -351,6 +409,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
       for (int i = 0; i < kMT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ob[nt][e] = 0.f;
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
@@ -386,31 +446,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
           k1[0] = c.x; k1[1] = c.y;
         }
         const uint8_t* ks = stp + St::kKS + (t * (D / 4)) / kBlock;
-        const float2 ss = __half22float2(
-            e4m3x2_to_half2(ks[r0 * (D / kBlock)] | (ks[r1 * (D / kBlock)] << 8)));
-        const uint32_t s0 = pack_bf16(ss.x, ss.x), s1 = pack_bf16(ss.y, ss.y);
-        const uint32_t z0 = pack_bf16(-24.f * ss.x, -24.f * ss.x);
-        const uint32_t z1 = pack_bf16(-24.f * ss.y, -24.f * ss.y);
+        const __half2 ss = __hmul2(
+            e4m3x2_to_half2(ks[r0 * (D / kBlock)] | (ks[r1 * (D / kBlock)] << 8)), k2m4);
+        const uint32_t s0 = half2_bits(__low2half2(ss)), s1 = half2_bits(__high2half2(ss));
+        const __half2 zb = __hmul2(ss, m1024), zs = __hmul2(ss, m64);
+        const uint32_t zb0 = half2_bits(__low2half2(zb)), zb1 = half2_bits(__high2half2(zb));
+        const uint32_t zs0 = half2_bits(__low2half2(zs)), zs1 = half2_bits(__high2half2(zs));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[nt][half][e] = 0.f;
+          // the bias: thread t's K indices stand for its block (D = 64: its
+          // half of the block)
+          const uint32_t a[4] = {s0, s1, s0, s1};
+          mma_f16(sc[nt][half], a, qb[nt][0], qb[nt][1]);
+        }
 #pragma unroll
         for (int w = 0; w < kWK; ++w) {
           // nibbles j and j + 4 of a word: channels 8w + j, 8w + 4 + j
-          auto pair = [](uint32_t x, int j) {
-            const uint32_t y = j == 0 ? x << 3 : j == 1 ? x >> 1 : j == 2 ? x >> 5 : x >> 9;
-            return and_or<0x00780078u, 0x41804180u>(y);
-          };
+          uint32_t p0[4], p1[4];
+          expand(k0[w], s0, zb0, zs0, p0);
+          expand(k1[w], s1, zb1, zs1, p1);
 #pragma unroll
           for (int jj = 0; jj < 2; ++jj) {
-            const uint32_t a[4] = {bf2_fma(pair(k0[w], 2 * jj), s0, z0),
-                                   bf2_fma(pair(k1[w], 2 * jj), s1, z1),
-                                   bf2_fma(pair(k0[w], 2 * jj + 1), s0, z0),
-                                   bf2_fma(pair(k1[w], 2 * jj + 1), s1, z1)};
+            const uint32_t a[4] = {p0[2 * jj], p1[2 * jj], p0[2 * jj + 1], p1[2 * jj + 1]};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_bf16(sc[nt][half], a, qf[nt][2 * w + jj][0], qf[nt][2 * w + jj][1]);
+              mma_f16(sc[nt][half], a, qf[nt][2 * w + jj][0], qf[nt][2 * w + jj][1]);
           }
         }
       }
@@ -423,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
         for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float x = sc[nt][half][e] * P.score_mul;
+            float x = sc[nt][half][e] * mul[nt][e & 1];
             if (masked) {
               const int j = key0 + 16 * half + tile_key(g) + 8 * (e >> 1);
               const int tok = (rb * kRows + nt * 8 + 2 * t + (e & 1)) % P.Tq;
@@ -473,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
             a[e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - x);
             m[nt][e] = x;
             l[nt][e] *= a[e];
+            ob[nt][e] *= a[e];
           }
 #pragma unroll
           for (int i = 0; i < kMT; ++i) {
@@ -519,26 +582,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
           // rows behind the sequence hold anything: 0, so that 0 * it is 0
           if (masked && key0 + keys[i] >= len) sb[i] = 0;
         }
-        const __half2 sab = e4m3x2_to_half2(sb[0] | (sb[1] << 8));
-        const __half2 scd = e4m3x2_to_half2(sb[2] | (sb[3] << 8));
-        const __half2 m72 = __float2half2_rn(-72.f);
-        const uint32_t s0 = half2_bits(sab), z0 = half2_bits(__hmul2(sab, m72));
-        const uint32_t s1 = half2_bits(scd), z1 = half2_bits(__hmul2(scd, m72));
-        auto pair = [](uint32_t x, int j) {
-          const uint32_t y = j == 0 ? x << 4 : j == 1 ? x : j == 2 ? x >> 4 : x >> 8;
-          return and_or<0x00F000F0u, 0x54005400u>(y);
-        };
+        const __half2 sab = __hmul2(e4m3x2_to_half2(sb[0] | (sb[1] << 8)), k2m4);
+        const __half2 scd = __hmul2(e4m3x2_to_half2(sb[2] | (sb[3] << 8)), k2m4);
+        const uint32_t s0 = half2_bits(sab), s1 = half2_bits(scd);
+        const uint32_t zb0 = half2_bits(__hmul2(sab, m1024)), zs0 = half2_bits(__hmul2(sab, m64));
+        const uint32_t zb1 = half2_bits(__hmul2(scd, m1024)), zs1 = half2_bits(__hmul2(scd, m64));
+        // row g of the bias product is the scale of the thread's own channels
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t a[4] = {s0, 0u, s1, 0u};
+          mma_f16(ob[nt], a, pf[nt][half][0], pf[nt][half][1]);
+        }
 #pragma unroll
         for (int w = 0; w < kWV; ++w) {
           // channels 8w + 0..3 (low halves) and 8w + 4..7 of both keys
-          const uint32_t xl = __byte_perm(vw[0][w], vw[1][w], 0x5410);
-          const uint32_t xh = __byte_perm(vw[0][w], vw[1][w], 0x7632);
-          const uint32_t yl = __byte_perm(vw[2][w], vw[3][w], 0x5410);
-          const uint32_t yh = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+          uint32_t xl[4], xh[4], yl[4], yh[4];
+          expand(__byte_perm(vw[0][w], vw[1][w], 0x5410), s0, zb0, zs0, xl);
+          expand(__byte_perm(vw[0][w], vw[1][w], 0x7632), s0, zb0, zs0, xh);
+          expand(__byte_perm(vw[2][w], vw[3][w], 0x5410), s1, zb1, zs1, yl);
+          expand(__byte_perm(vw[2][w], vw[3][w], 0x7632), s1, zb1, zs1, yh);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t a[4] = {h2_fma(pair(xl, j), s0, z0), h2_fma(pair(xh, j), s0, z0),
-                                   h2_fma(pair(yl, j), s1, z1), h2_fma(pair(yh, j), s1, z1)};
+            const uint32_t a[4] = {xl[j], xh[j], yl[j], yh[j]};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma_f16(o[nt][4 * w + j], a, pf[nt][half][0], pf[nt][half][1]);
@@ -566,10 +631,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
       float* mine = red + (warp * 8 + 2 * t) * L::kRedStride + g;
 #pragma unroll
       for (int i = 0; i < kMT; ++i) {
-        mine[16 * i] = o[nt][i][0];
-        mine[L::kRedStride + 16 * i] = o[nt][i][1];
-        mine[16 * i + 8] = o[nt][i][2];
-        mine[L::kRedStride + 16 * i + 8] = o[nt][i][3];
+        mine[16 * i] = fmaf(-8.f, ob[nt][0], o[nt][i][0]);
+        mine[L::kRedStride + 16 * i] = fmaf(-8.f, ob[nt][1], o[nt][i][1]);
+        mine[16 * i + 8] = fmaf(-8.f, ob[nt][0], o[nt][i][2]);
+        mine[L::kRedStride + 16 * i + 8] = fmaf(-8.f, ob[nt][1], o[nt][i][3]);
       }
       __syncthreads();
       for (int x = threadIdx.x; x < 8 * D; x += kThreads) {
@@ -795,7 +860,7 @@ usp_status_t launch_decode_kv4(const DecodeKv4Args& a, void* workspace, cudaStre
   P.nrb = (P.R + 8 * nt - 1) / (8 * nt);
   P.grid = nt == 1 ? kGridMax : kGridMax / 2;
   P.score_mul = a.scale * kLog2e * a.k_descale;
-  P.v_descale = a.v_descale;
+  P.v_descale = a.v_descale * 16.f;  // the kernel's V is 2^-4 of the cache's
   P.causal = a.causal;
   P.window = a.window;
   P.sink = a.sink;

@@ -6,20 +6,27 @@
 // ("Long Context Attention" notes, "Motivation": the LSE is what the forward
 // keeps; with it a probability needs no second pass over its row.)
 //
-// Tensor-core kernel (bf16). One CTA owns 256 keys (two tiles of 128) of one
-// KV head and takes the query tiles of 64 that may see them, for some of the
-// group's query heads and a segment of the queries: S^T = K Q^T, keys on the
-// 128 TMEM lanes, so that a softmax thread owns a key and the column sum is a
-// register. Nothing is normalised or rescaled, and nothing goes back to the
-// tensor core. 256 keys share each query tile: 16 KB of Q per 2 x 128 x 64
-// scores keeps the L2 traffic at a quarter of what one tile of 64 would need.
-// Roles (320 threads, two CTAs per SM):
-//   warps 0-7  softmax: warp w owns keys [32 w, 32 w + 32) of the 256
-//   warp 8     producer: finds the query tiles that can see the keys (32 at a
-//              time, one per lane), loads Q (two slots) and, with all lanes,
-//              the tile's LSE and natural positions (a ring of eight)
-//   warp 9     MMA issuer, owner of tensor memory: S^T of key tile a, buffer c
-//              in columns [128 a + 64 c, + 64)
+// Tensor-core kernel (bf16). One CTA owns KT tiles of 128 keys of one KV head
+// and takes the query tiles of 128 that may see them, for some of the group's
+// query heads and a segment of the queries: S^T = K Q^T, keys on the 128 TMEM
+// lanes, so that a softmax thread owns a key and the column sum is a register.
+// Nothing is normalised or rescaled, and nothing goes back to the tensor core.
+// Per 128 x 128 tile (D = 128) the products take 512 clocks, and so do the
+// exponentials (32 per clock and SM) and the products' reads of shared memory
+// (64 KB); all keys of a CTA share each query tile, which keeps the loads of Q
+// to 32 KB per KT x 512 clocks.
+//   KT = 4  (one CTA per SM, two Q slots): 512 keys
+//   KT = 2  (two CTAs per SM, one Q slot): short problems, where the loads of
+//           K are what counts and one CTA's overlap the other's work
+// A key tile has one 128-column buffer of scores: while the softmax takes it
+// out, the products of the other key tiles run.
+// Roles (32 (4 KT + 2) threads):
+//   warps 0 .. 4 KT - 1  softmax: warp w owns keys [32 w, 32 w + 32)
+//   the next   producer: finds the query tiles that can see the keys (32 at a
+//              time, one per lane), loads Q and, with all lanes, the tile's
+//              LSE (asked for one tile ahead) and natural positions
+//   the last   MMA issuer, owner of tensor memory: S^T of key tile a in
+//              columns [128 a, + 128)
 // Positions are read per query from shared memory, so a tile may cross chunk
 // and shard boundaries: any layout and any length has this kernel.
 //
@@ -29,6 +36,7 @@
 // CUDA-core kernel (fp32 inputs, and as a cross-check): 64 x 64 tiles.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cstdio>
 
 #include "internal.h"
@@ -42,16 +50,22 @@ using namespace tc;
 
 __device__ int g_key_weights_status = 0;
 
-constexpr int kQT = 64;             // queries per tile
-constexpr int kKeys = 2 * kTile;    // keys per CTA
-constexpr int kSoftWarps = 8;
-constexpr int kProducerWarp = kSoftWarps;
-constexpr int kMmaWarp = kProducerWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr int kRing = 8;            // entries of query statistics
+constexpr int kQT = kTile;           // queries per tile
+constexpr int kRing = 4;            // entries of query statistics
 constexpr int kEnd = -1;
 constexpr int kNowhere = -(1 << 30);  // position of a row that is not observed
 constexpr float kLog2e = 1.4426950408889634f;
+
+// True in one lane of the warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 
 struct WeightParams {
   AttnParams P;
@@ -64,25 +78,37 @@ struct WeightParams {
   int ntiles;    // query tiles
 };
 
-template <int D>
+template <int D, int KT>
 struct WSmem {
+  static constexpr int kKeys = KT * kTile;
+  static constexpr int kSoftWarps = 4 * KT;
+  static constexpr int kProducerWarp = kSoftWarps;
+  static constexpr int kMmaWarp = kProducerWarp + 1;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr int kSlots = KT == 2 ? 1 : 2;  // Q tiles
+  // A ring entry is written for tile x once the products of tile x - kSlots
+  // are done; the softmax is then past the scores of tile x - kSlots - 1, so
+  // past the statistics of tile x - kSlots - 2.
+  static_assert(kRing >= kSlots + 2, "a statistics entry is free");
   static constexpr int kHalves = D / 64;
   static constexpr int kKHalf = kTile * 128;            // 64 channels of one key tile
   static constexpr int kKTile = kKHalf * kHalves;
   static constexpr int kQHalf = kQT * 128;
   static constexpr int kQTile = kQHalf * kHalves;
   static constexpr int kK = 0;
-  static constexpr int kQ = kK + 2 * kKTile;            // 2 slots
-  static constexpr int kStat = kQ + 2 * kQTile;         // kRing x (lse2[64], pos[64])
+  static constexpr int kQ = kK + KT * kKTile;           // kSlots
+  static constexpr int kStat = kQ + kSlots * kQTile;    // kRing x (-lse2[128], pos[128])
   static constexpr int kStatBytes = 2 * kQT * 4;
   static constexpr int kSched = kStat + kRing * kStatBytes;  // kRing ints
   static constexpr int kBar = kSched + kRing * 4;
-  static constexpr int kKFull = 0, kQFull = 1, kQFree = 3, kSFull = 5, kSFree = 9, kStatFull = 13,
-                       kMmaDone = kStatFull + kRing, kNumBars = kMmaDone + 1;
+  static constexpr int kKFull = 0 /* KT */, kQFull = KT, kQFree = kQFull + kSlots,
+                       kSFull = kQFree + kSlots /* KT */, kSFree = kSFull + KT,
+                       kStatFull = kSFree + KT, kMmaDone = kStatFull + kRing,
+                       kNumBars = kMmaDone + 1;
   static constexpr int kMisc = (kBar + 8 * kNumBars + 15) / 16 * 16;
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
-  static_assert(kAlloc <= 113 * 1024, "two CTAs per SM");
+  static_assert(kAlloc <= (KT == 2 ? 113 : 227) * 1024, "two CTAs (KT = 2), one (4) per SM");
   static_assert(kBar % 8 == 0 && kStat % 16 == 0, "alignment");
 };
 
@@ -149,9 +175,9 @@ struct KeyBlock {
   PosRange q;     // of the queries that may see one of them
   int seg0, seg1; // packed sequences of the first and last key
 };
-__device__ __forceinline__ KeyBlock key_block(const AttnParams& P, int key0) {
+__device__ __forceinline__ KeyBlock key_block(const AttnParams& P, int key0, int keys) {
   KeyBlock b;
-  b.k = row_bounds(P, key0, kKeys);
+  b.k = row_bounds(P, key0, keys);
   int s0 = 0, e1 = P.S;
   b.seg0 = b.seg1 = 0;
   if (P.cu != nullptr) {
@@ -193,11 +219,11 @@ __device__ __forceinline__ int classify_tile(const WeightParams& W, int qt, cons
   return all ? kClsFull : kClsMasked;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int D, int KT>
+__global__ void __launch_bounds__(WSmem<D, KT>::kThreads, KT == 2 ? 2 : 1)
 key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k) {
-  using L = WSmem<D>;
+  using L = WSmem<D, KT>;
   const AttnParams& P = W.P;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -219,15 +245,16 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
   idx /= P.Hkv;
   const int bt = idx % P.Bt, kb = idx / P.Bt;
   const int seg = part / groups, h0 = g * P.G + (part % groups) * W.hpi;
-  const int key0 = kb * kKeys;
+  const int key0 = kb * L::kKeys;
+  const int ktiles = min(KT, (P.S - key0 + kTile - 1) / kTile);  // with keys in them
 
-  if (warp == kProducerWarp && lane == 0) {
-    mbar_init(bar(L::kKFull), 1);
-    for (int s = 0; s < 2; ++s) {
+  if (warp == L::kProducerWarp && lane == 0) {
+    for (int a = 0; a < KT; ++a) mbar_init(bar(L::kKFull + a), 1);
+    for (int s = 0; s < L::kSlots; ++s) {
       mbar_init(bar(L::kQFull + s), 1);
       mbar_init(bar(L::kQFree + s), 1);
     }
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < KT; ++s) {
       mbar_init(bar(L::kSFull + s), 1);
       mbar_init(bar(L::kSFree + s), 4);  // the four warps of a key tile
     }
@@ -236,14 +263,15 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch(&tm_q);
-    mbar_expect_tx(bar(L::kKFull), 2 * L::kKTile);
-    for (int a = 0; a < 2; ++a)
+    for (int a = 0; a < ktiles; ++a) {
+      mbar_expect_tx(bar(L::kKFull + a), L::kKTile);
       for (int hf = 0; hf < L::kHalves; ++hf)
-        tma_load_4d(sbase + L::kK + a * L::kKTile + hf * L::kKHalf, &tm_k, bar(L::kKFull), hf * 64,
-                    g, key0 + a * kTile, bt);
+        tma_load_4d(sbase + L::kK + a * L::kKTile + hf * L::kKHalf, &tm_k, bar(L::kKFull + a),
+                    hf * 64, g, key0 + a * kTile, bt);
+    }
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(sbase + L::kMisc, 256);
+  if (warp == L::kMmaWarp) {
+    tmem_alloc(sbase + L::kMisc, 128 * KT);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -251,110 +279,166 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp == kProducerWarp) {
+  if (warp == L::kProducerWarp) {
     // ------------------------------------------------------------ producer
-    const KeyBlock blk = key_block(P, key0);
-    int n = 0;
-    bool ok = true;
+    const KeyBlock blk = key_block(P, key0, L::kKeys);
     int first = seg * W.tps, last = min(W.ntiles, first + W.tps);
     if (P.layout == kContiguous) {  // rank-major order is natural order
       first = max(first, blk.q.lo / kQT);
       last = min(last, blk.q.hi / kQT + 1);
       if (W.observe > 0 && P.cu == nullptr) first = max(first, max(0, P.S - W.observe) / kQT);
     }
-    for (int base = first; base < last && ok; base += 32) {
-      const int mine = base + lane < last ? classify_tile(W, base + lane, blk) : kClsEmpty;
-      unsigned todo = __ballot_sync(0xffffffffu, mine != kClsEmpty);
-      while (todo && ok) {
+    // The next (tile, head), its rows' positions and LSE. This runs once per
+    // tile in one warp, so it is kept short: what takes divisions is found for
+    // 32 tiles at a time, one per lane.
+    struct Item {
+      int qt, cls, h, pos[kQT / 32];
+      float lse[kQT / 32];
+    };
+    const float* lse_head = P.lse + lse_index(P, bt, h0, 0);
+    const int step = P.layout == kStripe ? P.cp : 1;
+    const int run = P.layout == kZigzag ? P.chunk : P.shard;
+    int base = first - 32, cls_mine = kClsEmpty, lo_mine = 0, hh = 0;
+    unsigned todo = 0;
+    Item nx{};
+    bool more = true;
+    auto fetch = [&]() {
+      if (hh == 0) {  // a new tile
+        while (todo == 0 && (base += 32) < last) {
+          const int t = base + lane;
+          cls_mine = t < last ? classify_tile(W, t, blk) : kClsEmpty;
+          todo = __ballot_sync(0xffffffffu, cls_mine != kClsEmpty);
+          // first position, or -1: the rows are not one run of a chunk, or
+          // which are observed depends on the sequence
+          lo_mine = -1;
+          if (cls_mine != kClsEmpty && (W.observe == 0 || P.cu == nullptr)) {
+            const int p0 = t * kQT, p1 = min(p0 + kQT, P.S) - 1;
+            if (p0 / run == p1 / run || P.layout == kContiguous) lo_mine = nat_pos(P, p0);
+          }
+        }
+        if (todo == 0) {
+          more = false;
+          return;
+        }
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
-        const int qt = base + src;
-        const int cls = __shfl_sync(0xffffffffu, mine, src);
-        int pos[2];
-        for (int e = 0; e < 2; ++e) pos[e] = observed_pos(W, qt * kQT + lane + 32 * e);
-        for (int hh = 0; hh < W.hpi && ok; ++hh) {
-          const int h = h0 + hh, slot = n & 1, ring = n & (kRing - 1);
-          float lse[2];
-          for (int e = 0; e < 2; ++e) {
-            const int p = qt * kQT + lane + 32 * e;
-            lse[e] = pos[e] >= 0 ? __ldg(P.lse + lse_index(P, bt, h, p)) : 0.f;
+        nx.qt = base + src;
+        nx.cls = __shfl_sync(0xffffffffu, cls_mine, src);
+        const int lo = __shfl_sync(0xffffffffu, lo_mine, src);
+        const int from = W.observe > 0 ? P.S - W.observe : 0;
+#pragma unroll
+        for (int e = 0; e < kQT / 32; ++e) {
+          const int r = lane + 32 * e;
+          if (lo >= 0) {
+            const int i = lo + r * step;
+            nx.pos[e] = nx.qt * kQT + r < P.S && i >= from ? i : kNowhere;
+          } else {
+            nx.pos[e] = observed_pos(W, nx.qt * kQT + r);
           }
-          if (n >= 2)  // the slot's previous tile has been multiplied
-            ok = mbar_wait(bar(L::kQFree + slot), ((n >> 1) - 1) & 1, abort_flag, status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          // The ring entry is free: the products of tile n - 2 are done, so
-          // the softmax has read the scores of tile n - 4 and is past the
-          // statistics of tile n - 8.
-          float* st = reinterpret_cast<float*>(sm + L::kStat + ring * L::kStatBytes);
-          for (int e = 0; e < 2; ++e) {
-            const float x = lse[e] * kLog2e;
-            // a row that sees nothing adds nothing
-            const bool none = pos[e] < 0 || x == -INFINITY;
-            st[lane + 32 * e] = none ? INFINITY : x;
-            reinterpret_cast<int*>(st)[kQT + lane + 32 * e] = pos[e];
-          }
-          if (lane == 0) sched[ring] = cls;
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(L::kStatFull + ring));
-            mbar_expect_tx(bar(L::kQFull + slot), L::kQTile);
-            for (int hf = 0; hf < L::kHalves; ++hf)
-              tma_load_4d(sbase + L::kQ + slot * L::kQTile + hf * L::kQHalf, &tm_q,
-                          bar(L::kQFull + slot), hf * 64, h, qt * kQT, bt);
-          }
-          ++n;
         }
+      }
+      nx.h = h0 + hh;
+      const float* src_lse = lse_head + hh * P.lse_sh + nx.qt * kQT + lane;
+#pragma unroll
+      for (int e = 0; e < kQT / 32; ++e) nx.lse[e] = nx.pos[e] >= 0 ? __ldg(src_lse + 32 * e) : 0.f;
+      if (++hh == W.hpi) hh = 0;
+    };
+    fetch();
+    int n = 0, slot = 0, phase = 1;  // (the first waits on a free slot pass)
+    bool ok = true;
+    while (more) {
+      const Item it = nx;
+      fetch();  // its loads are on their way during this tile's waits
+      if (n >= L::kSlots) {  // the slot's previous tile has been multiplied
+        ok = mbar_wait(bar(L::kQFree + slot), phase, abort_flag, status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      }
+      const int ring = n & (kRing - 1);
+      if (lane == 0) {
+        mbar_expect_tx(bar(L::kQFull + slot), L::kQTile);
+        for (int hf = 0; hf < L::kHalves; ++hf)
+          tma_load_4d(sbase + L::kQ + slot * L::kQTile + hf * L::kQHalf, &tm_q,
+                      bar(L::kQFull + slot), hf * 64, it.h, it.qt * kQT, bt);
+      }
+      float* st = reinterpret_cast<float*>(sm + L::kStat + ring * L::kStatBytes);
+#pragma unroll
+      for (int e = 0; e < kQT / 32; ++e) {
+        const float x = it.lse[e] * kLog2e;
+        // a row that sees nothing adds nothing
+        const bool none = it.pos[e] < 0 || x == -INFINITY;
+        st[lane + 32 * e] = none ? -INFINITY : -x;
+        reinterpret_cast<int*>(st)[kQT + lane + 32 * e] = it.pos[e];
+      }
+      if (lane == 0) sched[ring] = it.cls;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kStatFull + ring));
+      ++n;
+      if (++slot == L::kSlots) {
+        slot = 0;
+        phase ^= 1;
       }
     }
     if (lane == 0) {
-      if (ok) {
-        const int ring = n & (kRing - 1);
-        // as above: the entry is free once the products of tile n - 2 are done
-        if (n < 2 || mbar_wait(bar(L::kQFree + (n & 1)), ((n >> 1) - 1) & 1, abort_flag, status)) {
-          sched[ring] = kEnd;
-          mbar_arrive(bar(L::kStatFull + ring));
-        }
+      if (ok && (n < L::kSlots || mbar_wait(bar(L::kQFree + slot), phase, abort_flag, status))) {
+        sched[n & (kRing - 1)] = kEnd;
+        mbar_arrive(bar(L::kStatFull + (n & (kRing - 1))));
       }
       // copies in flight land before the CTA ends, aborted or without a tile
-      mbar_wait_drain(bar(L::kKFull), 0);
+      for (int a = 0; a < ktiles; ++a) mbar_wait_drain(bar(L::kKFull + a), 0);
       if (*abort_flag)
-        for (int i = n >= 2 ? n - 2 : 0; i < n; ++i)
-          mbar_wait_drain(bar(L::kQFull + (i & 1)), (i >> 1) & 1);
+        for (int i = n > L::kSlots ? n - L::kSlots : 0; i < n; ++i)
+          mbar_wait_drain(bar(L::kQFull + i % L::kSlots), (i / L::kSlots) & 1);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == L::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kId = idesc_bf16_f32(kTile, kQT, 0, 0);
-      const uint64_t dk = sdesc_sw128(sbase + L::kK, 16, 1024);
-      const uint64_t dq = sdesc_sw128(sbase + L::kQ, 16, 1024);
-      bool ok = true;
-      for (int n = 0; ok; ++n) {
-        const int slot = n & 1, ring = n & (kRing - 1);
-        if (!(ok = mbar_wait(bar(L::kStatFull + ring), (n / kRing) & 1, abort_flag, status))) break;
-        if (sched[ring] == kEnd) break;
-        if (n == 0 && !(ok = mbar_wait(bar(L::kKFull), 0, abort_flag, status))) break;
-        if (!(ok = mbar_wait(bar(L::kQFull + slot), (n >> 1) & 1, abort_flag, status))) break;
-        for (int a = 0; a < 2; ++a) {
-          // the buffer's previous scores (tile n - 2) have been read
-          if (n >= 2 && !(ok = mbar_wait(bar(L::kSFree + 2 * a + slot), ((n >> 1) - 1) & 1,
-                                         abort_flag, status)))
-            break;
-          tc_fence_after();
+    // Every lane runs the loop and one elected lane issues: the descriptors
+    // then are uniform values, which the issue takes as they are. (In a loop
+    // of one lane alone each of its operands is first moved to a uniform
+    // register, 76 clocks per 32-clock product.)
+    constexpr uint32_t kId = idesc_bf16_f32(kTile, kQT, 0, 0);
+    const uint64_t dk = sdesc_sw128(sbase + L::kK, 16, 1024);
+    const uint64_t dq = sdesc_sw128(sbase + L::kQ, 16, 1024);
+    const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
+    bool ok = true;
+    int slot = 0, phase = 0;
+    for (int n = 0; ok; ++n) {
+      const int ring = n & (kRing - 1);
+      ok = mbar_wait(bar(L::kStatFull + ring), (n / kRing) & 1, abort_flag, status);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (__shfl_sync(0xffffffffu, sched[ring], 0) == kEnd) break;
+      ok = mbar_wait(bar(L::kQFull + slot), phase, abort_flag, status);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+#pragma unroll
+      for (int a = 0; a < KT; ++a) {
+        if (a >= ktiles) break;
+        if (n == 0) ok = mbar_wait(bar(L::kKFull + a), 0, abort_flag, status);
+        // the previous scores have been read
+        if (n >= 1) ok = mbar_wait(bar(L::kSFree + a), (n - 1) & 1, abort_flag, status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        const uint32_t d = t0 + 128 * a;
+        const uint64_t da = sdesc_add(dk, a * L::kKTile);
+        const uint64_t db = sdesc_add(dq, slot * L::kQTile);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + 128 * a + 64 * slot,
-                   sdesc_add(dk, a * L::kKTile + (kk >> 2) * L::kKHalf + (kk & 3) * 32),
-                   sdesc_add(dq, slot * L::kQTile + (kk >> 2) * L::kQHalf + (kk & 3) * 32), kId,
-                   kk > 0 ? 1u : 0u);
-          mma_commit(bar(L::kSFull + 2 * a + slot));
+            mma_ss(d, sdesc_add(da, (kk >> 2) * L::kKHalf + (kk & 3) * 32),
+                   sdesc_add(db, (kk >> 2) * L::kQHalf + (kk & 3) * 32), kId, kk > 0 ? 1u : 0u);
+          mma_commit(bar(L::kSFull + a));
         }
-        if (!ok) break;
-        mma_commit(bar(L::kQFree + slot));
+        __syncwarp();
       }
-      mma_commit(bar(L::kMmaDone));
-      mbar_wait_drain(bar(L::kMmaDone), 0);
+      if (!ok) break;
+      if (elect_one()) mma_commit(bar(L::kQFree + slot));
+      __syncwarp();
+      if (++slot == L::kSlots) {
+        slot = 0;
+        phase ^= 1;
+      }
     }
-  } else {
+    if (elect_one()) mma_commit(bar(L::kMmaDone));
+    mbar_wait_drain(bar(L::kMmaDone), 0);
+  } else if ((warp >> 2) < ktiles) {
     // ------------------------------------------------------------ softmax
     const int a = warp >> 2;  // key tile
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -362,66 +446,74 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     Seen vis{1, 0};
     if (kp < P.S) vis = seen_by(P, nat_pos(P, kp));
     const uint64_t sc2 = f2_pack(P.scale_log2, P.scale_log2);
-    uint64_t sum[2] = {0ull, 0ull};
+    uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
     bool ok = true;
     for (int n = 0;; ++n) {
-      const int slot = n & 1, ring = n & (kRing - 1);
+      const int ring = n & (kRing - 1);
       ok = mbar_wait(bar(L::kStatFull + ring), (n / kRing) & 1, abort_flag, status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const int cls = sched[ring];
       if (cls == kEnd) break;
-      ok = mbar_wait(bar(L::kSFull + 2 * a + slot), (n >> 1) & 1, abort_flag, status);
+      ok = mbar_wait(bar(L::kSFull + a), n & 1, abort_flag, status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc_fence_after();
+      const float4* nlse = reinterpret_cast<const float4*>(sm + L::kStat + ring * L::kStatBytes);
+      const int4* pos = reinterpret_cast<const int4*>(nlse + kQT / 4);
+      // 32 columns at a time, the next ones on their way meanwhile
       uint32_t v[2][32];
-      tmem_ld32(tmem + lane_off + 128 * a + 64 * slot, v[0]);
-      tmem_ld32(tmem + lane_off + 128 * a + 64 * slot + 32, v[1]);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kSFree + 2 * a + slot));
-      const float4* lse2 = reinterpret_cast<const float4*>(sm + L::kStat + ring * L::kStatBytes);
-      const int4* pos = reinterpret_cast<const int4*>(lse2 + kQT / 4);
-      if (cls == kClsFull) {
+      tmem_ld32(tmem + lane_off + 128 * a, v[0]);
 #pragma unroll
-        for (int k = 0; k < kQT / 4; ++k) {
-          const float4 l = lse2[k];
-          const uint32_t* s = &v[k >> 3][4 * (k & 7)];
-          const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2,
-                                    f2_pack(-l.x, -l.y));
-          const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3])), sc2,
-                                    f2_pack(-l.z, -l.w));
-          float x0, x1, y0, y1;
-          f2_unpack(x, x0, x1);
-          f2_unpack(y, y0, y1);
-          sum[0] = f2_add(sum[0], f2_pack(ex2(x0), ex2(x1)));
-          sum[1] = f2_add(sum[1], f2_pack(ex2(y0), ex2(y1)));
+      for (int c = 0; c < kQT / 32; ++c) {
+        tmem_wait_ld();
+        if (c + 1 < kQT / 32) {
+          tmem_ld32(tmem + lane_off + 128 * a + 32 * (c + 1), v[(c + 1) & 1]);
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kSFree + a));
         }
-      } else {
+        const uint32_t(&vc)[32] = v[c & 1];
+        if (cls == kClsFull) {
 #pragma unroll
-        for (int k = 0; k < kQT / 4; ++k) {
-          const float4 l = lse2[k];
-          const int4 i = pos[k];
-          const uint32_t* s = &v[k >> 3][4 * (k & 7)];
-          auto one = [&](uint32_t sv, float lv, int iv) {
-            const float p = ex2(fmaf(__uint_as_float(sv), P.scale_log2, -lv));
-            return iv >= vis.lo && iv <= vis.hi ? p : 0.f;
-          };
-          sum[0] = f2_add(sum[0], f2_pack(one(s[0], l.x, i.x), one(s[1], l.y, i.y)));
-          sum[1] = f2_add(sum[1], f2_pack(one(s[2], l.z, i.z), one(s[3], l.w, i.w)));
+          for (int k = 0; k < 8; ++k) {
+            const float4 l = nlse[8 * c + k];
+            const uint32_t* s = &vc[4 * k];
+            const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2,
+                                      f2_pack(l.x, l.y));
+            const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3])), sc2,
+                                      f2_pack(l.z, l.w));
+            float x0, x1, y0, y1;
+            f2_unpack(x, x0, x1);
+            f2_unpack(y, y0, y1);
+            sum[(2 * k) & 3] = f2_add(sum[(2 * k) & 3], f2_pack(ex2(x0), ex2(x1)));
+            sum[(2 * k + 1) & 3] = f2_add(sum[(2 * k + 1) & 3], f2_pack(ex2(y0), ex2(y1)));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 l = nlse[8 * c + k];
+            const int4 i = pos[8 * c + k];
+            const uint32_t* s = &vc[4 * k];
+            auto one = [&](uint32_t sv, float lv, int iv) {
+              const float p = ex2(fmaf(__uint_as_float(sv), P.scale_log2, lv));
+              return iv >= vis.lo && iv <= vis.hi ? p : 0.f;
+            };
+            sum[0] = f2_add(sum[0], f2_pack(one(s[0], l.x, i.x), one(s[1], l.y, i.y)));
+            sum[1] = f2_add(sum[1], f2_pack(one(s[2], l.z, i.z), one(s[3], l.w, i.w)));
+          }
         }
       }
     }
     if (ok && kp < P.S) {
       float x, y;
-      f2_unpack(f2_add(sum[0], sum[1]), x, y);
+      f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), x, y);
       W.part[(((long long)part * P.Bt + bt) * P.Hkv + g) * P.S + kp] = x + y;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 256);
+  if (warp == L::kMmaWarp) tmem_dealloc(tmem, 128 * KT);
 }
 
 // weight[i] = the parts' sum, in order.
@@ -553,29 +645,30 @@ bool make_map(CUtensorMap* m, const void* base, int Bt, int S, int H, int D, int
 
 // How the problem is cut (host side, from the shapes alone).
 struct Cut {
-  int hpi, nseg, tps, nkb, ntiles, parts;
+  int kt, hpi, nseg, tps, nkb, ntiles, parts;
 };
 Cut cut_of(int B, int S, int Hq, int Hkv, int observe) {
   Cut c{};
   const int G = Hq / Hkv;
-  c.nkb = (S + kKeys - 1) / kKeys;
   c.ntiles = (S + kQT - 1) / kQT;
+  // query tiles that a key block meets at most
+  const int tiles = observe > 0 ? std::min((observe + kQT - 1) / kQT + 1, c.ntiles) : c.ntiles;
+  c.kt = tiles >= 16 ? 4 : 2;
+  c.nkb = (S + c.kt * kTile - 1) / (c.kt * kTile);
   c.hpi = G;
   c.nseg = 1;
+  const int slots = c.kt == 4 ? 152 : 304;
   const long long blocks = (long long)c.nkb * Hkv * B;
-  const long long want = 8LL * 304;  // eight CTAs per resident slot even out the masks
-  // few observed queries: a CTA has only a few tiles, all heads in one
-  const int tiles = observe > 0 ? (observe + kQT - 1) / kQT + 1 : c.ntiles;
-  if (blocks < want && tiles > 2) {
+  const long long want = 8LL * slots;  // CTAs that even out what the masks leave
+  if (blocks < want && tiles >= 8) {  // (each CTA loads its keys anew)
     c.hpi = 1;
     const long long have = blocks * G;
-    if (have < want) {
+    if (have < want && observe == 0) {
       long long n = (want + have - 1) / have;
-      const long long most = (tiles + 7) / 8;  // at least eight tiles each
+      const long long most = (tiles + 7) / 8;  // at least 8 tiles each
       if (n > most) n = most;
       if (n > 16) n = 16;
-      // with few observed queries they sit in the last segments
-      c.nseg = observe > 0 ? 1 : (int)n;
+      c.nseg = (int)n;
     }
   }
   c.tps = (c.ntiles + c.nseg - 1) / c.nseg;
@@ -583,21 +676,22 @@ Cut cut_of(int B, int S, int Hq, int Hkv, int observe) {
   return c;
 }
 
-template <int D>
+template <int D, int KT>
 usp_status_t launch_tc(const WeightParams& W, cudaStream_t st) {
   const AttnParams& P = W.P;
+  using L = WSmem<D, KT>;
   CUtensorMap mq, mk;
   if (!make_map(&mq, P.q, P.Bt, P.S, P.Hq, D, kQT) || !make_map(&mk, P.k, P.Bt, P.S, P.Hkv, D, kTile))
     return USP_ERR_CUDA;
-  const int smem = WSmem<D>::kAlloc;
-  cudaError_t e = cudaFuncSetAttribute(key_weights_tc_kernel<D>,
+  const int smem = L::kAlloc;
+  cudaError_t e = cudaFuncSetAttribute(key_weights_tc_kernel<D, KT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
   const long long blocks = (long long)W.nkb * P.Bt * P.Hkv * (P.G / W.hpi) * W.nseg;
   if (blocks > 0x7fffffffLL) return USP_ERR_UNSUPPORTED;
   {
     ProfScope ps(st, "attn_key_weights");
-    key_weights_tc_kernel<D><<<(unsigned)blocks, kThreads, smem, st>>>(W, mq, mk);
+    key_weights_tc_kernel<D, KT><<<(unsigned)blocks, L::kThreads, smem, st>>>(W, mq, mk);
   }
   note_launch();
   return check_launch();
@@ -615,7 +709,9 @@ usp_status_t launch_key_weights_tc(const AttnParams& P, float* weight, int obser
   const Cut c = cut_of(P.Bt, P.S, P.Hq, P.Hkv, observe);
   WeightParams W{P, c.parts > 1 ? static_cast<float*>(workspace) : weight, observe, c.hpi, c.nseg,
                  c.tps, c.nkb, c.ntiles};
-  usp_status_t r = P.D == 128 ? launch_tc<128>(W, st) : launch_tc<64>(W, st);
+  usp_status_t r;
+  if (P.D == 128) r = c.kt == 4 ? launch_tc<128, 4>(W, st) : launch_tc<128, 2>(W, st);
+  else r = c.kt == 4 ? launch_tc<64, 4>(W, st) : launch_tc<64, 2>(W, st);
   if (r != USP_OK || c.parts == 1) return r;
   const long long n = (long long)P.Bt * P.Hkv * P.S;
   const long long blocks = (n + 255) / 256;

@@ -1,19 +1,24 @@
 // Filling the 4-bit KV cache and reading it back.
 //
 // Both are copies with a few operations per element: bound by HBM for prompts
-// and by launch latency for single tokens.
+// (the append about evenly by instruction issue) and by launch latency for
+// single tokens.
 //
-// Append. A warp takes one tensor (K or V) of one KV head and eight tokens
-// that follow one another, so its writes are contiguous rows of the head. A
-// lane holds eight channels (16 bytes of bf16), four lanes a block of 32: the
-// block's maximum takes two shuffles, and the codes of eight channels are one
-// word. The quotients are true divisions: max|y| / 7 rounds to a tie of E4M3,
-// and y / s to a tie of the integers, only where the exact quotient is one
-// (numerators have at most 24 significant bits, the ties times the divisor at
-// most 8), so the codes are those of the definition whatever the inputs.
+// A warp takes one tensor (K or V) of one KV head and eight tokens that follow
+// one another, so that its side of the cache is one contiguous run. A lane
+// holds eight channels of a row: 16 bytes of bf16, one word of codes; four
+// lanes share a block of 32, whose maximum takes two shuffles.
 //
-// Read. A lane decodes eight channels of one row and writes them as 16 (bf16)
-// or 32 (fp32) bytes; the lanes run over the output in its own order.
+// The codes are those of the definition for every input, although no true
+// division is made. For a quotient y / s, with r within an ulp or two of 1 / s,
+//     t = y r,   e = y - t s,   t' = t + e r
+// leaves t' = y / s (1 + 2^-43) before its one rounding (t s has 28 bits and e
+// cancels to a few, so e is exact). t' then rounds to an integer, and ties are
+// what matters. Exact tie y = (h + 1/2) s: t' is h + 1/2, exactly. Not a tie:
+// y is at least one ulp(y) from (h + 1/2) s, and ulp(y) / s exceeds half an ulp
+// of h + 1/2 by the factor 2 / sigma >= 16/15, sigma <= 15/8 the significand
+// of s (4 bits), so t' does not round onto the tie. The same holds for
+// max|y| / 7 against E4M3's ties (sigma = 7/4).
 #include "internal.h"
 #include "kv4.cuh"
 #include "kv4_host.h"
@@ -24,8 +29,9 @@ namespace {
 
 using namespace kv4;
 
-constexpr int kGroup = 8;          // tokens per warp of the append
-constexpr int kAppendThreads = 256;
+constexpr int kGroup = 8;  // tokens per warp
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
 struct AppendParams {
   Cache c;
@@ -38,94 +44,161 @@ struct AppendParams {
   float k_inv, v_inv;
 };
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// a / d for the roundings above (finite a); r: about 1 / d.
+__device__ __forceinline__ float quotient(float a, float d, float r) {
+  const float t = a * r;
+  return fmaf(fmaf(-t, d, a), r, t);
+}
+
+// Eight channels of a row as loaded, their largest magnitude (not a NaN's;
+// `odd`: there may be one), and as floats.
 template <typename T>
-__device__ __forceinline__ void load8(const T* src, float (&x)[8]);
+struct Raw;
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* src, float (&x)[8]) {
-  const uint4 r = __ldg(reinterpret_cast<const uint4*>(src));
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+struct Raw<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    r = __ldg(reinterpret_cast<const uint4*>(p));
   }
-}
+  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ float amax(bool& odd) const {
+    // magnitudes as 16-bit integers, which order like the numbers; a NaN's is
+    // above infinity's
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t x = __vmaxu2(__vmaxu2(r.x & m, r.y & m), __vmaxu2(r.z & m, r.w & m));
+    const uint32_t y = max(x >> 16, x & 0xffffu);
+    odd = y > 0x7f80u;
+    return __uint_as_float(y << 16);
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
 template <>
-__device__ __forceinline__ void load8<float>(const float* src, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(src));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(src) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float amax(bool& odd) const {
+    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    odd = m > 0x7f800000u;
+    return __uint_as_float(m);
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+
+// The codes' word and the block's scale byte of a lane's eight channels.
+template <typename T>
+__device__ __forceinline__ uint32_t encode(const Raw<T>& raw, float inv, uint32_t& sbyte) {
+  bool odd;
+  // rounding is monotonic, so the largest |x| gives the largest |x inv|
+  float amax = raw.amax(odd) * inv;
+  float x[8];
+  raw.floats(x);
+  if (odd) {  // a NaN counts as 0
+    amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (isnan(x[e])) x[e] = 0.f;
+      amax = fmaxf(amax, fabsf(x[e] * inv));
+    }
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  amax = fminf(amax, 1e38f);  // infinite: saturates like this
+  sbyte = tc::pack_e4m3(quotient(amax, 7.f, 1.f / 7.f), 0.f) & 0xffu;
+  const float s = e4m3_to_float(sbyte);
+  uint32_t word = 0;
+  // The sum with 1.5 2^23 + 8 rounds to an integer, half to even, and leaves
+  // c + 8 in the low bits; the constant's own bits drop out of the word.
+  constexpr float kMagic = 12582912.f + 8.f;
+  constexpr uint32_t kBits = 0x4B400000u;
+  if (sbyte >= 8u && sbyte < 0x7Eu) {
+    // a normal scale is within 2^-4 of max / 7: |y / s| < 7.5, no clamp
+    const float r = rcp_approx(s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float c = quotient(x[e] * inv, s, r) + kMagic;
+      word += (__float_as_uint(c) - kBits) << (4 * e);
+    }
+  } else {
+    const float r = s > 0.f ? rcp_approx(s) : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float y = x[e] * inv;
+      // far outside (or infinite): no remainder needed
+      const float t = fminf(fmaxf(y * r, -8.f), 8.f);
+      const float q = fabsf(t) == 8.f ? t : fmaf(fmaf(-t, s, y), r, t);
+      const float c = fminf(fmaxf(q, -7.f), 7.f) + kMagic;
+      word += (__float_as_uint(c) - kBits) << (4 * e);
+    }
+  }
+  return word;
 }
 
-// New tokens of sequence b, given its boundaries (packed) or T.
-__device__ __forceinline__ int new_tokens(const AppendParams& P, int b) {
-  return P.cu ? max(0, __ldg(P.cu + b + 1) - __ldg(P.cu + b)) : P.T;
-}
-
-// One warp's item: tensor `which` (0: K, 1: V), KV head h, tokens
-// [tok0, tok0 + kGroup) of the input's rows (all sequences in a row), those
-// below `end`. seq: the sequence they belong to, or -1: look each one up.
+// One warp's item: tensor `which` (0: K, 1: V), KV head h, input rows
+// [tok0, tok0 + kGroup) below `end`. b: their sequence, whose first row is
+// `first`, or -1 (packed): each row's is looked up.
 template <typename T, int D>
-__device__ __forceinline__ void append_item(const AppendParams& P, int which, int h,
-                                            long long tok0, long long end, int seq) {
+__device__ __forceinline__ void append_item(const AppendParams& P, int which, int h, int b,
+                                            long long first, long long tok0, long long end) {
   constexpr int kLanes = D / 8;          // lanes per row
   constexpr int kRows = 32 / kLanes;     // rows per pass
+  constexpr int kPasses = kGroup / kRows;
   const int lane = threadIdx.x & 31;
   const int lr = lane / kLanes, lc = lane % kLanes;
   const T* src = static_cast<const T*>(which ? P.v : P.k);
   uint8_t* codes = which ? P.c.vc : P.c.kc;
   uint8_t* scales = which ? P.c.vs : P.c.ks;
   const float inv = which ? P.v_inv : P.k_inv;
-  float x[kGroup / kRows][8];
+  Raw<T> raw[kPasses];
 #pragma unroll
-  for (int i = 0; i < kGroup / kRows; ++i) {
+  for (int i = 0; i < kPasses; ++i) {
     const long long tok = tok0 + i * kRows + lr;
-    if (tok < end) load8<T>(src + (tok * P.c.H + h) * D + lc * 8, x[i]);
+    if (tok < end) raw[i].load(src + (tok * P.c.H + h) * D + lc * 8);
+    else raw[i].zero();
   }
 #pragma unroll
-  for (int i = 0; i < kGroup / kRows; ++i) {
+  for (int i = 0; i < kPasses; ++i) {
     const long long tok = tok0 + i * kRows + lr;
-    const bool in = tok < end;
-    float amax = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float y = in ? x[i][e] * inv : 0.f;
-      if (isnan(y)) y = 0.f;
-      x[i][e] = y;
-      amax = fmaxf(amax, fabsf(y));
+    uint32_t sbyte;
+    const uint32_t word = encode<T>(raw[i], inv, sbyte);
+    if (tok >= end) continue;
+    int bb = b;
+    long long t = tok - first;
+    if (b < 0) {
+      bb = seg_of(P.cu, P.c.B, (int)tok);
+      t = tok - __ldg(P.cu + bb);
     }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const uint32_t sbyte = tc::pack_e4m3(__fdiv_rn(amax, 7.f), 0.f) & 0xffu;
-    const float s = e4m3_to_float(sbyte);
-    uint32_t word = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float c = s > 0.f ? rintf(__fdiv_rn(x[i][e], s)) : 0.f;
-      c = fminf(fmaxf(c, -7.f), 7.f);
-      word |= static_cast<uint32_t>(static_cast<int>(c) + 8) << (4 * e);
-    }
-    if (!in) continue;
-    int b = seq;
-    long long t;
-    if (P.cu) {
-      if (b < 0) b = seg_of(P.cu, P.c.B, (int)tok);
-      t = tok - __ldg(P.cu + b);
-    } else {
-      if (b < 0) b = (int)(tok / P.T);
-      t = tok - (long long)b * P.T;
-    }
-    const long long pos = clamp_len(P.c.lens[b], P.c.C) + t;
+    const long long pos = clamp_len(P.c.lens[bb], P.c.C) + t;
     if (t < 0 || pos >= P.c.C) continue;  // no room (or malformed boundaries)
-    const long long row = head_row(P.c, b, h) + pos;
+    const long long row = head_row(P.c, bb, h) + pos;
     *reinterpret_cast<uint32_t*>(codes + row * (D / 2) + lc * 4) = word;
     if ((lc & 3) == 0) scales[row * (D / kBlock) + (lc >> 2)] = (uint8_t)sbyte;
     if (which == 0 && lc == 0 && P.c.w != nullptr) {
       float w = 0.f;
       if (P.new_w)
         w = P.cu ? P.new_w[(long long)h * P.T + tok]
-                 : P.new_w[((long long)b * P.c.H + h) * P.T + t];
+                 : P.new_w[((long long)bb * P.c.H + h) * P.T + t];
       P.c.w[row] = w;
     }
   }
@@ -133,60 +206,64 @@ __device__ __forceinline__ void append_item(const AppendParams& P, int which, in
 
 // One block per sequence, which also writes the sequence's new length.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads) append_seq_kernel(const AppendParams P) {
+__global__ void __launch_bounds__(kThreads) append_seq_kernel(const AppendParams P) {
   const int b = blockIdx.x;
   const long long first = (long long)b * P.T;
   const int groups = (P.T + kGroup - 1) / kGroup;
-  for (int it = threadIdx.x >> 5; it < 2 * P.c.H * groups; it += kAppendThreads / 32) {
-    const int which = it & 1, h = (it >> 1) % P.c.H, g = (it >> 1) / P.c.H;
-    append_item<T, D>(P, which, h, first + (long long)g * kGroup, first + P.T, b);
+  for (int it = threadIdx.x >> 5; it < 2 * P.c.H * groups; it += kWarps) {
+    const int g = it / (2 * P.c.H), x = it - g * 2 * P.c.H;
+    append_item<T, D>(P, x & 1, x >> 1, b, first, first + (long long)g * kGroup, first + P.T);
   }
   __syncthreads();  // every warp has read the old length
   if (threadIdx.x == 0 && P.lens_out)
     P.lens_out[b] = (int)min((long long)P.c.C, (long long)clamp_len(P.c.lens[b], P.c.C) + P.T);
 }
 
-// Warps over (group of tokens, head, tensor); the lengths are written by a
-// launch of their own behind this one.
+// grid (items, sequences; packed: 1): warps over (group of tokens, head,
+// tensor). The lengths are written by a launch of their own behind this one.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads)
-append_kernel(const AppendParams P, long long tokens, long long items) {
-  const long long it = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P, unsigned items) {
+  const unsigned it = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (it >= items) return;
-  const int which = (int)(it & 1), h = (int)((it >> 1) % P.c.H);
-  const long long g = (it >> 1) / P.c.H;
-  append_item<T, D>(P, which, h, g * kGroup, min(tokens, (g + 1) * kGroup), -1);
+  const unsigned g = it / (2 * P.c.H), x = it - g * 2 * P.c.H;
+  const int b = P.cu ? -1 : (int)blockIdx.y;
+  const long long first = P.cu ? 0 : (long long)b * P.T;
+  append_item<T, D>(P, x & 1, x >> 1, b, first, first + (long long)g * kGroup, first + P.T);
 }
 
 __global__ void append_lens_kernel(const AppendParams P) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b < P.c.B)
-    P.lens_out[b] =
-        (int)min((long long)P.c.C, (long long)clamp_len(P.c.lens[b], P.c.C) + new_tokens(P, b));
+  if (b >= P.c.B) return;
+  const long long n = P.cu ? max(0, __ldg(P.cu + b + 1) - __ldg(P.cu + b)) : P.T;
+  P.lens_out[b] = (int)min((long long)P.c.C, clamp_len(P.c.lens[b], P.c.C) + n);
+}
+
+// Items of one sequence's (packed: the batch's) T tokens, 0 if too many.
+long long items_of(int T, int H) {
+  const long long n = ((long long)T + kGroup - 1) / kGroup * H * 2;
+  return n / kWarps < 0x7fffffffLL - 1 && n < 0xffffffffLL ? n : -1;
 }
 
 template <typename T, int D>
 usp_status_t launch_append_t(const AppendParams& P, cudaStream_t st) {
-  const long long tokens = P.cu ? P.T : (long long)P.c.B * P.T;
-  const long long groups = (tokens + kGroup - 1) / kGroup;
   // Few tokens per sequence: one launch, whose blocks own their sequences'
   // lengths. Else the items are spread over the whole GPU and a second,
-  // one-block launch (about 2 us) updates the lengths in stream order.
+  // small launch (about 2 us) updates the lengths in stream order.
   if (!P.cu && (long long)P.T * P.c.H <= 64) {
     {
       ProfScope ps(st, "kv4_append");
-      append_seq_kernel<T, D><<<P.c.B, kAppendThreads, 0, st>>>(P);
+      append_seq_kernel<T, D><<<P.c.B, kThreads, 0, st>>>(P);
     }
     note_launch();
     return check_launch();
   }
-  const long long items = groups * P.c.H * 2;
-  const long long blocks = (items + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
-  if (blocks > 0x7fffffffLL) return USP_ERR_UNSUPPORTED;
-  if (blocks > 0) {
+  const long long items = items_of(P.T, P.c.H);
+  if (items < 0) return USP_ERR_UNSUPPORTED;
+  if (items > 0) {
+    const dim3 grid((unsigned)((items + kWarps - 1) / kWarps), P.cu ? 1 : P.c.B);
     {
       ProfScope ps(st, "kv4_append");
-      append_kernel<T, D><<<(unsigned)blocks, kAppendThreads, 0, st>>>(P, tokens, items);
+      append_kernel<T, D><<<grid, kThreads, 0, st>>>(P, (unsigned)items);
     }
     note_launch();
     usp_status_t r = check_launch();
@@ -223,45 +300,54 @@ __device__ __forceinline__ void store8<float>(float* dst, const float (&x)[8]) {
   reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// grid (chunks of the sequence's T * H * D/8 outputs, tensor, sequence)
+// grid (items, sequences), as the append
 template <typename T, int D>
-__global__ void __launch_bounds__(256) read_kernel(const ReadParams P) {
-  const int b = blockIdx.z, which = blockIdx.y;
-  const long long n8 = (long long)P.T * P.c.H * (D / 8);
+__global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams P, unsigned items) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kPasses = kGroup / kRows;
+  const unsigned it = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (it >= items) return;
+  const unsigned g = it / (2 * P.c.H), x = it - g * 2 * P.c.H;
+  const int b = blockIdx.y, which = x & 1, h = x >> 1;
+  const int lane = threadIdx.x & 31, lr = lane / kLanes, lc = lane % kLanes;
   const uint8_t* codes = which ? P.c.vc : P.c.kc;
   const uint8_t* scales = which ? P.c.vs : P.c.ks;
-  T* out = static_cast<T*>(which ? P.v : P.k) + (long long)b * n8 * 8;
+  T* out = static_cast<T*>(which ? P.v : P.k);
   const float descale = which ? P.v_descale : P.k_descale;
   const int len = clamp_len(__ldg(P.c.lens + b), P.c.C);
   const long long start = P.start ? __ldg(P.start + b) : 0;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n8; i += (long long)gridDim.x * 256) {
-    const int lc = (int)(i % (D / 8));
-    const long long th = i / (D / 8);
-    const int h = (int)(th % P.c.H);
-    const long long pos = start + th / P.c.H;
-    float x[8];
+  const long long head = head_row(P.c, b, h);
+  uint32_t w[kPasses], sb[kPasses];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+  for (int i = 0; i < kPasses; ++i) {
+    const long long pos = start + (long long)g * kGroup + i * kRows + lr;
+    w[i] = 0x88888888u;  // zeros
+    sb[i] = 0;
     if (pos >= 0 && pos < len) {
-      const long long row = head_row(P.c, b, h) + pos;
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (D / 2)) + lc);
-      const float s = e4m3_to_float(__ldg(scales + row * (D / kBlock) + (lc >> 2)));
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = (static_cast<float>(static_cast<int>((w >> (4 * e)) & 15u) - 8) * s) * descale;
+      w[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + (head + pos) * (D / 2)) + lc);
+      sb[i] = __ldg(scales + (head + pos) * (D / kBlock) + (lc >> 2));
     }
-    store8<T>(out + i * 8, x);
+  }
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const long long t = (long long)g * kGroup + i * kRows + lr;
+    if (t >= P.T) continue;
+    const float s = e4m3_to_float(sb[i]);
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      y[e] = (static_cast<float>(static_cast<int>((w[i] >> (4 * e)) & 15u) - 8) * s) * descale;
+    store8<T>(out + (((long long)b * P.T + t) * P.c.H + h) * D + lc * 8, y);
   }
 }
 
 template <typename T, int D>
 usp_status_t launch_read_t(const ReadParams& P, cudaStream_t st) {
-  const long long n8 = (long long)P.T * P.c.H * (D / 8);
-  long long blocks = (n8 + 255) / 256;
-  if (blocks > 152 * 16) blocks = 152 * 16;
+  const long long items = items_of(P.T, P.c.H);
+  if (items < 0) return USP_ERR_UNSUPPORTED;
   {
     ProfScope ps(st, "kv4_read");
-    read_kernel<T, D><<<dim3((unsigned)blocks, 2, P.c.B), 256, 0, st>>>(P);
+    read_kernel<T, D><<<dim3((unsigned)((items + kWarps - 1) / kWarps), P.c.B), kThreads, 0, st>>>(
+        P, (unsigned)items);
   }
   note_launch();
   return check_launch();

@@ -59,6 +59,17 @@ __device__ __forceinline__ uint32_t peer_load(const uint32_t* p, uint32_t rank) 
   return v;
 }
 
+__device__ __forceinline__ uint4 peer_load4(const uint32_t* p, uint32_t rank) {
+  uint32_t a;
+  uint4 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
 struct EvictParams {
   Cache src, dst;
   int* kept;
@@ -80,11 +91,20 @@ struct __align__(16) EvictSmem {
 __device__ __forceinline__ void find_bin(EvictSmem& s, int pass, int cluster, uint32_t need) {
   // thread t owns the kOwn bins from kBins - 1 - kOwn t downwards
   constexpr int kOwn = kBins / kThreads;
+  static_assert(kOwn == 4, "one vector per peer");
   const int b0 = kBins - 1 - kOwn * threadIdx.x;
-  uint32_t n[kOwn] = {}, mine = 0;
-  for (int r = 0; r < cluster; ++r)
+  uint4 peer[kMaxCluster];  // all on their way before the first is needed
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) n[i] += peer_load(&s.hist[pass][b0 - i], r);
+  for (int r = 0; r < kMaxCluster; ++r)
+    peer[r] = r < cluster ? peer_load4(&s.hist[pass][b0 - 3], r) : make_uint4(0, 0, 0, 0);
+  uint32_t n[kOwn] = {}, mine = 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) {
+    n[0] += peer[r].w;
+    n[1] += peer[r].z;
+    n[2] += peer[r].y;
+    n[3] += peer[r].x;
+  }
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) mine += n[i];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -158,30 +178,47 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
       }
     }
     __syncthreads();
-    auto key_at = [&](int i) { return in_smem ? mine[i] : order_key(__ldg(w + first + i)); };
+    // keys i .. i + 3 of the warp's part (i a multiple of 4)
+    auto keys_at = [&](int i) {
+      if (in_smem) return *reinterpret_cast<const uint4*>(mine + i);
+      const float4 x = __ldg(reinterpret_cast<const float4*>(w + first + i));
+      return make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
+    };
+    // which of them: not behind the part (n) and, relative to it, in [lo, hi)
+    const int c_lo = (int)max(0LL, min((long long)n, lo - first));
+    const int c_hi = (int)max((long long)c_lo, min((long long)n, hi - first));
     uint32_t prefix = 0;  // the n-th largest key's bits found so far
     if (need > 0) {
       constexpr int kShift[3] = {21, 10, 0};
       constexpr uint32_t kMask[3] = {0u, 0xffe00000u, 0xfffffc00u};
 #pragma unroll
       for (int pass = 0; pass < 3; ++pass) {
-        for (int i0 = 0; i0 < n; i0 += 32) {
-          const int i = i0 + lane;
-          const long long j = first + i;
-          bool in = i < n && j >= lo && j < hi;
-          uint32_t key = 0;
-          if (in) {
-            key = key_at(i);
-            in = (key & kMask[pass]) == prefix;
+        const uint32_t bin_mask = pass == 2 ? 1023u : 2047u;
+#pragma unroll 2
+        for (int i0 = c_lo / 128 * 128; i0 < c_hi; i0 += 128) {
+          const int i = i0 + 4 * lane;
+          uint32_t key[4] = {0, 0, 0, 0};
+          uint32_t bin[4];
+          if (i < c_hi) {
+            const uint4 k = keys_at(i);
+            key[0] = k.x; key[1] = k.y; key[2] = k.z; key[3] = k.w;
           }
-          const uint32_t bin = (key >> kShift[pass]) & (pass == 2 ? 1023u : 2047u);
+          bool in[4], alike = true;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            in[e] = i + e >= c_lo && i + e < c_hi && (key[e] & kMask[pass]) == prefix;
+            bin[e] = (key[e] >> kShift[pass]) & bin_mask;
+            alike = alike && in[e] && bin[e] == bin[0];
+          }
           // one addition where a whole warp agrees (runs of equal weights)
           int same;
-          __match_all_sync(0xffffffffu, in ? bin : 0xffffffffu, &same);
+          __match_all_sync(0xffffffffu, alike ? bin[0] : 0x80000000u + lane, &same);
           if (same) {
-            if (in && lane == 0) atomicAdd(&s.hist[pass][bin], 32u);
-          } else if (in) {
-            atomicAdd(&s.hist[pass][bin], 1u);
+            if (lane == 0) atomicAdd(&s.hist[pass][bin[0]], 128u);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (in[e]) atomicAdd(&s.hist[pass][bin[e]], 1u);
           }
         }
         cluster_sync();
@@ -191,20 +228,34 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
       }
     }
     const bool any = P.keep - P.sink - P.recent > 0;
-    // kept for sure (sinks, recent, above the n-th largest), and equal to it
-    uint32_t above = 0, tie = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane;
-      const long long j = first + i;
-      bool a = false, t = false;
-      if (i < n) {
-        const bool fixed = j < lo || j >= hi;
-        const uint32_t key = !fixed && any ? key_at(i) : 0u;
-        a = fixed || (any && key > prefix);
-        t = !fixed && any && key == prefix;
+    // of keys i .. i + 3: kept for sure (sinks, recent, above the n-th largest:
+    // bits 0-3) and equal to it (bits 4-7)
+    auto flags_at = [&](int i) {
+      uint32_t f = 0;
+      if (i >= n) return f;
+      uint4 k = make_uint4(0, 0, 0, 0);
+      if (any) k = keys_at(i);
+      const uint32_t key[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (i + e >= n) continue;
+        const bool fixed = i + e < c_lo || i + e >= c_hi;
+        if (fixed || (any && key[e] > prefix)) f |= 1u << e;
+        else if (any && key[e] == prefix) f |= 16u << e;
       }
-      above += __popc(__ballot_sync(0xffffffffu, a));
-      tie += __popc(__ballot_sync(0xffffffffu, t));
+      return f;
+    };
+    uint32_t above = 0, tie = 0;
+#pragma unroll 2
+    for (int i = 4 * lane; i < n; i += 128) {
+      const uint32_t f = flags_at(i);
+      above += __popc(f & 15u);
+      tie += __popc(f >> 4);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      above += __shfl_xor_sync(0xffffffffu, above, o);
+      tie += __shfl_xor_sync(0xffffffffu, tie, o);
     }
     if (lane == 0) {
       s.above[warp] = above;
@@ -232,28 +283,42 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
       }
     }
     cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      a_before += peer_load(&s.total[0], r);
-      t_before += peer_load(&s.total[1], r);
-    }
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane;
-      const long long j = first + i;
-      bool a = false, t = false;
-      if (i < n) {
-        const bool fixed = j < lo || j >= hi;
-        const uint32_t key = !fixed && any ? key_at(i) : 0u;
-        a = fixed || (any && key > prefix);
-        t = !fixed && any && key == prefix;
+    {
+      // of the CTAs before this one
+      uint32_t x = lane < rank ? peer_load(&s.total[0], lane) : 0u;
+      uint32_t y = lane < rank ? peer_load(&s.total[1], lane) : 0u;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        y += __shfl_xor_sync(0xffffffffu, y, o);
       }
-      const uint32_t below = (1u << lane) - 1u;
-      const uint32_t ab = __ballot_sync(0xffffffffu, a), tb = __ballot_sync(0xffffffffu, t);
-      // the first `need` ties are kept
-      const uint32_t t_at = t_before + __popc(tb & below);
-      const uint32_t at = a_before + __popc(ab & below) + min(t_at, need);
-      if ((a || (t && t_at < need)) && at < (uint32_t)P.keep) kept[at] = (int)j;
-      a_before += __popc(ab);
-      t_before += __popc(tb);
+      a_before += x;
+      t_before += y;
+    }
+    for (int i0 = 0; i0 < n; i0 += 128) {
+      const int i = i0 + 4 * lane;
+      const uint32_t f = flags_at(i);
+      const uint32_t own = __popc(f & 15u) + (__popc(f >> 4) << 16);
+      uint32_t inc = own;  // at most 128 each
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);
+      uint32_t a = a_before + ((inc - own) & 0xffffu), t = t_before + ((inc - own) >> 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool tied = (f >> (4 + e)) & 1u;
+        // the first `need` ties are kept
+        const uint32_t at = a + min(t, need);
+        if ((((f >> e) & 1u) || (tied && t < need)) && at < (uint32_t)P.keep)
+          kept[at] = (int)(first + i + e);
+        a += (f >> e) & 1u;
+        t += tied;
+      }
+      a_before += all & 0xffffu;
+      t_before += all >> 16;
     }
   }
   cluster_sync();  // the list is complete; no CTA needs another's memory any more
