@@ -6,27 +6,29 @@
 // ("Long Context Attention" notes, "Motivation": the LSE is what the forward
 // keeps; with it a probability needs no second pass over its row.)
 //
-// Tensor-core kernel (bf16). One CTA owns KT tiles of 128 keys of one KV head
-// and takes the query tiles of 128 that may see them, for some of the group's
-// query heads and a segment of the queries: S^T = K Q^T, keys on the 128 TMEM
-// lanes, so that a softmax thread owns a key and the column sum is a register.
-// Nothing is normalised or rescaled, and nothing goes back to the tensor core.
-// Per 128 x 128 tile (D = 128) the products take 512 clocks, and so do the
-// exponentials (32 per clock and SM) and the products' reads of shared memory
-// (64 KB); all keys of a CTA share each query tile, which keeps the loads of Q
-// to 32 KB per KT x 512 clocks.
-//   KT = 4  (one CTA per SM, two Q slots): 512 keys
-//   KT = 2  (two CTAs per SM, one Q slot): short problems, where the loads of
-//           K are what counts and one CTA's overlap the other's work
-// A key tile has one 128-column buffer of scores: while the softmax takes it
-// out, the products of the other key tiles run.
-// Roles (32 (4 KT + 2) threads):
-//   warps 0 .. 4 KT - 1  softmax: warp w owns keys [32 w, 32 w + 32)
-//   the next   producer: finds the query tiles that can see the keys (32 at a
-//              time, one per lane), loads Q and, with all lanes, the tile's
-//              LSE (asked for one tile ahead) and natural positions
-//   the last   MMA issuer, owner of tensor memory: S^T of key tile a in
-//              columns [128 a, + 128)
+// Tensor-core kernel (bf16). One CTA owns 256 keys (two tiles of 128) of one
+// KV head and takes the query tiles of 64 that may see them, for some of the
+// group's query heads and a segment of the queries: S^T = K Q^T, keys on the
+// 128 TMEM lanes, so that a softmax thread owns a key and the column sum is a
+// register. Nothing is normalised or rescaled, and nothing goes back to the
+// tensor core. The keys are the A operand and stay in tensor memory, put there
+// by the threads that own them: from shared memory the products would read
+// 6 KB in the 32 clocks of a 128 x 64 x 16 product, where 4 KB is what it can
+// give (measured: 57 clocks each). So only Q (2 KB per product) passes through
+// shared memory. The products of a 128 x 64 tile (D = 128) take 256 clocks,
+// its exponentials (32 per clock and SM) as many. A key tile has one 64-column
+// buffer of scores: the softmax takes it into registers at once, and while it
+// works the other products run. What then limits is the MMA warp, whose
+// products are issued no faster than they run and which waits between them:
+// so two CTAs per SM, each with its own, and as few barriers for it as can be
+// (512 keys in one CTA: 2400 clocks per 512 x 64 scores).
+// Roles (320 threads):
+//   warps 0-7  softmax: warp w owns keys [32 w, 32 w + 32)
+//   warp 8     producer: finds the query tiles that can see the keys (32 at a
+//              time, one per lane), loads Q (five slots) and, with all lanes,
+//              the tile's LSE (asked for one tile ahead) and positions
+//   warp 9     MMA issuer, owner of tensor memory: K of key tile a in columns
+//              [a D/2, + D/2), its S^T in [D + 64 a, + 64)
 // Positions are read per query from shared memory, so a tile may cross chunk
 // and shard boundaries: any layout and any length has this kernel.
 //
@@ -50,8 +52,15 @@ using namespace tc;
 
 __device__ int g_key_weights_status = 0;
 
-constexpr int kQT = kTile;           // queries per tile
-constexpr int kRing = 4;            // entries of query statistics
+constexpr int kQT = 64;             // queries per tile
+constexpr int kKT = 2;              // key tiles per CTA
+constexpr int kKeys = kKT * kTile;  // keys per CTA
+constexpr int kSoftWarps = 4 * kKT;
+constexpr int kProducerWarp = kSoftWarps;
+constexpr int kMmaWarp = kProducerWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kSlots = 5;           // Q tiles
+constexpr int kRing = 8;           // entries of query statistics
 constexpr int kEnd = -1;
 constexpr int kNowhere = -(1 << 30);  // position of a row that is not observed
 constexpr float kLog2e = 1.4426950408889634f;
@@ -75,40 +84,36 @@ struct WeightParams {
   int nseg;      // segments of query tiles
   int tps;       // query tiles per segment
   int nkb;       // key blocks
+  int q0;        // first row of tile 0: where the observed rows begin, if they
+                 // are one run to the end; else 0
   int ntiles;    // query tiles
 };
 
-template <int D, int KT>
+template <int D>
 struct WSmem {
-  static constexpr int kKeys = KT * kTile;
-  static constexpr int kSoftWarps = 4 * KT;
-  static constexpr int kProducerWarp = kSoftWarps;
-  static constexpr int kMmaWarp = kProducerWarp + 1;
-  static constexpr int kThreads = 32 * (kMmaWarp + 1);
-  static constexpr int kSlots = KT == 2 ? 1 : 2;  // Q tiles
   // A ring entry is written for tile x once the products of tile x - kSlots
   // are done; the softmax is then past the scores of tile x - kSlots - 1, so
   // past the statistics of tile x - kSlots - 2.
   static_assert(kRing >= kSlots + 2, "a statistics entry is free");
   static constexpr int kHalves = D / 64;
-  static constexpr int kKHalf = kTile * 128;            // 64 channels of one key tile
-  static constexpr int kKTile = kKHalf * kHalves;
-  static constexpr int kQHalf = kQT * 128;
+  static constexpr int kQHalf = kQT * 128;              // 64 channels of a Q tile
   static constexpr int kQTile = kQHalf * kHalves;
-  static constexpr int kK = 0;
-  static constexpr int kQ = kK + KT * kKTile;           // kSlots
-  static constexpr int kStat = kQ + kSlots * kQTile;    // kRing x (-lse2[128], pos[128])
+  static constexpr int kQ = 0;
+  static constexpr int kStat = kQ + kSlots * kQTile;    // kRing x (-lse2[64], pos[64])
   static constexpr int kStatBytes = 2 * kQT * 4;
   static constexpr int kSched = kStat + kRing * kStatBytes;  // kRing ints
   static constexpr int kBar = kSched + kRing * 4;
-  static constexpr int kKFull = 0 /* KT */, kQFull = KT, kQFree = kQFull + kSlots,
-                       kSFull = kQFree + kSlots /* KT */, kSFree = kSFull + KT,
-                       kStatFull = kSFree + KT, kMmaDone = kStatFull + kRing,
+  static constexpr int kKReady = 0, kQFull = kKReady + kKT, kQFree = kQFull + kSlots,
+                       kSFull = kQFree + kSlots, kSFree = kSFull + kKT,
+                       kStatFull = kSFree + kKT, kMmaDone = kStatFull + kRing,
                        kNumBars = kMmaDone + 1;
+  static constexpr int kTmemS = kKT * D / 2;            // columns
+  static constexpr int kTmem = 256;
+  static_assert(kTmemS + kQT * kKT <= kTmem, "tensor memory");
   static constexpr int kMisc = (kBar + 8 * kNumBars + 15) / 16 * 16;
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
-  static_assert(kAlloc <= (KT == 2 ? 113 : 227) * 1024, "two CTAs (KT = 2), one (4) per SM");
+  static_assert(kAlloc <= 113 * 1024, "two CTAs per SM");
   static_assert(kBar % 8 == 0 && kStat % 16 == 0, "alignment");
 };
 
@@ -175,9 +180,9 @@ struct KeyBlock {
   PosRange q;     // of the queries that may see one of them
   int seg0, seg1; // packed sequences of the first and last key
 };
-__device__ __forceinline__ KeyBlock key_block(const AttnParams& P, int key0, int keys) {
+__device__ __forceinline__ KeyBlock key_block(const AttnParams& P, int key0) {
   KeyBlock b;
-  b.k = row_bounds(P, key0, keys);
+  b.k = row_bounds(P, key0, kKeys);
   int s0 = 0, e1 = P.S;
   b.seg0 = b.seg1 = 0;
   if (P.cu != nullptr) {
@@ -195,9 +200,10 @@ __device__ __forceinline__ KeyBlock key_block(const AttnParams& P, int key0, int
 // empty / full / masked for the queries of tile qt against the key block.
 __device__ __forceinline__ int classify_tile(const WeightParams& W, int qt, const KeyBlock& b) {
   const AttnParams& P = W.P;
-  const PosRange q = row_bounds(P, qt * kQT, kQT);
+  const int p0 = W.q0 + qt * kQT;
+  const PosRange q = row_bounds(P, p0, kQT);
   if (q.lo > q.hi || q.hi < b.q.lo || q.lo > b.q.hi) return kClsEmpty;
-  bool all = qt * kQT + kQT <= P.S;
+  bool all = true;  // rows behind S are zeros with LSE = inf: no mask needed
   if (W.observe > 0) {
     if (P.cu == nullptr) {
       if (q.hi < P.S - W.observe) return kClsEmpty;
@@ -219,11 +225,10 @@ __device__ __forceinline__ int classify_tile(const WeightParams& W, int qt, cons
   return all ? kClsFull : kClsMasked;
 }
 
-template <int D, int KT>
-__global__ void __launch_bounds__(WSmem<D, KT>::kThreads, KT == 2 ? 2 : 1)
-key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap tm_q,
-                      const __grid_constant__ CUtensorMap tm_k) {
-  using L = WSmem<D, KT>;
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap tm_q) {
+  using L = WSmem<D>;
   const AttnParams& P = W.P;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -245,16 +250,17 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
   idx /= P.Hkv;
   const int bt = idx % P.Bt, kb = idx / P.Bt;
   const int seg = part / groups, h0 = g * P.G + (part % groups) * W.hpi;
-  const int key0 = kb * L::kKeys;
-  const int ktiles = min(KT, (P.S - key0 + kTile - 1) / kTile);  // with keys in them
+  const int key0 = kb * kKeys;
+  const int ktiles = min(kKT, (P.S - key0 + kTile - 1) / kTile);  // with keys in them
 
-  if (warp == L::kProducerWarp && lane == 0) {
-    for (int a = 0; a < KT; ++a) mbar_init(bar(L::kKFull + a), 1);
-    for (int s = 0; s < L::kSlots; ++s) {
+  if (warp == kProducerWarp && lane == 0) {
+    // the four warps of a key tile: its keys are in tensor memory
+    for (int a = 0; a < kKT; ++a) mbar_init(bar(L::kKReady + a), 4);
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(L::kQFull + s), 1);
       mbar_init(bar(L::kQFree + s), 1);
     }
-    for (int s = 0; s < KT; ++s) {
+    for (int s = 0; s < kKT; ++s) {
       mbar_init(bar(L::kSFull + s), 1);
       mbar_init(bar(L::kSFree + s), 4);  // the four warps of a key tile
     }
@@ -263,15 +269,9 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch(&tm_q);
-    for (int a = 0; a < ktiles; ++a) {
-      mbar_expect_tx(bar(L::kKFull + a), L::kKTile);
-      for (int hf = 0; hf < L::kHalves; ++hf)
-        tma_load_4d(sbase + L::kK + a * L::kKTile + hf * L::kKHalf, &tm_k, bar(L::kKFull + a),
-                    hf * 64, g, key0 + a * kTile, bt);
-    }
   }
-  if (warp == L::kMmaWarp) {
-    tmem_alloc(sbase + L::kMisc, 128 * KT);
+  if (warp == kMmaWarp) {
+    tmem_alloc(sbase + L::kMisc, L::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -279,20 +279,19 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp == L::kProducerWarp) {
+  if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
-    const KeyBlock blk = key_block(P, key0, L::kKeys);
+    const KeyBlock blk = key_block(P, key0);
     int first = seg * W.tps, last = min(W.ntiles, first + W.tps);
     if (P.layout == kContiguous) {  // rank-major order is natural order
-      first = max(first, blk.q.lo / kQT);
-      last = min(last, blk.q.hi / kQT + 1);
-      if (W.observe > 0 && P.cu == nullptr) first = max(first, max(0, P.S - W.observe) / kQT);
+      first = max(first, (blk.q.lo - W.q0) / kQT);  // (towards 0: an extra tile is skipped)
+      last = blk.q.hi < W.q0 ? 0 : min(last, (blk.q.hi - W.q0) / kQT + 1);
     }
     // The next (tile, head), its rows' positions and LSE. This runs once per
     // tile in one warp, so it is kept short: what takes divisions is found for
     // 32 tiles at a time, one per lane.
     struct Item {
-      int qt, cls, h, pos[kQT / 32];
+      int row, cls, h, pos[kQT / 32];  // row: the tile's first
       float lse[kQT / 32];
     };
     const float* lse_head = P.lse + lse_index(P, bt, h0, 0);
@@ -312,7 +311,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           // which are observed depends on the sequence
           lo_mine = -1;
           if (cls_mine != kClsEmpty && (W.observe == 0 || P.cu == nullptr)) {
-            const int p0 = t * kQT, p1 = min(p0 + kQT, P.S) - 1;
+            const int p0 = W.q0 + t * kQT, p1 = min(p0 + kQT, P.S) - 1;
             if (p0 / run == p1 / run || P.layout == kContiguous) lo_mine = nat_pos(P, p0);
           }
         }
@@ -322,7 +321,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
         }
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
-        nx.qt = base + src;
+        nx.row = W.q0 + (base + src) * kQT;
         nx.cls = __shfl_sync(0xffffffffu, cls_mine, src);
         const int lo = __shfl_sync(0xffffffffu, lo_mine, src);
         const int from = W.observe > 0 ? P.S - W.observe : 0;
@@ -331,14 +330,14 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           const int r = lane + 32 * e;
           if (lo >= 0) {
             const int i = lo + r * step;
-            nx.pos[e] = nx.qt * kQT + r < P.S && i >= from ? i : kNowhere;
+            nx.pos[e] = nx.row + r < P.S && i >= from ? i : kNowhere;
           } else {
-            nx.pos[e] = observed_pos(W, nx.qt * kQT + r);
+            nx.pos[e] = observed_pos(W, nx.row + r);
           }
         }
       }
       nx.h = h0 + hh;
-      const float* src_lse = lse_head + hh * P.lse_sh + nx.qt * kQT + lane;
+      const float* src_lse = lse_head + hh * P.lse_sh + nx.row + lane;
 #pragma unroll
       for (int e = 0; e < kQT / 32; ++e) nx.lse[e] = nx.pos[e] >= 0 ? __ldg(src_lse + 32 * e) : 0.f;
       if (++hh == W.hpi) hh = 0;
@@ -349,17 +348,11 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     while (more) {
       const Item it = nx;
       fetch();  // its loads are on their way during this tile's waits
-      if (n >= L::kSlots) {  // the slot's previous tile has been multiplied
+      if (n >= kSlots) {  // the slot's previous tile has been multiplied
         ok = mbar_wait(bar(L::kQFree + slot), phase, abort_flag, status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
       }
       const int ring = n & (kRing - 1);
-      if (lane == 0) {
-        mbar_expect_tx(bar(L::kQFull + slot), L::kQTile);
-        for (int hf = 0; hf < L::kHalves; ++hf)
-          tma_load_4d(sbase + L::kQ + slot * L::kQTile + hf * L::kQHalf, &tm_q,
-                      bar(L::kQFull + slot), hf * 64, it.h, it.qt * kQT, bt);
-      }
       float* st = reinterpret_cast<float*>(sm + L::kStat + ring * L::kStatBytes);
 #pragma unroll
       for (int e = 0; e < kQT / 32; ++e) {
@@ -371,59 +364,62 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       }
       if (lane == 0) sched[ring] = it.cls;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kStatFull + ring));
+      if (lane == 0) {
+        // (the MMA warp reads the entry's class behind the Q tile's barrier)
+        mbar_expect_tx(bar(L::kQFull + slot), L::kQTile);
+        for (int hf = 0; hf < L::kHalves; ++hf)
+          tma_load_4d(sbase + L::kQ + slot * L::kQTile + hf * L::kQHalf, &tm_q,
+                      bar(L::kQFull + slot), hf * 64, it.h, it.row, bt);
+        mbar_arrive(bar(L::kStatFull + ring));
+      }
       ++n;
-      if (++slot == L::kSlots) {
+      if (++slot == kSlots) {
         slot = 0;
         phase ^= 1;
       }
     }
     if (lane == 0) {
-      if (ok && (n < L::kSlots || mbar_wait(bar(L::kQFree + slot), phase, abort_flag, status))) {
+      if (ok && (n < kSlots || mbar_wait(bar(L::kQFree + slot), phase, abort_flag, status))) {
         sched[n & (kRing - 1)] = kEnd;
         mbar_arrive(bar(L::kStatFull + (n & (kRing - 1))));
+        mbar_arrive(bar(L::kQFull + slot));
       }
-      // copies in flight land before the CTA ends, aborted or without a tile
-      for (int a = 0; a < ktiles; ++a) mbar_wait_drain(bar(L::kKFull + a), 0);
+      // aborted: the copies in flight land before the CTA ends
       if (*abort_flag)
-        for (int i = n > L::kSlots ? n - L::kSlots : 0; i < n; ++i)
-          mbar_wait_drain(bar(L::kQFull + i % L::kSlots), (i / L::kSlots) & 1);
+        for (int i = n > kSlots ? n - kSlots : 0; i < n; ++i)
+          mbar_wait_drain(bar(L::kQFull + i % kSlots), (i / kSlots) & 1);
     }
-  } else if (warp == L::kMmaWarp) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     // Every lane runs the loop and one elected lane issues: the descriptors
     // then are uniform values, which the issue takes as they are. (In a loop
     // of one lane alone each of its operands is first moved to a uniform
     // register, 76 clocks per 32-clock product.)
     constexpr uint32_t kId = idesc_bf16_f32(kTile, kQT, 0, 0);
-    const uint64_t dk = sdesc_sw128(sbase + L::kK, 16, 1024);
     const uint64_t dq = sdesc_sw128(sbase + L::kQ, 16, 1024);
     const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
     bool ok = true;
     int slot = 0, phase = 0;
     for (int n = 0; ok; ++n) {
       const int ring = n & (kRing - 1);
-      ok = mbar_wait(bar(L::kStatFull + ring), (n / kRing) & 1, abort_flag, status);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      if (__shfl_sync(0xffffffffu, sched[ring], 0) == kEnd) break;
       ok = mbar_wait(bar(L::kQFull + slot), phase, abort_flag, status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (__shfl_sync(0xffffffffu, sched[ring], 0) == kEnd) break;
 #pragma unroll
-      for (int a = 0; a < KT; ++a) {
+      for (int a = 0; a < kKT; ++a) {
         if (a >= ktiles) break;
-        if (n == 0) ok = mbar_wait(bar(L::kKFull + a), 0, abort_flag, status);
+        if (n == 0) ok = mbar_wait(bar(L::kKReady + a), 0, abort_flag, status);
         // the previous scores have been read
         if (n >= 1) ok = mbar_wait(bar(L::kSFree + a), (n - 1) & 1, abort_flag, status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
-        const uint32_t d = t0 + 128 * a;
-        const uint64_t da = sdesc_add(dk, a * L::kKTile);
+        const uint32_t d = t0 + L::kTmemS + 64 * a, ka = t0 + a * (D / 2);
         const uint64_t db = sdesc_add(dq, slot * L::kQTile);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(d, sdesc_add(da, (kk >> 2) * L::kKHalf + (kk & 3) * 32),
-                   sdesc_add(db, (kk >> 2) * L::kQHalf + (kk & 3) * 32), kId, kk > 0 ? 1u : 0u);
+            mma_ts(d, ka + 8 * kk, sdesc_add(db, (kk >> 2) * L::kQHalf + (kk & 3) * 32), kId,
+                   kk > 0 ? 1u : 0u);
           mma_commit(bar(L::kSFull + a));
         }
         __syncwarp();
@@ -431,7 +427,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       if (!ok) break;
       if (elect_one()) mma_commit(bar(L::kQFree + slot));
       __syncwarp();
-      if (++slot == L::kSlots) {
+      if (++slot == kSlots) {
         slot = 0;
         phase ^= 1;
       }
@@ -443,6 +439,28 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     const int a = warp >> 2;  // key tile
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int kp = key0 + warp * 32 + lane;
+    {
+      // the key's row into tensor memory: lane, channels 2c and 2c + 1 in column c
+      const uint4* row = reinterpret_cast<const uint4*>(
+          static_cast<const __nv_bfloat16*>(P.k) + (((long long)bt * P.S + kp) * P.Hkv + g) * D);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t x[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = kp < P.S ? __ldg(row + 8 * c + i) : make_uint4(0, 0, 0, 0);
+          x[4 * i] = v.x;
+          x[4 * i + 1] = v.y;
+          x[4 * i + 2] = v.z;
+          x[4 * i + 3] = v.w;
+        }
+        tmem_st32(tmem + lane_off + a * (D / 2) + 32 * c, x);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kKReady + a));
+    }
     Seen vis{1, 0};
     if (kp < P.S) vis = seen_by(P, nat_pos(P, kp));
     const uint64_t sc2 = f2_pack(P.scale_log2, P.scale_log2);
@@ -457,50 +475,42 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       ok = mbar_wait(bar(L::kSFull + a), n & 1, abort_flag, status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc_fence_after();
+      uint32_t v[2][32];
+      tmem_ld32(tmem + lane_off + L::kTmemS + 64 * a, v[0]);
+      tmem_ld32(tmem + lane_off + L::kTmemS + 64 * a + 32, v[1]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kSFree + a));
       const float4* nlse = reinterpret_cast<const float4*>(sm + L::kStat + ring * L::kStatBytes);
       const int4* pos = reinterpret_cast<const int4*>(nlse + kQT / 4);
-      // 32 columns at a time, the next ones on their way meanwhile
-      uint32_t v[2][32];
-      tmem_ld32(tmem + lane_off + 128 * a, v[0]);
+      if (cls == kClsFull) {
 #pragma unroll
-      for (int c = 0; c < kQT / 32; ++c) {
-        tmem_wait_ld();
-        if (c + 1 < kQT / 32) {
-          tmem_ld32(tmem + lane_off + 128 * a + 32 * (c + 1), v[(c + 1) & 1]);
-        } else {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::kSFree + a));
+        for (int k = 0; k < kQT / 4; ++k) {
+          const float4 l = nlse[k];
+          const uint32_t* s = &v[k >> 3][4 * (k & 7)];
+          const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2,
+                                    f2_pack(l.x, l.y));
+          const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3])), sc2,
+                                    f2_pack(l.z, l.w));
+          float x0, x1, y0, y1;
+          f2_unpack(x, x0, x1);
+          f2_unpack(y, y0, y1);
+          sum[(2 * k) & 3] = f2_add(sum[(2 * k) & 3], f2_pack(ex2(x0), ex2(x1)));
+          sum[(2 * k + 1) & 3] = f2_add(sum[(2 * k + 1) & 3], f2_pack(ex2(y0), ex2(y1)));
         }
-        const uint32_t(&vc)[32] = v[c & 1];
-        if (cls == kClsFull) {
+      } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 l = nlse[8 * c + k];
-            const uint32_t* s = &vc[4 * k];
-            const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2,
-                                      f2_pack(l.x, l.y));
-            const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3])), sc2,
-                                      f2_pack(l.z, l.w));
-            float x0, x1, y0, y1;
-            f2_unpack(x, x0, x1);
-            f2_unpack(y, y0, y1);
-            sum[(2 * k) & 3] = f2_add(sum[(2 * k) & 3], f2_pack(ex2(x0), ex2(x1)));
-            sum[(2 * k + 1) & 3] = f2_add(sum[(2 * k + 1) & 3], f2_pack(ex2(y0), ex2(y1)));
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 l = nlse[8 * c + k];
-            const int4 i = pos[8 * c + k];
-            const uint32_t* s = &vc[4 * k];
-            auto one = [&](uint32_t sv, float lv, int iv) {
-              const float p = ex2(fmaf(__uint_as_float(sv), P.scale_log2, lv));
-              return iv >= vis.lo && iv <= vis.hi ? p : 0.f;
-            };
-            sum[0] = f2_add(sum[0], f2_pack(one(s[0], l.x, i.x), one(s[1], l.y, i.y)));
-            sum[1] = f2_add(sum[1], f2_pack(one(s[2], l.z, i.z), one(s[3], l.w, i.w)));
-          }
+        for (int k = 0; k < kQT / 4; ++k) {
+          const float4 l = nlse[k];
+          const int4 i = pos[k];
+          const uint32_t* s = &v[k >> 3][4 * (k & 7)];
+          auto one = [&](uint32_t sv, float lv, int iv) {
+            const float p = ex2(fmaf(__uint_as_float(sv), P.scale_log2, lv));
+            return iv >= vis.lo && iv <= vis.hi ? p : 0.f;
+          };
+          sum[0] = f2_add(sum[0], f2_pack(one(s[0], l.x, i.x), one(s[1], l.y, i.y)));
+          sum[1] = f2_add(sum[1], f2_pack(one(s[2], l.z, i.z), one(s[3], l.w, i.w)));
         }
       }
     }
@@ -513,7 +523,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == L::kMmaWarp) tmem_dealloc(tmem, 128 * KT);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, L::kTmem);
 }
 
 // weight[i] = the parts' sum, in order.
@@ -645,27 +655,29 @@ bool make_map(CUtensorMap* m, const void* base, int Bt, int S, int H, int D, int
 
 // How the problem is cut (host side, from the shapes alone).
 struct Cut {
-  int kt, hpi, nseg, tps, nkb, ntiles, parts;
+  int hpi, nseg, tps, nkb, q0, ntiles, parts;
 };
-Cut cut_of(int B, int S, int Hq, int Hkv, int observe) {
+// tail: the observed queries are the last rows (natural order, one sequence).
+Cut cut_of(int B, int S, int Hq, int Hkv, int observe, bool tail) {
   Cut c{};
   const int G = Hq / Hkv;
-  c.ntiles = (S + kQT - 1) / kQT;
-  // query tiles that a key block meets at most
-  const int tiles = observe > 0 ? std::min((observe + kQT - 1) / kQT + 1, c.ntiles) : c.ntiles;
-  c.kt = tiles >= 16 ? 4 : 2;
-  c.nkb = (S + c.kt * kTile - 1) / (c.kt * kTile);
+  if (observe >= S) observe = 0;
+  c.q0 = observe > 0 && tail ? S - observe : 0;
+  c.ntiles = (S - c.q0 + kQT - 1) / kQT;
+  // query tiles that a key block meets at most, of one sequence
+  const int all = (S + kQT - 1) / kQT;
+  const int tiles = observe > 0 ? std::min((observe + kQT - 1) / kQT + 1, all) : all;
+  c.nkb = (S + kKeys - 1) / kKeys;
   c.hpi = G;
   c.nseg = 1;
-  const int slots = c.kt == 4 ? 152 : 304;
   const long long blocks = (long long)c.nkb * Hkv * B;
-  const long long want = 8LL * slots;  // CTAs that even out what the masks leave
-  if (blocks < want && tiles >= 8) {  // (each CTA loads its keys anew)
+  const long long want = 8LL * 304;  // CTAs that even out what the masks leave
+  if (blocks < want && tiles >= 16) {  // (each CTA loads its keys anew)
     c.hpi = 1;
     const long long have = blocks * G;
     if (have < want && observe == 0) {
       long long n = (want + have - 1) / have;
-      const long long most = (tiles + 7) / 8;  // at least 8 tiles each
+      const long long most = (tiles + 15) / 16;  // at least 16 tiles each
       if (n > most) n = most;
       if (n > 16) n = 16;
       c.nseg = (int)n;
@@ -676,22 +688,21 @@ Cut cut_of(int B, int S, int Hq, int Hkv, int observe) {
   return c;
 }
 
-template <int D, int KT>
+template <int D>
 usp_status_t launch_tc(const WeightParams& W, cudaStream_t st) {
   const AttnParams& P = W.P;
-  using L = WSmem<D, KT>;
-  CUtensorMap mq, mk;
-  if (!make_map(&mq, P.q, P.Bt, P.S, P.Hq, D, kQT) || !make_map(&mk, P.k, P.Bt, P.S, P.Hkv, D, kTile))
-    return USP_ERR_CUDA;
+  using L = WSmem<D>;
+  CUtensorMap mq;
+  if (!make_map(&mq, P.q, P.Bt, P.S, P.Hq, D, kQT)) return USP_ERR_CUDA;
   const int smem = L::kAlloc;
-  cudaError_t e = cudaFuncSetAttribute(key_weights_tc_kernel<D, KT>,
+  cudaError_t e = cudaFuncSetAttribute(key_weights_tc_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
   const long long blocks = (long long)W.nkb * P.Bt * P.Hkv * (P.G / W.hpi) * W.nseg;
   if (blocks > 0x7fffffffLL) return USP_ERR_UNSUPPORTED;
   {
     ProfScope ps(st, "attn_key_weights");
-    key_weights_tc_kernel<D, KT><<<(unsigned)blocks, L::kThreads, smem, st>>>(W, mq, mk);
+    key_weights_tc_kernel<D><<<(unsigned)blocks, kThreads, smem, st>>>(W, mq);
   }
   note_launch();
   return check_launch();
@@ -700,18 +711,16 @@ usp_status_t launch_tc(const WeightParams& W, cudaStream_t st) {
 }  // namespace
 
 size_t key_weights_workspace(int B, int S, int Hq, int Hkv, int observe) {
-  const Cut c = cut_of(B, S, Hq, Hkv, observe);
+  const Cut c = cut_of(B, S, Hq, Hkv, observe, false);  // (parts do not depend on `tail`)
   return c.parts > 1 ? (size_t)c.parts * B * Hkv * S * 4 : 0;
 }
 
 usp_status_t launch_key_weights_tc(const AttnParams& P, float* weight, int observe,
                                    void* workspace, cudaStream_t st) {
-  const Cut c = cut_of(P.Bt, P.S, P.Hq, P.Hkv, observe);
-  WeightParams W{P, c.parts > 1 ? static_cast<float*>(workspace) : weight, observe, c.hpi, c.nseg,
-                 c.tps, c.nkb, c.ntiles};
-  usp_status_t r;
-  if (P.D == 128) r = c.kt == 4 ? launch_tc<128, 4>(W, st) : launch_tc<128, 2>(W, st);
-  else r = c.kt == 4 ? launch_tc<64, 4>(W, st) : launch_tc<64, 2>(W, st);
+  const Cut c = cut_of(P.Bt, P.S, P.Hq, P.Hkv, observe, P.layout == kContiguous && !P.cu);
+  WeightParams W{P, c.parts > 1 ? static_cast<float*>(workspace) : weight,
+                 observe < P.S ? observe : 0, c.hpi, c.nseg, c.tps, c.nkb, c.q0, c.ntiles};
+  usp_status_t r = P.D == 128 ? launch_tc<128>(W, st) : launch_tc<64>(W, st);
   if (r != USP_OK || c.parts == 1) return r;
   const long long n = (long long)P.Bt * P.Hkv * P.S;
   const long long blocks = (n + 255) / 256;
