@@ -6,29 +6,31 @@
 // ("Long Context Attention" notes, "Motivation": the LSE is what the forward
 // keeps; with it a probability needs no second pass over its row.)
 //
-// Tensor-core kernel (bf16). One CTA owns 256 keys (two tiles of 128) of one
-// KV head and takes the query tiles of 64 that may see them, for some of the
-// group's query heads and a segment of the queries: S^T = K Q^T, keys on the
-// 128 TMEM lanes, so that a softmax thread owns a key and the column sum is a
-// register. Nothing is normalised or rescaled, and nothing goes back to the
-// tensor core. The keys are the A operand and stay in tensor memory, put there
-// by the threads that own them: from shared memory the products would read
-// 6 KB in the 32 clocks of a 128 x 64 x 16 product, where 4 KB is what it can
-// give (measured: 57 clocks each). So only Q (2 KB per product) passes through
-// shared memory. The products of a 128 x 64 tile (D = 128) take 256 clocks,
-// its exponentials (32 per clock and SM) as many. A key tile has one 64-column
-// buffer of scores: the softmax takes it into registers at once, and while it
-// works the other products run. What then limits is the MMA warp, whose
-// products are issued no faster than they run and which waits between them:
-// so two CTAs per SM, each with its own, and as few barriers for it as can be
-// (512 keys in one CTA: 2400 clocks per 512 x 64 scores).
-// Roles (320 threads):
-//   warps 0-7  softmax: warp w owns keys [32 w, 32 w + 32)
-//   warp 8     producer: finds the query tiles that can see the keys (32 at a
-//              time, one per lane), loads Q (five slots) and, with all lanes,
-//              the tile's LSE (asked for one tile ahead) and positions
-//   warp 9     MMA issuer, owner of tensor memory: K of key tile a in columns
-//              [a D/2, + D/2), its S^T in [D + 64 a, + 64)
+// Tensor-core kernel (bf16). S^T = K Q^T, keys on the 128 TMEM lanes, so that a
+// softmax thread owns a key and the column sum is a register. Nothing is
+// normalised or rescaled, and nothing goes back to the tensor core. An item of
+// work is 256 keys (two tiles of 128) of one KV head with the query tiles of
+// 128 that may see them, for some of the group's query heads and a segment of
+// the queries; one CTA per SM takes items in turn, and its roles run ahead of
+// one another across items.
+// What bounds it: per 128 x 128 tile (D = 128) the products take 512 clocks
+// (616 with both operands from shared memory, 64 KB), the exponentials (32 per
+// clock and SM) 512, and what a tile needs besides, waits on barriers and
+// tensor memory's latency, about 1500 per buffer of scores. So scores have
+// four 128-column buffers (all of tensor memory) and each key tile two groups
+// of softmax warps, which take its query tiles in turn: fewer or smaller
+// buffers left the tensor core and the exponentials idle two thirds of the
+// time (8K prompt, zigzag ring of 8: 314 us with one buffer per key tile of
+// 512 keys, 320 with keys in tensor memory and 64 columns).
+// Roles (608 threads):
+//   warps 0-15 softmax: warp w takes keys [32 (w & 7), + 32) and the query
+//              tiles of parity w >> 3
+//   warp 16    producer: finds the query tiles that can see the item's keys (32
+//              at a time, one per lane), loads K (a ring of three tiles, the
+//              next item's ahead of time), Q (three slots) and, with all
+//              lanes, the tile's LSE (asked for one tile ahead) and positions
+//   warps 17, 18  MMA issuers, one per key tile (what a warp waits between its
+//              products the other fills); 17 owns tensor memory
 // Positions are read per query from shared memory, so a tile may cross chunk
 // and shard boundaries: any layout and any length has this kernel.
 //
@@ -52,15 +54,18 @@ using namespace tc;
 
 __device__ int g_key_weights_status = 0;
 
-constexpr int kQT = 64;             // queries per tile
-constexpr int kKT = 2;              // key tiles per CTA
-constexpr int kKeys = kKT * kTile;  // keys per CTA
-constexpr int kSoftWarps = 4 * kKT;
+constexpr int kQT = 128;            // queries per tile
+constexpr int kKT = 2;              // key tiles per item
+constexpr int kKeys = kKT * kTile;  // keys per item
+constexpr int kSoftWarps = 8 * kKT; // two groups of four per key tile
 constexpr int kProducerWarp = kSoftWarps;
 constexpr int kMmaWarp = kProducerWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr int kSlots = 5;           // Q tiles
-constexpr int kRing = 8;           // entries of query statistics
+constexpr int kThreads = 32 * (kMmaWarp + kKT);
+constexpr int kSlots = 3;           // Q tiles
+constexpr int kKSlots = 3;          // K tiles
+constexpr int kSBufs = 4;           // score buffers of 128 columns
+constexpr int kRing = 16;           // entries of query statistics
+constexpr int kCtas = 152;          // one per SM
 constexpr int kEnd = -1;
 constexpr int kNowhere = -(1 << 30);  // position of a row that is not observed
 constexpr float kLog2e = 1.4426950408889634f;
@@ -87,35 +92,67 @@ struct WeightParams {
   int q0;        // first row of tile 0: where the observed rows begin, if they
                  // are one run to the end; else 0
   int ntiles;    // query tiles
+  int items;
 };
 
 template <int D>
 struct WSmem {
   // A ring entry is written for tile x once the products of tile x - kSlots
-  // are done; the softmax is then past the scores of tile x - kSlots - 1, so
-  // past the statistics of tile x - kSlots - 2.
-  static_assert(kRing >= kSlots + 2, "a statistics entry is free");
+  // are done. With one key tile per item the scores four tiles before that
+  // have then been taken out, so entries up to x - kSlots - kSBufs - 2 are not
+  // used any more (the group that took tile x - kSlots - kSBufs is past its
+  // previous one).
+  static_assert(kRing >= kSlots + kSBufs + 2, "a statistics entry is free");
   static constexpr int kHalves = D / 64;
-  static constexpr int kQHalf = kQT * 128;              // 64 channels of a Q tile
-  static constexpr int kQTile = kQHalf * kHalves;
-  static constexpr int kQ = 0;
-  static constexpr int kStat = kQ + kSlots * kQTile;    // kRing x (-lse2[64], pos[64])
+  static constexpr int kHalf = kTile * 128;             // 64 channels of a K or Q tile
+  static constexpr int kTileBytes = kHalf * kHalves;
+  static constexpr int kK = 0;                          // kKSlots
+  static constexpr int kQ = kK + kKSlots * kTileBytes;  // kSlots
+  static constexpr int kStat = kQ + kSlots * kTileBytes;  // kRing x (-lse2[128], pos[128])
   static constexpr int kStatBytes = 2 * kQT * 4;
-  static constexpr int kSched = kStat + kRing * kStatBytes;  // kRing ints
-  static constexpr int kBar = kSched + kRing * 4;
-  static constexpr int kKReady = 0, kQFull = kKReady + kKT, kQFree = kQFull + kSlots,
-                       kSFull = kQFree + kSlots, kSFree = kSFull + kKT,
-                       kStatFull = kSFree + kKT, kMmaDone = kStatFull + kRing,
-                       kNumBars = kMmaDone + 1;
-  static constexpr int kTmemS = kKT * D / 2;            // columns
-  static constexpr int kTmem = 256;
-  static_assert(kTmemS + kQT * kKT <= kTmem, "tensor memory");
+  static constexpr int kJoin = kStat + kRing * kStatBytes;  // [2][kKeys] sums of group 1
+  static constexpr int kSched = kJoin + 2 * kKeys * 4;  // kRing ints: class | rows << 8
+  static constexpr int kItem = kSched + kRing * 4;      // [2] ItemRecord
+  static constexpr int kBar = kItem + 2 * 16;
+  static constexpr int kKFull = 0, kKFree = kKFull + kKSlots, kQFull = kKFree + kKSlots,
+                       kQFree = kQFull + kSlots, kSFull = kQFree + kSlots,
+                       kSFree = kSFull + kSBufs, kStatFull = kSFree + kSBufs,
+                       kItemFull = kStatFull + kRing, kItemFree = kItemFull + 2,
+                       kJoinFull = kItemFree + 2 /* [2][kKT] */, kMmaDone = kJoinFull + 2 * kKT,
+                       kNumBars = kMmaDone + kKT;
   static constexpr int kMisc = (kBar + 8 * kNumBars + 15) / 16 * 16;
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
-  static_assert(kAlloc <= 113 * 1024, "two CTAs per SM");
-  static_assert(kBar % 8 == 0 && kStat % 16 == 0, "alignment");
+  static_assert(kAlloc <= 232448, "exceeds the per-CTA shared memory limit");
+  static_assert(kBar % 8 == 0 && kStat % 16 == 0 && kItem % 16 == 0, "alignment");
 };
+
+// What the roles know of an item: the number of (query tile, head) pairs, or
+// kEnd, and which item it is.
+struct ItemRecord {
+  int count, item, pad[2];
+};
+struct ItemPos {
+  int part, g, bt, key0, h0, seg, ktiles;
+};
+__device__ __forceinline__ ItemPos item_pos(const WeightParams& W, int item) {
+  const AttnParams& P = W.P;
+  // key blocks outermost: with a causal mask the heaviest (first) start first
+  const int groups = P.G / W.hpi;  // items per KV head, key block and segment
+  ItemPos r;
+  r.part = item % (groups * W.nseg);
+  item /= groups * W.nseg;
+  r.g = item % P.Hkv;
+  item /= P.Hkv;
+  r.bt = item % P.Bt;
+  // ... in natural order, where a block of keys is one
+  r.key0 = item / P.Bt * kKeys;
+  if (P.layout == kZigzag && P.chunk % kKeys == 0) r.key0 = permuted_of(P, r.key0);
+  r.seg = r.part / groups;
+  r.h0 = r.g * P.G + (r.part % groups) * W.hpi;
+  r.ktiles = min(kKT, (P.S - r.key0 + kTile - 1) / kTile);  // with keys in them
+  return r;
+}
 
 // The queries that see the key at natural position j, as positions [lo, hi].
 struct Seen {
@@ -225,9 +262,12 @@ __device__ __forceinline__ int classify_tile(const WeightParams& W, int qt, cons
   return all ? kClsFull : kClsMasked;
 }
 
+// 19 warps: five share a 16K-register sub-partition, so <= 102 each (96 in the
+// allocation's steps of 8).
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
-key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap tm_q) {
+__global__ void __launch_bounds__(kThreads, 1)
+key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_k) {
   using L = WSmem<D>;
   const AttnParams& P = W.P;
   extern __shared__ uint8_t smem_raw[];
@@ -236,42 +276,39 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
   const uint32_t sbase = smem_u32(sm);
   auto bar = [&](int i) { return sbase + L::kBar + 8 * i; };
   volatile int* sched = reinterpret_cast<volatile int*>(sm + L::kSched);
+  volatile ItemRecord* record = reinterpret_cast<volatile ItemRecord*>(sm + L::kItem);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
   int* status = &g_key_weights_status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // key blocks outermost: with a causal mask the heaviest (first) start first
-  const int groups = P.G / W.hpi;  // CTAs per KV head and segment
-  int idx = blockIdx.x;
-  const int part = idx % (groups * W.nseg);
-  idx /= groups * W.nseg;
-  const int g = idx % P.Hkv;
-  idx /= P.Hkv;
-  const int bt = idx % P.Bt, kb = idx / P.Bt;
-  const int seg = part / groups, h0 = g * P.G + (part % groups) * W.hpi;
-  const int key0 = kb * kKeys;
-  const int ktiles = min(kKT, (P.S - key0 + kTile - 1) / kTile);  // with keys in them
-
   if (warp == kProducerWarp && lane == 0) {
-    // the four warps of a key tile: its keys are in tensor memory
-    for (int a = 0; a < kKT; ++a) mbar_init(bar(L::kKReady + a), 4);
+    for (int s = 0; s < kKSlots; ++s) {
+      mbar_init(bar(L::kKFull + s), 1);
+      mbar_init(bar(L::kKFree + s), 1);
+    }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(L::kQFull + s), 1);
-      mbar_init(bar(L::kQFree + s), 1);
+      mbar_init(bar(L::kQFree + s), kKT);  // both MMA warps
     }
-    for (int s = 0; s < kKT; ++s) {
+    for (int s = 0; s < kSBufs; ++s) {
       mbar_init(bar(L::kSFull + s), 1);
-      mbar_init(bar(L::kSFree + s), 4);  // the four warps of a key tile
+      mbar_init(bar(L::kSFree + s), 4);  // the four warps that take it
     }
     for (int s = 0; s < kRing; ++s) mbar_init(bar(L::kStatFull + s), 1);
-    mbar_init(bar(L::kMmaDone), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(L::kItemFull + s), 1);
+      mbar_init(bar(L::kItemFree + s), kSoftWarps + kKT);  // and the MMA warps
+      for (int a = 0; a < kKT; ++a) mbar_init(bar(L::kJoinFull + kKT * s + a), 4);
+    }
+    for (int a = 0; a < kKT; ++a) mbar_init(bar(L::kMmaDone + a), 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch(&tm_q);
+    tma_prefetch(&tm_k);
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(sbase + L::kMisc, L::kTmem);
+    tmem_alloc(sbase + L::kMisc, 512);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -281,249 +318,323 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
-    const KeyBlock blk = key_block(P, key0);
-    int first = seg * W.tps, last = min(W.ntiles, first + W.tps);
-    if (P.layout == kContiguous) {  // rank-major order is natural order
-      first = max(first, (blk.q.lo - W.q0) / kQT);  // (towards 0: an extra tile is skipped)
-      last = blk.q.hi < W.q0 ? 0 : min(last, (blk.q.hi - W.q0) / kQT + 1);
-    }
-    // The next (tile, head), its rows' positions and LSE. This runs once per
-    // tile in one warp, so it is kept short: what takes divisions is found for
-    // 32 tiles at a time, one per lane.
-    struct Item {
-      int row, cls, h, pos[kQT / 32];  // row: the tile's first
-      float lse[kQT / 32];
-    };
-    const float* lse_head = P.lse + lse_index(P, bt, h0, 0);
+    bool ok = true;
+    int n = 0, slot = 0, phase = 1;      // Q tiles (the first waits are skipped)
+    int kn = 0, kslot = 0, kphase = 1;   // K tiles
+    int it = 0;                          // items
     const int step = P.layout == kStripe ? P.cp : 1;
     const int run = P.layout == kZigzag ? P.chunk : P.shard;
-    int base = first - 32, cls_mine = kClsEmpty, lo_mine = 0, hh = 0;
-    unsigned todo = 0;
-    Item nx{};
-    bool more = true;
-    auto fetch = [&]() {
-      if (hh == 0) {  // a new tile
-        while (todo == 0 && (base += 32) < last) {
-          const int t = base + lane;
-          cls_mine = t < last ? classify_tile(W, t, blk) : kClsEmpty;
-          todo = __ballot_sync(0xffffffffu, cls_mine != kClsEmpty);
-          // first position, or -1: the rows are not one run of a chunk, or
-          // which are observed depends on the sequence
-          lo_mine = -1;
-          if (cls_mine != kClsEmpty && (W.observe == 0 || P.cu == nullptr)) {
-            const int p0 = W.q0 + t * kQT, p1 = min(p0 + kQT, P.S) - 1;
-            if (p0 / run == p1 / run || P.layout == kContiguous) lo_mine = nat_pos(P, p0);
-          }
-        }
-        if (todo == 0) {
-          more = false;
-          return;
-        }
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        nx.row = W.q0 + (base + src) * kQT;
-        nx.cls = __shfl_sync(0xffffffffu, cls_mine, src);
-        const int lo = __shfl_sync(0xffffffffu, lo_mine, src);
-        const int from = W.observe > 0 ? P.S - W.observe : 0;
-#pragma unroll
-        for (int e = 0; e < kQT / 32; ++e) {
-          const int r = lane + 32 * e;
-          if (lo >= 0) {
-            const int i = lo + r * step;
-            nx.pos[e] = nx.row + r < P.S && i >= from ? i : kNowhere;
-          } else {
-            nx.pos[e] = observed_pos(W, nx.row + r);
-          }
-        }
+    const int from = W.observe > 0 ? P.S - W.observe : 0;
+    for (; ok; ++it) {
+      // the items are sorted by their work as far as the mask goes: there and
+      // back, every CTA gets its share
+      const long long at = (long long)it * gridDim.x +
+                           ((it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      const int item = (int)at;
+      const bool end = at >= W.items;
+      const ItemPos ip = item_pos(W, end ? 0 : item);
+      const KeyBlock blk = key_block(P, ip.key0);
+      int first = ip.seg * W.tps, last = min(W.ntiles, first + W.tps);
+      if (P.layout == kContiguous) {  // rank-major order is natural order
+        first = max(first, (blk.q.lo - W.q0) / kQT);  // (towards 0: an extra tile is skipped)
+        last = blk.q.hi < W.q0 ? 0 : min(last, (blk.q.hi - W.q0) / kQT + 1);
       }
-      nx.h = h0 + hh;
-      const float* src_lse = lse_head + hh * P.lse_sh + nx.row + lane;
-#pragma unroll
-      for (int e = 0; e < kQT / 32; ++e) nx.lse[e] = nx.pos[e] >= 0 ? __ldg(src_lse + 32 * e) : 0.f;
-      if (++hh == W.hpi) hh = 0;
-    };
-    fetch();
-    int n = 0, slot = 0, phase = 1;  // (the first waits on a free slot pass)
-    bool ok = true;
-    while (more) {
-      const Item it = nx;
-      fetch();  // its loads are on their way during this tile's waits
-      if (n >= kSlots) {  // the slot's previous tile has been multiplied
-        ok = mbar_wait(bar(L::kQFree + slot), phase, abort_flag, status);
+      int tiles = 0;
+      for (int base = first; base < last; base += 32)
+        tiles += __popc(__ballot_sync(
+            0xffffffffu, base + lane < last && classify_tile(W, base + lane, blk) != kClsEmpty));
+      if (it >= 2) {  // every role is done with the record's previous item
+        ok = mbar_wait(bar(L::kItemFree + (it & 1)), ((it >> 1) - 1) & 1, abort_flag, status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
       }
-      const int ring = n & (kRing - 1);
-      float* st = reinterpret_cast<float*>(sm + L::kStat + ring * L::kStatBytes);
-#pragma unroll
-      for (int e = 0; e < kQT / 32; ++e) {
-        const float x = it.lse[e] * kLog2e;
-        // a row that sees nothing adds nothing
-        const bool none = it.pos[e] < 0 || x == -INFINITY;
-        st[lane + 32 * e] = none ? -INFINITY : -x;
-        reinterpret_cast<int*>(st)[kQT + lane + 32 * e] = it.pos[e];
-      }
-      if (lane == 0) sched[ring] = it.cls;
-      __syncwarp();
       if (lane == 0) {
-        // (the MMA warp reads the entry's class behind the Q tile's barrier)
-        mbar_expect_tx(bar(L::kQFull + slot), L::kQTile);
-        for (int hf = 0; hf < L::kHalves; ++hf)
-          tma_load_4d(sbase + L::kQ + slot * L::kQTile + hf * L::kQHalf, &tm_q,
-                      bar(L::kQFull + slot), hf * 64, it.h, it.row, bt);
-        mbar_arrive(bar(L::kStatFull + ring));
+        record[it & 1].count = end ? kEnd : tiles * W.hpi;
+        record[it & 1].item = item;
+        mbar_arrive(bar(L::kItemFull + (it & 1)));
       }
-      ++n;
-      if (++slot == kSlots) {
-        slot = 0;
-        phase ^= 1;
+      if (end) break;
+      if (tiles == 0) continue;
+      for (int a = 0; a < ip.ktiles; ++a) {
+        if (kn >= kKSlots) {  // the slot's previous keys have been multiplied
+          ok = mbar_wait(bar(L::kKFree + kslot), kphase, abort_flag, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        }
+        if (lane == 0) {
+          mbar_expect_tx(bar(L::kKFull + kslot), L::kTileBytes);
+          for (int hf = 0; hf < L::kHalves; ++hf)
+            tma_load_4d(sbase + L::kK + kslot * L::kTileBytes + hf * L::kHalf, &tm_k,
+                        bar(L::kKFull + kslot), hf * 64, ip.g, ip.key0 + a * kTile, ip.bt);
+        }
+        ++kn;
+        if (++kslot == kKSlots) {
+          kslot = 0;
+          kphase ^= 1;
+        }
+      }
+      if (!ok) break;
+      // The next (tile, head), its rows' positions and LSE. This runs once per
+      // tile in one warp, so it is kept short: what takes divisions is found
+      // for 32 tiles at a time, one per lane.
+      struct Next {
+        int row, cls, h, pos[kQT / 32];  // row: the tile's first
+        float lse[kQT / 32];
+      };
+      const float* lse_head = P.lse + lse_index(P, ip.bt, ip.h0, 0);
+      int base = first - 32, cls_mine = kClsEmpty, lo_mine = 0, hh = 0;
+      unsigned todo = 0;
+      Next nx{};
+      bool more = true;
+      auto fetch = [&]() {
+        if (hh == 0) {  // a new tile
+          while (todo == 0 && (base += 32) < last) {
+            const int t = base + lane;
+            cls_mine = t < last ? classify_tile(W, t, blk) : kClsEmpty;
+            todo = __ballot_sync(0xffffffffu, cls_mine != kClsEmpty);
+            // first position, or -1: the rows are not one run of a chunk, or
+            // which are observed depends on the sequence
+            lo_mine = -1;
+            if (cls_mine != kClsEmpty && (W.observe == 0 || P.cu == nullptr)) {
+              const int p0 = W.q0 + t * kQT, p1 = min(p0 + kQT, P.S) - 1;
+              if (p0 / run == p1 / run || P.layout == kContiguous) lo_mine = nat_pos(P, p0);
+            }
+          }
+          if (todo == 0) {
+            more = false;
+            return;
+          }
+          const int src = __ffs(todo) - 1;
+          todo &= todo - 1;
+          nx.row = W.q0 + (base + src) * kQT;
+          nx.cls = __shfl_sync(0xffffffffu, cls_mine, src);
+          const int lo = __shfl_sync(0xffffffffu, lo_mine, src);
+#pragma unroll
+          for (int e = 0; e < kQT / 32; ++e) {
+            const int r = lane + 32 * e;
+            if (lo >= 0) {
+              const int i = lo + r * step;
+              nx.pos[e] = nx.row + r < P.S && i >= from ? i : kNowhere;
+            } else {
+              nx.pos[e] = observed_pos(W, nx.row + r);
+            }
+          }
+        }
+        nx.h = ip.h0 + hh;
+        const float* src_lse = lse_head + hh * P.lse_sh + nx.row + lane;
+#pragma unroll
+        for (int e = 0; e < kQT / 32; ++e) nx.lse[e] = nx.pos[e] >= 0 ? __ldg(src_lse + 32 * e) : 0.f;
+        if (++hh == W.hpi) hh = 0;
+      };
+      fetch();
+      while (more) {
+        const Next cur = nx;
+        fetch();  // its loads are on their way during this tile's waits
+        if (n >= kSlots) {  // the slot's previous tile has been multiplied
+          ok = mbar_wait(bar(L::kQFree + slot), phase, abort_flag, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        }
+        const int ring = n & (kRing - 1), rows = min(kQT, P.S - cur.row);
+        float* st = reinterpret_cast<float*>(sm + L::kStat + ring * L::kStatBytes);
+#pragma unroll
+        for (int e = 0; e < kQT / 32; ++e) {
+          const float x = cur.lse[e] * kLog2e;
+          // a row that sees nothing adds nothing
+          const bool none = cur.pos[e] < 0 || x == -INFINITY;
+          st[lane + 32 * e] = none ? -INFINITY : -x;
+          reinterpret_cast<int*>(st)[kQT + lane + 32 * e] = cur.pos[e];
+        }
+        if (lane == 0) sched[ring] = cur.cls | rows << 8;
+        __syncwarp();
+        if (lane == 0) {
+          // 64 rows at a time (the MMA warp reads the entry behind the Q tile's
+          // barrier)
+          const int boxes = rows > 64 ? 2 : 1;
+          mbar_expect_tx(bar(L::kQFull + slot), L::kTileBytes / 2 * boxes);
+          for (int r = 0; r < boxes; ++r)
+            for (int hf = 0; hf < L::kHalves; ++hf)
+              tma_load_4d(sbase + L::kQ + slot * L::kTileBytes + hf * L::kHalf + r * (L::kHalf / 2),
+                          &tm_q, bar(L::kQFull + slot), hf * 64, cur.h, cur.row + 64 * r, ip.bt);
+          mbar_arrive(bar(L::kStatFull + ring));
+        }
+        ++n;
+        if (++slot == kSlots) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
     }
-    if (lane == 0) {
-      if (ok && (n < kSlots || mbar_wait(bar(L::kQFree + slot), phase, abort_flag, status))) {
-        sched[n & (kRing - 1)] = kEnd;
-        mbar_arrive(bar(L::kStatFull + (n & (kRing - 1))));
-        mbar_arrive(bar(L::kQFull + slot));
-      }
-      // aborted: the copies in flight land before the CTA ends
-      if (*abort_flag)
-        for (int i = n > kSlots ? n - kSlots : 0; i < n; ++i)
-          mbar_wait_drain(bar(L::kQFull + i % kSlots), (i / kSlots) & 1);
+    // aborted: the copies in flight land before the CTA ends
+    if (lane == 0 && *abort_flag) {
+      for (int i = n > kSlots ? n - kSlots : 0; i < n; ++i)
+        mbar_wait_drain(bar(L::kQFull + i % kSlots), (i / kSlots) & 1);
+      for (int i = kn > kKSlots ? kn - kKSlots : 0; i < kn; ++i)
+        mbar_wait_drain(bar(L::kKFull + i % kKSlots), (i / kKSlots) & 1);
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp >= kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuers
     // Every lane runs the loop and one elected lane issues: the descriptors
     // then are uniform values, which the issue takes as they are. (In a loop
     // of one lane alone each of its operands is first moved to a uniform
-    // register, 76 clocks per 32-clock product.)
-    constexpr uint32_t kId = idesc_bf16_f32(kTile, kQT, 0, 0);
+    // register, 76 clocks per product.)
+    constexpr uint32_t kId128 = idesc_bf16_f32(kTile, 128, 0, 0);
+    constexpr uint32_t kId64 = idesc_bf16_f32(kTile, 64, 0, 0);
+    const uint64_t dk = sdesc_sw128(sbase + L::kK, 16, 1024);
     const uint64_t dq = sdesc_sw128(sbase + L::kQ, 16, 1024);
     const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
+    const int a = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);  // key tile
     bool ok = true;
-    int slot = 0, phase = 0;
-    for (int n = 0; ok; ++n) {
-      const int ring = n & (kRing - 1);
-      ok = mbar_wait(bar(L::kQFull + slot), phase, abort_flag, status);
+    int n = 0, slot = 0, phase = 0, kn = 0, si = 0;
+    for (int it = 0; ok; ++it) {
+      ok = mbar_wait(bar(L::kItemFull + (it & 1)), (it >> 1) & 1, abort_flag, status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      if (__shfl_sync(0xffffffffu, sched[ring], 0) == kEnd) break;
-#pragma unroll
-      for (int a = 0; a < kKT; ++a) {
-        if (a >= ktiles) break;
-        if (n == 0) ok = mbar_wait(bar(L::kKReady + a), 0, abort_flag, status);
-        // the previous scores have been read
-        if (n >= 1) ok = mbar_wait(bar(L::kSFree + a), (n - 1) & 1, abort_flag, status);
+      const int count = __shfl_sync(0xffffffffu, record[it & 1].count, 0);
+      const int item = __shfl_sync(0xffffffffu, record[it & 1].item, 0);
+      if (count == kEnd) break;
+      const int ktiles = item_pos(W, item).ktiles;
+      for (int j = 0; j < count && ok; ++j, ++n) {
+        ok = mbar_wait(bar(L::kQFull + slot), phase, abort_flag, status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        tc_fence_after();
-        const uint32_t d = t0 + L::kTmemS + 64 * a, ka = t0 + a * (D / 2);
-        const uint64_t db = sdesc_add(dq, slot * L::kQTile);
-        if (elect_one()) {
+        const int rows = __shfl_sync(0xffffffffu, sched[n & (kRing - 1)], 0) >> 8;
+        const uint32_t id = rows > 64 ? kId128 : kId64;
+        if (a < ktiles) {
+          const int ks = (kn + a) % kKSlots, sj = si + j * ktiles + a, buf = sj % kSBufs;
+          if (j == 0) ok = mbar_wait(bar(L::kKFull + ks), ((kn + a) / kKSlots) & 1, abort_flag, status);
+          // the buffer's previous scores have been taken out
+          if (ok && sj >= kSBufs)
+            ok = mbar_wait(bar(L::kSFree + buf), (sj / kSBufs - 1) & 1, abort_flag, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc_fence_after();
+          const uint64_t da = sdesc_add(dk, ks * L::kTileBytes);
+          const uint64_t db = sdesc_add(dq, slot * L::kTileBytes);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ts(d, ka + 8 * kk, sdesc_add(db, (kk >> 2) * L::kQHalf + (kk & 3) * 32), kId,
-                   kk > 0 ? 1u : 0u);
-          mma_commit(bar(L::kSFull + a));
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * L::kHalf + (kk & 3) * 32;
+              mma_ss(t0 + 128 * buf, sdesc_add(da, off), sdesc_add(db, off), id, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(bar(L::kSFull + buf));
+            if (j + 1 == count) mma_commit(bar(L::kKFree + ks));
+            mma_commit(bar(L::kQFree + slot));
+          }
+        } else if (lane == 0) {
+          mbar_arrive(bar(L::kQFree + slot));  // no such key tile
         }
         __syncwarp();
+        if (++slot == kSlots) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
-      if (!ok) break;
-      if (elect_one()) mma_commit(bar(L::kQFree + slot));
+      if (count > 0) kn += ktiles;
+      si += count * ktiles;
       __syncwarp();
-      if (++slot == kSlots) {
-        slot = 0;
-        phase ^= 1;
-      }
+      if (lane == 0) mbar_arrive(bar(L::kItemFree + (it & 1)));
     }
-    if (elect_one()) mma_commit(bar(L::kMmaDone));
-    mbar_wait_drain(bar(L::kMmaDone), 0);
-  } else if ((warp >> 2) < ktiles) {
+    if (elect_one()) mma_commit(bar(L::kMmaDone + a));
+    mbar_wait_drain(bar(L::kMmaDone + a), 0);
+  } else {
     // ------------------------------------------------------------ softmax
-    const int a = warp >> 2;  // key tile
+    const int a = (warp >> 2) & 1, group = warp >> 3;  // key tile, parity of the query tiles
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int kp = key0 + warp * 32 + lane;
-    {
-      // the key's row into tensor memory: lane, channels 2c and 2c + 1 in column c
-      const uint4* row = reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(P.k) + (((long long)bt * P.S + kp) * P.Hkv + g) * D);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t x[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 v = kp < P.S ? __ldg(row + 8 * c + i) : make_uint4(0, 0, 0, 0);
-          x[4 * i] = v.x;
-          x[4 * i + 1] = v.y;
-          x[4 * i + 2] = v.z;
-          x[4 * i + 3] = v.w;
-        }
-        tmem_st32(tmem + lane_off + a * (D / 2) + 32 * c, x);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kKReady + a));
-    }
-    Seen vis{1, 0};
-    if (kp < P.S) vis = seen_by(P, nat_pos(P, kp));
     const uint64_t sc2 = f2_pack(P.scale_log2, P.scale_log2);
-    uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
     bool ok = true;
-    for (int n = 0;; ++n) {
-      const int ring = n & (kRing - 1);
-      ok = mbar_wait(bar(L::kStatFull + ring), (n / kRing) & 1, abort_flag, status);
+    int n = 0, si = 0, joins[2] = {0, 0};
+    for (int it = 0; ok; ++it) {
+      ok = mbar_wait(bar(L::kItemFull + (it & 1)), (it >> 1) & 1, abort_flag, status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      const int cls = sched[ring];
-      if (cls == kEnd) break;
-      ok = mbar_wait(bar(L::kSFull + a), n & 1, abort_flag, status);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      tc_fence_after();
-      uint32_t v[2][32];
-      tmem_ld32(tmem + lane_off + L::kTmemS + 64 * a, v[0]);
-      tmem_ld32(tmem + lane_off + L::kTmemS + 64 * a + 32, v[1]);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kSFree + a));
-      const float4* nlse = reinterpret_cast<const float4*>(sm + L::kStat + ring * L::kStatBytes);
-      const int4* pos = reinterpret_cast<const int4*>(nlse + kQT / 4);
-      if (cls == kClsFull) {
+      const int count = record[it & 1].count, item = record[it & 1].item;
+      if (count == kEnd) break;
+      const ItemPos ip = item_pos(W, item);
+      if (a < ip.ktiles) {
+        const int kp = ip.key0 + (warp & 7) * 32 + lane;
+        Seen vis{1, 0};
+        if (kp < P.S) vis = seen_by(P, nat_pos(P, kp));
+        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+        for (int j = (n ^ group) & 1; j < count; j += 2) {
+          const int ring = (n + j) & (kRing - 1), sj = si + j * ip.ktiles + a, buf = sj % kSBufs;
+          ok = mbar_wait(bar(L::kSFull + buf), (sj / kSBufs) & 1, abort_flag, status);
+          // (long complete: the tile's statistics were written before its load)
+          if (ok) ok = mbar_wait(bar(L::kStatFull + ring), ((n + j) / kRing) & 1, abort_flag, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc_fence_after();
+          const uint32_t t_s = tmem + lane_off + 128 * buf;
+          uint32_t v[32];
+          const int entry = sched[ring], cls = entry & 255, rows = entry >> 8;
+          const float4* nlse = reinterpret_cast<const float4*>(sm + L::kStat + ring * L::kStatBytes);
+          const int4* pos = reinterpret_cast<const int4*>(nlse + kQT / 4);
+          // one copy of the code, 32 columns at a time (unrolled, with the next
+          // columns loaded ahead, it spills and takes 1.25 times as long)
+#pragma unroll 1
+          for (int c = 0; 32 * c < rows; ++c) {
+            tmem_ld32(t_s + 32 * c, v);
+            tmem_wait_ld();
+            if (32 * (c + 1) >= rows) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(L::kSFree + buf));
+            }
+            if (cls == kClsFull) {
 #pragma unroll
-        for (int k = 0; k < kQT / 4; ++k) {
-          const float4 l = nlse[k];
-          const uint32_t* s = &v[k >> 3][4 * (k & 7)];
-          const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2,
-                                    f2_pack(l.x, l.y));
-          const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3])), sc2,
-                                    f2_pack(l.z, l.w));
-          float x0, x1, y0, y1;
-          f2_unpack(x, x0, x1);
-          f2_unpack(y, y0, y1);
-          sum[(2 * k) & 3] = f2_add(sum[(2 * k) & 3], f2_pack(ex2(x0), ex2(x1)));
-          sum[(2 * k + 1) & 3] = f2_add(sum[(2 * k + 1) & 3], f2_pack(ex2(y0), ex2(y1)));
-        }
-      } else {
+              for (int k = 0; k < 8; ++k) {
+                const float4 l = nlse[8 * c + k];
+                const uint32_t* s = &v[4 * k];
+                const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2,
+                                          f2_pack(l.x, l.y));
+                const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3])), sc2,
+                                          f2_pack(l.z, l.w));
+                float x0, x1, y0, y1;
+                f2_unpack(x, x0, x1);
+                f2_unpack(y, y0, y1);
+                sum[(2 * k) & 3] = f2_add(sum[(2 * k) & 3], f2_pack(ex2(x0), ex2(x1)));
+                sum[(2 * k + 1) & 3] = f2_add(sum[(2 * k + 1) & 3], f2_pack(ex2(y0), ex2(y1)));
+              }
+            } else {
 #pragma unroll
-        for (int k = 0; k < kQT / 4; ++k) {
-          const float4 l = nlse[k];
-          const int4 i = pos[k];
-          const uint32_t* s = &v[k >> 3][4 * (k & 7)];
-          auto one = [&](uint32_t sv, float lv, int iv) {
-            const float p = ex2(fmaf(__uint_as_float(sv), P.scale_log2, lv));
-            return iv >= vis.lo && iv <= vis.hi ? p : 0.f;
-          };
-          sum[0] = f2_add(sum[0], f2_pack(one(s[0], l.x, i.x), one(s[1], l.y, i.y)));
-          sum[1] = f2_add(sum[1], f2_pack(one(s[2], l.z, i.z), one(s[3], l.w, i.w)));
+              for (int k = 0; k < 8; ++k) {
+                const float4 l = nlse[8 * c + k];
+                const int4 i = pos[8 * c + k];
+                const uint32_t* s = &v[4 * k];
+                auto one = [&](uint32_t sv, float lv, int iv) {
+                  const float p = ex2(fmaf(__uint_as_float(sv), P.scale_log2, lv));
+                  return iv >= vis.lo && iv <= vis.hi ? p : 0.f;
+                };
+                sum[0] = f2_add(sum[0], f2_pack(one(s[0], l.x, i.x), one(s[1], l.y, i.y)));
+                sum[1] = f2_add(sum[1], f2_pack(one(s[2], l.z, i.z), one(s[3], l.w, i.w)));
+              }
+            }
+          }
         }
+        if (!ok) break;
+        // the two groups' sums; a buffer is used again two items on, which
+        // start when every role is done with this one
+        float x, y;
+        f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), x, y);
+        float* join = reinterpret_cast<float*>(sm + L::kJoin) + (it & 1) * kKeys;
+        const int at = (warp & 7) * 32 + lane;
+        if (group == 1) {
+          join[at] = x + y;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kJoinFull + kKT * (it & 1) + a));
+        }
+        // (the count of these phases is kept by both groups alike: one per item
+        // with this key tile and this parity)
+        if (group == 0) {
+          ok = mbar_wait(bar(L::kJoinFull + kKT * (it & 1) + a), joins[it & 1] & 1, abort_flag, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (kp < P.S)
+            W.part[(((long long)ip.part * P.Bt + ip.bt) * P.Hkv + ip.g) * P.S + kp] = x + y + join[at];
+        }
+        ++joins[it & 1];
       }
-    }
-    if (ok && kp < P.S) {
-      float x, y;
-      f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), x, y);
-      W.part[(((long long)part * P.Bt + bt) * P.Hkv + g) * P.S + kp] = x + y;
+      n += count;
+      si += count * ip.ktiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kItemFree + (it & 1)));
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, L::kTmem);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 // weight[i] = the parts' sum, in order.
@@ -671,13 +782,13 @@ Cut cut_of(int B, int S, int Hq, int Hkv, int observe, bool tail) {
   c.hpi = G;
   c.nseg = 1;
   const long long blocks = (long long)c.nkb * Hkv * B;
-  const long long want = 8LL * 304;  // CTAs that even out what the masks leave
-  if (blocks < want && tiles >= 16) {  // (each CTA loads its keys anew)
+  const long long want = 4LL * kCtas;  // items that even out what the masks leave
+  if (blocks < want && tiles >= 8) {  // (each item loads its keys anew)
     c.hpi = 1;
     const long long have = blocks * G;
     if (have < want && observe == 0) {
       long long n = (want + have - 1) / have;
-      const long long most = (tiles + 15) / 16;  // at least 16 tiles each
+      const long long most = (tiles + 15) / 16;  // at least 16 query tiles each
       if (n > most) n = most;
       if (n > 16) n = 16;
       c.nseg = (int)n;
@@ -692,17 +803,17 @@ template <int D>
 usp_status_t launch_tc(const WeightParams& W, cudaStream_t st) {
   const AttnParams& P = W.P;
   using L = WSmem<D>;
-  CUtensorMap mq;
-  if (!make_map(&mq, P.q, P.Bt, P.S, P.Hq, D, kQT)) return USP_ERR_CUDA;
+  CUtensorMap mq, mk;
+  if (!make_map(&mq, P.q, P.Bt, P.S, P.Hq, D, 64) || !make_map(&mk, P.k, P.Bt, P.S, P.Hkv, D, kTile))
+    return USP_ERR_CUDA;
   const int smem = L::kAlloc;
   cudaError_t e = cudaFuncSetAttribute(key_weights_tc_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
-  const long long blocks = (long long)W.nkb * P.Bt * P.Hkv * (P.G / W.hpi) * W.nseg;
-  if (blocks > 0x7fffffffLL) return USP_ERR_UNSUPPORTED;
+  const int blocks = W.items < kCtas ? W.items : kCtas;
   {
     ProfScope ps(st, "attn_key_weights");
-    key_weights_tc_kernel<D><<<(unsigned)blocks, kThreads, smem, st>>>(W, mq);
+    key_weights_tc_kernel<D><<<blocks, kThreads, smem, st>>>(W, mq, mk);
   }
   note_launch();
   return check_launch();
@@ -719,7 +830,10 @@ usp_status_t launch_key_weights_tc(const AttnParams& P, float* weight, int obser
                                    void* workspace, cudaStream_t st) {
   const Cut c = cut_of(P.Bt, P.S, P.Hq, P.Hkv, observe, P.layout == kContiguous && !P.cu);
   WeightParams W{P, c.parts > 1 ? static_cast<float*>(workspace) : weight,
-                 observe < P.S ? observe : 0, c.hpi, c.nseg, c.tps, c.nkb, c.q0, c.ntiles};
+                 observe < P.S ? observe : 0, c.hpi, c.nseg, c.tps, c.nkb, c.q0, c.ntiles, 0};
+  const long long items = (long long)c.nkb * P.Bt * P.Hkv * (P.G / c.hpi) * c.nseg;
+  if (items > 0x3fffffffLL) return USP_ERR_UNSUPPORTED;
+  W.items = (int)items;
   usp_status_t r = P.D == 128 ? launch_tc<128>(W, st) : launch_tc<64>(W, st);
   if (r != USP_OK || c.parts == 1) return r;
   const long long n = (long long)P.Bt * P.Hkv * P.S;
