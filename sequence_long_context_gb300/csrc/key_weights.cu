@@ -116,8 +116,7 @@ struct WSmem {
   static constexpr int kBar = kItem + 2 * 16;
   static constexpr int kKFull = 0, kKFree = kKFull + kKSlots, kQFull = kKFree + kKSlots,
                        kQFree = kQFull + kSlots, kSFull = kQFree + kSlots,
-                       kSFree = kSFull + kSBufs, kStatFull = kSFree + kSBufs,
-                       kItemFull = kStatFull + kRing, kItemFree = kItemFull + 2,
+                       kSFree = kSFull + kSBufs, kItemFull = kSFree + kSBufs, kItemFree = kItemFull + 2,
                        kJoinFull = kItemFree + 2 /* [2][kKT] */, kMmaDone = kJoinFull + 2 * kKT,
                        kNumBars = kMmaDone + kKT;
   static constexpr int kMisc = (kBar + 8 * kNumBars + 15) / 16 * 16;
@@ -292,10 +291,11 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       mbar_init(bar(L::kQFree + s), kKT);  // both MMA warps
     }
     for (int s = 0; s < kSBufs; ++s) {
-      mbar_init(bar(L::kSFull + s), 1);
+      // the products' commit, and the MMA warp's own arrival: it has seen the
+      // tile's statistics (behind the Q tile's barrier), so the softmax may
+      mbar_init(bar(L::kSFull + s), 2);
       mbar_init(bar(L::kSFree + s), 4);  // the four warps that take it
     }
-    for (int s = 0; s < kRing; ++s) mbar_init(bar(L::kStatFull + s), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(L::kItemFull + s), 1);
       mbar_init(bar(L::kItemFree + s), kSoftWarps + kKT);  // and the MMA warps
@@ -445,15 +445,13 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
         if (lane == 0) sched[ring] = cur.cls | rows << 8;
         __syncwarp();
         if (lane == 0) {
-          // 64 rows at a time (the MMA warp reads the entry behind the Q tile's
-          // barrier)
+          // 64 rows at a time; the barrier stands for the ring's entry too
           const int boxes = rows > 64 ? 2 : 1;
           mbar_expect_tx(bar(L::kQFull + slot), L::kTileBytes / 2 * boxes);
           for (int r = 0; r < boxes; ++r)
             for (int hf = 0; hf < L::kHalves; ++hf)
               tma_load_4d(sbase + L::kQ + slot * L::kTileBytes + hf * L::kHalf + r * (L::kHalf / 2),
                           &tm_q, bar(L::kQFull + slot), hf * 64, cur.h, cur.row + 64 * r, ip.bt);
-          mbar_arrive(bar(L::kStatFull + ring));
         }
         ++n;
         if (++slot == kSlots) {
@@ -502,6 +500,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           if (ok && sj >= kSBufs)
             ok = mbar_wait(bar(L::kSFree + buf), (sj / kSBufs - 1) & 1, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (lane == 0) mbar_arrive(bar(L::kSFull + buf));
           tc_fence_after();
           const uint64_t da = sdesc_add(dk, ks * L::kTileBytes);
           const uint64_t db = sdesc_add(dq, slot * L::kTileBytes);
@@ -552,30 +551,16 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
         for (int j = (n ^ group) & 1; j < count; j += 2) {
           const int ring = (n + j) & (kRing - 1), sj = si + j * ip.ktiles + a, buf = sj % kSBufs;
           ok = mbar_wait(bar(L::kSFull + buf), (sj / kSBufs) & 1, abort_flag, status);
-          // (long complete: the tile's statistics were written before its load)
-          if (ok) ok = mbar_wait(bar(L::kStatFull + ring), ((n + j) / kRing) & 1, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           tc_fence_after();
           const uint32_t t_s = tmem + lane_off + 128 * buf;
-          uint32_t v[32];
           const int entry = sched[ring], cls = entry & 255, rows = entry >> 8;
           const float4* nlse = reinterpret_cast<const float4*>(sm + L::kStat + ring * L::kStatBytes);
-          const int4* pos = reinterpret_cast<const int4*>(nlse + kQT / 4);
-          // one copy of the code, 32 columns at a time (unrolled, with the next
-          // columns loaded ahead, it spills and takes 1.25 times as long)
-#pragma unroll 1
-          for (int c = 0; 32 * c < rows; ++c) {
-            tmem_ld32(t_s + 32 * c, v);
-            tmem_wait_ld();
-            if (32 * (c + 1) >= rows) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(L::kSFree + buf));
-            }
+          auto add = [&](const uint32_t(&v)[32], const float4* nl) {
             if (cls == kClsFull) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const float4 l = nlse[8 * c + k];
+                const float4 l = nl[k];
                 const uint32_t* s = &v[4 * k];
                 const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2,
                                           f2_pack(l.x, l.y));
@@ -588,10 +573,11 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
                 sum[(2 * k + 1) & 3] = f2_add(sum[(2 * k + 1) & 3], f2_pack(ex2(y0), ex2(y1)));
               }
             } else {
+              const int4* pos = reinterpret_cast<const int4*>(nl + kQT / 4);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const float4 l = nlse[8 * c + k];
-                const int4 i = pos[8 * c + k];
+                const float4 l = nl[k];
+                const int4 i = pos[k];
                 const uint32_t* s = &v[4 * k];
                 auto one = [&](uint32_t sv, float lv, int iv) {
                   const float p = ex2(fmaf(__uint_as_float(sv), P.scale_log2, lv));
@@ -601,6 +587,21 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
                 sum[1] = f2_add(sum[1], f2_pack(one(s[2], l.z, i.z), one(s[3], l.w, i.w)));
               }
             }
+          };
+          // 32 columns at a time, one copy of the code. (With the next columns
+          // loaded ahead it spills, and takes 1.25 to 1.5 times as long: the
+          // other warps fill the time.)
+          uint32_t v[32];
+#pragma unroll 1
+          for (int c = 0; c < rows; c += 32) {
+            tmem_ld32(t_s + c, v);
+            tmem_wait_ld();
+            if (c + 32 >= rows) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(L::kSFree + buf));
+            }
+            add(v, nlse + c / 4);
           }
         }
         if (!ok) break;
