@@ -15,9 +15,11 @@
 // the slots differ, and a unit's partials are consecutive. The merge kernel
 // finds them from the same arithmetic.
 //
-// One CTA. Eight warps take the steps of a run in turn. Each warp has its own
-// ring of stages (codes and scales of 32 keys, four untiled bulk copies) and
-// its own online softmax; warps meet only at the end of a unit. The keys and
+// One CTA. A round is one step for each warp; its codes and scales are one
+// contiguous piece of each array (two where the sinks end), brought in by
+// untiled bulk copies two or three rounds ahead, which the warps issue in
+// turn. Every warp has its own online softmax; the warps meet only at the end
+// of a unit. The keys and
 // channels are the M side of the matrix products and the query rows the N
 // side (8 rows per product, where 16 would be padding for most head groups):
 //   S^T [keys x rows]  = K [keys x D] Q^T      (fp16 m16n8k16, fp32 sums)
@@ -60,10 +62,11 @@ using namespace tc;
 
 __device__ int g_decode_kv4_status = 0;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;                 // keys per step
 constexpr int kGridMax = 304;             // 152 SMs x 2 resident CTAs
+// Up to eight query rows: two CTAs of eight warps per SM at 128 registers;
+// sixteen: one of ten at 200, with Q^T in shared memory.
+__host__ __device__ constexpr int warps_for(int nt) { return nt == 1 ? 8 : 10; }
 constexpr float kLazy = 8.f;              // the max moves when it grows by 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -78,7 +81,7 @@ struct Params {
   float* scores;    // accumulate: [B][H][C][Rs] log2-scaled scores, else nullptr
   float2* ml;       // accumulate: [B][H][Rs] merged (m, 1 / l)
   int Tq, Hq, G, R, Rs, nrb;  // R = G Tq rows per KV head, nrb blocks of them
-  int grid;
+  int grid, warps;
   float score_mul;            // softmax scale * log2(e) * k_descale
   float v_descale;
   int causal, window, sink;
@@ -115,7 +118,7 @@ __device__ __forceinline__ long long total_steps_warp(const Params& P) {
   return n;
 }
 __device__ __forceinline__ long long active_ctas(const Params& P, long long T) {
-  const long long want = (T + kWarps - 1) / kWarps;
+  const long long want = (T + P.warps - 1) / P.warps;
   return want < P.grid ? want : P.grid;
 }
 
@@ -148,27 +151,28 @@ __device__ __forceinline__ bool next_unit(const Params& P, Walk& w) {
   return true;
 }
 
-template <int D>
-struct Stage {
-  static constexpr int kCodes = kStep * D / 2;
-  static constexpr int kScales = kStep * D / kBlock;
-  static constexpr int kKC = 0, kVC = kCodes, kKS = 2 * kCodes, kVS = 2 * kCodes + kScales;
-  static constexpr int kBytes = 2 * kCodes + 2 * kScales;
-};
-// Two resident CTAs (8 rows) have 113 KB each, which leaves two stages per
-// warp at D = 128; one CTA (16 rows, by registers) has room for four.
 template <int D, int NT>
 struct Smem {
-  static constexpr int kStages = (D == 128 && NT == 1) ? 2 : 4;
-  static constexpr int kStage = 0;  // [kWarps][kStages]
+  static constexpr int kWarps = warps_for(NT);
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kKeys = kWarps * kStep;  // of a round
+  // a stage: one round's codes and scales
+  static constexpr int kCodes = kKeys * D / 2, kScales = kKeys * D / kBlock;
+  static constexpr int kKC = 0, kVC = kCodes, kKS = 2 * kCodes, kVS = 2 * kCodes + kScales;
+  static constexpr int kStageBytes = 2 * kCodes + 2 * kScales;
+  static constexpr int kStages = D == 64 ? 4 : NT == 1 ? 2 : 3;
   static constexpr int kRedStride = D + 4;
-  static constexpr int kRed = kStage + kWarps * kStages * Stage<D>::kBytes;  // [kWarps][8][D + 4]
-  static constexpr int kML = kRed + kWarps * 8 * kRedStride * 4;             // [kWarps][8] float2
-  static constexpr int kBar = kML + kWarps * 8 * 8;
-  static constexpr int kMisc = kBar + kWarps * kStages * 8;  // abort, run
+  static constexpr int kRed = kStages * kStageBytes;              // [kWarps][8][D + 4]
+  static constexpr int kML = kRed + kWarps * 8 * kRedStride * 4;  // [kWarps][8] float2
+  static constexpr int kQ = kML + kWarps * 8 * 8;                 // 16 rows: [D/16][NT][32] uint2
+  static constexpr int kBar = kQ + (NT == 1 ? 0 : D / 16 * NT * 32 * 8);
+  static constexpr int kMisc = kBar + 2 * kStages * 8;            // abort, run
   static constexpr int kBytes = kMisc + 64;
   static_assert(kBytes <= (NT == 1 ? 113 : 227) * 1024, "residency");
-  static_assert(kRed % 16 == 0 && kML % 16 == 0 && kBar % 8 == 0 && kMisc % 16 == 0, "alignment");
+  static_assert(kRed % 16 == 0 && kML % 16 == 0 && kQ % 16 == 0 && kBar % 8 == 0 &&
+                    kMisc % 16 == 0 && kStageBytes % 128 == 0,
+                "alignment");
+  static_assert(kStages <= kWarps, "a warp has at most one round's copies in flight");
 };
 
 __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
@@ -213,27 +217,38 @@ __device__ __forceinline__ void expand(uint32_t x, uint32_t s, uint32_t zb, uint
   a[3] = h2_fma(and_or<0x00F000F0u, 0x54005400u>(y), s, zs);
 }
 
-// Starts the copies of one step into a stage.
-template <int D>
-__device__ __forceinline__ void load_step(const Params& P, const Walk& w, uint32_t stage,
-                                          uint32_t bar) {
-  const int key0 = (w.s < w.q.sinks ? w.s : w.s + w.q.skip) * kStep;
-  // whole 16-row groups that hold cached keys (the capacity is a multiple of 16)
-  const int rows = w.len - key0 > kRowAlign ? kStep : kRowAlign;
-  const long long row = w.row + key0;
-  const uint32_t cb = rows * (D / 2), sb = rows * (D / kBlock);
-  mbar_expect_tx(bar, 2 * (cb + sb));
-  bulk_load(stage + Stage<D>::kKC, P.c.kc + row * (D / 2), cb, bar);
-  bulk_load(stage + Stage<D>::kKS, P.c.ks + row * (D / kBlock), sb, bar);
-  bulk_load(stage + Stage<D>::kVC, P.c.vc + row * (D / 2), cb, bar);
-  bulk_load(stage + Stage<D>::kVS, P.c.vs + row * (D / kBlock), sb, bar);
+// Starts the copies of the round that begins at w.s into a stage.
+template <int D, int NT>
+__device__ __forceinline__ void load_round(const Params& P, const Walk& w, uint32_t stage,
+                                           uint32_t bar) {
+  using L = Smem<D, NT>;
+  const int s1 = min(w.s + L::kWarps, w.end), sp = min(max(w.q.sinks, w.s), s1);
+  // rows of steps [a, e): whole 16-row groups that hold cached keys (the
+  // capacity is a multiple of 16)
+  auto rows_of = [&](int a, int e, int key0) {
+    return min((e - a) * kStep, (w.len - key0 + kRowAlign - 1) / kRowAlign * kRowAlign);
+  };
+  // steps before the window's skip, and behind it
+  const int k0 = w.s * kStep, k1 = (sp + w.q.skip) * kStep;
+  const int n0 = sp > w.s ? rows_of(w.s, sp, k0) : 0, n1 = s1 > sp ? rows_of(sp, s1, k1) : 0;
+  mbar_expect_tx(bar, static_cast<uint32_t>(n0 + n1) * 2 * (D / 2 + D / kBlock));
+  auto piece = [&](int at, int key0, int n) {
+    const long long row = w.row + key0;
+    const uint32_t cb = n * (D / 2), sb = n * (D / kBlock);
+    bulk_load(stage + L::kKC + at * (D / 2), P.c.kc + row * (D / 2), cb, bar);
+    bulk_load(stage + L::kKS + at * (D / kBlock), P.c.ks + row * (D / kBlock), sb, bar);
+    bulk_load(stage + L::kVC + at * (D / 2), P.c.vc + row * (D / 2), cb, bar);
+    bulk_load(stage + L::kVS + at * (D / kBlock), P.c.vs + row * (D / kBlock), sb, bar);
+  };
+  if (n0 > 0) piece(0, k0, n0);
+  if (n1 > 0) piece((sp - w.s) * kStep, k1, n1);
 }
 
 template <int D, int NT, bool SC>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(const Params P) {
+__global__ void __launch_bounds__(Smem<D, NT>::kThreads, NT == 1 ? 2 : 1)
+decode_kv4_kernel(const Params P) {
   using L = Smem<D, NT>;
-  constexpr int kStages = L::kStages;
-  using St = Stage<D>;
+  constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kStages = L::kStages;
   constexpr int kRows = 8 * NT;
   constexpr int kWK = D / 32;      // 32-bit words of codes a thread has per K row
   constexpr int kWV = D / 64;      // and per V row
@@ -242,14 +257,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
   const uint32_t sbase = smem_u32(sm);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kMisc);
   long long* run = reinterpret_cast<long long*>(sm + L::kMisc + 16);  // first step, count, ..
+  uint2* qs = reinterpret_cast<uint2*>(sm + L::kQ);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t my_stage = sbase + L::kStage + warp * kStages * St::kBytes;
-  uint8_t* my_stage_p = sm + L::kStage + warp * kStages * St::kBytes;
-  const uint32_t my_bar = sbase + L::kBar + warp * kStages * 8;
+  auto full = [&](int st) { return sbase + L::kBar + 8 * st; };
+  auto empty = [&](int st) { return sbase + L::kBar + 8 * (kStages + st); };
 
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(my_bar + 8 * s, 1);
+  if (threadIdx.x == 32) {
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(full(st), 1);
+      mbar_init(empty(st), kWarps);
+    }
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -308,29 +326,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
     cur.end = (int)min((long long)n, cur.s + run[1]);
     cur.left = run[1] - (cur.end - cur.s);
   }
-  // this warp's copies run ahead of its computation, over the ends of units
+  // the copies run kStages rounds ahead of the computation, over the ends of
+  // units; the warps issue them in turn
   Walk pre = cur;
-  pre.s += warp;
   bool more = true;
-  auto settle = [&]() {  // to the warp's next step, maybe in a later unit
-    while (more && pre.s >= pre.end) {
-      more = next_unit(P, pre);
-      pre.s += warp;
-    }
-  };
-  settle();
-  int issued = 0, used = 0;
+  int issued = 0, used = 0, mine = -1;  // rounds; the last one this warp issued
   auto issue = [&]() {
-    if (!more) return;
-    if (lane == 0)
-      load_step<D>(P, pre, my_stage + (issued % kStages) * St::kBytes,
-                   my_bar + 8 * (issued % kStages));
+    if (warp == issued % kWarps) {
+      mine = issued;
+      const int st = issued % kStages;
+      if (lane == 0)
+        load_round<D, NT>(P, pre, sbase + st * L::kStageBytes, full(st));
+    }
     ++issued;
     pre.s += kWarps;
-    settle();
+    if (pre.s >= pre.end) more = next_unit(P, pre);
   };
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) issue();
+  for (int st = 0; st < kStages; ++st)
+    if (more) issue();
 
   const __half2 k2m4 = __float2half2_rn(0.0625f);
   const __half2 m1024 = __float2half2_rn(-1024.f), m64 = __float2half2_rn(-64.f);
@@ -343,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
     // Q^T fragments: product kk = 2w + jj takes channels (8w + 2jj, + 4) and
     // (8w + 2jj + 1, + 4) of the thread's run of D/4; qb: -8 times the run's
     // (its block's part's) sum in three parts
-    uint32_t qf[NT][2 * kWK][2], qb[NT][2];
+    constexpr bool kQs = NT > 1;  // Q^T in shared memory, else in registers
+    uint32_t qf[kQs ? 1 : NT][kQs ? 1 : 2 * kWK][2], qb[NT][2];
     float mul[NT][2];  // of rows 2t, 2t + 1: scores to log2 units
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -380,14 +395,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
           f[2 * i + 1] = __uint_as_float(e[i] & 0xffff0000u) * up;
         }
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj)
+        for (int jj = 0; jj < 2; ++jj) {
+          uint32_t pr[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const __half2 p = __floats2half2_rn(f[2 * jj + i], f[2 * jj + i + 4]);
-            qf[nt][2 * w + jj][i] = half2_bits(p);
+            pr[i] = half2_bits(p);
             const float2 back = __half22float2(p);
             sum += back.x + back.y;
           }
+          if constexpr (kQs) {
+            if (warp == 0) qs[((2 * w + jj) * NT + nt) * 32 + lane] = make_uint2(pr[0], pr[1]);
+          } else {
+            qf[nt][2 * w + jj][0] = pr[0];
+            qf[nt][2 * w + jj][1] = pr[1];
+          }
+        }
       }
       sum *= -8.f;
       const __half hi = __float2half_rn(sum);
@@ -401,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
       for (int e = 0; e < 2; ++e)
         mul[nt][e] = __shfl_sync(0xffffffffu, row_mul, 4 * (2 * t + e));
     }
+    if constexpr (kQs) __syncthreads();
     float o[NT][kMT][4], ob[NT][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -415,13 +439,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
       l[nt][0] = l[nt][1] = 0.f;
     }
     const int i_first = len - P.Tq;  // position of token 0
-    for (int s = cur.s + warp; s < cur.end; s += kWarps) {
-      const int st = used % kStages;
-      if (!mbar_wait(my_bar + 8 * st, (used / kStages) & 1, abort_flag, &g_decode_kv4_status))
-        ok = false;
+    for (int s0 = cur.s; s0 < cur.end; s0 += kWarps) {
+     const int st = used % kStages, s = s0 + warp;
+     if (s < cur.end) {
+      if (!mbar_wait(full(st), (used / kStages) & 1, abort_flag, &g_decode_kv4_status)) ok = false;
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      ++used;
-      const uint8_t* stp = my_stage_p + st * St::kBytes;
+      const uint8_t* stp = sm + st * L::kStageBytes;
+      const uint8_t* kcodes = stp + L::kKC + warp * (kStep * D / 2);
+      const uint8_t* vcodes = stp + L::kVC + warp * (kStep * D / 2);
+      const uint8_t* kscales = stp + L::kKS + warp * (kStep * D / kBlock);
+      const uint8_t* vscales = stp + L::kVS + warp * (kStep * D / kBlock);
       const int key0 = (s < steps.sinks ? s : s + steps.skip) * kStep;
       // does the mask (or the sequence's end) hide any of the step's keys?
       const int last = key0 + kStep - 1;
@@ -433,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
       for (int half = 0; half < 2; ++half) {
         const int r0 = 16 * half + tile_key(g), r1 = r0 + 8;
         uint32_t k0[kWK], k1[kWK];
-        const uint8_t* kc = stp + St::kKC + t * (D / 8);
+        const uint8_t* kc = kcodes + t * (D / 8);
         if constexpr (D == 128) {
           const uint4 a = *reinterpret_cast<const uint4*>(kc + r0 * (D / 2));
           const uint4 c = *reinterpret_cast<const uint4*>(kc + r1 * (D / 2));
@@ -445,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
           k0[0] = a.x; k0[1] = a.y;
           k1[0] = c.x; k1[1] = c.y;
         }
-        const uint8_t* ks = stp + St::kKS + (t * (D / 4)) / kBlock;
+        const uint8_t* ks = kscales + (t * (D / 4)) / kBlock;
         const __half2 ss = __hmul2(
             e4m3x2_to_half2(ks[r0 * (D / kBlock)] | (ks[r1 * (D / kBlock)] << 8)), k2m4);
         const uint32_t s0 = half2_bits(__low2half2(ss)), s1 = half2_bits(__high2half2(ss));
@@ -471,38 +498,43 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
           for (int jj = 0; jj < 2; ++jj) {
             const uint32_t a[4] = {p0[2 * jj], p1[2 * jj], p0[2 * jj + 1], p1[2 * jj + 1]};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(sc[nt][half], a, qf[nt][2 * w + jj][0], qf[nt][2 * w + jj][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (kQs) {
+                const uint2 q2 = qs[((2 * w + jj) * NT + nt) * 32 + lane];
+                mma_f16(sc[nt][half], a, q2.x, q2.y);
+              } else {
+                mma_f16(sc[nt][half], a, qf[nt][2 * w + jj][0], qf[nt][2 * w + jj][1]);
+              }
+            }
           }
         }
       }
       // ----------------------------------------------------------- softmax
-      bool grow = false;
-      float mx[NT][2];
+      if (masked) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+          for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = sc[nt][half][e] * mul[nt][e & 1];
-            if (masked) {
+            for (int e = 0; e < 4; ++e) {
               const int j = key0 + 16 * half + tile_key(g) + 8 * (e >> 1);
               const int tok = (rb * kRows + nt * 8 + 2 * t + (e & 1)) % P.Tq;
               const int i = i_first + tok;
               const bool see = j < len && i >= 0 && (!P.causal || j <= i) &&
                                (P.window <= 0 || i - j < P.window || j < P.sink);
-              if (!see) x = -INFINITY;
+              if (!see) sc[nt][half][e] = -INFINITY;
             }
-            sc[nt][half][e] = x;
-          }
+      }
+      bool grow = false;
+      float mx[NT][2];  // in log2 units (the factor is positive)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[nt][e] = fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][e + 2]),
-                            fmaxf(sc[nt][1][e], sc[nt][1][e + 2]));
+          mx[nt][e] = mul[nt][e] * fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][e + 2]),
+                                         fmaxf(sc[nt][1][e], sc[nt][1][e + 2]));
           grow |= mx[nt][e] > m[nt][e] + kLazy;
         }
-      }
       if constexpr (SC) {
         // the weights need every score once the whole row's sum is known
         float* dst = P.scores + head_row(P.c, b, h) * P.Rs;
@@ -517,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
               const int j = key0 + 16 * half + tile_key(g) + 8 * (e >> 1);
               if (j < len)
                 *reinterpret_cast<float2*>(dst + (long long)j * P.Rs + r) =
-                    make_float2(sc[nt][half][e], sc[nt][half][e + 1]);
+                    make_float2(sc[nt][half][e] * mul[nt][0], sc[nt][half][e + 1] * mul[nt][1]);
             }
         }
       }
@@ -549,13 +581,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
       uint32_t pf[NT][2][2];  // P^T fragments: [half][keys 0-7, 8-15]
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-        const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        const float m0 = m[nt][0] == -INFINITY ? 0.f : -m[nt][0];
+        const float m1 = m[nt][1] == -INFINITY ? 0.f : -m[nt][1];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           float p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[e] = ex2(sc[nt][half][e] - ((e & 1) ? m1 : m0));
+          for (int e = 0; e < 4; ++e)
+            p[e] = ex2(fmaf(sc[nt][half][e], mul[nt][e & 1], (e & 1) ? m1 : m0));
           l[nt][0] += p[0] + p[2];
           l[nt][1] += p[1] + p[3];
           pf[nt][half][0] = movmatrix_t(half2_bits(__floats2half2_rn(p[0], p[1])));
@@ -570,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
         uint32_t vw[4][kWV], sb[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint8_t* vc = stp + St::kVC + keys[i] * (D / 2) + g * (D / 16);
+          const uint8_t* vc = vcodes + keys[i] * (D / 2) + g * (D / 16);
           if constexpr (D == 128) {
             const uint2 x = *reinterpret_cast<const uint2*>(vc);
             vw[i][0] = x.x;
@@ -578,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
           } else {
             vw[i][0] = *reinterpret_cast<const uint32_t*>(vc);
           }
-          sb[i] = stp[St::kVS + keys[i] * (D / kBlock) + (g * (D / 8)) / kBlock];
+          sb[i] = vscales[keys[i] * (D / kBlock) + (g * (D / 8)) / kBlock];
           // rows behind the sequence hold anything: 0, so that 0 * it is 0
           if (masked && key0 + keys[i] >= len) sb[i] = 0;
         }
@@ -610,8 +643,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
           }
         }
       }
+     }
       __syncwarp();  // the stage has been read
-      issue();
+      if (lane == 0) mbar_arrive(empty(st));
+      if (more) {
+        // the round after the next ones goes where this one was, once every
+        // warp is done with it
+        if (warp == issued % kWarps) {
+          ok = mbar_wait(empty(st), (used / kStages) & 1, abort_flag, &g_decode_kv4_status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        }
+        issue();
+      }
+      ++used;
     }
     // ------------------------------------------------- the unit's partial
     // O in the order (tile i, half, g): element 16 i + 8 half + g of a row is
@@ -658,9 +702,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kv4_kernel(c
     if (*abort_flag) break;
     if (!next_unit(P, cur)) break;
   }
-  // an aborted warp lets its copies in flight land before the CTA ends
-  if (lane == 0 && *abort_flag)
-    for (; used < issued; ++used) mbar_wait_drain(my_bar + 8 * (used % kStages), (used / kStages) & 1);
+  // aborted: the copies that this warp has in flight land before the CTA ends
+  if (lane == 0 && *abort_flag && mine >= 0)
+    mbar_wait_drain(full(mine % kStages), (mine / kStages) & 1);
 }
 
 // One block per (unit, 8 NT rows): the unit's partials, which are consecutive
@@ -801,7 +845,7 @@ usp_status_t launch_t(const Params& P, cudaStream_t st) {
   if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
   {
     ProfScope ps(st, "attn_decode_kv4");
-    decode_kv4_kernel<D, NT, SC><<<P.grid, kThreads, smem, st>>>(P);
+    decode_kv4_kernel<D, NT, SC><<<P.grid, Smem<D, NT>::kThreads, smem, st>>>(P);
   }
   note_launch();
   usp_status_t r = check_launch();
@@ -859,6 +903,7 @@ usp_status_t launch_decode_kv4(const DecodeKv4Args& a, void* workspace, cudaStre
   const int nt = tiles_for(P.R);
   P.nrb = (P.R + 8 * nt - 1) / (8 * nt);
   P.grid = nt == 1 ? kGridMax : kGridMax / 2;
+  P.warps = warps_for(nt);
   P.score_mul = a.scale * kLog2e * a.k_descale;
   P.v_descale = a.v_descale * 16.f;  // the kernel's V is 2^-4 of the cache's
   P.causal = a.causal;
