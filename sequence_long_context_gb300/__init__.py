@@ -623,12 +623,13 @@ def attn_decode_kv4(q: torch.Tensor, cache: KV4Cache, *, causal=True, window=0, 
     if accumulate and cache.key_weight is None:
         raise ValueError("accumulate needs a cache with key_weight")
     lib = _lib.load()
+    dev = q.device
     out = torch.empty_like(q)
-    lse = q.new_empty((B, Tq, Hq), dtype=_F32)
+    lse = torch.empty((B, Tq, Hq), dtype=_F32, device=dev)
     need = lib.usp_attn_decode_kv4_workspace_size(B, Tq, s.capacity, Hq, s.Hkv, D,
                                                   1 if accumulate else 0)
-    ws = q.new_empty(need, dtype=_U8) if workspace is None else \
-        _use_workspace(workspace, need, q.device)[0]
+    ws = torch.empty(need, dtype=_U8, device=dev) if workspace is None else \
+        _use_workspace(workspace, need, dev)[0]
     _call(lib.usp_attn_decode_kv4, at, stream, ctypes.addressof(s), q.data_ptr(), out.data_ptr(),
           lse.data_ptr(), Tq, Hq, softmax_scale, 1 if causal else 0, window, sink_tokens,
           1 if accumulate else 0, 0, ws.data_ptr(), ws.numel())
@@ -654,13 +655,13 @@ def attn_key_weights(q, k, lse, *, causal=True, window=0, sink_tokens=0, cu_seql
     if cu_seqlens is not None:
         _require(cu_seqlens, "cu_seqlens", _I32, (B + 1,), at, q)
     lib = _lib.load()
-    weight = q.new_empty(lead + (Hkv, S), dtype=_F32)
+    weight = torch.empty(lead + (Hkv, S), dtype=_F32, device=q.device)
     need = lib.usp_attn_key_weights_workspace_size(Bl, S, Hq, Hkv, observe, DTYPE[dt], flags)
     ws = workspace
     if ws is not None:
         ws = _use_workspace(ws, need, q.device)[0]
     elif need:
-        ws = q.new_empty(need, dtype=_U8)
+        ws = torch.empty(need, dtype=_U8, device=q.device)
     _call(lib.usp_attn_key_weights, at, stream, q.data_ptr(), k.data_ptr(), lse.data_ptr(),
           weight.data_ptr(), B, S, Hq, Hkv, D, softmax_scale, 1 if causal else 0, window,
           sink_tokens, None if cu_seqlens is None else cu_seqlens.data_ptr(), cp,
@@ -688,7 +689,7 @@ def kv4_evict(cache: KV4Cache, keep: int, *, recent=0, sink_tokens=0, out=None, 
             raise ValueError("both caches must be on one device")
         if (s.k_descale, s.v_descale) != (d.k_descale, d.v_descale):
             raise ValueError("both caches must have the same descales")
-    kept = cache.seq_lens.new_empty((s.B, s.Hkv, keep))
+    kept = torch.empty((s.B, s.Hkv, keep), dtype=_I32, device=cache.k.device)
     _call(_lib.load().usp_kv4_evict, at, stream, ctypes.addressof(s), ctypes.addressof(d),
           kept.data_ptr(), keep, recent, sink_tokens)
     return dst, kept

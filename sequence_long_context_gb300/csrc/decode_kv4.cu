@@ -65,8 +65,10 @@ __device__ int g_decode_kv4_status = 0;
 constexpr int kStep = 32;                 // keys per step
 constexpr int kGridMax = 304;             // 152 SMs x 2 resident CTAs
 // Up to eight query rows: two CTAs of eight warps per SM at 128 registers;
-// sixteen: one of ten at 200, with Q^T in shared memory.
-__host__ __device__ constexpr int warps_for(int nt) { return nt == 1 ? 8 : 10; }
+// sixteen: one CTA (with ten or twelve warps at 168 registers and Q^T in shared
+// memory it spills: 63 and 69 us instead of 51 for 4 x 32K keys and 12 rows).
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
 constexpr float kLazy = 8.f;              // the max moves when it grows by 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -78,10 +80,9 @@ struct Params {
   float* lse;
   float* o_part;    // [slots][8 NT][D], columns in the kernel's order
   float2* ml_part;  // [slots][8 NT]: (m, l) in log2 units
-  float* scores;    // accumulate: [B][H][C][Rs] log2-scaled scores, else nullptr
-  float2* ml;       // accumulate: [B][H][Rs] merged (m, 1 / l)
+  float2* scores;   // accumulate: [B][H][Rs / 2][C] log2-scaled scores of two rows
   int Tq, Hq, G, R, Rs, nrb;  // R = G Tq rows per KV head, nrb blocks of them
-  int grid, warps;
+  int grid;
   float score_mul;            // softmax scale * log2(e) * k_descale
   float v_descale;
   int causal, window, sink;
@@ -118,8 +119,17 @@ __device__ __forceinline__ long long total_steps_warp(const Params& P) {
   return n;
 }
 __device__ __forceinline__ long long active_ctas(const Params& P, long long T) {
-  const long long want = (T + P.warps - 1) / P.warps;
+  const long long want = (T + kWarps - 1) / kWarps;
   return want < P.grid ? want : P.grid;
+}
+
+// The launch of the dependent kernel may proceed; and, in that one: the kernel
+// before it has ended and its writes are visible.
+__device__ __forceinline__ void grid_dependency_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // A walk over the steps of a CTA's run: the current unit's steps [s, end).
@@ -153,8 +163,6 @@ __device__ __forceinline__ bool next_unit(const Params& P, Walk& w) {
 
 template <int D, int NT>
 struct Smem {
-  static constexpr int kWarps = warps_for(NT);
-  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kKeys = kWarps * kStep;  // of a round
   // a stage: one round's codes and scales
   static constexpr int kCodes = kKeys * D / 2, kScales = kKeys * D / kBlock;
@@ -164,12 +172,11 @@ struct Smem {
   static constexpr int kRedStride = D + 4;
   static constexpr int kRed = kStages * kStageBytes;              // [kWarps][8][D + 4]
   static constexpr int kML = kRed + kWarps * 8 * kRedStride * 4;  // [kWarps][8] float2
-  static constexpr int kQ = kML + kWarps * 8 * 8;                 // 16 rows: [D/16][NT][32] uint2
-  static constexpr int kBar = kQ + (NT == 1 ? 0 : D / 16 * NT * 32 * 8);
+  static constexpr int kBar = kML + kWarps * 8 * 8;
   static constexpr int kMisc = kBar + 2 * kStages * 8;            // abort, run
   static constexpr int kBytes = kMisc + 64;
   static_assert(kBytes <= (NT == 1 ? 113 : 227) * 1024, "residency");
-  static_assert(kRed % 16 == 0 && kML % 16 == 0 && kQ % 16 == 0 && kBar % 8 == 0 &&
+  static_assert(kRed % 16 == 0 && kML % 16 == 0 && kBar % 8 == 0 &&
                     kMisc % 16 == 0 && kStageBytes % 128 == 0,
                 "alignment");
   static_assert(kStages <= kWarps, "a warp has at most one round's copies in flight");
@@ -222,7 +229,7 @@ template <int D, int NT>
 __device__ __forceinline__ void load_round(const Params& P, const Walk& w, uint32_t stage,
                                            uint32_t bar) {
   using L = Smem<D, NT>;
-  const int s1 = min(w.s + L::kWarps, w.end), sp = min(max(w.q.sinks, w.s), s1);
+  const int s1 = min(w.s + kWarps, w.end), sp = min(max(w.q.sinks, w.s), s1);
   // rows of steps [a, e): whole 16-row groups that hold cached keys (the
   // capacity is a multiple of 16)
   auto rows_of = [&](int a, int e, int key0) {
@@ -245,10 +252,10 @@ __device__ __forceinline__ void load_round(const Params& P, const Walk& w, uint3
 }
 
 template <int D, int NT, bool SC>
-__global__ void __launch_bounds__(Smem<D, NT>::kThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 decode_kv4_kernel(const Params P) {
   using L = Smem<D, NT>;
-  constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kStages = L::kStages;
+  constexpr int kStages = L::kStages;
   constexpr int kRows = 8 * NT;
   constexpr int kWK = D / 32;      // 32-bit words of codes a thread has per K row
   constexpr int kWV = D / 64;      // and per V row
@@ -257,12 +264,12 @@ decode_kv4_kernel(const Params P) {
   const uint32_t sbase = smem_u32(sm);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kMisc);
   long long* run = reinterpret_cast<long long*>(sm + L::kMisc + 16);  // first step, count, ..
-  uint2* qs = reinterpret_cast<uint2*>(sm + L::kQ);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   auto full = [&](int st) { return sbase + L::kBar + 8 * st; };
   auto empty = [&](int st) { return sbase + L::kBar + 8 * (kStages + st); };
 
+  grid_dependency_launch();
   if (threadIdx.x == 32) {
     for (int st = 0; st < kStages; ++st) {
       mbar_init(full(st), 1);
@@ -357,8 +364,7 @@ decode_kv4_kernel(const Params P) {
     // Q^T fragments: product kk = 2w + jj takes channels (8w + 2jj, + 4) and
     // (8w + 2jj + 1, + 4) of the thread's run of D/4; qb: -8 times the run's
     // (its block's part's) sum in three parts
-    constexpr bool kQs = NT > 1;  // Q^T in shared memory, else in registers
-    uint32_t qf[kQs ? 1 : NT][kQs ? 1 : 2 * kWK][2], qb[NT][2];
+    uint32_t qf[NT][2 * kWK][2], qb[NT][2];
     float mul[NT][2];  // of rows 2t, 2t + 1: scores to log2 units
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -395,22 +401,14 @@ decode_kv4_kernel(const Params P) {
           f[2 * i + 1] = __uint_as_float(e[i] & 0xffff0000u) * up;
         }
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          uint32_t pr[2];
+        for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const __half2 p = __floats2half2_rn(f[2 * jj + i], f[2 * jj + i + 4]);
-            pr[i] = half2_bits(p);
+            qf[nt][2 * w + jj][i] = half2_bits(p);
             const float2 back = __half22float2(p);
             sum += back.x + back.y;
           }
-          if constexpr (kQs) {
-            if (warp == 0) qs[((2 * w + jj) * NT + nt) * 32 + lane] = make_uint2(pr[0], pr[1]);
-          } else {
-            qf[nt][2 * w + jj][0] = pr[0];
-            qf[nt][2 * w + jj][1] = pr[1];
-          }
-        }
       }
       sum *= -8.f;
       const __half hi = __float2half_rn(sum);
@@ -424,7 +422,6 @@ decode_kv4_kernel(const Params P) {
       for (int e = 0; e < 2; ++e)
         mul[nt][e] = __shfl_sync(0xffffffffu, row_mul, 4 * (2 * t + e));
     }
-    if constexpr (kQs) __syncthreads();
     float o[NT][kMT][4], ob[NT][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -498,14 +495,8 @@ decode_kv4_kernel(const Params P) {
           for (int jj = 0; jj < 2; ++jj) {
             const uint32_t a[4] = {p0[2 * jj], p1[2 * jj], p0[2 * jj + 1], p1[2 * jj + 1]};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (kQs) {
-                const uint2 q2 = qs[((2 * w + jj) * NT + nt) * 32 + lane];
-                mma_f16(sc[nt][half], a, q2.x, q2.y);
-              } else {
-                mma_f16(sc[nt][half], a, qf[nt][2 * w + jj][0], qf[nt][2 * w + jj][1]);
-              }
-            }
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(sc[nt][half], a, qf[nt][2 * w + jj][0], qf[nt][2 * w + jj][1]);
           }
         }
       }
@@ -537,7 +528,7 @@ decode_kv4_kernel(const Params P) {
         }
       if constexpr (SC) {
         // the weights need every score once the whole row's sum is known
-        float* dst = P.scores + head_row(P.c, b, h) * P.Rs;
+        float2* dst = P.scores + head_row(P.c, b, h) * (P.Rs / 2);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int r = rb * kRows + nt * 8 + 2 * t;
@@ -548,7 +539,7 @@ decode_kv4_kernel(const Params P) {
             for (int e = 0; e < 4; e += 2) {
               const int j = key0 + 16 * half + tile_key(g) + 8 * (e >> 1);
               if (j < len)
-                *reinterpret_cast<float2*>(dst + (long long)j * P.Rs + r) =
+                dst[(long long)(r / 2) * P.c.C + j] =
                     make_float2(sc[nt][half][e] * mul[nt][0], sc[nt][half][e + 1] * mul[nt][1]);
             }
         }
@@ -707,103 +698,164 @@ decode_kv4_kernel(const Params P) {
     mbar_wait_drain(full(mine % kStages), (mine / kStages) & 1);
 }
 
-// One block per (unit, 8 NT rows): the unit's partials, which are consecutive
-// slots, are merged in key order by blocks of D threads per part.
-template <int D, int NT>
-__global__ void __launch_bounds__(256) merge_kv4_kernel(const Params P) {
-  constexpr int kRows = 8 * NT;
-  constexpr int kParts = 256 / D;
-  __shared__ float s_o[kParts][D];
-  __shared__ float2 s_ml[kParts];
-  __shared__ long long s_n[2];
-  const int unit = blockIdx.x, r = blockIdx.y;  // r: row within the block
+// The slots of unit (b, hr)'s partials, given the steps of all sequences and
+// of those before b (per unit of a sequence).
+struct Slots {
+  long long first, last;
+};
+__device__ __forceinline__ Slots unit_slots(const Params& P, long long all, long long before, int b,
+                                            int hr) {
   const int per_seq = P.c.H * P.nrb;
-  const int b = unit / per_seq, hr = unit - b * per_seq;
-  const int h = hr / P.nrb, rb = hr - h * P.nrb;
-  const int row = rb * kRows + r;
-  if (row >= P.R) return;
-  if (threadIdx.x < 32) {
-    // steps of all sequences, and of those before b
-    long long all = 0, before = 0;
-    for (int i = threadIdx.x; i < P.c.B; i += 32) {
-      const long long n = seq_steps(P, seq_len(P, i)).n;
-      all += n;
-      if (i < b) before += n;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      all += __shfl_xor_sync(0xffffffffu, all, o);
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-    }
-    if (threadIdx.x == 0) {
-      const long long T = all * per_seq, N = active_ctas(P, T);
-      const long long n = seq_steps(P, seq_len(P, b)).n;
-      const long long a = before * per_seq + n * hr;
-      // CTA c holds step x iff c = ((x + 1) N - 1) / T
-      s_n[0] = n > 0 ? ((a + 1) * N - 1) / T : 0;
-      s_n[1] = n > 0 ? ((a + n) * N - 1) / T : -1;
-    }
+  const long long T = all * per_seq, N = active_ctas(P, T);
+  const long long n = seq_steps(P, seq_len(P, b)).n;
+  const long long a = before * per_seq + n * hr, unit = (long long)b * per_seq + hr;
+  if (n == 0) return {0, -1};
+  // CTA c holds step x iff c = ((x + 1) N - 1) / T
+  return {((a + 1) * N - 1) / T + unit, ((a + n) * N - 1) / T + unit};
+}
+// By one warp: those two sums.
+__device__ __forceinline__ void steps_before(const Params& P, int b, long long& all,
+                                             long long& before) {
+  all = before = 0;
+  for (int i = threadIdx.x & 31; i < P.c.B; i += 32) {
+    const long long n = seq_steps(P, seq_len(P, i)).n;
+    all += n;
+    if (i < b) before += n;
   }
-  __syncthreads();
-  const long long c0 = s_n[0] + unit, c1 = s_n[1] + unit;  // slots
-  const int part = threadIdx.x / D, d = threadIdx.x - part * D;
-  float M = -INFINITY, ls = 0.f, os = 0.f;
-  for (long long s = c0 + part; s <= c1; s += kParts) {
-    const float2 a = P.ml_part[s * kRows + r];
-    const float x = P.o_part[(s * kRows + r) * D + d];
-    const float Mn = fmaxf(M, a.x);
-    const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn);
-    const float f1 = a.x == -INFINITY ? 0.f : ex2(a.x - Mn);
-    os = os * f0 + x * f1;
-    ls = ls * f0 + a.y * f1;
-    M = Mn;
-  }
-  s_o[part][d] = os;
-  if (d == 0) s_ml[part] = make_float2(M, ls);
-  __syncthreads();
-  if (part != 0) return;
-  float Mt = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kParts; ++i) Mt = fmaxf(Mt, s_ml[i].x);
-  float lt = 0.f, ot = 0.f;
-#pragma unroll
-  for (int i = 0; i < kParts; ++i) {
-    const float f = s_ml[i].x == -INFINITY ? 0.f : ex2(s_ml[i].x - Mt);
-    lt += s_ml[i].y * f;
-    ot += s_o[i][d] * f;
-  }
-  const int hh = row / P.Tq, tok = row - hh * P.Tq;
-  const long long o_row = ((long long)b * P.Tq + tok) * P.Hq + h * P.G + hh;
-  const bool none = lt == 0.f;  // no visible key (a NaN score makes lt NaN)
-  const float inv = none ? 0.f : 1.f / lt;
-  const int i = d >> 4, half = (d >> 3) & 1, g = d & 7;
-  const int ch = g * (D / 8) + 8 * (i >> 2) + (i & 3) + 4 * half;
-  P.out[o_row * D + ch] = __float2bfloat16_rn(none ? 0.f : ot * inv * P.v_descale);
-  if (d == 0) {
-    P.lse[o_row] = none ? -INFINITY : (Mt + log2f(lt)) * kLn2;
-    if (P.ml) P.ml[((long long)b * P.c.H + h) * P.Rs + row] = make_float2(none ? 0.f : Mt, inv);
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
   }
 }
 
-// key_weight[j] += sum over the rows of 2^(score - m) / l.
-__global__ void __launch_bounds__(256) weight_kv4_kernel(const Params P) {
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int len = seq_len(P, b);
-  const SeqSteps q = seq_steps(P, len);
-  const long long head = head_row(P.c, b, h);
-  const float2* ml = P.ml + ((long long)b * P.c.H + h) * P.Rs;
-  for (long long x = blockIdx.x * 256ll + threadIdx.x; x < (long long)q.n * kStep;
-       x += (long long)gridDim.x * 256) {
-    const int s = (int)(x / kStep);
-    const int j = (s < q.sinks ? s : s + q.skip) * kStep + (int)(x % kStep);
-    if (j >= len) continue;
-    const float* sc = P.scores + (head + j) * P.Rs;
-    float w = 0.f;
-    for (int r = 0; r < P.R; ++r) {
-      const float2 a = __ldg(ml + r);
-      w += ex2(sc[r] - a.x) * a.y;
+constexpr int kMergeThreads = 256;
+constexpr int kMaxWeightRows = 64;  // (m, 1 / l) kept at a time
+
+// Block x < units * 8 NT: a row of a unit, whose partials (consecutive slots)
+// are merged in key order by D threads per part of them. Blocks behind those
+// (accumulate): a piece of the keys of a (sequence, KV head):
+//   key_weight[j] += sum over the rows of 2^(score - m) / l.
+// Launched while the kernel above still runs; nothing it writes is read before
+// the wait.
+template <int D, int NT, bool SC>
+__global__ void __launch_bounds__(kMergeThreads) merge_kv4_kernel(const Params P, int pieces) {
+  constexpr int kRows = 8 * NT;
+  constexpr int kParts = kMergeThreads / D;
+  __shared__ float s_o[kParts][D];
+  __shared__ float2 s_ml[SC && kMaxWeightRows > kParts ? kMaxWeightRows : kParts];
+  __shared__ long long s_n[2];
+  const int per_seq = P.c.H * P.nrb;
+  const int merges = P.c.B * per_seq * kRows;
+  if (!SC || (int)blockIdx.x < merges) {
+    const int unit = blockIdx.x / kRows, r = blockIdx.x % kRows;  // r: row within the block
+    const int b = unit / per_seq, hr = unit - b * per_seq;
+    const int h = hr / P.nrb, rb = hr - h * P.nrb;
+    const int row = rb * kRows + r;
+    if (row >= P.R) return;
+    if (threadIdx.x < 32) {
+      long long all, before;
+      steps_before(P, b, all, before);
+      if (threadIdx.x == 0) {
+        const Slots s = unit_slots(P, all, before, b, hr);
+        s_n[0] = s.first;
+        s_n[1] = s.last;
+      }
     }
-    P.c.w[head + j] += w;
+    __syncthreads();
+    grid_dependency_wait();
+    const int part = threadIdx.x / D, d = threadIdx.x - part * D;
+    float M = -INFINITY, ls = 0.f, os = 0.f;
+    for (long long s = s_n[0] + part; s <= s_n[1]; s += kParts) {
+      const float2 a = P.ml_part[s * kRows + r];
+      const float x = P.o_part[(s * kRows + r) * D + d];
+      const float Mn = fmaxf(M, a.x);
+      const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn);
+      const float f1 = a.x == -INFINITY ? 0.f : ex2(a.x - Mn);
+      os = os * f0 + x * f1;
+      ls = ls * f0 + a.y * f1;
+      M = Mn;
+    }
+    s_o[part][d] = os;
+    if (d == 0) s_ml[part] = make_float2(M, ls);
+    __syncthreads();
+    if (part != 0) return;
+    float Mt = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) Mt = fmaxf(Mt, s_ml[i].x);
+    float lt = 0.f, ot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      const float f = s_ml[i].x == -INFINITY ? 0.f : ex2(s_ml[i].x - Mt);
+      lt += s_ml[i].y * f;
+      ot += s_o[i][d] * f;
+    }
+    const int hh = row / P.Tq, tok = row - hh * P.Tq;
+    const long long o_row = ((long long)b * P.Tq + tok) * P.Hq + h * P.G + hh;
+    const bool none = lt == 0.f;  // no visible key (a NaN score makes lt NaN)
+    const float inv = none ? 0.f : 1.f / lt;
+    const int i = d >> 4, half = (d >> 3) & 1, g = d & 7;
+    const int ch = g * (D / 8) + 8 * (i >> 2) + (i & 3) + 4 * half;
+    P.out[o_row * D + ch] = __float2bfloat16_rn(none ? 0.f : ot * inv * P.v_descale);
+    if (d == 0) P.lse[o_row] = none ? -INFINITY : (Mt + log2f(lt)) * kLn2;
+    return;
+  }
+  if constexpr (SC) {
+    const int x = blockIdx.x - merges, piece = x % pieces, bh = x / pieces;
+    const int b = bh / P.c.H, h = bh - b * P.c.H;
+    __shared__ Slots s_slots[kMaxWeightRows / kRows];
+    long long all, before;
+    steps_before(P, b, all, before);  // (every warp)
+    const int len = seq_len(P, b);
+    const SeqSteps q = seq_steps(P, len);
+    const long long head = head_row(P.c, b, h);
+    const long long keys = (long long)q.n * kStep;
+    if ((long long)piece * kMergeThreads >= keys) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dependency_wait();
+    for (int r0 = 0; r0 < P.R; r0 += kMaxWeightRows) {
+      const int n = min(kMaxWeightRows, P.Rs - r0);
+      __syncthreads();
+      if (threadIdx.x < kMaxWeightRows / kRows && r0 / kRows + threadIdx.x < P.nrb)
+        s_slots[threadIdx.x] =
+            unit_slots(P, all, before, b, h * P.nrb + r0 / kRows + threadIdx.x);
+      __syncthreads();
+      for (int r = warp; r < n; r += kMergeThreads / 32) {  // a warp per row
+        const int rr = r % kRows;
+        const Slots s = s_slots[r / kRows];
+        float M = -INFINITY, l = 0.f;
+        for (long long i = s.first + lane; i <= s.last; i += 32)
+          M = fmaxf(M, P.ml_part[i * kRows + rr].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (long long i = s.first + lane; i <= s.last; i += 32) {
+          const float2 a = P.ml_part[i * kRows + rr];
+          l += a.y * (a.x == -INFINITY ? 0.f : ex2(a.x - M));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        const bool none = l == 0.f || r0 + r >= P.R;
+        if (lane == 0) s_ml[r] = make_float2(none ? 0.f : M, none ? 0.f : 1.f / l);
+      }
+      __syncthreads();
+      for (long long i = (long long)piece * kMergeThreads + threadIdx.x; i < keys;
+           i += (long long)pieces * kMergeThreads) {
+        const int s = (int)(i / kStep);
+        const int j = (s < q.sinks ? s : s + q.skip) * kStep + (int)(i % kStep);
+        if (j >= len) continue;
+        const float2* sc = P.scores + head * (P.Rs / 2) + (long long)(r0 / 2) * P.c.C + j;
+        float w = 0.f;
+#pragma unroll 4
+        for (int r = 0; r < n; r += 2) {
+          const float2 v = sc[(long long)(r / 2) * P.c.C];
+          const float2 a0 = s_ml[r], a1 = s_ml[r + 1];
+          w += ex2(v.x - a0.x) * a0.y;
+          // (the odd last row's partner was never written)
+          if (r0 + r + 1 < P.R) w += ex2(v.y - a1.x) * a1.y;
+        }
+        P.c.w[head + j] += w;
+      }
+    }
   }
 }
 
@@ -811,7 +863,7 @@ __global__ void __launch_bounds__(256) weight_kv4_kernel(const Params P) {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Ws {
-  size_t o, ml, scores, merged, total;
+  size_t o, ml, scores, total;
 };
 int tiles_for(int R) { return R <= 8 ? 1 : 2; }
 
@@ -830,8 +882,6 @@ Ws layout(int B, int Tq, int C, int Hq, int Hkv, int D, int accumulate) {
   if (accumulate) {
     w.scores = at;
     at += up256((size_t)B * Hkv * C * Rs * 4);
-    w.merged = at;
-    at += up256((size_t)B * Hkv * Rs * 8);
   }
   w.total = at;
   return w;
@@ -840,33 +890,45 @@ Ws layout(int B, int Tq, int C, int Hq, int Hkv, int D, int accumulate) {
 template <int D, int NT, bool SC>
 usp_status_t launch_t(const Params& P, cudaStream_t st) {
   const int smem = Smem<D, NT>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(decode_kv4_kernel<D, NT, SC>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemAttr attr;
+  cudaError_t e = attr.set(decode_kv4_kernel<D, NT, SC>, smem);
   if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
   {
     ProfScope ps(st, "attn_decode_kv4");
-    decode_kv4_kernel<D, NT, SC><<<P.grid, Smem<D, NT>::kThreads, smem, st>>>(P);
+    decode_kv4_kernel<D, NT, SC><<<P.grid, kThreads, smem, st>>>(P);
   }
   note_launch();
   usp_status_t r = check_launch();
   if (r != USP_OK) return r;
+  // the merge's launch and set-up overlap the end of the kernel before it
+  long long blocks = (long long)P.c.B * P.c.H * P.nrb * 8 * NT;
+  int pieces = 0;
+  if constexpr (SC) {
+    const int most = (P.c.C + kMergeThreads - 1) / kMergeThreads;
+    const int want = 152 * 4 / (P.c.B * P.c.H) + 1;  // half the GPU's warps, over the heads
+    pieces = most < want ? most : want;
+    blocks += (long long)P.c.B * P.c.H * pieces;
+  }
+  if (blocks > 0x7fffffffLL) return USP_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
   {
     ProfScope ps(st, "attn_decode_kv4_merge");
-    merge_kv4_kernel<D, NT><<<dim3(P.c.B * P.c.H * P.nrb, 8 * NT), 256, 0, st>>>(P);
+    e = cudaLaunchKernelEx(&cfg, merge_kv4_kernel<D, NT, SC>, P, pieces);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail_cuda("kernel launch", e);
   }
   note_launch();
-  if ((r = check_launch()) != USP_OK) return r;
-  if constexpr (SC) {
-    int bx = (P.c.C + 255) / 256;
-    const int cap = 152 * 16 / (P.c.B * P.c.H) + 1;
-    {
-      ProfScope ps(st, "attn_decode_kv4_weight");
-      weight_kv4_kernel<<<dim3(bx < cap ? bx : cap, P.c.H, P.c.B), 256, 0, st>>>(P);
-    }
-    note_launch();
-    r = check_launch();
-  }
-  return r;
+  return USP_OK;
 }
 
 template <int D>
@@ -892,8 +954,7 @@ usp_status_t launch_decode_kv4(const DecodeKv4Args& a, void* workspace, cudaStre
   P.o_part = reinterpret_cast<float*>(base + w.o);
   P.ml_part = reinterpret_cast<float2*>(base + w.ml);
   if (a.accumulate) {
-    P.scores = reinterpret_cast<float*>(base + w.scores);
-    P.ml = reinterpret_cast<float2*>(base + w.merged);
+    P.scores = reinterpret_cast<float2*>(base + w.scores);
   }
   P.Tq = a.Tq;
   P.Hq = a.Hq;
@@ -903,7 +964,6 @@ usp_status_t launch_decode_kv4(const DecodeKv4Args& a, void* workspace, cudaStre
   const int nt = tiles_for(P.R);
   P.nrb = (P.R + 8 * nt - 1) / (8 * nt);
   P.grid = nt == 1 ? kGridMax : kGridMax / 2;
-  P.warps = warps_for(nt);
   P.score_mul = a.scale * kLog2e * a.k_descale;
   P.v_descale = a.v_descale * 16.f;  // the kernel's V is 2^-4 of the cache's
   P.causal = a.causal;

@@ -44,6 +44,7 @@
 #include <cstdio>
 
 #include "internal.h"
+#include "kv4_host.h"
 #include "tc_ptx.cuh"
 #include "tile_sched.cuh"
 
@@ -808,8 +809,8 @@ usp_status_t launch_tc(const WeightParams& W, cudaStream_t st) {
   if (!make_map(&mq, P.q, P.Bt, P.S, P.Hq, D, 64) || !make_map(&mk, P.k, P.Bt, P.S, P.Hkv, D, kTile))
     return USP_ERR_CUDA;
   const int smem = L::kAlloc;
-  cudaError_t e = cudaFuncSetAttribute(key_weights_tc_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemAttr attr;
+  cudaError_t e = attr.set(key_weights_tc_kernel<D>, smem);
   if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
   const int blocks = W.items < kCtas ? W.items : kCtas;
   {

@@ -393,9 +393,8 @@ usp_status_t launch_d(const EvictParams& P, cudaStream_t st) {
   const int per = ((P.src.C + P.cluster * kWarps - 1) / (P.cluster * kWarps) + 127) / 128 * 128;
   const int n = per * kWarps <= kKeysInSmem ? per * kWarps : kKeysInSmem;
   const size_t smem = sizeof(EvictSmem) + (size_t)n * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(sizeof(EvictSmem) + kKeysInSmem * 4));
+  static SmemAttr smem_attr;
+  cudaError_t e = smem_attr.set(evict_kernel<D>, (int)(sizeof(EvictSmem) + kKeysInSmem * 4));
   if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(P.cluster, P.src.H, P.src.B);

@@ -3,10 +3,29 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "../../include/usp.h"
 #include "kv4.cuh"
 
 namespace usp {
+
+// A kernel's limit of dynamic shared memory, set once per device (the call
+// takes about a microsecond).
+struct SmemAttr {
+  std::atomic<unsigned long long> done{0};
+  template <typename K>
+  cudaError_t set(K kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 // kv4_cache.cu
 usp_status_t launch_kv4_append(const kv4::Cache& c, int D, const void* k, const void* v,
