@@ -4,9 +4,11 @@
 // contiguous part of the head's weights, brings it into shared memory once as
 // order-preserving 32-bit keys, and the cluster finds the n-th largest key by
 // three radix passes (11, 11 and 10 bits): each CTA counts its part into its
-// own histogram, and after one cluster barrier every CTA adds up the
-// cluster's histograms through distributed shared memory and scans them, so
-// that all reach the same bin with no further exchange. One more barrier
+// own histogram, also in groups of 32 bins; after one cluster barrier every CTA
+// adds up the cluster's groups through distributed shared memory, and then the
+// bins of the one group that matters (3 KB read from the others; all of their
+// histograms would be 64 KB), so that all reach the same bin with no further
+// exchange. One more barrier
 // gives every CTA how many keys are kept before its part, and it writes their
 // rows in ascending order; after another the cluster copies the kept rows'
 // codes, scales and weights.
@@ -16,6 +18,8 @@
 // the copy goes in rounds: every row of a round is in registers before a
 // barrier, and written after it; later rounds read behind every row that
 // earlier ones write.
+#include <type_traits>
+
 #include "internal.h"
 #include "kv4.cuh"
 #include "kv4_host.h"
@@ -59,17 +63,6 @@ __device__ __forceinline__ uint32_t peer_load(const uint32_t* p, uint32_t rank) 
   return v;
 }
 
-__device__ __forceinline__ uint4 peer_load4(const uint32_t* p, uint32_t rank) {
-  uint32_t a;
-  uint4 v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
-
 struct EvictParams {
   Cache src, dst;
   int* kept;
@@ -78,65 +71,58 @@ struct EvictParams {
   int cluster;  // CTAs per (sequence, KV head)
 };
 
+constexpr int kGroups = kBins / 32;
 struct __align__(16) EvictSmem {
   uint32_t hist[3][kBins];
-  uint32_t scan[kWarps];
+  uint32_t groups[3][kGroups];          // sums of 32 bins
+  uint32_t sums[kGroups];               // of the cluster
   uint32_t above[kWarps], tie[kWarps];  // of each warp's part
   uint32_t total[2];                    // kept for sure and ties of this CTA
-  uint32_t bin, left;
 };
 
-// Adds the cluster's histograms, and finds the bin (from the top) in which the
-// need-th key lies and how many of the bin are needed: s.bin, s.left.
-__device__ __forceinline__ void find_bin(EvictSmem& s, int pass, int cluster, uint32_t need) {
-  // thread t owns the kOwn bins from kBins - 1 - kOwn t downwards
-  constexpr int kOwn = kBins / kThreads;
-  static_assert(kOwn == 4, "one vector per peer");
-  const int b0 = kBins - 1 - kOwn * threadIdx.x;
-  uint4 peer[kMaxCluster];  // all on their way before the first is needed
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    peer[r] = r < cluster ? peer_load4(&s.hist[pass][b0 - 3], r) : make_uint4(0, 0, 0, 0);
-  uint32_t n[kOwn] = {}, mine = 0;
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r) {
-    n[0] += peer[r].w;
-    n[1] += peer[r].z;
-    n[2] += peer[r].y;
-    n[3] += peer[r].x;
-  }
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i) mine += n[i];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t inc = mine;
+// Of 32 counts, lane l's being that of item 31 - l: which item holds the
+// need-th one from the top; leaves in `need` how many of that item are needed.
+__device__ __forceinline__ int item_of(uint32_t count, uint32_t& need) {
+  const int lane = threadIdx.x & 31;
+  uint32_t inc = count;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
-  if (lane == 31) s.scan[warp] = inc;
-  __syncthreads();
-  uint32_t before = 0;
-  {
-    const uint32_t x = lane < kWarps ? s.scan[lane] : 0u;
-    uint32_t y = x;
+  const int l = __ffs(__ballot_sync(0xffffffffu, inc >= need)) - 1;
+  need -= __shfl_sync(0xffffffffu, inc - count, l);
+  return 31 - l;
+}
+
+// The bin (from the top) in which the cluster's need-th key lies; `need`
+// becomes how many of the bin are needed. Every warp finds it for itself.
+__device__ __forceinline__ uint32_t find_bin(EvictSmem& s, int pass, int cluster, uint32_t& need) {
+  const int lane = threadIdx.x & 31;
+  const int item = threadIdx.x >> 3, r = threadIdx.x & 7;  // eight lanes: one per CTA
+  static_assert(kThreads == 8 * kGroups && kMaxCluster == 8, "a group per eight threads");
+  uint32_t x = r < cluster ? peer_load(&s.groups[pass][item], r) : 0u;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += z;
-    }
-    before = __shfl_sync(0xffffffffu, y - x, warp);
-  }
-  uint32_t above = before + inc - mine;  // keys in higher bins than b0
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    if (above < need && need <= above + n[i]) {
-      s.bin = b0 - i;
-      s.left = need - above;
-    }
-    above += n[i];
+  for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (r == 0) s.sums[item] = x;
+  __syncthreads();
+  const uint32_t hi = s.sums[kGroups - 1 - 2 * lane], lo = s.sums[kGroups - 2 - 2 * lane];
+  const int pair = item_of(hi + lo, need);  // groups 2 pair + 1 and 2 pair
+  const uint32_t top = __shfl_sync(0xffffffffu, hi, 31 - pair);
+  int group = 2 * pair + 1;
+  if (need > top) {
+    need -= top;
+    group = 2 * pair;
   }
   __syncthreads();
+  if (item < 32) {  // (whole warps)
+    x = r < cluster ? peer_load(&s.hist[pass][32 * group + item], r) : 0u;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (r == 0) s.sums[item] = x;
+  }
+  __syncthreads();
+  return 32 * group + item_of(s.sums[31 - lane], need);
 }
 
 template <int D>
@@ -194,63 +180,77 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
 #pragma unroll
       for (int pass = 0; pass < 3; ++pass) {
         const uint32_t bin_mask = pass == 2 ? 1023u : 2047u;
-#pragma unroll 2
-        for (int i0 = c_lo / 128 * 128; i0 < c_hi; i0 += 128) {
-          const int i = i0 + 4 * lane;
-          uint32_t key[4] = {0, 0, 0, 0};
-          uint32_t bin[4];
-          if (i < c_hi) {
-            const uint4 k = keys_at(i);
-            key[0] = k.x; key[1] = k.y; key[2] = k.z; key[3] = k.w;
-          }
-          bool in[4], alike = true;
+        // several keys per lane at a time, so that their latencies overlap
+        auto count = [&](auto vectors, int i0) {
+          constexpr int kV = decltype(vectors)::value, kN = 4 * kV;
+          uint32_t key[kN];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            in[e] = i + e >= c_lo && i + e < c_hi && (key[e] & kMask[pass]) == prefix;
-            bin[e] = (key[e] >> kShift[pass]) & bin_mask;
-            alike = alike && in[e] && bin[e] == bin[0];
+          for (int u = 0; u < kV; ++u) {
+            const int i = i0 + 128 * u + 4 * lane;
+            uint4 k = make_uint4(0, 0, 0, 0);
+            if (i < c_hi) k = keys_at(i);
+            key[4 * u] = k.x; key[4 * u + 1] = k.y; key[4 * u + 2] = k.z; key[4 * u + 3] = k.w;
           }
-          // one addition where a whole warp agrees (runs of equal weights)
-          int same;
-          __match_all_sync(0xffffffffu, alike ? bin[0] : 0x80000000u + lane, &same);
-          if (same) {
-            if (lane == 0) atomicAdd(&s.hist[pass][bin[0]], 128u);
+          uint32_t in = 0;
+          bool alike = true;
+#pragma unroll
+          for (int e = 0; e < kN; ++e) {
+            const int i = i0 + 128 * (e >> 2) + 4 * lane + (e & 3);
+            if (i >= c_lo && i < c_hi && (key[e] & kMask[pass]) == prefix) in |= 1u << e;
+            key[e] = (key[e] >> kShift[pass]) & bin_mask;
+            alike = alike && key[e] == key[0];
+          }
+          // one addition where the whole warp agrees (runs of equal weights)
+          if (__all_sync(0xffffffffu, alike && in == (1u << kN) - 1u) &&
+              __all_sync(0xffffffffu, key[0] == __shfl_sync(0xffffffffu, key[0], 0))) {
+            if (lane == 0) atomicAdd(&s.hist[pass][key[0]], 32u * kN);
           } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (in[e]) atomicAdd(&s.hist[pass][bin[e]], 1u);
+            for (int e = 0; e < kN; ++e)
+              if ((in >> e) & 1u) atomicAdd(&s.hist[pass][key[e]], 1u);
           }
+        };
+        int i0 = c_lo / 128 * 128;
+        for (; i0 + 384 < c_hi; i0 += 512) count(std::integral_constant<int, 4>{}, i0);
+        for (; i0 < c_hi; i0 += 128) count(std::integral_constant<int, 1>{}, i0);
+        __syncthreads();
+        {
+          const uint4 x = reinterpret_cast<const uint4*>(s.hist[pass])[threadIdx.x];
+          uint32_t sum = x.x + x.y + x.z + x.w;
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if ((threadIdx.x & 7) == 0) s.groups[pass][threadIdx.x >> 3] = sum;
         }
         cluster_sync();
-        find_bin(s, pass, P.cluster, need);
-        prefix |= s.bin << kShift[pass];
-        need = s.left;
+        prefix |= find_bin(s, pass, P.cluster, need) << kShift[pass];
       }
     }
     const bool any = P.keep - P.sink - P.recent > 0;
-    // of keys i .. i + 3: kept for sure (sinks, recent, above the n-th largest:
-    // bits 0-3) and equal to it (bits 4-7)
-    auto flags_at = [&](int i) {
-      uint32_t f = 0;
-      if (i >= n) return f;
-      uint4 k = make_uint4(0, 0, 0, 0);
-      if (any) k = keys_at(i);
-      const uint32_t key[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (i + e >= n) continue;
-        const bool fixed = i + e < c_lo || i + e >= c_hi;
-        if (fixed || (any && key[e] > prefix)) f |= 1u << e;
-        else if (any && key[e] == prefix) f |= 16u << e;
+    // Of the 32 rows of 32 keys from i0 on, lane l gets row l's: kept for sure
+    // (sinks, recent, above the n-th largest), and equal to it.
+    auto masks_at = [&](int i0, uint32_t& sure, uint32_t& tied) {
+      sure = tied = 0;
+      const int rows = min(32, (n - i0 + 31) / 32);
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) {
+        const int i = i0 + 32 * r + lane;
+        uint32_t key = 0;
+        if (any && i < n) key = in_smem ? mine[i] : order_key(__ldg(w + first + i));
+        const bool fixed = i < n && (i < c_lo || i >= c_hi);
+        const bool free = i >= c_lo && i < c_hi && any;
+        const uint32_t a = __ballot_sync(0xffffffffu, fixed || (free && key > prefix));
+        const uint32_t t = __ballot_sync(0xffffffffu, free && key == prefix);
+        if (lane == r) {
+          sure = a;
+          tied = t;
+        }
       }
-      return f;
     };
-    uint32_t above = 0, tie = 0;
-#pragma unroll 2
-    for (int i = 4 * lane; i < n; i += 128) {
-      const uint32_t f = flags_at(i);
-      above += __popc(f & 15u);
-      tie += __popc(f >> 4);
+    uint32_t above = 0, tie = 0, sure = 0, tied = 0;
+    for (int i0 = 0; i0 < n; i0 += 1024) {
+      masks_at(i0, sure, tied);
+      above += __popc(sure);
+      tie += __popc(tied);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -295,38 +295,40 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
       a_before += x;
       t_before += y;
     }
-    for (int i0 = 0; i0 < n; i0 += 128) {
-      const int i = i0 + 4 * lane;
-      const uint32_t f = flags_at(i);
-      const uint32_t own = __popc(f & 15u) + (__popc(f >> 4) << 16);
-      uint32_t inc = own;  // at most 128 each
+    for (int i0 = 0; i0 < n; i0 += 1024) {
+      if (n > 1024) masks_at(i0, sure, tied);  // (else they are still there)
+      uint32_t ai = __popc(sure), ti = __popc(tied);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+        const uint32_t ao = __shfl_up_sync(0xffffffffu, ai, o);
+        const uint32_t to = __shfl_up_sync(0xffffffffu, ti, o);
+        if (lane >= o) {
+          ai += ao;
+          ti += to;
+        }
       }
-      const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);
-      uint32_t a = a_before + ((inc - own) & 0xffffu), t = t_before + ((inc - own) >> 16);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool tied = (f >> (4 + e)) & 1u;
-        // the first `need` ties are kept
-        const uint32_t at = a + min(t, need);
-        if ((((f >> e) & 1u) || (tied && t < need)) && at < (uint32_t)P.keep)
-          kept[at] = (int)(first + i + e);
-        a += (f >> e) & 1u;
-        t += tied;
+      uint32_t a = a_before + ai - __popc(sure), t = t_before + ti - __popc(tied);
+      a_before += __shfl_sync(0xffffffffu, ai, 31);
+      t_before += __shfl_sync(0xffffffffu, ti, 31);
+      // the lane's keys that may be kept, from the first on
+      for (uint32_t left = sure | tied; left != 0; left &= left - 1) {
+        const int bit = __ffs(left) - 1;
+        const bool tie_bit = (tied >> bit) & 1u;
+        const uint32_t at = a + min(t, need);  // the first `need` ties are kept
+        if ((!tie_bit || t < need) && at < (uint32_t)P.keep)
+          kept[at] = (int)(first + i0 + 32 * lane + bit);
+        a += !tie_bit;
+        t += tie_bit;
       }
-      a_before += all & 0xffffu;
-      t_before += all >> 16;
     }
   }
   cluster_sync();  // the list is complete; no CTA needs another's memory any more
 
   // ------------------------------------------------------------------ move
   constexpr int kChunks = D / 16;  // 16-byte pieces of a row's K and V codes
-  constexpr int kPer = 4;          // pieces in a thread's registers
-  constexpr int kRows = kThreads * kPer / kChunks;  // rows per CTA and round
+  constexpr int kPer = D / 16;     // pieces in a thread's registers: 512 rows per CTA and round
+  constexpr int kRows = kThreads * kPer / kChunks;
+  static_assert(kRows == kThreads, "a row per thread");
   const int c = threadIdx.x % kChunks;
   const uint8_t* from_codes = (c < kChunks / 2 ? P.src.kc : P.src.vc) + (c % (kChunks / 2)) * 16;
   uint8_t* to_codes = (c < kChunks / 2 ? P.dst.kc : P.dst.vc) + (c % (kChunks / 2)) * 16;
