@@ -62,8 +62,12 @@ constexpr int kSoftWarps = 8 * kKT; // two groups of four per key tile
 constexpr int kProducerWarp = kSoftWarps;
 constexpr int kMmaWarp = kProducerWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + kKT);
-constexpr int kSlots = 3;           // Q tiles
-constexpr int kKSlots = 3;          // K tiles
+// Tiles of K and Q in shared memory: three each, or four of K and two of Q
+// where an item has no more than two query tiles (its loads are what counts
+// then, and the next item's keys wait for no slot).
+constexpr int kTileSlots = 6;
+constexpr int kSlots = 3;           // Q tiles, at most
+constexpr int kKSlots = 4;          // K tiles, at most
 constexpr int kSBufs = 4;           // score buffers of 128 columns
 constexpr int kRing = 16;           // entries of query statistics
 constexpr int kCtas = 152;          // one per SM
@@ -93,6 +97,8 @@ struct WeightParams {
   int q0;        // first row of tile 0: where the observed rows begin, if they
                  // are one run to the end; else 0
   int ntiles;    // query tiles
+  int pair;      // 2: one tile of at most 64 rows, two heads share the 128; else 1
+  int qslots, kslots;
   int items;
 };
 
@@ -107,9 +113,8 @@ struct WSmem {
   static constexpr int kHalves = D / 64;
   static constexpr int kHalf = kTile * 128;             // 64 channels of a K or Q tile
   static constexpr int kTileBytes = kHalf * kHalves;
-  static constexpr int kK = 0;                          // kKSlots
-  static constexpr int kQ = kK + kKSlots * kTileBytes;  // kSlots
-  static constexpr int kStat = kQ + kSlots * kTileBytes;  // kRing x (-lse2[128], pos[128])
+  static constexpr int kK = 0;                          // kslots tiles of K, then Q
+  static constexpr int kStat = kTileSlots * kTileBytes;  // kRing x (-lse2[128], pos[128])
   static constexpr int kStatBytes = 2 * kQT * 4;
   static constexpr int kJoin = kStat + kRing * kStatBytes;  // [2][kKeys] sums of group 1
   static constexpr int kSched = kJoin + 2 * kKeys * 4;  // kRing ints: class | rows << 8
@@ -140,16 +145,24 @@ __device__ __forceinline__ ItemPos item_pos(const WeightParams& W, int item) {
   // key blocks outermost: with a causal mask the heaviest (first) start first
   const int groups = P.G / W.hpi;  // items per KV head, key block and segment
   ItemPos r;
-  r.part = item % (groups * W.nseg);
-  item /= groups * W.nseg;
-  r.g = item % P.Hkv;
-  item /= P.Hkv;
-  r.bt = item % P.Bt;
+  r.part = r.g = r.bt = 0;
+  if (groups * W.nseg > 1) {
+    r.part = item % (groups * W.nseg);
+    item /= groups * W.nseg;
+  }
+  if (P.Hkv > 1) {
+    r.g = item % P.Hkv;
+    item /= P.Hkv;
+  }
+  if (P.Bt > 1) {
+    r.bt = item % P.Bt;
+    item /= P.Bt;
+  }
   // ... in natural order, where a block of keys is one
-  r.key0 = item / P.Bt * kKeys;
+  r.key0 = item * kKeys;
   if (P.layout == kZigzag && P.chunk % kKeys == 0) r.key0 = permuted_of(P, r.key0);
   r.seg = r.part / groups;
-  r.h0 = r.g * P.G + (r.part % groups) * W.hpi;
+  r.h0 = r.g * P.G + (r.part - r.seg * groups) * W.hpi;
   r.ktiles = min(kKT, (P.S - r.key0 + kTile - 1) / kTile);  // with keys in them
   return r;
 }
@@ -191,15 +204,15 @@ __device__ __forceinline__ PosRange row_bounds(const AttnParams& P, int p0, int 
   PosRange r{1, 0};
   const int p1 = min(p0 + n, P.S) - 1;
   if (p1 < p0) return r;
+  if (P.layout == kContiguous) {
+    r.lo = p0;
+    r.hi = p1;
+    return r;
+  }
   const int run = P.layout == kZigzag ? P.chunk : P.shard;
   if (p0 / run == p1 / run) {
     r.lo = nat_pos(P, p0);
     r.hi = nat_pos(P, p1);
-    return r;
-  }
-  if (P.layout == kContiguous) {
-    r.lo = p0;
-    r.hi = p1;
     return r;
   }
   r.lo = P.S;
@@ -281,6 +294,8 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
   int* status = &g_key_weights_status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qslots = W.qslots, kslots = W.kslots;
+  const uint32_t q_at = sbase + kslots * L::kTileBytes;  // the Q tiles
 
   if (warp == kProducerWarp && lane == 0) {
     for (int s = 0; s < kKSlots; ++s) {
@@ -349,14 +364,14 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
       }
       if (lane == 0) {
-        record[it & 1].count = end ? kEnd : tiles * W.hpi;
+        record[it & 1].count = end ? kEnd : tiles * (W.hpi / W.pair);
         record[it & 1].item = item;
         mbar_arrive(bar(L::kItemFull + (it & 1)));
       }
       if (end) break;
       if (tiles == 0) continue;
       for (int a = 0; a < ip.ktiles; ++a) {
-        if (kn >= kKSlots) {  // the slot's previous keys have been multiplied
+        if (kn >= kslots) {  // the slot's previous keys have been multiplied
           ok = mbar_wait(bar(L::kKFree + kslot), kphase, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
         }
@@ -367,7 +382,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
                         bar(L::kKFull + kslot), hf * 64, ip.g, ip.key0 + a * kTile, ip.bt);
         }
         ++kn;
-        if (++kslot == kKSlots) {
+        if (++kslot == kslots) {
           kslot = 0;
           kphase ^= 1;
         }
@@ -396,7 +411,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
             lo_mine = -1;
             if (cls_mine != kClsEmpty && (W.observe == 0 || P.cu == nullptr)) {
               const int p0 = W.q0 + t * kQT, p1 = min(p0 + kQT, P.S) - 1;
-              if (p0 / run == p1 / run || P.layout == kContiguous) lo_mine = nat_pos(P, p0);
+              if (P.layout == kContiguous || p0 / run == p1 / run) lo_mine = nat_pos(P, p0);
             }
           }
           if (todo == 0) {
@@ -410,7 +425,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           const int lo = __shfl_sync(0xffffffffu, lo_mine, src);
 #pragma unroll
           for (int e = 0; e < kQT / 32; ++e) {
-            const int r = lane + 32 * e;
+            const int r = W.pair == 2 ? lane + 32 * (e & 1) : lane + 32 * e;
             if (lo >= 0) {
               const int i = lo + r * step;
               nx.pos[e] = nx.row + r < P.S && i >= from ? i : kNowhere;
@@ -422,18 +437,22 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
         nx.h = ip.h0 + hh;
         const float* src_lse = lse_head + hh * P.lse_sh + nx.row + lane;
 #pragma unroll
-        for (int e = 0; e < kQT / 32; ++e) nx.lse[e] = nx.pos[e] >= 0 ? __ldg(src_lse + 32 * e) : 0.f;
-        if (++hh == W.hpi) hh = 0;
+        for (int e = 0; e < kQT / 32; ++e) {
+          const float* at = W.pair == 2 ? src_lse + (e >> 1) * P.lse_sh + 32 * (e & 1) : src_lse + 32 * e;
+          nx.lse[e] = nx.pos[e] >= 0 ? __ldg(at) : 0.f;
+        }
+        hh += W.pair;
+        if (hh == W.hpi) hh = 0;
       };
       fetch();
       while (more) {
         const Next cur = nx;
         fetch();  // its loads are on their way during this tile's waits
-        if (n >= kSlots) {  // the slot's previous tile has been multiplied
+        if (n >= qslots) {  // the slot's previous tile has been multiplied
           ok = mbar_wait(bar(L::kQFree + slot), phase, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
         }
-        const int ring = n & (kRing - 1), rows = min(kQT, P.S - cur.row);
+        const int ring = n & (kRing - 1), rows = W.pair == 2 ? kQT : min(kQT, P.S - cur.row);
         float* st = reinterpret_cast<float*>(sm + L::kStat + ring * L::kStatBytes);
 #pragma unroll
         for (int e = 0; e < kQT / 32; ++e) {
@@ -451,11 +470,13 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           mbar_expect_tx(bar(L::kQFull + slot), L::kTileBytes / 2 * boxes);
           for (int r = 0; r < boxes; ++r)
             for (int hf = 0; hf < L::kHalves; ++hf)
-              tma_load_4d(sbase + L::kQ + slot * L::kTileBytes + hf * L::kHalf + r * (L::kHalf / 2),
-                          &tm_q, bar(L::kQFull + slot), hf * 64, cur.h, cur.row + 64 * r, ip.bt);
+              tma_load_4d(q_at + slot * L::kTileBytes + hf * L::kHalf + r * (L::kHalf / 2),
+                          &tm_q, bar(L::kQFull + slot), hf * 64,
+                          W.pair == 2 ? cur.h + r : cur.h, W.pair == 2 ? cur.row : cur.row + 64 * r,
+                          ip.bt);
         }
         ++n;
-        if (++slot == kSlots) {
+        if (++slot == qslots) {
           slot = 0;
           phase ^= 1;
         }
@@ -463,10 +484,10 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     }
     // aborted: the copies in flight land before the CTA ends
     if (lane == 0 && *abort_flag) {
-      for (int i = n > kSlots ? n - kSlots : 0; i < n; ++i)
-        mbar_wait_drain(bar(L::kQFull + i % kSlots), (i / kSlots) & 1);
-      for (int i = kn > kKSlots ? kn - kKSlots : 0; i < kn; ++i)
-        mbar_wait_drain(bar(L::kKFull + i % kKSlots), (i / kKSlots) & 1);
+      for (int i = n > qslots ? n - qslots : 0; i < n; ++i)
+        mbar_wait_drain(bar(L::kQFull + i % qslots), (i / qslots) & 1);
+      for (int i = kn > kslots ? kn - kslots : 0; i < kn; ++i)
+        mbar_wait_drain(bar(L::kKFull + i % kslots), (i / kslots) & 1);
     }
   } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------ MMA issuers
@@ -477,7 +498,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     constexpr uint32_t kId128 = idesc_bf16_f32(kTile, 128, 0, 0);
     constexpr uint32_t kId64 = idesc_bf16_f32(kTile, 64, 0, 0);
     const uint64_t dk = sdesc_sw128(sbase + L::kK, 16, 1024);
-    const uint64_t dq = sdesc_sw128(sbase + L::kQ, 16, 1024);
+    const uint64_t dq = sdesc_sw128(q_at, 16, 1024);
     const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
     const int a = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);  // key tile
     bool ok = true;
@@ -495,8 +516,8 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
         const int rows = __shfl_sync(0xffffffffu, sched[n & (kRing - 1)], 0) >> 8;
         const uint32_t id = rows > 64 ? kId128 : kId64;
         if (a < ktiles) {
-          const int ks = (kn + a) % kKSlots, sj = si + j * ktiles + a, buf = sj % kSBufs;
-          if (j == 0) ok = mbar_wait(bar(L::kKFull + ks), ((kn + a) / kKSlots) & 1, abort_flag, status);
+          const int ks = (kn + a) % kslots, sj = si + j * ktiles + a, buf = sj % kSBufs;
+          if (j == 0) ok = mbar_wait(bar(L::kKFull + ks), ((kn + a) / kslots) & 1, abort_flag, status);
           // the buffer's previous scores have been taken out
           if (ok && sj >= kSBufs)
             ok = mbar_wait(bar(L::kSFree + buf), (sj / kSBufs - 1) & 1, abort_flag, status);
@@ -519,7 +540,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           mbar_arrive(bar(L::kQFree + slot));  // no such key tile
         }
         __syncwarp();
-        if (++slot == kSlots) {
+        if (++slot == qslots) {
           slot = 0;
           phase ^= 1;
         }
@@ -771,7 +792,9 @@ struct Cut {
   int hpi, nseg, tps, nkb, q0, ntiles, parts;
 };
 // tail: the observed queries are the last rows (natural order, one sequence).
-Cut cut_of(int B, int S, int Hq, int Hkv, int observe, bool tail) {
+// packed: a key block meets the queries of its own sequences alone, so the
+// queries are not cut.
+Cut cut_of(int B, int S, int Hq, int Hkv, int observe, bool tail, bool packed) {
   Cut c{};
   const int G = Hq / Hkv;
   if (observe >= S) observe = 0;
@@ -788,7 +811,7 @@ Cut cut_of(int B, int S, int Hq, int Hkv, int observe, bool tail) {
   if (blocks < want && tiles >= 8) {  // (each item loads its keys anew)
     c.hpi = 1;
     const long long have = blocks * G;
-    if (have < want && observe == 0) {
+    if (have < want && observe == 0 && !packed) {
       long long n = (want + have - 1) / have;
       const long long most = (tiles + 15) / 16;  // at least 16 query tiles each
       if (n > most) n = most;
@@ -824,15 +847,21 @@ usp_status_t launch_tc(const WeightParams& W, cudaStream_t st) {
 }  // namespace
 
 size_t key_weights_workspace(int B, int S, int Hq, int Hkv, int observe) {
-  const Cut c = cut_of(B, S, Hq, Hkv, observe, false);  // (parts do not depend on `tail`)
+  const Cut c = cut_of(B, S, Hq, Hkv, observe, false, false);  // (no more parts if `tail` or packed)
   return c.parts > 1 ? (size_t)c.parts * B * Hkv * S * 4 : 0;
 }
 
 usp_status_t launch_key_weights_tc(const AttnParams& P, float* weight, int observe,
                                    void* workspace, cudaStream_t st) {
-  const Cut c = cut_of(P.Bt, P.S, P.Hq, P.Hkv, observe, P.layout == kContiguous && !P.cu);
+  const Cut c = cut_of(P.Bt, P.S, P.Hq, P.Hkv, observe, P.layout == kContiguous && !P.cu,
+                       P.cu != nullptr);
   WeightParams W{P, c.parts > 1 ? static_cast<float*>(workspace) : weight,
-                 observe < P.S ? observe : 0, c.hpi, c.nseg, c.tps, c.nkb, c.q0, c.ntiles, 0};
+                 observe < P.S ? observe : 0, c.hpi, c.nseg, c.tps, c.nkb, c.q0, c.ntiles, 1, 3, 3, 0};
+  if (c.ntiles == 1 && P.S - c.q0 <= 64 && c.hpi % 2 == 0) W.pair = 2;
+  if (c.ntiles * (c.hpi / W.pair) <= 2) {
+    W.qslots = 2;
+    W.kslots = 4;
+  }
   const long long items = (long long)c.nkb * P.Bt * P.Hkv * (P.G / c.hpi) * c.nseg;
   if (items > 0x3fffffffLL) return USP_ERR_UNSUPPORTED;
   W.items = (int)items;

@@ -339,6 +339,12 @@ WEIGHTS = [
     (1, 640, 4, 4, 64, True, 40, 2, 2, "zigzag", 30, [0, 5, 300, 640]),
     (1, 512, 2, 1, 64, False, 0, 0, 4, "stripe", 10, [0, 100, 512]),
     (1, 4096, 8, 2, 128, True, 0, 0, 1, "contiguous", 0, None),  # several parts
+    # one tile of at most 64 observed rows: two heads share it (an odd group: not)
+    (2, 700, 8, 2, 128, True, 0, 0, 1, "contiguous", 64, None),
+    (1, 130, 4, 2, 64, False, 0, 0, 1, "contiguous", 33, None),
+    (1, 1100, 3, 1, 128, True, 0, 0, 1, "contiguous", 1, None),
+    (1, 50, 2, 1, 64, True, 0, 0, 1, "contiguous", 0, None),
+    (2, 640, 4, 1, 128, True, 70, 2, 1, "contiguous", 40, None),
 ]
 
 
