@@ -12,8 +12,8 @@
 // of N = min(grid, T / 8) CTAs; a run may cover the end of one unit and the
 // start of others. It leaves one partial (m, l, O) per unit it meets, in slot
 // c + unit: between two consecutive partials either c or the unit grows, so
-// the slots differ, and a unit's partials are consecutive. The merge kernel
-// finds them from the same arithmetic.
+// the slots differ, and a unit's partials are consecutive. The CTAs that hold a
+// unit's first and last step leave those two slots for the merge kernel.
 //
 // One CTA. A round is one step for each warp; its codes and scales are one
 // contiguous piece of each array (two where the sinks end), brought in by
@@ -80,6 +80,7 @@ struct Params {
   float* lse;
   float* o_part;    // [slots][8 NT][D], columns in the kernel's order
   float2* ml_part;  // [slots][8 NT]: (m, l) in log2 units
+  int2* span;       // [units]: first and last slot (units that have steps)
   float2* scores;   // accumulate: [B][H][Rs / 2][C] log2-scaled scores of two rows
   int Tq, Hq, G, R, Rs, nrb;  // R = G Tq rows per KV head, nrb blocks of them
   int grid;
@@ -651,7 +652,12 @@ decode_kv4_kernel(const Params P) {
     // ------------------------------------------------- the unit's partial
     // O in the order (tile i, half, g): element 16 i + 8 half + g of a row is
     // channel g D/8 + 8 (i / 4) + i % 4 + 4 half
-    const long long slot = (long long)blockIdx.x + (long long)b * P.c.H * P.nrb + cur.hr;
+    const int unit = b * P.c.H * P.nrb + cur.hr;
+    const long long slot = (long long)blockIdx.x + unit;
+    if (threadIdx.x == 0) {
+      if (cur.s == 0) P.span[unit].x = (int)slot;
+      if (cur.end == steps.n) P.span[unit].y = (int)slot;
+    }
     float* red = reinterpret_cast<float*>(sm + L::kRed);
     float2* ml = reinterpret_cast<float2*>(sm + L::kML);
 #pragma unroll
@@ -698,38 +704,8 @@ decode_kv4_kernel(const Params P) {
     mbar_wait_drain(full(mine % kStages), (mine / kStages) & 1);
 }
 
-// The slots of unit (b, hr)'s partials, given the steps of all sequences and
-// of those before b (per unit of a sequence).
-struct Slots {
-  long long first, last;
-};
-__device__ __forceinline__ Slots unit_slots(const Params& P, long long all, long long before, int b,
-                                            int hr) {
-  const int per_seq = P.c.H * P.nrb;
-  const long long T = all * per_seq, N = active_ctas(P, T);
-  const long long n = seq_steps(P, seq_len(P, b)).n;
-  const long long a = before * per_seq + n * hr, unit = (long long)b * per_seq + hr;
-  if (n == 0) return {0, -1};
-  // CTA c holds step x iff c = ((x + 1) N - 1) / T
-  return {((a + 1) * N - 1) / T + unit, ((a + n) * N - 1) / T + unit};
-}
-// By one warp: those two sums.
-__device__ __forceinline__ void steps_before(const Params& P, int b, long long& all,
-                                             long long& before) {
-  all = before = 0;
-  for (int i = threadIdx.x & 31; i < P.c.B; i += 32) {
-    const long long n = seq_steps(P, seq_len(P, i)).n;
-    all += n;
-    if (i < b) before += n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-}
-
 constexpr int kMergeThreads = 256;
+constexpr int kWeightKeys = 4;      // keys per thread at a time
 constexpr int kMaxWeightRows = 64;  // (m, 1 / l) kept at a time
 
 // Block x < units * 8 NT: a row of a unit, whose partials (consecutive slots)
@@ -744,7 +720,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kv4_kernel(const Params P
   constexpr int kParts = kMergeThreads / D;
   __shared__ float s_o[kParts][D];
   __shared__ float2 s_ml[SC && kMaxWeightRows > kParts ? kMaxWeightRows : kParts];
-  __shared__ long long s_n[2];
   const int per_seq = P.c.H * P.nrb;
   const int merges = P.c.B * per_seq * kRows;
   if (!SC || (int)blockIdx.x < merges) {
@@ -753,20 +728,14 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kv4_kernel(const Params P
     const int h = hr / P.nrb, rb = hr - h * P.nrb;
     const int row = rb * kRows + r;
     if (row >= P.R) return;
-    if (threadIdx.x < 32) {
-      long long all, before;
-      steps_before(P, b, all, before);
-      if (threadIdx.x == 0) {
-        const Slots s = unit_slots(P, all, before, b, hr);
-        s_n[0] = s.first;
-        s_n[1] = s.last;
-      }
-    }
-    __syncthreads();
+    int2 span = make_int2(0, -1);  // no steps, no partials
+    const bool some = seq_steps(P, seq_len(P, b)).n > 0;
     grid_dependency_wait();
+    if (some) span = P.span[unit];
     const int part = threadIdx.x / D, d = threadIdx.x - part * D;
     float M = -INFINITY, ls = 0.f, os = 0.f;
-    for (long long s = s_n[0] + part; s <= s_n[1]; s += kParts) {
+    #pragma unroll 2
+    for (long long s = span.x + part; s <= span.y; s += kParts) {
       const float2 a = P.ml_part[s * kRows + r];
       const float x = P.o_part[(s * kRows + r) * D + d];
       const float Mn = fmaxf(M, a.x);
@@ -803,58 +772,63 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kv4_kernel(const Params P
   if constexpr (SC) {
     const int x = blockIdx.x - merges, piece = x % pieces, bh = x / pieces;
     const int b = bh / P.c.H, h = bh - b * P.c.H;
-    __shared__ Slots s_slots[kMaxWeightRows / kRows];
-    long long all, before;
-    steps_before(P, b, all, before);  // (every warp)
     const int len = seq_len(P, b);
     const SeqSteps q = seq_steps(P, len);
     const long long head = head_row(P.c, b, h);
-    const long long keys = (long long)q.n * kStep;
-    if ((long long)piece * kMergeThreads >= keys) return;
+    const int keys = q.n * kStep;
+    int k0 = piece * (kWeightKeys * kMergeThreads);
+    if (k0 >= keys) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dependency_wait();
-    for (int r0 = 0; r0 < P.R; r0 += kMaxWeightRows) {
-      const int n = min(kMaxWeightRows, P.Rs - r0);
-      __syncthreads();
-      if (threadIdx.x < kMaxWeightRows / kRows && r0 / kRows + threadIdx.x < P.nrb)
-        s_slots[threadIdx.x] =
-            unit_slots(P, all, before, b, h * P.nrb + r0 / kRows + threadIdx.x);
-      __syncthreads();
-      for (int r = warp; r < n; r += kMergeThreads / 32) {  // a warp per row
-        const int rr = r % kRows;
-        const Slots s = s_slots[r / kRows];
-        float M = -INFINITY, l = 0.f;
-        for (long long i = s.first + lane; i <= s.last; i += 32)
-          M = fmaxf(M, P.ml_part[i * kRows + rr].x);
+    for (; k0 < keys; k0 += pieces * (kWeightKeys * kMergeThreads)) {
+      int j[kWeightKeys];
+      float old[kWeightKeys], w[kWeightKeys];  // (the step's sum is added at once)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        for (long long i = s.first + lane; i <= s.last; i += 32) {
-          const float2 a = P.ml_part[i * kRows + rr];
-          l += a.y * (a.x == -INFINITY ? 0.f : ex2(a.x - M));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        const bool none = l == 0.f || r0 + r >= P.R;
-        if (lane == 0) s_ml[r] = make_float2(none ? 0.f : M, none ? 0.f : 1.f / l);
+      for (int u = 0; u < kWeightKeys; ++u) {
+        const int i = k0 + u * kMergeThreads + threadIdx.x, s = i / kStep;
+        j[u] = (s < q.sinks ? s : s + q.skip) * kStep + i % kStep;
+        if (i >= keys || j[u] >= len) j[u] = -1;
+        old[u] = j[u] >= 0 ? P.c.w[head + j[u]] : 0.f;
+        w[u] = 0.f;
       }
-      __syncthreads();
-      for (long long i = (long long)piece * kMergeThreads + threadIdx.x; i < keys;
-           i += (long long)pieces * kMergeThreads) {
-        const int s = (int)(i / kStep);
-        const int j = (s < q.sinks ? s : s + q.skip) * kStep + (int)(i % kStep);
-        if (j >= len) continue;
-        const float2* sc = P.scores + head * (P.Rs / 2) + (long long)(r0 / 2) * P.c.C + j;
-        float w = 0.f;
-#pragma unroll 4
+      for (int r0 = 0; r0 < P.R; r0 += kMaxWeightRows) {
+        const int n = min(kMaxWeightRows, P.Rs - r0);
+        __syncthreads();
+        for (int r = warp; r < n; r += kMergeThreads / 32) {  // a warp per row
+          const int rb = (r0 + r) / kRows, rr = r0 + r - rb * kRows;
+          const int2 span = P.span[b * per_seq + h * P.nrb + rb];
+          float M = -INFINITY, l = 0.f;
+          for (long long i = span.x + lane; i <= span.y; i += 32)
+            M = fmaxf(M, P.ml_part[i * kRows + rr].x);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+          for (long long i = span.x + lane; i <= span.y; i += 32) {
+            const float2 a = P.ml_part[i * kRows + rr];
+            l += a.y * (a.x == -INFINITY ? 0.f : ex2(a.x - M));
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+          const bool none = l == 0.f || r0 + r >= P.R;
+          if (lane == 0) s_ml[r] = make_float2(none ? 0.f : M, none ? 0.f : 1.f / l);
+        }
+        __syncthreads();
+        const float2* sc = P.scores + head * (P.Rs / 2) + (long long)(r0 / 2) * P.c.C;
+#pragma unroll 2
         for (int r = 0; r < n; r += 2) {
-          const float2 v = sc[(long long)(r / 2) * P.c.C];
           const float2 a0 = s_ml[r], a1 = s_ml[r + 1];
-          w += ex2(v.x - a0.x) * a0.y;
-          // (the odd last row's partner was never written)
-          if (r0 + r + 1 < P.R) w += ex2(v.y - a1.x) * a1.y;
+          const bool odd = r0 + r + 1 >= P.R;  // the last row's partner was never written
+#pragma unroll
+          for (int u = 0; u < kWeightKeys; ++u) {
+            if (j[u] < 0) continue;
+            const float2 v = sc[(long long)(r / 2) * P.c.C + j[u]];
+            w[u] += ex2(v.x - a0.x) * a0.y;
+            if (!odd) w[u] += ex2(v.y - a1.x) * a1.y;
+          }
         }
-        P.c.w[head + j] += w;
       }
+#pragma unroll
+      for (int u = 0; u < kWeightKeys; ++u)
+        if (j[u] >= 0) P.c.w[head + j[u]] = old[u] + w[u];
     }
   }
 }
@@ -863,7 +837,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kv4_kernel(const Params P
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Ws {
-  size_t o, ml, scores, total;
+  size_t o, ml, span, scores, total;
 };
 int tiles_for(int R) { return R <= 8 ? 1 : 2; }
 
@@ -879,6 +853,8 @@ Ws layout(int B, int Tq, int C, int Hq, int Hkv, int D, int accumulate) {
   at += up256((size_t)slots * rows * D * 4);
   w.ml = at;
   at += up256((size_t)slots * rows * 8);
+  w.span = at;
+  at += up256((size_t)B * Hkv * nrb * 8);
   if (accumulate) {
     w.scores = at;
     at += up256((size_t)B * Hkv * C * Rs * 4);
@@ -904,8 +880,8 @@ usp_status_t launch_t(const Params& P, cudaStream_t st) {
   long long blocks = (long long)P.c.B * P.c.H * P.nrb * 8 * NT;
   int pieces = 0;
   if constexpr (SC) {
-    const int most = (P.c.C + kMergeThreads - 1) / kMergeThreads;
-    const int want = 152 * 4 / (P.c.B * P.c.H) + 1;  // half the GPU's warps, over the heads
+    const int most = (P.c.C + kWeightKeys * kMergeThreads - 1) / (kWeightKeys * kMergeThreads);
+    const int want = 152 * 6 / (P.c.B * P.c.H) + 1;  // most of the GPU's warps, over the heads
     pieces = most < want ? most : want;
     blocks += (long long)P.c.B * P.c.H * pieces;
   }
@@ -953,6 +929,7 @@ usp_status_t launch_decode_kv4(const DecodeKv4Args& a, void* workspace, cudaStre
   P.lse = a.lse;
   P.o_part = reinterpret_cast<float*>(base + w.o);
   P.ml_part = reinterpret_cast<float2*>(base + w.ml);
+  P.span = reinterpret_cast<int2*>(base + w.span);
   if (a.accumulate) {
     P.scores = reinterpret_cast<float2*>(base + w.scores);
   }
