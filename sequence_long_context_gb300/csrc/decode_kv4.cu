@@ -439,9 +439,13 @@ decode_kv4_kernel(const Params P) {
     const int i_first = len - P.Tq;  // position of token 0
     for (int s0 = cur.s; s0 < cur.end; s0 += kWarps) {
      const int st = used % kStages, s = s0 + warp;
+     // A warp without a step in the unit's last round waits for the copies too:
+     // they are issued once every warp has released the stage's round before, so
+     // its arrival on `empty` below cannot count for that round, in place of a
+     // warp that still reads it.
+     if (!mbar_wait(full(st), (used / kStages) & 1, abort_flag, &g_decode_kv4_status)) ok = false;
+     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
      if (s < cur.end) {
-      if (!mbar_wait(full(st), (used / kStages) & 1, abort_flag, &g_decode_kv4_status)) ok = false;
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       const uint8_t* stp = sm + st * L::kStageBytes;
       const uint8_t* kcodes = stp + L::kKC + warp * (kStep * D / 2);
       const uint8_t* vcodes = stp + L::kVC + warp * (kStep * D / 2);

@@ -291,6 +291,34 @@ def test_decode_nan_query_stays_in_its_rows():
     assert torch.equal(gl[~hit.to(dev)], wl[~hit.to(dev)])
 
 
+@pytest.mark.parametrize("D,Tq,lens,window,sink", [
+    (128, 1, [1007 - 61 * i for i in range(16)], 0, 0),     # 32 down to 3 steps
+    (128, 1, [5000 - 37 * i for i in range(16)], 1000, 4),  # 33 steps: one warp in the last round
+    (64, 1, [513 + 32 * i for i in range(16)], 0, 0),
+    (128, 9, [300 + 33 * i for i in range(16)], 0, 0),      # two tiles of query rows
+])
+def test_decode_many_units_whose_last_rounds_are_partial(D, Tq, lens, window, sink):
+    """512 units (or twice that) of 3 to 34 steps: each CTA passes several unit ends at which some
+    warps have no step, while the copies of the next units are under way. A warp
+    that releases such a round's stage early lets it be overwritten while another
+    reads it: outputs then differ between runs, or from the oracle's."""
+    dev = device()
+    B, H = len(lens), 32
+    c = random_cache(dev, B, max(lens), H, D, lens, seed=D + Tq)
+    q = torch.randn(B, Tq, H, D, generator=gen(Tq)).to(torch.bfloat16)
+    qd = q.to(dev)
+    out, lse = usp.attn_decode_kv4(qd, c, window=window, sink_tokens=sink)
+    usp.usp_device_status()
+    for _ in range(20):
+        again, lse2 = usp.attn_decode_kv4(qd, c, window=window, sink_tokens=sink)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+    usp.usp_device_status()
+    for b in (0, 7, 15):  # whole sequences against the oracle
+        one = c._replace(**{n: getattr(c, n)[b:b + 1] for n in FIELDS + ("seq_lens", "key_weight")})
+        check_decode(one, q[b:b + 1], out[b:b + 1], lse[b:b + 1], None, one.key_weight,
+                     lens[b:b + 1], True, window, sink)
+
+
 def test_decode_long_cache_offsets_pass_32_bits():
     """Codes of the last head start behind 4 GiB; only its rows are filled."""
     dev = device()
