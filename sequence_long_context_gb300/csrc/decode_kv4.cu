@@ -666,6 +666,7 @@ decode_kv4_kernel(const Params P) {
     float2* ml = reinterpret_cast<float2*>(sm + L::kML);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      const int rows = min(8, P.R - rb * kRows - nt * 8);  // that exist
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float x = l[nt][e];
@@ -674,15 +675,17 @@ decode_kv4_kernel(const Params P) {
         if (g == 0) ml[warp * 8 + 2 * t + e] = make_float2(m[nt][e], x);
       }
       float* mine = red + (warp * 8 + 2 * t) * L::kRedStride + g;
+      if (2 * t < rows) {
 #pragma unroll
-      for (int i = 0; i < kMT; ++i) {
-        mine[16 * i] = fmaf(-8.f, ob[nt][0], o[nt][i][0]);
-        mine[L::kRedStride + 16 * i] = fmaf(-8.f, ob[nt][1], o[nt][i][1]);
-        mine[16 * i + 8] = fmaf(-8.f, ob[nt][0], o[nt][i][2]);
-        mine[L::kRedStride + 16 * i + 8] = fmaf(-8.f, ob[nt][1], o[nt][i][3]);
+        for (int i = 0; i < kMT; ++i) {
+          mine[16 * i] = fmaf(-8.f, ob[nt][0], o[nt][i][0]);
+          mine[L::kRedStride + 16 * i] = fmaf(-8.f, ob[nt][1], o[nt][i][1]);
+          mine[16 * i + 8] = fmaf(-8.f, ob[nt][0], o[nt][i][2]);
+          mine[L::kRedStride + 16 * i + 8] = fmaf(-8.f, ob[nt][1], o[nt][i][3]);
+        }
       }
       __syncthreads();
-      for (int x = threadIdx.x; x < 8 * D; x += kThreads) {
+      for (int x = threadIdx.x; x < rows * D; x += kThreads) {
         const int r = x / D, d = x - r * D;
         float M = -INFINITY;
 #pragma unroll
