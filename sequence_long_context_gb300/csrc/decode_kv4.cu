@@ -67,6 +67,9 @@ constexpr int kGridMax = 304;             // 152 SMs x 2 resident CTAs
 // Up to eight query rows: two CTAs of eight warps per SM at 128 registers;
 // sixteen: one CTA (with ten or twelve warps at 168 registers and Q^T in shared
 // memory it spills: 63 and 69 us instead of 51 for 4 x 32K keys and 12 rows).
+// Rows 9..16 as two blocks of eight read and decode every key twice: 76 us
+// instead of 61 for 4 x 32K keys, 459 instead of 352 for 8 x 128K (12.3 instead
+// of 14.7 for 2K keys of one sequence, which no rule is made for).
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLazy = 8.f;              // the max moves when it grows by 2^8
