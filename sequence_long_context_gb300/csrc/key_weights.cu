@@ -454,15 +454,19 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
         }
         const int ring = n & (kRing - 1), rows = W.pair == 2 ? kQT : min(kQT, P.S - cur.row);
         float* st = reinterpret_cast<float*>(sm + L::kStat + ring * L::kStatBytes);
+        bool skips = false;
 #pragma unroll
         for (int e = 0; e < kQT / 32; ++e) {
           const float x = cur.lse[e] * kLog2e;
-          // a row that sees nothing adds nothing
+          // a row that sees nothing adds nothing, whatever it holds: its
+          // position is nowhere, and the tile's positions are looked at
           const bool none = cur.pos[e] < 0 || x == -INFINITY;
+          skips |= none;
           st[lane + 32 * e] = none ? -INFINITY : -x;
-          reinterpret_cast<int*>(st)[kQT + lane + 32 * e] = cur.pos[e];
+          reinterpret_cast<int*>(st)[kQT + lane + 32 * e] = none ? kNowhere : cur.pos[e];
         }
-        if (lane == 0) sched[ring] = cur.cls | rows << 8;
+        skips = __any_sync(0xffffffffu, skips);
+        if (lane == 0) sched[ring] = (skips ? kClsMasked : cur.cls) | rows << 8;
         __syncwarp();
         if (lane == 0) {
           // 64 rows at a time; the barrier stands for the ring's entry too

@@ -449,6 +449,26 @@ def test_key_weights_ignore_what_is_not_seen():
     assert torch.isfinite(w[:, :, :299]).all()
 
 
+@pytest.mark.parametrize("dtype,flags", [(torch.bfloat16, 0), (torch.bfloat16, 1),
+                                         (torch.float32, 0)])
+def test_key_weights_of_marked_queries_that_hold_nan(dtype, flags):
+    """Queries whose LSE is -inf (padding) add nothing, whatever they hold, in
+    tiles that the mask leaves whole as in others."""
+    dev = device()
+    g = gen(13)
+    q = torch.randn(1, 1000, 2, 64, generator=g).to(dtype).to(dev)
+    k = torch.randn(1, 1000, 1, 64, generator=g).to(dtype).to(dev)
+    _, lse = usp.attn_forward(q, k, k)
+    for a in (600, 990):
+        lse[:, :, a:a + 10] = -float("inf")
+    want = usp.attn_key_weights(q, k, lse, flags=flags)
+    assert torch.isfinite(want).all()
+    q[:, 600:605] = float("nan")
+    q[:, 605:610] = float("inf")
+    q[:, 990:1000] = float("nan")
+    assert torch.equal(usp.attn_key_weights(q, k, lse, flags=flags), want)
+
+
 # ------------------------------------------------------------------------- evict
 
 EVICT = [
