@@ -3,6 +3,7 @@
 // Every check happens on the host before any launch, so a call that returns
 // an error has enqueued nothing. The library allocates no device memory;
 // scratch is carved out of the caller's workspace in 256-byte aligned slices.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -785,7 +786,9 @@ usp_status_t usp_attn_key_weights(const void* q, const void* k, const float* lse
   const size_t need =
       usp_attn_key_weights_workspace_size(s.B_eff(), S, Hq, Hkv, observe, dtype, flags);
   if (need > 0 && (!workspace || workspace_bytes < need)) return USP_ERR_WORKSPACE;
-  AttnParams P = make_params(s, softmax_scale, causal, window, sink_tokens, cu_seqlens);
+  // a window or sinks of S reach every key; the kernels add them to positions
+  AttnParams P = make_params(s, softmax_scale, causal, std::min(window, S),
+                             std::min(sink_tokens, S), cu_seqlens);
   P.q = q;
   P.k = k;
   P.lse = const_cast<float*>(lse);

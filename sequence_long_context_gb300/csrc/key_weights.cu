@@ -253,7 +253,7 @@ __device__ __forceinline__ int classify_tile(const WeightParams& W, int qt, cons
   const int p0 = W.q0 + qt * kQT;
   const PosRange q = row_bounds(P, p0, kQT);
   if (q.lo > q.hi || q.hi < b.q.lo || q.lo > b.q.hi) return kClsEmpty;
-  bool all = true;  // rows behind S are zeros with LSE = inf: no mask needed
+  bool all = true;  // rows behind S have no position, which the producer sees
   if (W.observe > 0) {
     if (P.cu == nullptr) {
       if (q.hi < P.S - W.observe) return kClsEmpty;

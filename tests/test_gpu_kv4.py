@@ -469,6 +469,24 @@ def test_key_weights_of_marked_queries_that_hold_nan(dtype, flags):
     assert torch.equal(usp.attn_key_weights(q, k, lse, flags=flags), want)
 
 
+@pytest.mark.parametrize("flags", [0, 1])
+@pytest.mark.parametrize("cut", [None, [0, 300, 700]])
+def test_key_weights_of_the_largest_window_and_sinks(cut, flags):
+    dev = device()
+    g = gen(14)
+    shape = (700,) if cut else (1, 700)
+    q = torch.randn(*shape, 2, 64, generator=g).to(torch.bfloat16).to(dev)
+    k = torch.randn(*shape, 1, 64, generator=g).to(torch.bfloat16).to(dev)
+    kw = dict(cu_seqlens=torch.tensor(cut, dtype=torch.int32, device=dev)) if cut else {}
+    _, lse = usp.attn_forward(q, k, k, **kw)
+    big = 2 ** 31 - 1
+    want = usp.attn_key_weights(q, k, lse, flags=flags, **kw)
+    for window, sink in ((big, 0), (big, big), (1, big)):
+        got = usp.attn_key_weights(q, k, lse, flags=flags, window=window, sink_tokens=sink, **kw)
+        # (a window makes tiles masked, whose sums are taken in another order)
+        assert torch.allclose(got, want, rtol=700 * 2 * U)
+
+
 # ------------------------------------------------------------------------- evict
 
 EVICT = [
