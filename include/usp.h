@@ -487,8 +487,10 @@ typedef struct {
  * usp_kv4_append - store new tokens' keys and values in the cache.
  *
  * k, v  [B, T, Hkv, D] in natural order, bf16 or fp32 (dtype); with
- *      cu_seqlens [B + 1] (int32, device, trusted as in usp_attn_fwd) a
- *      packed batch [T, Hkv, D] of T tokens in all. T >= 0.
+ *      cu_seqlens [B + 1] (int32, device, non-decreasing, trusted as in
+ *      usp_attn_fwd) a packed batch [T, Hkv, D] of T tokens in all. T >= 0.
+ *      Tokens before cu_seqlens[0] and from cu_seqlens[B] on (padding) are not
+ *      stored.
  * Token t of sequence b goes to row seq_lens[b] + t of the sequence's rows;
  *      tokens that find no room are dropped.
  * new_weight  NULL, or the new keys' attention weights so far, fp32

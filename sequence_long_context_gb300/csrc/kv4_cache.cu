@@ -201,6 +201,7 @@ __device__ __forceinline__ void append_item(const AppendParams& P, int which, in
     if (b < 0) {
       bb = seg_of(P.cu, P.c.B, tok);
       t = tok - __ldg(P.cu + bb);
+      if (tok >= __ldg(P.cu + bb + 1)) continue;  // behind the last boundary
       pos0 = clamp_len(P.c.lens[bb], P.c.C);
       row0 = head_row(P.c, bb, h);
     }

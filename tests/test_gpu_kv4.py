@@ -133,6 +133,30 @@ def test_append_packed_is_each_sequence_alone(H, D, cut):
         assert torch.equal(x, y)
 
 
+def test_append_packed_leaves_tokens_outside_the_boundaries():
+    """A padded batch: tokens before the first boundary and behind the last
+    belong to no sequence, and no row behind a sequence's end is written."""
+    dev = device()
+    g = gen(10)
+    k, v = (torch.randn(60, 2, 64, generator=g).to(torch.bfloat16).to(dev) for _ in "kv")
+    w = torch.rand(2, 60, generator=g).to(dev)
+    c = usp.kv4_cache(2, 64, 2, 64, device=dev, key_weight=True)
+    for t in c[:4]:
+        t.fill_(0xAB)
+    c.key_weight.fill_(5)
+    cu = torch.tensor([4, 20, 41], dtype=torch.int32, device=dev)
+    assert usp.kv4_append(c, k, v, key_weight=w, cu_seqlens=cu).tolist() == [16, 21]
+    for b, n in enumerate((16, 21)):
+        for t in c[:4]:
+            assert (t[b, :, n:] == 0xAB).all()
+        assert (c.key_weight[b, :, n:] == 5).all()
+        s = slice(int(cu[b]), int(cu[b]) + n)
+        assert torch.equal(c.key_weight[b, :, :n], w[:, s])
+        codes, sb = kv4.quantize(k[s].cpu(), 1.0)
+        assert np.array_equal(c.k[b, :, :n].cpu().numpy(), codes.swapaxes(0, 1))
+        assert np.array_equal(c.k_scale[b, :, :n].cpu().numpy(), sb.swapaxes(0, 1))
+
+
 def test_append_without_weights_starts_new_keys_at_zero():
     dev = device()
     c = usp.kv4_cache(1, 32, 2, 64, device=dev, key_weight=True)
