@@ -49,6 +49,8 @@
 // same in both of O's sums.
 #include <cuda_fp16.h>
 
+#include <cfloat>
+
 #include "internal.h"
 #include "kv4.cuh"
 #include "kv4_host.h"
@@ -420,8 +422,8 @@ decode_kv4_kernel(const Params P) {
       const __half mid = __float2half_rn(rest);
       qb[nt][0] = half2_bits(__halves2half2(hi, mid));
       qb[nt][1] = half2_bits(__floats2half2_rn(rest - __half2float(mid), 0.f));
-      // 16 for the scale's 2^-4
-      const float row_mul = ldexpf(P.score_mul * 16.f, ex - 6);
+      // 16 for the scale's 2^-4; not 0, which a masked key's -inf would make NaN
+      const float row_mul = fmaxf(ldexpf(P.score_mul * 16.f, ex - 6), FLT_MIN);
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         mul[nt][e] = __shfl_sync(0xffffffffu, row_mul, 4 * (2 * t + e));
@@ -879,14 +881,6 @@ usp_status_t launch_t(const Params& P, cudaStream_t st) {
   static SmemAttr attr;
   cudaError_t e = attr.set(decode_kv4_kernel<D, NT, SC>, smem);
   if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
-  {
-    ProfScope ps(st, "attn_decode_kv4");
-    decode_kv4_kernel<D, NT, SC><<<P.grid, kThreads, smem, st>>>(P);
-  }
-  note_launch();
-  usp_status_t r = check_launch();
-  if (r != USP_OK) return r;
-  // the merge's launch and set-up overlap the end of the kernel before it
   long long blocks = (long long)P.c.B * P.c.H * P.nrb * 8 * NT;
   int pieces = 0;
   if constexpr (SC) {
@@ -896,6 +890,14 @@ usp_status_t launch_t(const Params& P, cudaStream_t st) {
     blocks += (long long)P.c.B * P.c.H * pieces;
   }
   if (blocks > 0x7fffffffLL) return USP_ERR_UNSUPPORTED;
+  {
+    ProfScope ps(st, "attn_decode_kv4");
+    decode_kv4_kernel<D, NT, SC><<<P.grid, kThreads, smem, st>>>(P);
+  }
+  note_launch();
+  usp_status_t r = check_launch();
+  if (r != USP_OK) return r;
+  // the merge's launch and set-up overlap the end of the kernel before it
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kMergeThreads);

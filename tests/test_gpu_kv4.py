@@ -301,6 +301,25 @@ def test_decode_large_scores_and_equal_keys():
     assert torch.allclose(out.float(), torch.full_like(out.float(), 16.0), rtol=2.0 ** -8 + 2.0 ** -10)
 
 
+@pytest.mark.parametrize("descale", [1e-30, 1e-37])
+def test_decode_zero_queries_with_a_tiny_descale(descale):
+    """Scores too small for fp32 are 0, and masked keys stay masked: the output
+    is the mean of the visible values (2^-8 of it, and of the mean of the
+    values' magnitudes 2^-11 and n u for the sums)."""
+    dev = device()
+    c = random_cache(dev, 1, 112, 1, 64, [100], seed=12)._replace(k_descale=descale)
+    q = torch.zeros(1, 3, 2, 64, dtype=torch.bfloat16, device=dev)
+    out, lse = usp.attn_decode_kv4(q, c)
+    vv = cache_values(c)[1]
+    for t in range(3):
+        n = 98 + t
+        x = vv[0, 0, :n].astype(np.float64)
+        bound = 2.0 ** -8 * np.abs(x.mean(0)) + np.abs(x).mean(0) * (2.0 ** -11 + 2 * n * U)
+        for h in range(2):
+            assert (np.abs(out[0, t, h].double().cpu().numpy() - x.mean(0)) <= bound).all()
+            assert abs(float(lse[0, t, h]) - np.log(n)) <= n * U + 4 * U * np.log(n) + 2.0 ** -22
+
+
 def test_decode_nan_query_stays_in_its_rows():
     dev = device()
     c = random_cache(dev, 2, 64, 2, 64, [60, 40], seed=4)
