@@ -532,6 +532,20 @@ def _call(fn, index, stream, *args) -> None:
         _check(st)
 
 
+def _on(stream, device):
+    """Context in which `stream` (a Stream or a raw handle) is the current one, so
+    that what a call allocates belongs to the stream it runs on: memory of
+    another stream may still be written by work queued there, or be handed on
+    while this call's kernels run."""
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(stream)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else \
+            torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 _U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
 
 
@@ -598,6 +612,9 @@ def kv4_read(cache: KV4Cache, tokens: int, *, starts=None, dtype=torch.bfloat16,
              ) -> Tuple[torch.Tensor, torch.Tensor]:
     """(k, v) [B, tokens, Hkv, D]: the values of rows starts[b] (default 0) ..
     of every sequence; zeros behind its length."""
+    if stream is not None:
+        with _on(stream, cache.k.device):
+            return kv4_read(cache, tokens, starts=starts, dtype=dtype)
     s, at = _kv4_struct(cache)
     if dtype not in DTYPE:
         raise ValueError("keys and values are read as bf16 or fp32")
@@ -605,7 +622,7 @@ def kv4_read(cache: KV4Cache, tokens: int, *, starts=None, dtype=torch.bfloat16,
         _require(starts, "starts", _I32, (s.B,), at, cache.k)
     k = torch.empty((s.B, tokens, s.Hkv, s.D), dtype=dtype, device=cache.k.device)
     v = torch.empty_like(k)
-    _call(_lib.load().usp_kv4_read, at, stream, ctypes.addressof(s),
+    _call(_lib.load().usp_kv4_read, at, None, ctypes.addressof(s),
           None if starts is None else starts.data_ptr(), tokens, k.data_ptr(), v.data_ptr(),
           DTYPE[dtype])
     return k, v
@@ -617,6 +634,11 @@ def attn_decode_kv4(q: torch.Tensor, cache: KV4Cache, *, causal=True, window=0, 
     """(out [B,Tq,Hq,D], lse [B,Tq,Hq]) of the newest Tq tokens q [B,Tq,Hq,D]
     (already in the cache) against the cached keys; accumulate adds each key's
     attention weight of this step to cache.key_weight."""
+    if stream is not None:
+        with _on(stream, q.device):
+            return attn_decode_kv4(q, cache, causal=causal, window=window,
+                                   sink_tokens=sink_tokens, accumulate=accumulate,
+                                   softmax_scale=softmax_scale, workspace=workspace)
     s, at = _kv4_struct(cache)
     B, Tq, Hq, D = q.shape
     _require(q, "q", torch.bfloat16, (s.B, Tq, Hq, s.D), at, cache.k)
@@ -630,7 +652,7 @@ def attn_decode_kv4(q: torch.Tensor, cache: KV4Cache, *, causal=True, window=0, 
                                                   1 if accumulate else 0)
     ws = torch.empty(need, dtype=_U8, device=dev) if workspace is None else \
         _use_workspace(workspace, need, dev)[0]
-    _call(lib.usp_attn_decode_kv4, at, stream, ctypes.addressof(s), q.data_ptr(), out.data_ptr(),
+    _call(lib.usp_attn_decode_kv4, at, None, ctypes.addressof(s), q.data_ptr(), out.data_ptr(),
           lse.data_ptr(), Tq, Hq, softmax_scale, 1 if causal else 0, window, sink_tokens,
           1 if accumulate else 0, 0, ws.data_ptr(), ws.numel())
     return out, lse
@@ -643,6 +665,12 @@ def attn_key_weights(q, k, lse, *, causal=True, window=0, sink_tokens=0, cu_seql
     collected from the observed queries (observe = n: the last n of each
     sequence; 0: all) and the query heads sharing its KV head, from the
     forward's q, k (rank-major) and lse."""
+    if stream is not None:
+        with _on(stream, q.device):
+            return attn_key_weights(q, k, lse, causal=causal, window=window,
+                                    sink_tokens=sink_tokens, cu_seqlens=cu_seqlens, cp=cp,
+                                    layout=layout, observe=observe, softmax_scale=softmax_scale,
+                                    flags=flags, workspace=workspace)
     B, S, Hq, Hkv, D, Bl = _dims(q, k, cu_seqlens)
     at = q.get_device()
     dt = q.dtype
@@ -662,7 +690,7 @@ def attn_key_weights(q, k, lse, *, causal=True, window=0, sink_tokens=0, cu_seql
         ws = _use_workspace(ws, need, q.device)[0]
     elif need:
         ws = torch.empty(need, dtype=_U8, device=q.device)
-    _call(lib.usp_attn_key_weights, at, stream, q.data_ptr(), k.data_ptr(), lse.data_ptr(),
+    _call(lib.usp_attn_key_weights, at, None, q.data_ptr(), k.data_ptr(), lse.data_ptr(),
           weight.data_ptr(), B, S, Hq, Hkv, D, softmax_scale, 1 if causal else 0, window,
           sink_tokens, None if cu_seqlens is None else cu_seqlens.data_ptr(), cp,
           _enum(LAYOUT, layout), observe, DTYPE[dt], flags,
@@ -676,6 +704,9 @@ def kv4_evict(cache: KV4Cache, keep: int, *, recent=0, sink_tokens=0, out=None, 
     keeps, in each KV head, its first sink_tokens, its last `recent` and the
     keys with the largest key_weight, in order; kept gives their old rows (-1
     behind the last). out: another cache that takes them (default: in place)."""
+    if stream is not None:
+        with _on(stream, cache.k.device):
+            return kv4_evict(cache, keep, recent=recent, sink_tokens=sink_tokens, out=out)
     if cache.key_weight is None:
         raise ValueError("eviction needs a cache with key_weight")
     if keep < 1:
@@ -690,6 +721,6 @@ def kv4_evict(cache: KV4Cache, keep: int, *, recent=0, sink_tokens=0, out=None, 
         if (s.k_descale, s.v_descale) != (d.k_descale, d.v_descale):
             raise ValueError("both caches must have the same descales")
     kept = torch.empty((s.B, s.Hkv, keep), dtype=_I32, device=cache.k.device)
-    _call(_lib.load().usp_kv4_evict, at, stream, ctypes.addressof(s), ctypes.addressof(d),
+    _call(_lib.load().usp_kv4_evict, at, None, ctypes.addressof(s), ctypes.addressof(d),
           kept.data_ptr(), keep, recent, sink_tokens)
     return dst, kept

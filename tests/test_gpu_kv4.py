@@ -711,6 +711,32 @@ def test_captured_step_grows_the_cache_on_replay():
     usp.usp_device_status()
 
 
+def test_explicit_stream_does_not_share_memory_with_the_current_one():
+    """What a call allocates belongs to the stream it runs on: memory that work
+    still queued on the current stream writes is not handed to it."""
+    dev = device()
+    c = random_cache(dev, 2, 512, 4, 128, [500, 300], seed=8)
+    q = torch.randn(2, 1, 16, 128, generator=gen(8)).to(torch.bfloat16).to(dev)
+    want, wl = usp.attn_decode_kv4(q, c)
+    k, v = usp.kv4_read(c, 500)
+    side = torch.cuda.Stream(device=dev)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for stream in (side, side.cuda_stream):
+            x = [torch.empty_like(t) for t in (want, wl, k, v)]
+            torch.cuda._sleep(20_000_000)  # some 10 ms
+            for t in x:
+                t.fill_(7)
+            del x, t
+            out, lse = usp.attn_decode_kv4(q, c, stream=stream)
+            k2, v2 = usp.kv4_read(c, 500, stream=stream)
+            side.synchronize()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(lse, wl)
+            assert torch.equal(k2, k) and torch.equal(v2, v)
+            del out, lse, k2, v2
+
+
 def test_two_streams_with_their_own_workspaces():
     dev = device()
     c = random_cache(dev, 2, 2048, 4, 128, [2000, 1500], seed=7)
