@@ -146,7 +146,7 @@ usp_status_t usp_kv4_evict(const usp_kv4_cache_t* src, const usp_kv4_cache_t* ds
                     src->v_codes == dst->v_codes && src->v_scales == dst->v_scales &&
                     src->key_weight == dst->key_weight && src->seq_lens == dst->seq_lens &&
                     src->capacity == dst->capacity;
-  if (!same) {
+  {  // (in place, `kept` alone may share nothing with the cache)
     const size_t rs = (size_t)src->B * src->Hkv * src->capacity;
     const size_t rd = (size_t)dst->B * dst->Hkv * dst->capacity;
     const size_t code = src->D / 2, scale = src->D / kv4::kBlock;
@@ -158,7 +158,7 @@ usp_status_t usp_kv4_evict(const usp_kv4_cache_t* src, const usp_kv4_cache_t* ds
     const size_t dn[] = {rd * code, rd * code, rd * scale, rd * scale, rd * 4, (size_t)dst->B * 4,
                          (size_t)src->B * src->Hkv * keep * 4};
     for (int i = 0; i < 6; ++i)
-      for (int j = 0; j < 7; ++j)
+      for (int j = same ? 6 : 0; j < 7; ++j)
         if (overlap(sp[i], sn[i], dp[j], dn[j])) return USP_ERR_INVALID_ARG;
   }
   return launch_kv4_evict(view(src), view(dst), src->D, kept, keep, recent, sink_tokens,

@@ -148,6 +148,12 @@ def test_evict_refuses_caches_that_do_not_fit_or_overlap(lib):
     assert evict(lib, src, cache(key_weight=None), kept=FAR) == 1
 
 
+def test_evict_in_place_refuses_a_list_inside_the_cache(lib):
+    c = cache()
+    for at in (c.k_codes, c.v_scales + 512, c.key_weight + 512, c.seq_lens):  # (arrays of 1 KB)
+        assert evict(lib, c, c, kept=at) == 1
+
+
 def test_nothing_to_do(lib):
     none = dict(k_codes=None, k_scales=None, v_codes=None, v_scales=None, key_weight=None,
                 seq_lens=None, B=0)
