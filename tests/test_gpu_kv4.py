@@ -362,6 +362,32 @@ def test_decode_many_units_whose_last_rounds_are_partial(D, Tq, lens, window, si
                      lens[b:b + 1], True, window, sink)
 
 
+@pytest.mark.parametrize("B,Tq,C,G,H,D", [(1, 1, 131072, 1, 64, 64), (1, 1, 2 ** 20, 1, 16, 128),
+                                          (2, 3, 131072, 4, 16, 128)])
+def test_decode_long_rows_lose_nothing_but_the_roundings(B, Tq, C, G, H, D):
+    """Random values, whose weighted mean is some hundred times smaller than they
+    are. bf16 rounds O by at most 2^-8 of it, each evenly spread: 2^-8 / sqrt 3 rms
+    at most; P's roundings (2^-11 each, independent) add 2^-11 / sqrt 3 of O; the
+    rest of the error, of sums in fp32, may be a tenth of that of bf16."""
+    dev = device()
+    c = usp.kv4_cache(B, C, H, D, device=dev)
+    torch.manual_seed(B + C)
+    for _ in range(C // 8192):
+        k, v = (torch.randn(B, 8192, H, D, device=dev, dtype=torch.bfloat16) for _ in "kv")
+        usp.kv4_append(c, k, v)
+    q = torch.randn(B, Tq, G * H, D, device=dev).to(torch.bfloat16)
+    out, _ = usp.attn_decode_kv4(q, c, causal=False)
+    err = ref = 0.0
+    for h in range(0, H, H // 4):
+        one = usp.KV4Cache(*(t[:1, h:h + 1].contiguous() for t in c[:4]), c.seq_lens[:1])
+        kv, vv = (t[0, :, 0].double() for t in usp.kv4_read(one, C, dtype=torch.float32))
+        s = q[0, :, h * G:(h + 1) * G].double() @ kv.T / D ** 0.5
+        o = torch.softmax(s, -1) @ vv
+        err += float(((out[0, :, h * G:(h + 1) * G].double() - o) ** 2).sum())
+        ref += float((o ** 2).sum())
+    assert (err / ref) ** 0.5 <= (1.1 * 2.0 ** -8 + 2.0 ** -11) / 3 ** 0.5
+
+
 def test_decode_long_cache_offsets_pass_32_bits():
     """Codes of the last head start behind 4 GiB; only its rows are filled."""
     dev = device()
