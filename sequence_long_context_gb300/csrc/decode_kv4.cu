@@ -7,13 +7,14 @@
 //
 // Division of the work. A unit is one (sequence, KV head, block of up to 8 NT
 // query rows); a step is 32 of its keys. All steps of all units, in unit
-// order, are one line of T steps that the CTAs share in equal runs, whatever
-// the lengths (read on the device). CTA c takes steps [T c / N, T (c+1) / N)
-// of N = min(grid, T / 8) CTAs; a run may cover the end of one unit and the
-// start of others. It leaves one partial (m, l, O) per unit it meets, in slot
-// c + unit: between two consecutive partials either c or the unit grows, so
-// the slots differ, and a unit's partials are consecutive. The CTAs that hold a
-// unit's first and last step leave those two slots for the merge kernel.
+// order and each unit followed by a few that stand for the cost of its end, are
+// one line of length T that the CTAs share in equal runs, whatever the lengths
+// (read on the device). CTA c takes [T c / N, T (c+1) / N) of N = min(grid, T / 8)
+// CTAs; a run may cover the end of one unit and the start of others. It leaves
+// one partial (m, l, O) per unit of which it has steps, in slot c + unit:
+// between two consecutive partials either c or the unit grows, so the slots
+// differ, and a unit's partials are consecutive. The CTAs that hold a unit's
+// first and last step leave those two slots for the merge kernel.
 //
 // One CTA. A round is one step for each warp; its codes and scales are one
 // contiguous piece of each array (two where the sinks end), brought in by
@@ -77,6 +78,11 @@ constexpr int kGridMax = 304;             // 152 SMs x 2 resident CTAs
 // of 14.7 for 2K keys of one sequence, which no rule is made for).
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+// What a unit costs besides its steps, in steps: its last round is half empty on
+// average, and the combination and the next queries take 2.8 us, a round of
+// eight steps 2. (16 x 32 units of at most 33 steps: 37.2 us without it, 33.4
+// with 8, 32.3 with 12, 33.1 with 16.)
+constexpr int kUnitCost = 12;
 constexpr float kLazy = 8.f;              // the max moves when it grows by 2^8
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -119,17 +125,23 @@ __device__ __forceinline__ int seq_len(const Params& P, int b) {
   return clamp_len(__ldg(P.c.lens + b), P.c.C);
 }
 
-// Steps of all sequences, per (KV head, row block), by one warp.
-__device__ __forceinline__ long long total_steps_warp(const Params& P) {
-  long long n = 0;
-  for (int b = threadIdx.x & 31; b < P.c.B; b += 32) n += seq_steps(P, seq_len(P, b)).n;
+// Length of a unit of n steps on the line that the CTAs share.
+__device__ __forceinline__ int line_len(int n) { return n > 0 ? n + kUnitCost : 0; }
+
+// The sequences [b0, b0 + 32) on the line, one per lane: where each ends.
+__device__ __forceinline__ long long line_ends(const Params& P, int b0, int per_seq) {
+  const int b = b0 + (threadIdx.x & 31);
+  long long inc = b < P.c.B ? (long long)line_len(seq_steps(P, seq_len(P, b)).n) * per_seq : 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    if ((threadIdx.x & 31) >= o) inc += x;
+  }
+  return inc;
 }
-__device__ __forceinline__ long long active_ctas(const Params& P, long long T) {
-  const long long want = (T + kWarps - 1) / kWarps;
-  return want < P.grid ? want : P.grid;
+__device__ __forceinline__ long long scaled(long long T, unsigned c, unsigned N) {  // T c / N
+  if (T <= 0xffffffffLL / kGridMax) return (unsigned)T * c / N;  // (a 64-bit division is slow)
+  return T * c / N;
 }
 
 // The launch of the dependent kernel may proceed; and, in that one: the kernel
@@ -148,7 +160,7 @@ struct Walk {
   int len;          // of the sequence
   SeqSteps q;
   long long row;    // before the head's first
-  long long left;   // steps of the run behind this unit
+  long long left;   // of the run's part of the line, behind this unit
 };
 __device__ __forceinline__ void enter_seq(const Params& P, Walk& w) {
   w.len = seq_len(P, w.b);
@@ -166,7 +178,7 @@ __device__ __forceinline__ bool next_unit(const Params& P, Walk& w) {
   w.row = head_row(P.c, w.b, w.hr / P.nrb);
   w.s = 0;
   w.end = (int)min((long long)w.q.n, w.left);
-  w.left -= w.end;
+  w.left -= line_len(w.q.n);
   return true;
 }
 
@@ -233,6 +245,21 @@ __device__ __forceinline__ void expand(uint32_t x, uint32_t s, uint32_t zb, uint
   a[3] = h2_fma(and_or<0x00F000F0u, 0x54005400u>(y), s, zs);
 }
 
+// Asks for a unit's query rows to be brought into L2, by one warp.
+template <int D, int NT>
+__device__ __forceinline__ void want_q(const Params& P, const Walk& w) {
+  constexpr int kLines = D / 64;  // of 128 bytes
+  const int h = w.hr / P.nrb, rb = w.hr - h * P.nrb;
+  const int x = threadIdx.x & 31, r = rb * 8 * NT + x / kLines;
+  static_assert(8 * NT * kLines <= 32, "a line per lane");
+  if (x < 8 * NT * kLines && r < P.R) {
+    const int hh = r / P.Tq, tok = r - hh * P.Tq;
+    const __nv_bfloat16* p = P.q + (((long long)w.b * P.Tq + tok) * P.Hq + h * P.G + hh) * D +
+                             x % kLines * 64;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+  }
+}
+
 // Starts the copies of the round that begins at w.s into a stage.
 template <int D, int NT>
 __device__ __forceinline__ void load_round(const Params& P, const Walk& w, uint32_t stage,
@@ -288,38 +315,36 @@ decode_kv4_kernel(const Params P) {
   }
   if (warp == 0) {
     const int per_seq = P.c.H * P.nrb;
-    const long long T = total_steps_warp(P) * per_seq;
-    const long long N = active_ctas(P, T);
+    long long ends = line_ends(P, 0, per_seq);
+    long long T = __shfl_sync(0xffffffffu, ends, 31);
+    for (int b = 32; b < P.c.B; b += 32)
+      T += __shfl_sync(0xffffffffu, line_ends(P, b, per_seq), 31);
+    const long long want = (T + kWarps - 1) / kWarps;
+    const unsigned N = (unsigned)min(want, (long long)P.grid);
     long long first = 0, count = 0;
     if (blockIdx.x < N) {
-      first = T * blockIdx.x / N;
-      count = T * (blockIdx.x + 1) / N - first;
+      first = scaled(T, blockIdx.x, N);
+      count = scaled(T, blockIdx.x + 1, N) - first;
     }
-    // the sequence that holds step `first`: sums over 32 sequences at a time
+    // the sequence that holds `first`
     int b0 = 0;
     long long before = 0;
     if (count > 0) {
-      for (;; b0 += 32) {
-        const int b = b0 + lane;
-        long long n = b < P.c.B ? (long long)seq_steps(P, seq_len(P, b)).n * per_seq : 0;
-        long long inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += x;
-        }
-        const unsigned over = __ballot_sync(0xffffffffu, before + inc > first);
+      for (;;) {
+        const unsigned over = __ballot_sync(0xffffffffu, before + ends > first);
         if (over) {
           const int src = __ffs(over) - 1;
-          before += __shfl_sync(0xffffffffu, inc - n, src);
+          if (src > 0) before += __shfl_sync(0xffffffffu, ends, src - 1);
           b0 += src;
           break;
         }
-        before += __shfl_sync(0xffffffffu, inc, 31);
-        if (b0 + 32 >= P.c.B) {  // not reached: first < T
+        before += __shfl_sync(0xffffffffu, ends, 31);
+        b0 += 32;
+        if (b0 >= P.c.B) {  // not reached: first < T
           count = 0;
           break;
         }
+        ends = line_ends(P, b0, per_seq);
       }
     }
     if (lane == 0) {
@@ -335,13 +360,19 @@ decode_kv4_kernel(const Params P) {
   {
     cur.b = (int)run[2];
     enter_seq(P, cur);
-    const int n = cur.q.n;
-    cur.hr = (int)(run[0] / n);
+    const int n = cur.q.n, ln = line_len(n);
+    cur.hr = run[0] <= 0xffffffffLL ? (int)((unsigned)run[0] / ln) : (int)(run[0] / ln);
+    const int at = (int)(run[0] - (long long)cur.hr * ln);
     cur.row = head_row(P.c, cur.b, cur.hr / P.nrb);
-    cur.s = (int)(run[0] - (long long)cur.hr * n);
-    cur.end = (int)min((long long)n, cur.s + run[1]);
-    cur.left = run[1] - (cur.end - cur.s);
+    cur.s = at;
+    cur.end = (int)min((long long)n, at + run[1]);
+    cur.left = run[1] - (ln - at);
+    // the run may begin behind a unit's last step, and end there too
+    if (at >= n && !next_unit(P, cur)) return;
   }
+  // Q is fetched ahead of use, and here ahead of the copies that it would
+  // otherwise queue behind (2 us)
+  if (warp == 0) want_q<D, NT>(P, cur);
   // the copies run kStages rounds ahead of the computation, over the ends of
   // units; the warps issue them in turn
   Walk pre = cur;
@@ -356,7 +387,10 @@ decode_kv4_kernel(const Params P) {
     }
     ++issued;
     pre.s += kWarps;
-    if (pre.s >= pre.end) more = next_unit(P, pre);
+    if (pre.s >= pre.end) {
+      more = next_unit(P, pre);
+      if (more && warp == issued % kWarps) want_q<D, NT>(P, pre);
+    }
   };
 #pragma unroll
   for (int st = 0; st < kStages; ++st)
