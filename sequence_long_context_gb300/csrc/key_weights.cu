@@ -22,15 +22,18 @@
 // buffers left the tensor core and the exponentials idle two thirds of the
 // time (8K prompt, zigzag ring of 8: 314 us with one buffer per key tile of
 // 512 keys, 320 with keys in tensor memory and 64 columns).
-// Roles (608 threads):
+// Roles (640 threads):
 //   warps 0-15 softmax: warp w takes keys [32 (w & 7), + 32) and the query
 //              tiles of parity w >> 3
-//   warp 16    producer: finds the query tiles that can see the item's keys (32
-//              at a time, one per lane), loads K (a ring of three tiles, the
-//              next item's ahead of time), Q (three slots) and, with all
-//              lanes, the tile's LSE (asked for one tile ahead) and positions
-//   warps 17, 18  MMA issuers, one per key tile (what a warp waits between its
-//              products the other fills); 17 owns tensor memory
+//   warp 16    items and keys: counts the query tiles that can see an item's
+//              keys (32 at a time, one per lane), publishes the item and loads
+//              its K (a ring of three tiles, the next item's ahead of time)
+//   warp 17    queries: loads an item's Q tiles (three slots) and, with all
+//              lanes, their LSE (asked for one tile ahead) and positions. (One
+//              warp for 16 and 17 took 4.2 us per item, which with few
+//              queries was all the time there is.)
+//   warps 18, 19  MMA issuers, one per key tile (what a warp waits between its
+//              products the other fills); 18 owns tensor memory
 // Positions are read per query from shared memory, so a tile may cross chunk
 // and shard boundaries: any layout and any length has this kernel.
 //
@@ -59,8 +62,9 @@ constexpr int kQT = 128;            // queries per tile
 constexpr int kKT = 2;              // key tiles per item
 constexpr int kKeys = kKT * kTile;  // keys per item
 constexpr int kSoftWarps = 8 * kKT; // two groups of four per key tile
-constexpr int kProducerWarp = kSoftWarps;
-constexpr int kMmaWarp = kProducerWarp + 1;
+constexpr int kKeyWarp = kSoftWarps;
+constexpr int kQueryWarp = kKeyWarp + 1;
+constexpr int kMmaWarp = kQueryWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + kKT);
 // Tiles of K and Q in shared memory: three each, or four of K and two of Q
 // where an item has no more than two query tiles (its loads are what counts
@@ -90,7 +94,8 @@ struct WeightParams {
   AttnParams P;
   float* part;   // [parts][Bt][Hkv][S]
   int observe;   // 0: all
-  int hpi;       // query heads per CTA
+  int hpi;       // query heads per item
+  int groups;    // items per KV head, key block and segment: G / hpi
   int nseg;      // segments of query tiles
   int tps;       // query tiles per segment
   int nkb;       // key blocks
@@ -143,7 +148,7 @@ struct ItemPos {
 __device__ __forceinline__ ItemPos item_pos(const WeightParams& W, int item) {
   const AttnParams& P = W.P;
   // key blocks outermost: with a causal mask the heaviest (first) start first
-  const int groups = P.G / W.hpi;  // items per KV head, key block and segment
+  const int groups = W.groups;
   ItemPos r;
   r.part = r.g = r.bt = 0;
   if (groups * W.nseg > 1) {
@@ -253,7 +258,7 @@ __device__ __forceinline__ int classify_tile(const WeightParams& W, int qt, cons
   const int p0 = W.q0 + qt * kQT;
   const PosRange q = row_bounds(P, p0, kQT);
   if (q.lo > q.hi || q.hi < b.q.lo || q.lo > b.q.hi) return kClsEmpty;
-  bool all = true;  // rows behind S have no position, which the producer sees
+  bool all = true;  // rows behind S have no position, which the query warp sees
   if (W.observe > 0) {
     if (P.cu == nullptr) {
       if (q.hi < P.S - W.observe) return kClsEmpty;
@@ -275,7 +280,7 @@ __device__ __forceinline__ int classify_tile(const WeightParams& W, int qt, cons
   return all ? kClsFull : kClsMasked;
 }
 
-// 19 warps: five share a 16K-register sub-partition, so <= 102 each (96 in the
+// 20 warps: five share a 16K-register sub-partition, so <= 102 each (96 in the
 // allocation's steps of 8).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -297,7 +302,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
   const int qslots = W.qslots, kslots = W.kslots;
   const uint32_t q_at = sbase + kslots * L::kTileBytes;  // the Q tiles
 
-  if (warp == kProducerWarp && lane == 0) {
+  if (warp == kKeyWarp && lane == 0) {
     for (int s = 0; s < kKSlots; ++s) {
       mbar_init(bar(L::kKFull + s), 1);
       mbar_init(bar(L::kKFree + s), 1);
@@ -314,7 +319,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(L::kItemFull + s), 1);
-      mbar_init(bar(L::kItemFree + s), kSoftWarps + kKT);  // and the MMA warps
+      mbar_init(bar(L::kItemFree + s), kSoftWarps + kKT + 1);  // MMA, queries
       for (int a = 0; a < kKT; ++a) mbar_init(bar(L::kJoinFull + kKT * s + a), 4);
     }
     for (int a = 0; a < kKT; ++a) mbar_init(bar(L::kMmaDone + a), 1);
@@ -332,16 +337,20 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp == kProducerWarp) {
-    // ------------------------------------------------------------ producer
+  // query tiles of an item's segment that may see its keys
+  auto tiles_of = [&](const ItemPos& ip, const KeyBlock& blk, int& first, int& last) {
+    first = ip.seg * W.tps;
+    last = min(W.ntiles, first + W.tps);
+    if (P.layout == kContiguous) {  // rank-major order is natural order
+      first = max(first, (blk.q.lo - W.q0) / kQT);  // (towards 0: an extra tile is skipped)
+      last = blk.q.hi < W.q0 ? 0 : min(last, (blk.q.hi - W.q0) / kQT + 1);
+    }
+  };
+  if (warp == kKeyWarp) {
+    // ------------------------------------------------------- items and keys
     bool ok = true;
-    int n = 0, slot = 0, phase = 1;      // Q tiles (the first waits are skipped)
-    int kn = 0, kslot = 0, kphase = 1;   // K tiles
-    int it = 0;                          // items
-    const int step = P.layout == kStripe ? P.cp : 1;
-    const int run = P.layout == kZigzag ? P.chunk : P.shard;
-    const int from = W.observe > 0 ? P.S - W.observe : 0;
-    for (; ok; ++it) {
+    int kn = 0, kslot = 0, kphase = 1;  // K tiles (the first waits are skipped)
+    for (int it = 0; ok; ++it) {
       // the items are sorted by their work as far as the mask goes: there and
       // back, every CTA gets its share
       const long long at = (long long)it * gridDim.x +
@@ -350,11 +359,8 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       const bool end = at >= W.items;
       const ItemPos ip = item_pos(W, end ? 0 : item);
       const KeyBlock blk = key_block(P, ip.key0);
-      int first = ip.seg * W.tps, last = min(W.ntiles, first + W.tps);
-      if (P.layout == kContiguous) {  // rank-major order is natural order
-        first = max(first, (blk.q.lo - W.q0) / kQT);  // (towards 0: an extra tile is skipped)
-        last = blk.q.hi < W.q0 ? 0 : min(last, (blk.q.hi - W.q0) / kQT + 1);
-      }
+      int first, last;
+      tiles_of(ip, blk, first, last);
       int tiles = 0;
       for (int base = first; base < last; base += 32)
         tiles += __popc(__ballot_sync(
@@ -387,7 +393,30 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           kphase ^= 1;
         }
       }
-      if (!ok) break;
+    }
+    // aborted: the copies in flight land before the CTA ends
+    if (lane == 0 && *abort_flag)
+      for (int i = kn > kslots ? kn - kslots : 0; i < kn; ++i)
+        mbar_wait_drain(bar(L::kKFull + i % kslots), (i / kslots) & 1);
+  } else if (warp == kQueryWarp) {
+    // ------------------------------------------------------------- queries
+    bool ok = true;
+    int n = 0, slot = 0, phase = 1;  // Q tiles (the first waits are skipped)
+    const int step = P.layout == kStripe ? P.cp : 1;
+    const int run = P.layout == kZigzag ? P.chunk : P.shard;
+    const int from = W.observe > 0 ? P.S - W.observe : 0;
+    for (int it = 0; ok; ++it) {
+      ok = mbar_wait(bar(L::kItemFull + (it & 1)), (it >> 1) & 1, abort_flag, status);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const int count = record[it & 1].count;
+      const ItemPos ip = item_pos(W, record[it & 1].item);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kItemFree + (it & 1)));  // the record has been read
+      if (count == kEnd) break;
+      if (count == 0) continue;
+      const KeyBlock blk = key_block(P, ip.key0);
+      int first, last;
+      tiles_of(ip, blk, first, last);
       // The next (tile, head), its rows' positions and LSE. This runs once per
       // tile in one warp, so it is kept short: what takes divisions is found
       // for 32 tiles at a time, one per lane.
@@ -487,12 +516,9 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       }
     }
     // aborted: the copies in flight land before the CTA ends
-    if (lane == 0 && *abort_flag) {
+    if (lane == 0 && *abort_flag)
       for (int i = n > qslots ? n - qslots : 0; i < n; ++i)
         mbar_wait_drain(bar(L::kQFull + i % qslots), (i / qslots) & 1);
-      for (int i = kn > kslots ? kn - kslots : 0; i < kn; ++i)
-        mbar_wait_drain(bar(L::kKFull + i % kslots), (i / kslots) & 1);
-    }
   } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------ MMA issuers
     // Every lane runs the loop and one elected lane issues: the descriptors
@@ -860,7 +886,7 @@ usp_status_t launch_key_weights_tc(const AttnParams& P, float* weight, int obser
   const Cut c = cut_of(P.Bt, P.S, P.Hq, P.Hkv, observe, P.layout == kContiguous && !P.cu,
                        P.cu != nullptr);
   WeightParams W{P, c.parts > 1 ? static_cast<float*>(workspace) : weight,
-                 observe < P.S ? observe : 0, c.hpi, c.nseg, c.tps, c.nkb, c.q0, c.ntiles, 1, 3, 3, 0};
+                 observe < P.S ? observe : 0, c.hpi, P.G / c.hpi, c.nseg, c.tps, c.nkb, c.q0, c.ntiles, 1, 3, 3, 0};
   if (c.ntiles == 1 && P.S - c.q0 <= 64 && c.hpi % 2 == 0) W.pair = 2;
   if (c.ntiles * (c.hpi / W.pair) <= 2) {
     W.qslots = 2;
@@ -884,7 +910,7 @@ usp_status_t launch_key_weights_tc(const AttnParams& P, float* weight, int obser
 
 usp_status_t launch_key_weights_simt(const AttnParams& P, float* weight, int observe, int bf16,
                                      cudaStream_t st) {
-  WeightParams W{P, nullptr, observe, P.G, 1, 0, 0, 0};
+  WeightParams W{P, nullptr, observe, P.G, 1, 1, 0, 0, 0};
   const dim3 grid((P.S + 63) / 64, P.Hkv, P.Bt);
   {
     ProfScope ps(st, "attn_key_weights_simt");
