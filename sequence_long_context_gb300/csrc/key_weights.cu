@@ -75,6 +75,7 @@ constexpr int kKSlots = 4;          // K tiles, at most
 constexpr int kSBufs = 4;           // score buffers of 128 columns
 constexpr int kRing = 16;           // entries of query statistics
 constexpr int kCtas = 152;          // one per SM
+constexpr int kRecords = 4;         // items that the roles may be apart
 constexpr int kEnd = -1;
 constexpr int kNowhere = -(1 << 30);  // position of a row that is not observed
 constexpr float kLog2e = 1.4426950408889634f;
@@ -121,14 +122,15 @@ struct WSmem {
   static constexpr int kK = 0;                          // kslots tiles of K, then Q
   static constexpr int kStat = kTileSlots * kTileBytes;  // kRing x (-lse2[128], pos[128])
   static constexpr int kStatBytes = 2 * kQT * 4;
-  static constexpr int kJoin = kStat + kRing * kStatBytes;  // [2][kKeys] sums of group 1
-  static constexpr int kSched = kJoin + 2 * kKeys * 4;  // kRing ints: class | rows << 8
-  static constexpr int kItem = kSched + kRing * 4;      // [2] ItemRecord
-  static constexpr int kBar = kItem + 2 * 16;
+  static constexpr int kJoin = kStat + kRing * kStatBytes;  // [kRecords][kKeys] sums of group 1
+  static constexpr int kSched = kJoin + kRecords * kKeys * 4;  // kRing ints: class | rows << 8
+  static constexpr int kItem = kSched + kRing * 4;      // [kRecords] ItemRecord
+  static constexpr int kBar = kItem + kRecords * 16;
   static constexpr int kKFull = 0, kKFree = kKFull + kKSlots, kQFull = kKFree + kKSlots,
                        kQFree = kQFull + kSlots, kSFull = kQFree + kSlots,
-                       kSFree = kSFull + kSBufs, kItemFull = kSFree + kSBufs, kItemFree = kItemFull + 2,
-                       kJoinFull = kItemFree + 2 /* [2][kKT] */, kMmaDone = kJoinFull + 2 * kKT,
+                       kSFree = kSFull + kSBufs, kItemFull = kSFree + kSBufs, kItemFree = kItemFull + kRecords,
+                       kJoinFull = kItemFree + kRecords /* [kRecords][kKT] */,
+                       kMmaDone = kJoinFull + kRecords * kKT,
                        kNumBars = kMmaDone + kKT;
   static constexpr int kMisc = (kBar + 8 * kNumBars + 15) / 16 * 16;
   static constexpr int kBytes = kMisc + 16;
@@ -317,7 +319,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       mbar_init(bar(L::kSFull + s), 2);
       mbar_init(bar(L::kSFree + s), 4);  // the four warps that take it
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kRecords; ++s) {
       mbar_init(bar(L::kItemFull + s), 1);
       mbar_init(bar(L::kItemFree + s), kSoftWarps + kKT + 1);  // MMA, queries
       for (int a = 0; a < kKT; ++a) mbar_init(bar(L::kJoinFull + kKT * s + a), 4);
@@ -365,14 +367,15 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       for (int base = first; base < last; base += 32)
         tiles += __popc(__ballot_sync(
             0xffffffffu, base + lane < last && classify_tile(W, base + lane, blk) != kClsEmpty));
-      if (it >= 2) {  // every role is done with the record's previous item
-        ok = mbar_wait(bar(L::kItemFree + (it & 1)), ((it >> 1) - 1) & 1, abort_flag, status);
+      const int rec = it % kRecords;
+      if (it >= kRecords) {  // every role is done with the record's previous item
+        ok = mbar_wait(bar(L::kItemFree + rec), (it / kRecords - 1) & 1, abort_flag, status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
       }
       if (lane == 0) {
-        record[it & 1].count = end ? kEnd : tiles * (W.hpi / W.pair);
-        record[it & 1].item = item;
-        mbar_arrive(bar(L::kItemFull + (it & 1)));
+        record[rec].count = end ? kEnd : tiles * (W.hpi / W.pair);
+        record[rec].item = item;
+        mbar_arrive(bar(L::kItemFull + rec));
       }
       if (end) break;
       if (tiles == 0) continue;
@@ -406,12 +409,13 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     const int run = P.layout == kZigzag ? P.chunk : P.shard;
     const int from = W.observe > 0 ? P.S - W.observe : 0;
     for (int it = 0; ok; ++it) {
-      ok = mbar_wait(bar(L::kItemFull + (it & 1)), (it >> 1) & 1, abort_flag, status);
+      const int rec = it % kRecords;
+      ok = mbar_wait(bar(L::kItemFull + rec), (it / kRecords) & 1, abort_flag, status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      const int count = record[it & 1].count;
-      const ItemPos ip = item_pos(W, record[it & 1].item);
+      const int count = record[rec].count;
+      const ItemPos ip = item_pos(W, record[rec].item);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kItemFree + (it & 1)));  // the record has been read
+      if (lane == 0) mbar_arrive(bar(L::kItemFree + rec));  // the record has been read
       if (count == kEnd) break;
       if (count == 0) continue;
       const KeyBlock blk = key_block(P, ip.key0);
@@ -534,10 +538,11 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     bool ok = true;
     int n = 0, slot = 0, phase = 0, kn = 0, si = 0;
     for (int it = 0; ok; ++it) {
-      ok = mbar_wait(bar(L::kItemFull + (it & 1)), (it >> 1) & 1, abort_flag, status);
+      const int rec = it % kRecords;
+      ok = mbar_wait(bar(L::kItemFull + rec), (it / kRecords) & 1, abort_flag, status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      const int count = __shfl_sync(0xffffffffu, record[it & 1].count, 0);
-      const int item = __shfl_sync(0xffffffffu, record[it & 1].item, 0);
+      const int count = __shfl_sync(0xffffffffu, record[rec].count, 0);
+      const int item = __shfl_sync(0xffffffffu, record[rec].item, 0);
       if (count == kEnd) break;
       const int ktiles = item_pos(W, item).ktiles;
       for (int j = 0; j < count && ok; ++j, ++n) {
@@ -578,7 +583,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       if (count > 0) kn += ktiles;
       si += count * ktiles;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kItemFree + (it & 1)));
+      if (lane == 0) mbar_arrive(bar(L::kItemFree + rec));
     }
     if (elect_one()) mma_commit(bar(L::kMmaDone + a));
     mbar_wait_drain(bar(L::kMmaDone + a), 0);
@@ -588,11 +593,13 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint64_t sc2 = f2_pack(P.scale_log2, P.scale_log2);
     bool ok = true;
-    int n = 0, si = 0, joins[2] = {0, 0};
+    int n = 0, si = 0;
+    unsigned joins = 0;  // a bit per record: the phase of its sums
     for (int it = 0; ok; ++it) {
-      ok = mbar_wait(bar(L::kItemFull + (it & 1)), (it >> 1) & 1, abort_flag, status);
+      const int rec = it % kRecords;
+      ok = mbar_wait(bar(L::kItemFull + rec), (it / kRecords) & 1, abort_flag, status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      const int count = record[it & 1].count, item = record[it & 1].item;
+      const int count = record[rec].count, item = record[rec].item;
       if (count == kEnd) break;
       const ItemPos ip = item_pos(W, item);
       if (a < ip.ktiles) {
@@ -657,31 +664,31 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           }
         }
         if (!ok) break;
-        // the two groups' sums; a buffer is used again two items on, which
-        // start when every role is done with this one
+        // the two groups' sums; a buffer is used again with the item's record,
+        // when every role is done with this one
         float x, y;
         f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), x, y);
-        float* join = reinterpret_cast<float*>(sm + L::kJoin) + (it & 1) * kKeys;
+        float* join = reinterpret_cast<float*>(sm + L::kJoin) + rec * kKeys;
         const int at = (warp & 7) * 32 + lane;
         if (group == 1) {
           join[at] = x + y;
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::kJoinFull + kKT * (it & 1) + a));
+          if (lane == 0) mbar_arrive(bar(L::kJoinFull + kKT * rec + a));
         }
         // (the count of these phases is kept by both groups alike: one per item
         // with this key tile and this parity)
         if (group == 0) {
-          ok = mbar_wait(bar(L::kJoinFull + kKT * (it & 1) + a), joins[it & 1] & 1, abort_flag, status);
+          ok = mbar_wait(bar(L::kJoinFull + kKT * rec + a), (joins >> rec) & 1, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           if (kp < P.S)
             W.part[(((long long)ip.part * P.Bt + ip.bt) * P.Hkv + ip.g) * P.S + kp] = x + y + join[at];
         }
-        ++joins[it & 1];
+        joins ^= 1u << rec;
       }
       n += count;
       si += count * ip.ktiles;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kItemFree + (it & 1)));
+      if (lane == 0) mbar_arrive(bar(L::kItemFree + rec));
     }
   }
   tc_fence_before();
