@@ -12,7 +12,10 @@
 // work is 256 keys (two tiles of 128) of one KV head with the query tiles of
 // 128 that may see them, for some of the group's query heads and a segment of
 // the queries; one CTA per SM takes items in turn, and its roles run ahead of
-// one another across items.
+// one another across items. Where an item's query tiles fit beside the keys
+// (few observed queries) they stay, and an item is a run of key blocks: 64
+// observed queries of a 32K prompt, 32 heads of 8, take 27 us (2.5 TB/s), and 36
+// with their queries and statistics prepared anew for every 256 keys.
 // What bounds it: per 128 x 128 tile (D = 128) the products take 512 clocks
 // (616 with both operands from shared memory, 64 KB), the exponentials (32 per
 // clock and SM) 512, and what a tile needs besides, waits on barriers and
@@ -20,15 +23,17 @@
 // four 128-column buffers (all of tensor memory) and each key tile two groups
 // of softmax warps, which take its query tiles in turn: fewer or smaller
 // buffers left the tensor core and the exponentials idle two thirds of the
-// time (8K prompt, zigzag ring of 8: 314 us with one buffer per key tile of
-// 512 keys, 320 with keys in tensor memory and 64 columns).
+// time (8K prompt, zigzag ring of 8, 32 heads of 8: 262 us, 1.05 PFLOP/s; 314
+// with one buffer per key tile of 512 keys, 320 with keys in tensor memory and
+// 64 columns). A 128 x 256 tile now takes 1.15 us, the exponentials half of it:
+// a warp that reads its next scores ahead needs code that is slower (below).
 // Roles (640 threads):
 //   warps 0-15 softmax: warp w takes keys [32 (w & 7), + 32) and the query
 //              tiles of parity w >> 3
 //   warp 16    items and keys: counts the query tiles that can see an item's
 //              keys (32 at a time, one per lane), publishes the item and loads
-//              its K (a ring of three tiles, the next item's ahead of time)
-//   warp 17    queries: loads an item's Q tiles (three slots) and, with all
+//              its K (a ring of two to four tiles, the next block's ahead of time)
+//   warp 17    queries: loads an item's Q tiles (two to four slots) and, with all
 //              lanes, their LSE (asked for one tile ahead) and positions. (One
 //              warp for 16 and 17 took 4.2 us per item, which with few
 //              queries was all the time there is.)
@@ -66,16 +71,18 @@ constexpr int kKeyWarp = kSoftWarps;
 constexpr int kQueryWarp = kKeyWarp + 1;
 constexpr int kMmaWarp = kQueryWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + kKT);
-// Tiles of K and Q in shared memory: three each, or four of K and two of Q
-// where an item has no more than two query tiles (its loads are what counts
-// then, and the next item's keys wait for no slot).
+// Tiles of K and Q in shared memory: three each; where no item has more than two
+// query tiles two of Q and four of K, and where none has more than four, four of
+// Q and two of K. An item's query tiles then stay while a run of key blocks
+// passes, if they are the same tiles for all of them.
 constexpr int kTileSlots = 6;
-constexpr int kSlots = 3;           // Q tiles, at most
+constexpr int kSlots = 4;           // Q tiles, at most
 constexpr int kKSlots = 4;          // K tiles, at most
 constexpr int kSBufs = 4;           // score buffers of 128 columns
 constexpr int kRing = 16;           // entries of query statistics
 constexpr int kCtas = 152;          // one per SM
 constexpr int kRecords = 4;         // items that the roles may be apart
+constexpr int kJoins = 2;           // key blocks that the softmax groups may be apart
 constexpr int kEnd = -1;
 constexpr int kNowhere = -(1 << 30);  // position of a row that is not observed
 constexpr float kLog2e = 1.4426950408889634f;
@@ -105,6 +112,7 @@ struct WeightParams {
   int ntiles;    // query tiles
   int pair;      // 2: one tile of at most 64 rows, two heads share the 128; else 1
   int qslots, kslots;
+  int run;       // key blocks per item
   int items;
 };
 
@@ -122,15 +130,16 @@ struct WSmem {
   static constexpr int kK = 0;                          // kslots tiles of K, then Q
   static constexpr int kStat = kTileSlots * kTileBytes;  // kRing x (-lse2[128], pos[128])
   static constexpr int kStatBytes = 2 * kQT * 4;
-  static constexpr int kJoin = kStat + kRing * kStatBytes;  // [kRecords][kKeys] sums of group 1
-  static constexpr int kSched = kJoin + kRecords * kKeys * 4;  // kRing ints: class | rows << 8
+  static constexpr int kJoin = kStat + kRing * kStatBytes;  // [kJoins][kKeys] sums of group 0
+  static constexpr int kSched = kJoin + kJoins * kKeys * 4;  // kRing ints: class | rows << 8
   static constexpr int kItem = kSched + kRing * 4;      // [kRecords] ItemRecord
   static constexpr int kBar = kItem + kRecords * 16;
   static constexpr int kKFull = 0, kKFree = kKFull + kKSlots, kQFull = kKFree + kKSlots,
                        kQFree = kQFull + kSlots, kSFull = kQFree + kSlots,
                        kSFree = kSFull + kSBufs, kItemFull = kSFree + kSBufs, kItemFree = kItemFull + kRecords,
-                       kJoinFull = kItemFree + kRecords /* [kRecords][kKT] */,
-                       kMmaDone = kJoinFull + kRecords * kKT,
+                       kJoinFull = kItemFree + kRecords /* [kJoins][kKT] */,
+                       kJoinFree = kJoinFull + kJoins * kKT,
+                       kMmaDone = kJoinFree + kJoins * kKT,
                        kNumBars = kMmaDone + kKT;
   static constexpr int kMisc = (kBar + 8 * kNumBars + 15) / 16 * 16;
   static constexpr int kBytes = kMisc + 16;
@@ -145,8 +154,13 @@ struct ItemRecord {
   int count, item, pad[2];
 };
 struct ItemPos {
-  int part, g, bt, key0, h0, seg, ktiles;
+  int part, g, bt, key0, h0, seg;
+  int blocks;  // of keys
 };
+// Key tiles of the block at key0 with keys in them.
+__device__ __forceinline__ int ktiles_of(const AttnParams& P, int key0) {
+  return min(kKT, (P.S - key0 + kTile - 1) / kTile);
+}
 __device__ __forceinline__ ItemPos item_pos(const WeightParams& W, int item) {
   const AttnParams& P = W.P;
   // key blocks outermost: with a causal mask the heaviest (first) start first
@@ -166,11 +180,11 @@ __device__ __forceinline__ ItemPos item_pos(const WeightParams& W, int item) {
     item /= P.Bt;
   }
   // ... in natural order, where a block of keys is one
-  r.key0 = item * kKeys;
+  r.key0 = item * W.run * kKeys;
+  r.blocks = min(W.run, W.nkb - item * W.run);
   if (P.layout == kZigzag && P.chunk % kKeys == 0) r.key0 = permuted_of(P, r.key0);
   r.seg = r.part / groups;
   r.h0 = r.g * P.G + (r.part - r.seg * groups) * W.hpi;
-  r.ktiles = min(kKT, (P.S - r.key0 + kTile - 1) / kTile);  // with keys in them
   return r;
 }
 
@@ -237,9 +251,9 @@ struct KeyBlock {
   PosRange q;     // of the queries that may see one of them
   int seg0, seg1; // packed sequences of the first and last key
 };
-__device__ __forceinline__ KeyBlock key_block(const AttnParams& P, int key0) {
+__device__ __forceinline__ KeyBlock key_block(const AttnParams& P, int key0, int blocks) {
   KeyBlock b;
-  b.k = row_bounds(P, key0, kKeys);
+  b.k = row_bounds(P, key0, blocks * kKeys);
   int s0 = 0, e1 = P.S;
   b.seg0 = b.seg1 = 0;
   if (P.cu != nullptr) {
@@ -322,7 +336,10 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     for (int s = 0; s < kRecords; ++s) {
       mbar_init(bar(L::kItemFull + s), 1);
       mbar_init(bar(L::kItemFree + s), kSoftWarps + kKT + 1);  // MMA, queries
-      for (int a = 0; a < kKT; ++a) mbar_init(bar(L::kJoinFull + kKT * s + a), 4);
+    }
+    for (int s = 0; s < kJoins * kKT; ++s) {
+      mbar_init(bar(L::kJoinFull + s), 4);
+      mbar_init(bar(L::kJoinFree + s), 4);
     }
     for (int a = 0; a < kKT; ++a) mbar_init(bar(L::kMmaDone + a), 1);
     *abort_flag = 0;
@@ -360,7 +377,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       const int item = (int)at;
       const bool end = at >= W.items;
       const ItemPos ip = item_pos(W, end ? 0 : item);
-      const KeyBlock blk = key_block(P, ip.key0);
+      const KeyBlock blk = key_block(P, ip.key0, ip.blocks);
       int first, last;
       tiles_of(ip, blk, first, last);
       int tiles = 0;
@@ -379,21 +396,24 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       }
       if (end) break;
       if (tiles == 0) continue;
-      for (int a = 0; a < ip.ktiles; ++a) {
-        if (kn >= kslots) {  // the slot's previous keys have been multiplied
-          ok = mbar_wait(bar(L::kKFree + kslot), kphase, abort_flag, status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        }
-        if (lane == 0) {
-          mbar_expect_tx(bar(L::kKFull + kslot), L::kTileBytes);
-          for (int hf = 0; hf < L::kHalves; ++hf)
-            tma_load_4d(sbase + L::kK + kslot * L::kTileBytes + hf * L::kHalf, &tm_k,
-                        bar(L::kKFull + kslot), hf * 64, ip.g, ip.key0 + a * kTile, ip.bt);
-        }
-        ++kn;
-        if (++kslot == kslots) {
-          kslot = 0;
-          kphase ^= 1;
+      for (int x = 0; ok && x < ip.blocks; ++x) {
+        const int key0 = ip.key0 + x * kKeys, ktiles = ktiles_of(P, key0);
+        for (int a = 0; ok && a < ktiles; ++a) {
+          if (kn >= kslots) {  // the slot's previous keys have been multiplied
+            ok = mbar_wait(bar(L::kKFree + kslot), kphase, abort_flag, status);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          }
+          if (lane == 0) {
+            mbar_expect_tx(bar(L::kKFull + kslot), L::kTileBytes);
+            for (int hf = 0; hf < L::kHalves; ++hf)
+              tma_load_4d(sbase + L::kK + kslot * L::kTileBytes + hf * L::kHalf, &tm_k,
+                          bar(L::kKFull + kslot), hf * 64, ip.g, key0 + a * kTile, ip.bt);
+          }
+          ++kn;
+          if (++kslot == kslots) {
+            kslot = 0;
+            kphase ^= 1;
+          }
         }
       }
     }
@@ -418,7 +438,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       if (lane == 0) mbar_arrive(bar(L::kItemFree + rec));  // the record has been read
       if (count == kEnd) break;
       if (count == 0) continue;
-      const KeyBlock blk = key_block(P, ip.key0);
+      const KeyBlock blk = key_block(P, ip.key0, ip.blocks);
       int first, last;
       tiles_of(ip, blk, first, last);
       // The next (tile, head), its rows' positions and LSE. This runs once per
@@ -544,44 +564,52 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       const int count = __shfl_sync(0xffffffffu, record[rec].count, 0);
       const int item = __shfl_sync(0xffffffffu, record[rec].item, 0);
       if (count == kEnd) break;
-      const int ktiles = item_pos(W, item).ktiles;
-      for (int j = 0; j < count && ok; ++j, ++n) {
-        ok = mbar_wait(bar(L::kQFull + slot), phase, abort_flag, status);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        const int rows = __shfl_sync(0xffffffffu, sched[n & (kRing - 1)], 0) >> 8;
-        const uint32_t id = rows > 64 ? kId128 : kId64;
-        if (a < ktiles) {
-          const int ks = (kn + a) % kslots, sj = si + j * ktiles + a, buf = sj % kSBufs;
-          if (j == 0) ok = mbar_wait(bar(L::kKFull + ks), ((kn + a) / kslots) & 1, abort_flag, status);
-          // the buffer's previous scores have been taken out
-          if (ok && sj >= kSBufs)
-            ok = mbar_wait(bar(L::kSFree + buf), (sj / kSBufs - 1) & 1, abort_flag, status);
+      const ItemPos ip = item_pos(W, item);
+      const int slot0 = slot, phase0 = phase;
+      for (int x = 0; x < ip.blocks && count > 0 && ok; ++x) {
+        const int ktiles = ktiles_of(P, ip.key0 + x * kKeys);
+        const bool last = x + 1 == ip.blocks;
+        slot = slot0;
+        phase = phase0;
+        for (int j = 0; j < count && ok; ++j) {
+          ok = mbar_wait(bar(L::kQFull + slot), phase, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          if (lane == 0) mbar_arrive(bar(L::kSFull + buf));
-          tc_fence_after();
-          const uint64_t da = sdesc_add(dk, ks * L::kTileBytes);
-          const uint64_t db = sdesc_add(dq, slot * L::kTileBytes);
-          if (elect_one()) {
+          const int rows = __shfl_sync(0xffffffffu, sched[(n + j) & (kRing - 1)], 0) >> 8;
+          const uint32_t id = rows > 64 ? kId128 : kId64;
+          if (a < ktiles) {
+            const int ks = (kn + a) % kslots, sj = si + j * ktiles + a, buf = sj % kSBufs;
+            if (j == 0) ok = mbar_wait(bar(L::kKFull + ks), ((kn + a) / kslots) & 1, abort_flag, status);
+            // the buffer's previous scores have been taken out
+            if (ok && sj >= kSBufs)
+              ok = mbar_wait(bar(L::kSFree + buf), (sj / kSBufs - 1) & 1, abort_flag, status);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (lane == 0) mbar_arrive(bar(L::kSFull + buf));
+            tc_fence_after();
+            const uint64_t da = sdesc_add(dk, ks * L::kTileBytes);
+            const uint64_t db = sdesc_add(dq, slot * L::kTileBytes);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * L::kHalf + (kk & 3) * 32;
-              mma_ss(t0 + 128 * buf, sdesc_add(da, off), sdesc_add(db, off), id, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * L::kHalf + (kk & 3) * 32;
+                mma_ss(t0 + 128 * buf, sdesc_add(da, off), sdesc_add(db, off), id, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(bar(L::kSFull + buf));
+              if (j + 1 == count) mma_commit(bar(L::kKFree + ks));
+              if (last) mma_commit(bar(L::kQFree + slot));
             }
-            mma_commit(bar(L::kSFull + buf));
-            if (j + 1 == count) mma_commit(bar(L::kKFree + ks));
-            mma_commit(bar(L::kQFree + slot));
+          } else if (last && lane == 0) {
+            mbar_arrive(bar(L::kQFree + slot));  // no such key tile
           }
-        } else if (lane == 0) {
-          mbar_arrive(bar(L::kQFree + slot));  // no such key tile
+          __syncwarp();
+          if (++slot == qslots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
-        __syncwarp();
-        if (++slot == qslots) {
-          slot = 0;
-          phase ^= 1;
-        }
+        kn += ktiles;
+        si += count * ktiles;
       }
-      if (count > 0) kn += ktiles;
-      si += count * ktiles;
+      n += count;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kItemFree + rec));
     }
@@ -593,8 +621,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint64_t sc2 = f2_pack(P.scale_log2, P.scale_log2);
     bool ok = true;
-    int n = 0, si = 0;
-    unsigned joins = 0;  // a bit per record: the phase of its sums
+    int n = 0, si = 0, joins = 0;
     for (int it = 0; ok; ++it) {
       const int rec = it % kRecords;
       ok = mbar_wait(bar(L::kItemFull + rec), (it / kRecords) & 1, abort_flag, status);
@@ -602,91 +629,101 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       const int count = record[rec].count, item = record[rec].item;
       if (count == kEnd) break;
       const ItemPos ip = item_pos(W, item);
-      if (a < ip.ktiles) {
-        const int kp = ip.key0 + (warp & 7) * 32 + lane;
-        Seen vis{1, 0};
-        if (kp < P.S) vis = seen_by(P, nat_pos(P, kp));
-        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-        for (int j = (n ^ group) & 1; j < count; j += 2) {
-          const int ring = (n + j) & (kRing - 1), sj = si + j * ip.ktiles + a, buf = sj % kSBufs;
-          ok = mbar_wait(bar(L::kSFull + buf), (sj / kSBufs) & 1, abort_flag, status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          tc_fence_after();
-          const uint32_t t_s = tmem + lane_off + 128 * buf;
-          const int entry = sched[ring], cls = entry & 255, rows = entry >> 8;
-          const float4* nlse = reinterpret_cast<const float4*>(sm + L::kStat + ring * L::kStatBytes);
-          auto add = [&](const uint32_t(&v)[32], const float4* nl) {
-            if (cls == kClsFull) {
+      for (int x = 0; x < ip.blocks; ++x) {
+        const int key0 = ip.key0 + x * kKeys, ktiles = ktiles_of(P, key0);
+        if (a < ktiles) {
+          const int kp = key0 + (warp & 7) * 32 + lane;
+          Seen vis{1, 0};
+          if (kp < P.S) vis = seen_by(P, nat_pos(P, kp));
+          uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+          for (int j = (n ^ group) & 1; j < count; j += 2) {
+            const int ring = (n + j) & (kRing - 1), sj = si + j * ktiles + a, buf = sj % kSBufs;
+            ok = mbar_wait(bar(L::kSFull + buf), (sj / kSBufs) & 1, abort_flag, status);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            const uint32_t t_s = tmem + lane_off + 128 * buf;
+            const int entry = sched[ring], cls = entry & 255, rows = entry >> 8;
+            const float4* nlse = reinterpret_cast<const float4*>(sm + L::kStat + ring * L::kStatBytes);
+            auto add = [&](const uint32_t(&v)[32], const float4* nl) {
+              if (cls == kClsFull) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float4 l = nl[k];
-                const uint32_t* s = &v[4 * k];
-                const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2,
-                                          f2_pack(l.x, l.y));
-                const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3])), sc2,
-                                          f2_pack(l.z, l.w));
-                float x0, x1, y0, y1;
-                f2_unpack(x, x0, x1);
-                f2_unpack(y, y0, y1);
-                sum[(2 * k) & 3] = f2_add(sum[(2 * k) & 3], f2_pack(ex2(x0), ex2(x1)));
-                sum[(2 * k + 1) & 3] = f2_add(sum[(2 * k + 1) & 3], f2_pack(ex2(y0), ex2(y1)));
-              }
-            } else {
-              const int4* pos = reinterpret_cast<const int4*>(nl + kQT / 4);
+                for (int k = 0; k < 8; ++k) {
+                  const float4 l = nl[k];
+                  const uint32_t* s = &v[4 * k];
+                  const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), sc2,
+                                            f2_pack(l.x, l.y));
+                  const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[2]), __uint_as_float(s[3])), sc2,
+                                            f2_pack(l.z, l.w));
+                  float x0, x1, y0, y1;
+                  f2_unpack(x, x0, x1);
+                  f2_unpack(y, y0, y1);
+                  sum[(2 * k) & 3] = f2_add(sum[(2 * k) & 3], f2_pack(ex2(x0), ex2(x1)));
+                  sum[(2 * k + 1) & 3] = f2_add(sum[(2 * k + 1) & 3], f2_pack(ex2(y0), ex2(y1)));
+                }
+              } else {
+                const int4* pos = reinterpret_cast<const int4*>(nl + kQT / 4);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float4 l = nl[k];
-                const int4 i = pos[k];
-                const uint32_t* s = &v[4 * k];
-                auto one = [&](uint32_t sv, float lv, int iv) {
-                  const float p = ex2(fmaf(__uint_as_float(sv), P.scale_log2, lv));
-                  return iv >= vis.lo && iv <= vis.hi ? p : 0.f;
-                };
-                sum[0] = f2_add(sum[0], f2_pack(one(s[0], l.x, i.x), one(s[1], l.y, i.y)));
-                sum[1] = f2_add(sum[1], f2_pack(one(s[2], l.z, i.z), one(s[3], l.w, i.w)));
+                for (int k = 0; k < 8; ++k) {
+                  const float4 l = nl[k];
+                  const int4 i = pos[k];
+                  const uint32_t* s = &v[4 * k];
+                  auto one = [&](uint32_t sv, float lv, int iv) {
+                    const float p = ex2(fmaf(__uint_as_float(sv), P.scale_log2, lv));
+                    return iv >= vis.lo && iv <= vis.hi ? p : 0.f;
+                  };
+                  sum[0] = f2_add(sum[0], f2_pack(one(s[0], l.x, i.x), one(s[1], l.y, i.y)));
+                  sum[1] = f2_add(sum[1], f2_pack(one(s[2], l.z, i.z), one(s[3], l.w, i.w)));
+                }
               }
-            }
-          };
-          // 32 columns at a time, one copy of the code. (With the next columns
-          // loaded ahead it spills, and takes 1.25 to 1.5 times as long: the
-          // other warps fill the time.)
-          uint32_t v[32];
+            };
+            // 32 columns at a time, one copy of the code. (With the next columns
+            // loaded ahead it spills, and takes 1.25 to 1.5 times as long; 16
+            // columns ahead of 16 do not spill, and take 1.05 times as long: the
+            // other warps fill the time.)
+            uint32_t v[32];
 #pragma unroll 1
-          for (int c = 0; c < rows; c += 32) {
-            tmem_ld32(t_s + c, v);
-            tmem_wait_ld();
-            if (c + 32 >= rows) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(L::kSFree + buf));
+            for (int c = 0; c < rows; c += 32) {
+              tmem_ld32(t_s + c, v);
+              tmem_wait_ld();
+              if (c + 32 >= rows) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::kSFree + buf));
+              }
+              add(v, nlse + c / 4);
             }
-            add(v, nlse + c / 4);
           }
+          if (!ok) break;
+          // the two groups' sums, which the second adds: with an even number of
+          // tiles the first is done first, and goes on without a wait (`joins`
+          // counts this key tile's blocks, alike in both groups)
+          float u, w;
+          f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), u, w);
+          const int jb = joins % kJoins * kKT + a;
+          float* join = reinterpret_cast<float*>(sm + L::kJoin) + joins % kJoins * kKeys;
+          const int at = (warp & 7) * 32 + lane;
+          if (group == 0) {
+            if (joins >= kJoins)  // the sums before have been read
+              ok = mbar_wait(bar(L::kJoinFree + jb), (joins / kJoins - 1) & 1, abort_flag, status);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            join[at] = u + w;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kJoinFull + jb));
+          } else {
+            ok = mbar_wait(bar(L::kJoinFull + jb), (joins / kJoins) & 1, abort_flag, status);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            const float other = join[at];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kJoinFree + jb));
+            if (kp < P.S)
+              W.part[(((long long)ip.part * P.Bt + ip.bt) * P.Hkv + ip.g) * P.S + kp] = u + w + other;
+          }
+          ++joins;
         }
-        if (!ok) break;
-        // the two groups' sums; a buffer is used again with the item's record,
-        // when every role is done with this one
-        float x, y;
-        f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), x, y);
-        float* join = reinterpret_cast<float*>(sm + L::kJoin) + rec * kKeys;
-        const int at = (warp & 7) * 32 + lane;
-        if (group == 1) {
-          join[at] = x + y;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::kJoinFull + kKT * rec + a));
-        }
-        // (the count of these phases is kept by both groups alike: one per item
-        // with this key tile and this parity)
-        if (group == 0) {
-          ok = mbar_wait(bar(L::kJoinFull + kKT * rec + a), (joins >> rec) & 1, abort_flag, status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          if (kp < P.S)
-            W.part[(((long long)ip.part * P.Bt + ip.bt) * P.Hkv + ip.g) * P.S + kp] = x + y + join[at];
-        }
-        joins ^= 1u << rec;
+        si += count * ktiles;
       }
+      if (!ok) break;
       n += count;
-      si += count * ip.ktiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kItemFree + rec));
     }
@@ -861,6 +898,22 @@ Cut cut_of(int B, int S, int Hq, int Hkv, int observe, bool tail, bool packed) {
   return c;
 }
 
+// Key blocks per item where an item's queries stay in shared memory: the fewest
+// steps of the busiest CTA, an item costing about as much besides as two blocks.
+int run_of(int nkb, long long heads) {
+  int best = 1;
+  long long least = -1;
+  for (int r = 1; r <= nkb && r <= 64; ++r) {
+    const long long items = (nkb + r - 1) / r * heads;
+    const long long t = (items + kCtas - 1) / kCtas * (r + 2);
+    if (least < 0 || t < least) {
+      least = t;
+      best = r;
+    }
+  }
+  return best;
+}
+
 template <int D>
 usp_status_t launch_tc(const WeightParams& W, cudaStream_t st) {
   const AttnParams& P = W.P;
@@ -893,13 +946,20 @@ usp_status_t launch_key_weights_tc(const AttnParams& P, float* weight, int obser
   const Cut c = cut_of(P.Bt, P.S, P.Hq, P.Hkv, observe, P.layout == kContiguous && !P.cu,
                        P.cu != nullptr);
   WeightParams W{P, c.parts > 1 ? static_cast<float*>(workspace) : weight,
-                 observe < P.S ? observe : 0, c.hpi, P.G / c.hpi, c.nseg, c.tps, c.nkb, c.q0, c.ntiles, 1, 3, 3, 0};
+                 observe < P.S ? observe : 0, c.hpi, P.G / c.hpi, c.nseg, c.tps, c.nkb, c.q0, c.ntiles, 1, 3, 3, 1, 0};
   if (c.ntiles == 1 && P.S - c.q0 <= 64 && c.hpi % 2 == 0) W.pair = 2;
-  if (c.ntiles * (c.hpi / W.pair) <= 2) {
+  const bool straight = P.layout == kContiguous && !P.cu;
+  const long long most = (long long)c.ntiles * (c.hpi / W.pair);  // query tiles of an item
+  if (most <= 2) {
     W.qslots = 2;
     W.kslots = 4;
+  } else if (most <= kSlots && straight) {
+    W.qslots = kSlots;
+    W.kslots = kTileSlots - kSlots;
   }
-  const long long items = (long long)c.nkb * P.Bt * P.Hkv * (P.G / c.hpi) * c.nseg;
+  const long long heads = (long long)P.Bt * P.Hkv * W.groups * c.nseg;
+  if (most <= W.qslots && straight) W.run = run_of(c.nkb, heads);
+  const long long items = (c.nkb + W.run - 1) / W.run * heads;
   if (items > 0x3fffffffLL) return USP_ERR_UNSUPPORTED;
   W.items = (int)items;
   usp_status_t r = P.D == 128 ? launch_tc<128>(W, st) : launch_tc<64>(W, st);

@@ -477,6 +477,47 @@ def test_key_weights_match_oracle(B, S, Hq, H, D, causal, window, sink, cp, layo
     assert (np.abs(w - want) <= bound + 1e-37).all(), (np.abs(w - want) / np.maximum(want, 1e-30)).max()
 
 
+@pytest.mark.parametrize("B,S,Hq,H,D,observe,window,sink", [
+    (1, 33333, 4, 2, 128, 64, 0, 0),       # two tiles of two heads each
+    (1, 20011, 8, 1, 64, 17, 0, 0),        # four
+    (2, 9000, 2, 1, 128, 130, 0, 0),       # two heads of two tiles
+    (1, 30000, 6, 2, 128, 90, 0, 0),       # three heads
+    (2, 9000, 3, 1, 128, 130, 0, 0),       # six tiles: no longer kept
+    (1, 16385, 2, 2, 128, 1, 0, 0),        # one query; one key in the last block
+    (1, 40000, 4, 4, 64, 100, 5000, 300),  # blocks between that nobody sees
+    (1, 70001, 1, 1, 64, 3, 0, 0),
+])
+def test_key_weights_of_few_queries_over_long_prompts(B, S, Hq, H, D, observe, window, sink):
+    """Runs of key blocks pass by an item's queries; the bound is that of the
+    comparison with the oracle."""
+    dev = device()
+    torch.manual_seed(S)
+    q = torch.randn(B, S, Hq, D, device=dev).to(torch.bfloat16)
+    k = torch.randn(B, S, H, D, device=dev).to(torch.bfloat16)
+    scale = 1 / np.sqrt(D)
+    i = torch.arange(S - observe, S, device=dev)[:, None]
+    j = torch.arange(S, device=dev)[None]
+    see = j <= i
+    if window:
+        see &= (i - j < window) | (j < sink)
+    lse = torch.full((B, Hq, S), float("nan"), device=dev)  # of the others: not read
+    want = torch.zeros(B, H, S, dtype=torch.float64, device=dev)
+    for b in range(B):
+        for h in range(Hq):
+            s = q[b, S - observe:, h].double() @ k[b, :, h // (Hq // H)].double().T * scale
+            s.masked_fill_(~see, -float("inf"))
+            lse[b, h, S - observe:] = s.logsumexp(-1).float()
+            want[b, h // (Hq // H)] += torch.exp(s - lse[b, h, S - observe:, None].double()).sum(0)
+    got = usp.attn_key_weights(q, k, lse, window=window, sink_tokens=sink, observe=observe)
+    usp.usp_device_status()
+    ds = D * U * scale * float(q.abs().max() * k.abs().max()) * D
+    top = float(lse[:, :, S - observe:].abs().max())
+    bound = want * (2 * ds + 4 * U * top + 2 * observe * Hq * U + 2.0 ** -20)
+    assert ((got.double() - want).abs() <= bound + 1e-37).all()
+    again = usp.attn_key_weights(q, k, lse, window=window, sink_tokens=sink, observe=observe)
+    assert torch.equal(got, again)
+
+
 def test_key_weights_of_the_librarys_own_forward():
     """Every observed query spreads a weight of one per head of its group."""
     dev = device()
