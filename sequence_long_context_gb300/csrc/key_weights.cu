@@ -83,6 +83,7 @@ constexpr int kRing = 16;           // entries of query statistics
 constexpr int kCtas = 152;          // one per SM
 constexpr int kRecords = 4;         // items that the roles may be apart
 constexpr int kJoins = 2;           // key blocks that the softmax groups may be apart
+constexpr int kDiag = 1 << 16;
 constexpr int kEnd = -1;
 constexpr int kNowhere = -(1 << 30);  // position of a row that is not observed
 constexpr float kLog2e = 1.4426950408889634f;
@@ -131,7 +132,7 @@ struct WSmem {
   static constexpr int kStat = kTileSlots * kTileBytes;  // kRing x (-lse2[128], pos[128])
   static constexpr int kStatBytes = 2 * kQT * 4;
   static constexpr int kJoin = kStat + kRing * kStatBytes;  // [kJoins][kKeys] sums of group 0
-  static constexpr int kSched = kJoin + kJoins * kKeys * 4;  // kRing ints: class | rows << 8
+  static constexpr int kSched = kJoin + kJoins * kKeys * 4;  // kRing ints: class | rows << 8 | kDiag
   static constexpr int kItem = kSched + kRing * 4;      // [kRecords] ItemRecord
   static constexpr int kBar = kItem + kRecords * 16;
   static constexpr int kKFull = 0, kKFree = kKFull + kKSlots, kQFull = kKFree + kKSlots,
@@ -514,12 +515,15 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           // a row that sees nothing adds nothing, whatever it holds: its
           // position is nowhere, and the tile's positions are looked at
           const bool none = cur.pos[e] < 0 || x == -INFINITY;
-          skips |= none;
+          skips |= cur.pos[e] >= 0 && none;
           st[lane + 32 * e] = none ? -INFINITY : -x;
           reinterpret_cast<int*>(st)[kQT + lane + 32 * e] = none ? kNowhere : cur.pos[e];
         }
         skips = __any_sync(0xffffffffu, skips);
-        if (lane == 0) sched[ring] = (skips ? kClsMasked : cur.cls) | rows << 8;
+        // where causality alone hides keys, of a run's last blocks only
+        const bool diag = !skips && W.run > 1 && P.causal && P.window == 0;
+        if (lane == 0)
+          sched[ring] = (skips ? kClsMasked : cur.cls) | rows << 8 | (diag ? kDiag : 0);
         __syncwarp();
         if (lane == 0) {
           // 64 rows at a time; the barrier stands for the ring's entry too
@@ -574,7 +578,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
         for (int j = 0; j < count && ok; ++j) {
           ok = mbar_wait(bar(L::kQFull + slot), phase, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          const int rows = __shfl_sync(0xffffffffu, sched[(n + j) & (kRing - 1)], 0) >> 8;
+          const int rows = __shfl_sync(0xffffffffu, sched[(n + j) & (kRing - 1)], 0) >> 8 & 255;
           const uint32_t id = rows > 64 ? kId128 : kId64;
           if (a < ktiles) {
             const int ks = (kn + a) % kslots, sj = si + j * ktiles + a, buf = sj % kSBufs;
@@ -642,8 +646,11 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
             const uint32_t t_s = tmem + lane_off + 128 * buf;
-            const int entry = sched[ring], cls = entry & 255, rows = entry >> 8;
             const float4* nlse = reinterpret_cast<const float4*>(sm + L::kStat + ring * L::kStatBytes);
+            const int entry = sched[ring], rows = entry >> 8 & 255;
+            int cls = entry & 255;
+            if ((entry & kDiag) && key0 + kKeys - 1 <= reinterpret_cast<const int*>(nlse)[kQT])
+              cls = kClsFull;  // before the tile's first query
             auto add = [&](const uint32_t(&v)[32], const float4* nl) {
               if (cls == kClsFull) {
 #pragma unroll
