@@ -35,8 +35,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 // keys of a CTA's part that fit beside the histograms with two CTAs per SM;
-// longer parts (beyond 8 x 20K tokens) are read again from L2 in each pass
-constexpr int kKeysInSmem = 20480;
+// longer parts (beyond 8 x 16K tokens) are read again from L2 in each pass
+constexpr int kKeysInSmem = 16384;
+// Where key i (a multiple of 4) of a warp's part stands: the 16-byte pieces of
+// 32 keys change places with the row, so that both ways of reading them (a warp
+// 128 in a row, or each lane 32 of its own) meet all banks.
+__device__ __forceinline__ int place(int i) { return i ^ (i >> 3 & 28); }
 
 // Larger float <=> larger key; +0 and -0 alike; a NaN above everything.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -62,6 +66,11 @@ __device__ __forceinline__ uint32_t peer_load(const uint32_t* p, uint32_t rank) 
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
+
+// A lane lists its kept keys by itself up to this many (about 10 instructions
+// each, one after the other; the 32 steps of the warp together take as long as
+// 12 of them).
+constexpr int kSparse = 12;
 
 struct EvictParams {
   Cache src, dst;
@@ -159,14 +168,14 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
 #pragma unroll 4
       for (int i = 4 * lane; i < n; i += 128) {
         const float4 x = __ldg(reinterpret_cast<const float4*>(w + first + i));
-        *reinterpret_cast<uint4*>(mine + i) =
+        *reinterpret_cast<uint4*>(mine + place(i)) =
             make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
       }
     }
     __syncthreads();
     // keys i .. i + 3 of the warp's part (i a multiple of 4)
     auto keys_at = [&](int i) {
-      if (in_smem) return *reinterpret_cast<const uint4*>(mine + i);
+      if (in_smem) return *reinterpret_cast<const uint4*>(mine + place(i));
       const float4 x = __ldg(reinterpret_cast<const float4*>(w + first + i));
       return make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
     };
@@ -191,17 +200,26 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
             if (i < c_hi) k = keys_at(i);
             key[4 * u] = k.x; key[4 * u + 1] = k.y; key[4 * u + 2] = k.z; key[4 * u + 3] = k.w;
           }
+          constexpr uint32_t kAll = (1u << kN) - 1u;
           uint32_t in = 0;
-          bool alike = true;
+#pragma unroll
+          for (int e = 0; e < kN; ++e) in |= ((key[e] & kMask[pass]) == prefix ? 1u : 0u) << e;
+          if (i0 < c_lo || i0 + 128 * kV > c_hi) {  // an end of the candidates
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+              const int i = i0 + 128 * (e >> 2) + 4 * lane + (e & 3);
+              if (i < c_lo || i >= c_hi) in &= ~(1u << e);
+            }
+          }
+          if (!__any_sync(0xffffffffu, in != 0)) return;
+          bool alike = in == kAll;
 #pragma unroll
           for (int e = 0; e < kN; ++e) {
-            const int i = i0 + 128 * (e >> 2) + 4 * lane + (e & 3);
-            if (i >= c_lo && i < c_hi && (key[e] & kMask[pass]) == prefix) in |= 1u << e;
             key[e] = (key[e] >> kShift[pass]) & bin_mask;
             alike = alike && key[e] == key[0];
           }
           // one addition where the whole warp agrees (runs of equal weights)
-          if (__all_sync(0xffffffffu, alike && in == (1u << kN) - 1u) &&
+          if (__all_sync(0xffffffffu, alike) &&
               __all_sync(0xffffffffu, key[0] == __shfl_sync(0xffffffffu, key[0], 0))) {
             if (lane == 0) atomicAdd(&s.hist[pass][key[0]], 32u * kN);
           } else {
@@ -226,25 +244,32 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
       }
     }
     const bool any = P.keep - P.sink - P.recent > 0;
-    // Of the 32 rows of 32 keys from i0 on, lane l gets row l's: kept for sure
-    // (sinks, recent, above the n-th largest), and equal to it.
+    // Of the lane's 32 keys from i0 + 32 lane on: those kept for sure (sinks,
+    // recent, above the n-th largest), and those equal to it.
     auto masks_at = [&](int i0, uint32_t& sure, uint32_t& tied) {
-      sure = tied = 0;
-      const int rows = min(32, (n - i0 + 31) / 32);
-#pragma unroll 4
-      for (int r = 0; r < rows; ++r) {
-        const int i = i0 + 32 * r + lane;
-        uint32_t key = 0;
-        if (any && i < n) key = in_smem ? mine[i] : order_key(__ldg(w + first + i));
-        const bool fixed = i < n && (i < c_lo || i >= c_hi);
-        const bool free = i >= c_lo && i < c_hi && any;
-        const uint32_t a = __ballot_sync(0xffffffffu, fixed || (free && key > prefix));
-        const uint32_t t = __ballot_sync(0xffffffffu, free && key == prefix);
-        if (lane == r) {
-          sure = a;
-          tied = t;
+      const int at = i0 + 32 * lane;
+      auto bits = [&](int lo, int hi) {  // of [lo, hi)
+        const int x = min(max(lo - at, 0), 32), y = min(max(hi - at, x), 32);
+        return static_cast<uint32_t>((1ull << y) - (1ull << x));
+      };
+      const uint32_t free = any ? bits(c_lo, c_hi) : 0u;
+      sure = bits(0, c_lo) | bits(c_hi, n);
+      tied = 0;
+      if (free == 0) return;
+      uint32_t above = 0;
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        uint4 k = make_uint4(0, 0, 0, 0);
+        if (at + 4 * v < n) k = keys_at(at + 4 * v);
+        const uint32_t key[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          above |= (key[e] > prefix ? 1u : 0u) << (4 * v + e);
+          tied |= (key[e] == prefix ? 1u : 0u) << (4 * v + e);
         }
       }
+      sure |= above & free;
+      tied &= free;
     };
     uint32_t above = 0, tie = 0, sure = 0, tied = 0;
     for (int i0 = 0; i0 < n; i0 += 1024) {
@@ -307,18 +332,28 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
           ti += to;
         }
       }
-      uint32_t a = a_before + ai - __popc(sure), t = t_before + ti - __popc(tied);
+      const uint32_t t = t_before + ti - __popc(tied);  // ties before the lane's
+      uint32_t out = a_before + ai - __popc(sure) + min(t, need);
       a_before += __shfl_sync(0xffffffffu, ai, 31);
       t_before += __shfl_sync(0xffffffffu, ti, 31);
-      // the lane's keys that may be kept, from the first on
-      for (uint32_t left = sure | tied; left != 0; left &= left - 1) {
-        const int bit = __ffs(left) - 1;
-        const bool tie_bit = (tied >> bit) & 1u;
-        const uint32_t at = a + min(t, need);  // the first `need` ties are kept
-        if ((!tie_bit || t < need) && at < (uint32_t)P.keep)
-          kept[at] = (int)(first + i0 + 32 * lane + bit);
-        a += !tie_bit;
-        t += tie_bit;
+      // the first `need` ties of all are kept
+      uint32_t ties = tied;
+      for (uint32_t left = __popc(tied), k = t < need ? need - t : 0u; left > k; --left)
+        ties &= ~(0x80000000u >> __clz(ties));
+      uint32_t word = sure | ties;
+      const int key0 = (int)first + i0 + 32 * lane;
+      if (__reduce_max_sync(0xffffffffu, __popc(word)) > kSparse) {
+        // lane by lane, the warp together
+#pragma unroll 4
+        for (int l = 0; l < 32; ++l) {
+          const uint32_t w = __shfl_sync(0xffffffffu, word, l);
+          const uint32_t at = __shfl_sync(0xffffffffu, out, l) + __popc(w & ((1u << lane) - 1u));
+          if (((w >> lane) & 1u) && at < (uint32_t)P.keep)
+            kept[at] = (int)first + i0 + 32 * l + lane;
+        }
+      } else {
+        for (; word != 0; word &= word - 1, ++out)
+          if (out < (uint32_t)P.keep) kept[out] = key0 + __ffs(word) - 1;
       }
     }
   }
