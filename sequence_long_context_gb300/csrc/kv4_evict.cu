@@ -3,20 +3,23 @@
 // A cluster of CTAs owns one (sequence, KV head). Every CTA takes an equal,
 // contiguous part of the head's weights, brings it into shared memory once as
 // order-preserving 32-bit keys, and the cluster finds the n-th largest key by
-// three radix passes (11, 11 and 10 bits): each CTA counts its part into its
+// three radix passes (11, 10 and 11 bits): each CTA counts its part into its
 // own histogram, also in groups of 32 bins; after one cluster barrier every CTA
 // adds up the cluster's groups through distributed shared memory, and then the
 // bins of the one group that matters (3 KB read from the others; all of their
 // histograms would be 64 KB), so that all reach the same bin with no further
-// exchange. One more barrier
-// gives every CTA how many keys are kept before its part, and it writes their
-// rows in ascending order; after another the cluster copies the kept rows'
-// codes, scales and weights.
+// exchange. One more barrier gives every CTA how many keys are kept before its
+// part, and it writes their rows in ascending order; after another the cluster
+// copies the kept rows' codes, scales and weights.
 //
-// Bound by HBM for long caches (the weights once, the kept rows twice), by the
-// five barriers for short ones. Rows only move towards the front, so in place
-// the copy goes in rounds: every row of a round is in registers before a
-// barrier, and written after it; later rounds read behind every row that
+// Bound by latency: a cluster takes about 20 us to choose (of which the weights'
+// load 3.5, each pass 2, the barriers 1 each) and 9 to move 8192 rows, at HBM's
+// rate, and 36 clusters of eight fit the GPU at once. 64 heads of up to 128K
+// tokens, 8192 kept: 72 us, 2.3 TB/s (45 with 256 kept; 153 with clusters of four,
+// 232 of two: choosing is as long as a CTA's part). 64 heads of 1088, 1024 kept:
+// 19 us, of which launch and barriers are most. Rows only move towards the front,
+// so in place the copy goes in rounds: every row of a round is in registers
+// before a barrier, and written after it; later rounds read behind every row that
 // earlier ones write.
 #include <type_traits>
 
@@ -34,8 +37,12 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-// keys of a CTA's part that fit beside the histograms with two CTAs per SM;
-// longer parts (beyond 8 x 16K tokens) are read again from L2 in each pass
+// Keys of a CTA's part in shared memory; longer parts (beyond 8 x 16K tokens) are
+// read again from L2 in each pass. Two CTAs of this size leave 92 KB of the SM to
+// L1, where the moved rows' gathers in flight are held: with 60 KB the 128K prompt
+// below took 78 us, with 28 KB 108. Twenty thousand keys: 150 us instead of 146
+// for 64 heads of 160K tokens, 123 instead of 97 for 32 of 256K, but 52 instead of
+// 59 for 16 of 160K.
 constexpr int kKeysInSmem = 16384;
 // Where key i (a multiple of 4) of a warp's part stands: the 16-byte pieces of
 // 32 keys change places with the row, so that both ways of reading them (a warp
@@ -82,7 +89,9 @@ struct EvictParams {
 
 constexpr int kGroups = kBins / 32;
 struct __align__(16) EvictSmem {
-  uint32_t hist[3][kBins];
+  __device__ __forceinline__ uint32_t* bins(int pass) { return pass == 1 ? hist1 : hist; }
+  uint32_t hist[kBins];                 // of the first and the third pass
+  uint32_t hist1[kBins / 2];            // of the second
   uint32_t groups[3][kGroups];          // sums of 32 bins
   uint32_t sums[kGroups];               // of the cluster
   uint32_t above[kWarps], tie[kWarps];  // of each warp's part
@@ -125,7 +134,7 @@ __device__ __forceinline__ uint32_t find_bin(EvictSmem& s, int pass, int cluster
   }
   __syncthreads();
   if (item < 32) {  // (whole warps)
-    x = r < cluster ? peer_load(&s.hist[pass][32 * group + item], r) : 0u;
+    x = r < cluster ? peer_load(&s.bins(pass)[32 * group + item], r) : 0u;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if (r == 0) s.sums[item] = x;
@@ -161,7 +170,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
     const int n = (int)max(0LL, min((long long)per, L - first));
     const bool in_smem = per * kWarps <= kKeysInSmem;
     uint32_t* mine = keys + warp * per;
-    for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) s.hist[0][i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+      s.hist[i] = 0;
+      if (i < kBins / 2) s.hist1[i] = 0;
+    }
     if (in_smem) {
       // 16 bytes per lane (the rows before a head are a multiple of 16); a
       // read behind L stays inside the capacity
@@ -184,11 +196,11 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
     const int c_hi = (int)max((long long)c_lo, min((long long)n, hi - first));
     uint32_t prefix = 0;  // the n-th largest key's bits found so far
     if (need > 0) {
-      constexpr int kShift[3] = {21, 10, 0};
-      constexpr uint32_t kMask[3] = {0u, 0xffe00000u, 0xfffffc00u};
+      constexpr int kShift[3] = {21, 11, 0};
+      constexpr uint32_t kMask[3] = {0u, 0xffe00000u, 0xfffff800u};
 #pragma unroll
       for (int pass = 0; pass < 3; ++pass) {
-        const uint32_t bin_mask = pass == 2 ? 1023u : 2047u;
+        const uint32_t bin_mask = pass == 1 ? 1023u : 2047u;
         // several keys per lane at a time, so that their latencies overlap
         auto count = [&](auto vectors, int i0) {
           constexpr int kV = decltype(vectors)::value, kN = 4 * kV;
@@ -221,11 +233,11 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
           // one addition where the whole warp agrees (runs of equal weights)
           if (__all_sync(0xffffffffu, alike) &&
               __all_sync(0xffffffffu, key[0] == __shfl_sync(0xffffffffu, key[0], 0))) {
-            if (lane == 0) atomicAdd(&s.hist[pass][key[0]], 32u * kN);
+            if (lane == 0) atomicAdd(&s.bins(pass)[key[0]], 32u * kN);
           } else {
 #pragma unroll
             for (int e = 0; e < kN; ++e)
-              if ((in >> e) & 1u) atomicAdd(&s.hist[pass][key[e]], 1u);
+              if ((in >> e) & 1u) atomicAdd(&s.bins(pass)[key[e]], 1u);
           }
         };
         int i0 = c_lo / 128 * 128;
@@ -233,13 +245,17 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams P)
         for (; i0 < c_hi; i0 += 128) count(std::integral_constant<int, 1>{}, i0);
         __syncthreads();
         {
-          const uint4 x = reinterpret_cast<const uint4*>(s.hist[pass])[threadIdx.x];
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (pass != 1 || threadIdx.x < kThreads / 2)
+            x = reinterpret_cast<const uint4*>(s.bins(pass))[threadIdx.x];
           uint32_t sum = x.x + x.y + x.z + x.w;
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
           if ((threadIdx.x & 7) == 0) s.groups[pass][threadIdx.x >> 3] = sum;
         }
         cluster_sync();
+        if (pass == 1)  // no CTA reads the first pass's counts any more
+          for (int i = threadIdx.x; i < kBins; i += kThreads) s.hist[i] = 0;
         prefix |= find_bin(s, pass, P.cluster, need) << kShift[pass];
       }
     }
