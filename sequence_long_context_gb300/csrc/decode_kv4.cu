@@ -764,7 +764,10 @@ decode_kv4_kernel(const Params P) {
 }
 
 constexpr int kMergeThreads = 256;
-constexpr int kWeightKeys = 4;      // keys per thread at a time
+// Keys per thread at a time, and, with the six pairs of rows unrolled, scores in
+// flight (4 x 32K keys, 12 rows, 50 MB of scores in L2: 24 us; with two pairs 29,
+// with two keys in twice as many blocks 23 to 27, with one key 31).
+constexpr int kWeightKeys = 4;
 constexpr int kMaxWeightRows = 64;  // (m, 1 / l) kept at a time
 
 // Block x < units * 8 NT: a row of a unit, whose partials (consecutive slots)
@@ -872,7 +875,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kv4_kernel(const Params P
         }
         __syncthreads();
         const float2* sc = P.scores + head * (P.Rs / 2) + (long long)(r0 / 2) * P.c.C;
-#pragma unroll 2
+#pragma unroll 6
         for (int r = 0; r < n; r += 2) {
           const float2 a0 = s_ml[r], a1 = s_ml[r + 1];
           const bool odd = r0 + r + 1 >= P.R;  // the last row's partner was never written
