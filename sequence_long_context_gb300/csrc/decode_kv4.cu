@@ -5,6 +5,12 @@
 // combine in any order): the newest Tq tokens of every sequence attend to its
 // cached keys, D (1 + 1/16) bytes per key and KV head.
 //
+// 8 x 128K keys, 32 query heads over 8, D = 128: 236 us, 4.8 TB/s, 0.71 of the
+// measured copy rate; bound by instruction issue (64 % of all slots, 660
+// instructions of a warp per 32 keys, 16 warps per SM) more than by HBM. 16
+// windows of 1000 keys and 32 heads: 32 us, of which rounds of keys 15, the start
+// 4, the ends of units the rest. 3 new tokens (12 rows) over 4 x 32K: 61 us.
+//
 // Division of the work. A unit is one (sequence, KV head, block of up to 8 NT
 // query rows); a step is 32 of its keys. All steps of all units, in unit
 // order and each unit followed by a few that stand for the cost of its end, are

@@ -1,8 +1,11 @@
 // Filling the 4-bit KV cache and reading it back.
 //
-// Both are copies with a few operations per element: bound by HBM for prompts
-// (the append about evenly by instruction issue) and by launch latency for
-// single tokens.
+// Both are copies with a few operations per element. 32K tokens of 8 heads of 128,
+// bf16 (170 MB): the append takes 44 us, 3.9 TB/s, bound by instruction issue (87
+// % of all slots, about 20 instructions per channel); the read 29 us, 5.8 TB/s. Single tokens are bound by launch latency (3.9 us). A descale of 1 (the
+// append, without its multiplications: 51 us) and powers of two (the read, two
+// values per packed multiply-add: 34 us) have code of their own, which both sides
+// of the rule make equal in every bit.
 //
 // A warp takes one tensor (K or V) of one KV head and eight tokens that follow
 // one another, so that its side of the cache is one contiguous run. A lane
@@ -259,8 +262,10 @@ long long items_of(int T, int H) {
 template <typename T, int D, bool kOne>
 usp_status_t launch_append_t(const AppendParams& P, cudaStream_t st) {
   // Few tokens per sequence: one launch, whose blocks own their sequences'
-  // lengths. Else the items are spread over the whole GPU and a second,
-  // small launch (about 2 us) updates the lengths in stream order.
+  // lengths. Else the items are spread over the whole GPU and a second, small
+  // launch updates the lengths in stream order. On the GPU both take 3.5 to 3.9
+  // us up to 8 tokens of 8 heads, and one launch saves its caller about 2 us; for
+  // 16 tokens one takes 6.1 us and two 3.9, for 32 10.9 and 3.8.
   if (!P.cu && (long long)P.T * P.c.H <= 64) {
     {
       ProfScope ps(st, "kv4_append");
