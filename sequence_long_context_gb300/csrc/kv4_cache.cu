@@ -1,11 +1,12 @@
 // Filling the 4-bit KV cache and reading it back.
 //
 // Both are copies with a few operations per element. 32K tokens of 8 heads of 128,
-// bf16 (170 MB): the append takes 44 us, 3.9 TB/s, bound by instruction issue (87
-// % of all slots, about 20 instructions per channel); the read 29 us, 5.8 TB/s. Single tokens are bound by launch latency (3.9 us). A descale of 1 (the
-// append, without its multiplications: 51 us) and powers of two (the read, two
-// values per packed multiply-add: 34 us) have code of their own, which both sides
-// of the rule make equal in every bit.
+// bf16 (170 MB): the append takes 44 us, 3.9 TB/s, bound by instruction issue
+// (87 % of all slots, about 20 instructions per channel); the read 29 us, 5.8
+// TB/s. Single tokens are bound by launch latency (3.9 us). An append with a
+// descale of 1 leaves out the multiplications by 1 (44 us instead of 51), and a
+// read in bf16 with powers of two makes two values per packed multiply-add, exactly
+// (29 instead of 34); every bit is the same either way.
 //
 // A warp takes one tensor (K or V) of one KV head and eight tokens that follow
 // one another, so that its side of the cache is one contiguous run. A lane
