@@ -105,8 +105,7 @@ struct WeightParams {
   int observe;   // 0: all
   int hpi;       // query heads per item
   int groups;    // items per KV head, key block and segment: G / hpi
-  int nseg;      // segments of query tiles
-  int tps;       // query tiles per segment
+  int nseg;      // segments: which of a key block's query tiles, in turn
   int nkb;       // key blocks
   int q0;        // first row of tile 0: where the observed rows begin, if they
                  // are one run to the end; else 0
@@ -357,14 +356,15 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  // query tiles of an item's segment that may see its keys
+  // query tiles first, first + nseg .. < last of an item's segment may see its keys
   auto tiles_of = [&](const ItemPos& ip, const KeyBlock& blk, int& first, int& last) {
-    first = ip.seg * W.tps;
-    last = min(W.ntiles, first + W.tps);
+    first = 0;
+    last = W.ntiles;
     if (P.layout == kContiguous) {  // rank-major order is natural order
-      first = max(first, (blk.q.lo - W.q0) / kQT);  // (towards 0: an extra tile is skipped)
+      first = max(0, (blk.q.lo - W.q0) / kQT);  // (towards 0: an extra tile is skipped)
       last = blk.q.hi < W.q0 ? 0 : min(last, (blk.q.hi - W.q0) / kQT + 1);
     }
+    first += ip.seg;
   };
   if (warp == kKeyWarp) {
     // ------------------------------------------------------- items and keys
@@ -382,9 +382,11 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
       int first, last;
       tiles_of(ip, blk, first, last);
       int tiles = 0;
-      for (int base = first; base < last; base += 32)
+      for (int base = first; base < last; base += 32 * W.nseg) {
+        const int t = base + lane * W.nseg;
         tiles += __popc(__ballot_sync(
-            0xffffffffu, base + lane < last && classify_tile(W, base + lane, blk) != kClsEmpty));
+            0xffffffffu, t < last && classify_tile(W, t, blk) != kClsEmpty));
+      }
       const int rec = it % kRecords;
       if (it >= kRecords) {  // every role is done with the record's previous item
         ok = mbar_wait(bar(L::kItemFree + rec), (it / kRecords - 1) & 1, abort_flag, status);
@@ -450,14 +452,14 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
         float lse[kQT / 32];
       };
       const float* lse_head = P.lse + lse_index(P, ip.bt, ip.h0, 0);
-      int base = first - 32, cls_mine = kClsEmpty, lo_mine = 0, hh = 0;
+      int base = first - 32 * W.nseg, cls_mine = kClsEmpty, lo_mine = 0, hh = 0;
       unsigned todo = 0;
       Next nx{};
       bool more = true;
       auto fetch = [&]() {
         if (hh == 0) {  // a new tile
-          while (todo == 0 && (base += 32) < last) {
-            const int t = base + lane;
+          while (todo == 0 && (base += 32 * W.nseg) < last) {
+            const int t = base + lane * W.nseg;
             cls_mine = t < last ? classify_tile(W, t, blk) : kClsEmpty;
             todo = __ballot_sync(0xffffffffu, cls_mine != kClsEmpty);
             // first position, or -1: the rows are not one run of a chunk, or
@@ -474,7 +476,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           }
           const int src = __ffs(todo) - 1;
           todo &= todo - 1;
-          nx.row = W.q0 + (base + src) * kQT;
+          nx.row = W.q0 + (base + src * W.nseg) * kQT;
           nx.cls = __shfl_sync(0xffffffffu, cls_mine, src);
           const int lo = __shfl_sync(0xffffffffu, lo_mine, src);
 #pragma unroll
@@ -868,14 +870,19 @@ bool make_map(CUtensorMap* m, const void* base, int Bt, int S, int H, int D, int
   return true;
 }
 
+// Query tiles of a segment, about, at least (4 packed sequences of 5003 tokens, 8
+// heads: 48 us uncut, 35 with 16, 40 with 8, 36 with 4; 4K tokens, 8 heads: 29,
+// 34, 38 with 16, 8, 4; 2K tokens: 27, 20, 19; a zigzag ring of 4 over 4K: 32, 39,
+// 43; and 3 to 4 us for the sum of the segments, where there are any).
+constexpr int kMinTiles = 16;
 // How the problem is cut (host side, from the shapes alone).
 struct Cut {
-  int hpi, nseg, tps, nkb, q0, ntiles, parts;
+  int hpi, nseg, nkb, q0, ntiles, parts;
 };
 // tail: the observed queries are the last rows (natural order, one sequence).
-// packed: a key block meets the queries of its own sequences alone, so the
-// queries are not cut.
-Cut cut_of(int B, int S, int Hq, int Hkv, int observe, bool tail, bool packed) {
+// nseq: packed sequences, or 0. A key block meets the queries of its own
+// sequences alone; a long one is taken to be twice the mean.
+Cut cut_of(int B, int S, int Hq, int Hkv, int observe, bool tail, int nseq) {
   Cut c{};
   const int G = Hq / Hkv;
   if (observe >= S) observe = 0;
@@ -892,15 +899,15 @@ Cut cut_of(int B, int S, int Hq, int Hkv, int observe, bool tail, bool packed) {
   if (blocks < want && tiles >= 8) {  // (each item loads its keys anew)
     c.hpi = 1;
     const long long have = blocks * G;
-    if (have < want && observe == 0 && !packed) {
+    if (have < want && observe == 0) {
       long long n = (want + have - 1) / have;
-      const long long most = (tiles + 15) / 16;  // at least 16 query tiles each
+      const int met = nseq > 1 ? std::min(tiles, 2 * tiles / nseq) : tiles;
+      const long long most = std::max((met + kMinTiles - 1) / kMinTiles, 1);
       if (n > most) n = most;
       if (n > 16) n = 16;
       c.nseg = (int)n;
     }
   }
-  c.tps = (c.ntiles + c.nseg - 1) / c.nseg;
   c.parts = (G / c.hpi) * c.nseg;
   return c;
 }
@@ -944,16 +951,16 @@ usp_status_t launch_tc(const WeightParams& W, cudaStream_t st) {
 }  // namespace
 
 size_t key_weights_workspace(int B, int S, int Hq, int Hkv, int observe) {
-  const Cut c = cut_of(B, S, Hq, Hkv, observe, false, false);  // (no more parts if `tail` or packed)
+  const Cut c = cut_of(B, S, Hq, Hkv, observe, false, 0);  // (no more parts if `tail` or packed)
   return c.parts > 1 ? (size_t)c.parts * B * Hkv * S * 4 : 0;
 }
 
 usp_status_t launch_key_weights_tc(const AttnParams& P, float* weight, int observe,
                                    void* workspace, cudaStream_t st) {
   const Cut c = cut_of(P.Bt, P.S, P.Hq, P.Hkv, observe, P.layout == kContiguous && !P.cu,
-                       P.cu != nullptr);
+                       P.cu ? P.nseq : 0);
   WeightParams W{P, c.parts > 1 ? static_cast<float*>(workspace) : weight,
-                 observe < P.S ? observe : 0, c.hpi, P.G / c.hpi, c.nseg, c.tps, c.nkb, c.q0, c.ntiles, 1, 3, 3, 1, 0};
+                 observe < P.S ? observe : 0, c.hpi, P.G / c.hpi, c.nseg, c.nkb, c.q0, c.ntiles, 1, 3, 3, 1, 0};
   if (c.ntiles == 1 && P.S - c.q0 <= 64 && c.hpi % 2 == 0) W.pair = 2;
   const bool straight = P.layout == kContiguous && !P.cu;
   const long long most = (long long)c.ntiles * (c.hpi / W.pair);  // query tiles of an item
@@ -984,7 +991,7 @@ usp_status_t launch_key_weights_tc(const AttnParams& P, float* weight, int obser
 
 usp_status_t launch_key_weights_simt(const AttnParams& P, float* weight, int observe, int bf16,
                                      cudaStream_t st) {
-  WeightParams W{P, nullptr, observe, P.G, 1, 1, 0, 0, 0};
+  WeightParams W{P, nullptr, observe, P.G, 1, 1, 0, 0};
   const dim3 grid((P.S + 63) / 64, P.Hkv, P.Bt);
   {
     ProfScope ps(st, "attn_key_weights_simt");
