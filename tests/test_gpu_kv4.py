@@ -518,6 +518,53 @@ def test_key_weights_of_few_queries_over_long_prompts(B, S, Hq, H, D, observe, w
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("causal,window,sink,observe", [(False, 0, 0, 64), (False, 3000, 9, 128),
+                                                        (True, 0, 0, 4000), (False, 0, 0, 1)])
+def test_key_weights_of_runs_match_the_cuda_core_kernel(causal, window, sink, observe):
+    """Both kernels' errors are within the bound of the comparison with the
+    oracle, so they differ by twice that at most."""
+    dev = device()
+    torch.manual_seed(observe)
+    S, D = 12345, 128
+    q = torch.randn(2, S, 4, D, device=dev).to(torch.bfloat16)
+    k = torch.randn(2, S, 2, D, device=dev).to(torch.bfloat16)
+    lse = torch.rand(2, 4, S, device=dev) + 10
+    kw = dict(causal=causal, window=window, sink_tokens=sink, observe=observe)
+    got, want = (usp.attn_key_weights(q, k, lse, flags=f, **kw) for f in (0, usp.FLAG_FORCE_SIMT))
+    usp.usp_device_status()
+    ds = D * U / np.sqrt(D) * float(q.abs().max() * k.abs().max()) * D
+    bound = 2 * (2 * ds + 4 * U * 11 + 2 * observe * 4 * U + 2.0 ** -20)
+    assert ((got - want).abs() <= bound * torch.maximum(got, want) + 1e-37).all()
+
+
+def test_key_weights_captured_twice_with_their_own_workspaces():
+    """Two graphs replayed at once on two streams, and with new inputs: cut
+    into segments (a workspace), and with few queries."""
+    dev = device()
+    torch.manual_seed(5)
+    q = torch.randn(1, 4096, 8, 128, device=dev).to(torch.bfloat16)
+    k = torch.randn(1, 4096, 8, 128, device=dev).to(torch.bfloat16)
+    _, lse = usp.attn_forward(q, k, k)
+    for observe in (0, 64):
+        graphs = []
+        for _ in range(2):
+            g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream(device=dev)
+            with torch.cuda.graph(g, stream=s):
+                w = usp.attn_key_weights(q, k, lse, observe=observe)
+            graphs.append((g, s, w))
+        for step in range(3):
+            q.copy_(torch.randn_like(q))
+            want = usp.attn_key_weights(q, k, lse, observe=observe)
+            torch.cuda.synchronize()
+            for g, s, w in graphs:
+                with torch.cuda.stream(s):
+                    g.replay()
+            torch.cuda.synchronize()
+            for _, _, w in graphs:
+                assert torch.equal(w, want)
+    usp.usp_device_status()
+
+
 def test_key_weights_of_the_librarys_own_forward():
     """Every observed query spreads a weight of one per head of its group."""
     dev = device()
@@ -735,6 +782,34 @@ def test_prompt_eviction_and_decoding_together():
     want = torch.from_numpy(kv4.kept_rows(before.cpu(), [133, 133], 100, 16, 4))
     assert torch.equal(kept.cpu(), want) and c.seq_lens.tolist() == [100, 100]
     usp.usp_device_status()
+
+
+def test_evict_in_place_captured_and_twice():
+    """An eviction in place, captured: each replay evicts what the cache holds
+    then; a second one right behind it finds nothing to do."""
+    dev = device()
+    lens = [900, 500, 64]
+    c = random_cache(dev, 3, 912, 2, 64, lens, seed=21)
+    start = snapshot(c)
+    eager = random_cache(dev, 3, 912, 2, 64, lens, seed=21)
+    _, kept = usp.kv4_evict(eager, 200, recent=20, sink_tokens=3)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        _, k1 = usp.kv4_evict(c, 200, recent=20, sink_tokens=3)
+        _, k2 = usp.kv4_evict(c, 200, recent=20, sink_tokens=3)
+    for _ in range(2):
+        for t, x in zip(c[:6], start):
+            t.copy_(x)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(k1, kept) and c.seq_lens.tolist() == [200, 200, 64]
+        for b, n in enumerate((200, 200, 64)):
+            want = torch.arange(200, device=dev, dtype=torch.int32)
+            want[n:] = -1
+            assert (k2[b] == want).all()
+        for x, y in zip(c[:6], eager[:6]):
+            assert torch.equal(x, y)
 
 
 def test_captured_step_grows_the_cache_on_replay():
