@@ -53,7 +53,11 @@
 // to a largest element of 64 .. 128 (elements below 2^-23 of it lose bits),
 // and -8 sum q is given as three fp16 parts. The rounding of p to fp16
 // (2^-11; bf16 would have 2^-8) is the only one of the products, and is the
-// same in both of O's sums. O's bias is taken off at the end of every step (32
+// same in both of O's sums. p is taken against a reference that starts 2^7 below
+// the running maximum, and so uses fp16's range up to 2^15: a p of down to 2^-21 of
+// the maximum keeps all 11 bits, and below that its error is at most 2^-32 of it
+// (against the maximum itself, keys below 2^-25 of a sink were 0 in O and still
+// counted in l). O's bias is taken off at the end of every step (32
 // multiply-adds of a thread's 700 instructions at D = 128; 240 us instead of 236
 // at 8 x 128K keys): taken off once at the end, the sums' roundings were 0.33 % of O at 128K keys per head and 3.3 % at 1M, where
 // bf16's own are 0.17 %.
@@ -89,7 +93,9 @@ constexpr int kThreads = 32 * kWarps;
 // eight steps 2. (16 x 32 units of at most 33 steps: 37.2 us without it, 33.4
 // with 8, 32.3 with 12, 33.1 with 16.)
 constexpr int kUnitCost = 12;
-constexpr float kLazy = 8.f;              // the max moves when it grows by 2^8
+// p = 2^(score - m), m the reference: set 2^kBelow below the running maximum, and
+// moved when a score exceeds it by 2^kAbove (fp16 ends at 2^16).
+constexpr float kBelow = 7.f, kAbove = 15.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -99,7 +105,7 @@ struct Params {
   __nv_bfloat16* out;
   float* lse;
   float* o_part;    // [slots][8 NT][D], columns in the kernel's order
-  float2* ml_part;  // [slots][8 NT]: (m, l) in log2 units
+  float2* ml_part;  // [slots][8 NT]: (m, l), m the reference in log2 units
   int2* span;       // [units]: first and last slot (units that have steps)
   float2* scores;   // accumulate: [B][H][Rs / 2][C] log2-scaled scores of two rows
   int Tq, Hq, G, R, Rs, nrb;  // R = G Tq rows per KV head, nrb blocks of them
@@ -575,7 +581,7 @@ decode_kv4_kernel(const Params P) {
         for (int e = 0; e < 2; ++e) {
           mx[nt][e] = mul[nt][e] * fmaxf(fmaxf(sc[nt][0][e], sc[nt][0][e + 2]),
                                          fmaxf(sc[nt][1][e], sc[nt][1][e + 2]));
-          grow |= mx[nt][e] > m[nt][e] + kLazy;
+          grow |= mx[nt][e] > m[nt][e] + kAbove;
         }
       if constexpr (SC) {
         // the weights need every score once the whole row's sum is known
@@ -605,7 +611,7 @@ decode_kv4_kernel(const Params P) {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1)
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-            x = fmaxf(x, m[nt][e]);
+            x = fmaxf(x - kBelow, m[nt][e]);
             a[e] = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - x);
             m[nt][e] = x;
             l[nt][e] *= a[e];

@@ -388,6 +388,39 @@ def test_decode_long_rows_lose_nothing_but_the_roundings(B, Tq, C, G, H, D):
     assert (err / ref) ** 0.5 <= (1.1 * 2.0 ** -8 + 2.0 ** -11) / 3 ** 0.5
 
 
+@pytest.mark.parametrize("sink_scale", [0.0, 0.25])
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 1), (128, 12)])
+def test_decode_keys_far_below_the_dominant_ones(D, G, sink_scale):
+    """304 units of 4096 keys, so that a CTA has one or two; eight keys, one in
+    each warp's share, outweigh every other by 2^23.4 and have V = 0. O is then
+    what the others give, each p = 1.57 2^-24 of the largest. Bound: bf16 (2^-8),
+    the rounding of p, held in steps of at most 2^-24 of 2^-7 of the largest
+    (2^-32 / p = 0.26 %), and the sums (2 n u). A block of zeros is stored with the
+    scale 0. Zero codes under a scale s (of a block with other numbers) stand in the
+    step's two sums as 8 s p_max and cancel: each of the step's 32 keys may lose an
+    ulp, 2^-23 of that, in each sum, so against l >= p_max 2^-17 8 s are added."""
+    dev = device()
+    B, H, L = 16, 19, 4096
+    c = usp.kv4_cache(B, L, H, D, device=dev)
+    c.k.fill_(0x88)          # codes 0
+    c.k_scale.fill_(0x38)    # 1
+    c.v.fill_(0xCC)          # code 4
+    c.v_scale.fill_(0x28)    # 1/4
+    c.k[:, :, 0:256:32, 0] = 0x8F  # channel 0: 7
+    c.v[:, :, 0:256:32] = 0x88
+    c.v_scale[:, :, 0:256:32] = 0x28 if sink_scale else 0
+    c.seq_lens.fill_(L)
+    q = torch.zeros(B, 1, G * H, D, dtype=torch.bfloat16, device=dev)
+    q[..., 0] = 2.3125
+    out, lse = usp.attn_decode_kv4(q, c, softmax_scale=1.0)
+    p, n = np.exp(-7 * 2.3125), L - 8
+    want = n * p / (8 + n * p)
+    bound = want * (2.0 ** -8 + 2.0 ** -32 / p + 2 * L * U + 2.0 ** -20) \
+        + 2.0 ** -17 * 8 * sink_scale
+    assert float((out.double() - want).abs().max()) <= bound
+    assert float((lse.double() - np.log(8 / p + n)).abs().max()) <= L * U + 20 * 4 * U + 2.0 ** -20
+
+
 def test_decode_long_cache_offsets_pass_32_bits():
     """Codes of the last head start behind 4 GiB; only its rows are filled."""
     dev = device()
