@@ -28,8 +28,9 @@
 // 64 columns). A 128 x 256 tile now takes 1.15 us, the exponentials half of it:
 // a warp that reads its next scores ahead needs code that is slower (below).
 // Roles (640 threads):
-//   warps 0-15 softmax: warp w takes keys [32 (w & 7), + 32) and the query
-//              tiles of parity w >> 3
+//   warps 0-15 softmax: warp w takes keys [32 (w & 7), + 32) and every other
+//              query tile (w >> 3: which), from a score buffer that its four
+//              warps have to themselves
 //   warp 16    items and keys: counts the query tiles that can see an item's
 //              keys (32 at a time, one per lane), publishes the item and loads
 //              its K (a ring of two to four tiles, the next block's ahead of time)
@@ -78,7 +79,7 @@ constexpr int kThreads = 32 * (kMmaWarp + kKT);
 constexpr int kTileSlots = 6;
 constexpr int kSlots = 4;           // Q tiles, at most
 constexpr int kKSlots = 4;          // K tiles, at most
-constexpr int kSBufs = 4;           // score buffers of 128 columns
+constexpr int kSBufs = 2 * kKT;     // score buffers of 128 columns: one per softmax group
 constexpr int kRing = 16;           // entries of query statistics
 constexpr int kCtas = 152;          // one per SM
 constexpr int kRecords = 4;         // items that the roles may be apart
@@ -562,7 +563,11 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
     const int a = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);  // key tile
     bool ok = true;
-    int n = 0, slot = 0, phase = 0, kn = 0, si = 0;
+    // Score buffer a + kKT g is written by this warp and read by key tile a's
+    // softmax group g alone, so each side sees every one of its phases (a parity
+    // cannot tell a phase from the one two before it). The groups take the tiles in
+    // turn, over the ends of blocks and items.
+    int n = 0, slot = 0, phase = 0, kn = 0, pairs = 0, used0 = 0, used1 = 0;
     for (int it = 0; ok; ++it) {
       const int rec = it % kRecords;
       ok = mbar_wait(bar(L::kItemFull + rec), (it / kRecords) & 1, abort_flag, status);
@@ -583,12 +588,15 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           const int rows = __shfl_sync(0xffffffffu, sched[(n + j) & (kRing - 1)], 0) >> 8 & 255;
           const uint32_t id = rows > 64 ? kId128 : kId64;
           if (a < ktiles) {
-            const int ks = (kn + a) % kslots, sj = si + j * ktiles + a, buf = sj % kSBufs;
+            const int g = (pairs + j) & 1, used = g ? used1 : used0;
+            const int ks = (kn + a) % kslots, buf = a + kKT * g;
             if (j == 0) ok = mbar_wait(bar(L::kKFull + ks), ((kn + a) / kslots) & 1, abort_flag, status);
             // the buffer's previous scores have been taken out
-            if (ok && sj >= kSBufs)
-              ok = mbar_wait(bar(L::kSFree + buf), (sj / kSBufs - 1) & 1, abort_flag, status);
+            if (ok && used > 0)
+              ok = mbar_wait(bar(L::kSFree + buf), (used - 1) & 1, abort_flag, status);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (g) ++used1;
+            else ++used0;
             if (lane == 0) mbar_arrive(bar(L::kSFull + buf));
             tc_fence_after();
             const uint64_t da = sdesc_add(dk, ks * L::kTileBytes);
@@ -613,7 +621,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           }
         }
         kn += ktiles;
-        si += count * ktiles;
+        pairs += count;
       }
       n += count;
       __syncwarp();
@@ -623,11 +631,12 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
     mbar_wait_drain(bar(L::kMmaDone + a), 0);
   } else {
     // ------------------------------------------------------------ softmax
-    const int a = (warp >> 2) & 1, group = warp >> 3;  // key tile, parity of the query tiles
+    const int a = (warp >> 2) & 1, group = warp >> 3;  // key tile, which of its groups
+    const int buf = a + kKT * group;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint64_t sc2 = f2_pack(P.scale_log2, P.scale_log2);
     bool ok = true;
-    int n = 0, si = 0, joins = 0;
+    int n = 0, pairs = 0, used = 0, joins = 0;
     for (int it = 0; ok; ++it) {
       const int rec = it % kRecords;
       ok = mbar_wait(bar(L::kItemFull + rec), (it / kRecords) & 1, abort_flag, status);
@@ -642,9 +651,9 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           Seen vis{1, 0};
           if (kp < P.S) vis = seen_by(P, nat_pos(P, kp));
           uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-          for (int j = (n ^ group) & 1; j < count; j += 2) {
-            const int ring = (n + j) & (kRing - 1), sj = si + j * ktiles + a, buf = sj % kSBufs;
-            ok = mbar_wait(bar(L::kSFull + buf), (sj / kSBufs) & 1, abort_flag, status);
+          for (int j = (pairs ^ group) & 1; j < count; j += 2, ++used) {
+            const int ring = (n + j) & (kRing - 1);
+            ok = mbar_wait(bar(L::kSFull + buf), used & 1, abort_flag, status);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
             const uint32_t t_s = tmem + lane_off + 128 * buf;
@@ -703,8 +712,8 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
             }
           }
           if (!ok) break;
-          // the two groups' sums, which the second adds: with an even number of
-          // tiles the first is done first, and goes on without a wait (`joins`
+          // the two groups' sums, which the second adds: where the first takes the
+          // first of an even number of tiles it is done first, and goes on without a wait (`joins`
           // counts this key tile's blocks, alike in both groups)
           float u, w;
           f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), u, w);
@@ -729,7 +738,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           }
           ++joins;
         }
-        si += count * ktiles;
+        pairs += count;
       }
       if (!ok) break;
       n += count;

@@ -551,6 +551,46 @@ def test_key_weights_of_few_queries_over_long_prompts(B, S, Hq, H, D, observe, w
     assert torch.equal(got, again)
 
 
+def check_weights_of_many_items(B, S, Hq, H, D, observe):
+    """The last `observe` queries of B prompts, against 64 bits (the bound of the
+    comparison with the oracle), and the same bits every time. With B H items of one
+    or more runs, above 152, a CTA takes several, one behind the other."""
+    dev = device()
+    torch.manual_seed(S + Hq)
+    q = torch.randn(B, S, Hq, D, device=dev).to(torch.bfloat16)
+    k = torch.randn(B, S, H, D, device=dev).to(torch.bfloat16)
+    scale, n = 1 / np.sqrt(D), min(observe, S) or S
+    see = torch.arange(S, device=dev)[None] <= torch.arange(S - n, S, device=dev)[:, None]
+    lse = torch.full((B, Hq, S), float("nan"), device=dev)  # of the others: not read
+    want = torch.zeros(B, H, S, dtype=torch.float64, device=dev)
+    for h in range(Hq):
+        s = torch.einsum("bqd,bkd->bqk", q[:, S - n:, h].double(), k[:, :, h // (Hq // H)].double())
+        s = (s * scale).masked_fill_(~see, -float("inf"))
+        lse[:, h, S - n:] = s.logsumexp(-1).float()
+        want[:, h // (Hq // H)] += torch.exp(s - lse[:, h, S - n:, None].double()).sum(1)
+    got = usp.attn_key_weights(q, k, lse, observe=observe)
+    usp.usp_device_status()
+    ds = D * U * scale * float(q.abs().max() * k.abs().max()) * D
+    top = float(lse[:, :, S - n:].abs().max())
+    bound = want * (2 * ds + 4 * U * top + 2 * n * Hq * U + 2.0 ** -20)
+    assert ((got.double() - want).abs() <= bound + 1e-37).all()
+    for _ in range(20):
+        assert torch.equal(got, usp.attn_key_weights(q, k, lse, observe=observe))
+    usp.usp_device_status()
+
+
+@pytest.mark.parametrize("B,S,Hq,H,D,observe", [
+    (32, 1280, 8, 8, 128, 64),   # one query tile per block of a run
+    (32, 1100, 8, 8, 64, 64),
+    (32, 1100, 24, 8, 64, 64),   # three
+    (40, 700, 8, 8, 64, 300),    # three of one head
+])
+def test_key_weights_of_odd_tile_counts_over_many_items(B, S, Hq, H, D, observe):
+    """An odd number of query tiles per block of keys: which group of softmax warps
+    has a block's first tile changes from block to block and item to item."""
+    check_weights_of_many_items(B, S, Hq, H, D, observe)
+
+
 @pytest.mark.parametrize("causal,window,sink,observe", [(False, 0, 0, 64), (False, 3000, 9, 128),
                                                         (True, 0, 0, 4000), (False, 0, 0, 1)])
 def test_key_weights_of_runs_match_the_cuda_core_kernel(causal, window, sink, observe):
