@@ -65,8 +65,8 @@ using namespace tc;
 __device__ int g_key_weights_status = 0;
 
 constexpr int kQT = 128;            // queries per tile
-constexpr int kKT = 2;              // key tiles per item
-constexpr int kKeys = kKT * kTile;  // keys per item
+constexpr int kKT = 2;              // key tiles per block of keys
+constexpr int kKeys = kKT * kTile;  // keys per block
 constexpr int kSoftWarps = 8 * kKT; // two groups of four per key tile
 constexpr int kKeyWarp = kSoftWarps;
 constexpr int kQueryWarp = kKeyWarp + 1;
@@ -322,7 +322,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
   if (warp == kKeyWarp && lane == 0) {
     for (int s = 0; s < kKSlots; ++s) {
       mbar_init(bar(L::kKFull + s), 1);
-      mbar_init(bar(L::kKFree + s), 1);
+      mbar_init(bar(L::kKFree + s), kKT);  // both MMA warps
     }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(L::kQFull + s), 1);
@@ -582,6 +582,16 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
         const bool last = x + 1 == ip.blocks;
         slot = slot0;
         phase = phase0;
+        // The ring's slots go from one key tile to the other: this warp sees and
+        // frees the other tile too (it has landed by the time that its own has, or
+        // been multiplied by), so that it knows every phase of every slot.
+        auto pass_tile = [&](int other) {
+          const int ks = (kn + other) % kslots;
+          ok = mbar_wait(bar(L::kKFull + ks), ((kn + other) / kslots) & 1, abort_flag, status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok && lane == 0) mbar_arrive(bar(L::kKFree + ks));
+        };
+        if (a > 0) pass_tile(0);
         for (int j = 0; j < count && ok; ++j) {
           ok = mbar_wait(bar(L::kQFull + slot), phase, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -620,6 +630,7 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
             phase ^= 1;
           }
         }
+        if (ok && a + 1 < ktiles) pass_tile(a + 1);
         kn += ktiles;
         pairs += count;
       }

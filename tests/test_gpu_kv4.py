@@ -591,6 +591,17 @@ def test_key_weights_of_odd_tile_counts_over_many_items(B, S, Hq, H, D, observe)
     check_weights_of_many_items(B, S, Hq, H, D, observe)
 
 
+@pytest.mark.parametrize("B,S,Hq,H,D,observe", [
+    (32, 1100, 8, 8, 128, 400),  # four query tiles: two slots of keys
+    (32, 1025, 32, 8, 64, 100),  # four, of two heads
+    (32, 1152, 24, 8, 128, 33),  # three
+])
+def test_key_weights_of_short_last_blocks_over_many_items(B, S, Hq, H, D, observe):
+    """One key tile in a run's last block: the next item's keys go on in the other
+    MMA warp's slot of the ring."""
+    check_weights_of_many_items(B, S, Hq, H, D, observe)
+
+
 @pytest.mark.parametrize("causal,window,sink,observe", [(False, 0, 0, 64), (False, 3000, 9, 128),
                                                         (True, 0, 0, 4000), (False, 0, 0, 1)])
 def test_key_weights_of_runs_match_the_cuda_core_kernel(causal, window, sink, observe):
