@@ -621,8 +621,10 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
               if (j + 1 == count) mma_commit(bar(L::kKFree + ks));
               if (last) mma_commit(bar(L::kQFree + slot));
             }
-          } else if (last && lane == 0) {
-            mbar_arrive(bar(L::kQFree + slot));  // no such key tile
+          } else if (last && elect_one()) {
+            // no such key tile, but products of the blocks before may still read
+            // the slot: it is free once those of this thread are done
+            mma_commit(bar(L::kQFree + slot));
           }
           __syncwarp();
           if (++slot == qslots) {

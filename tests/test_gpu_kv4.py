@@ -602,6 +602,17 @@ def test_key_weights_of_short_last_blocks_over_many_items(B, S, Hq, H, D, observ
     check_weights_of_many_items(B, S, Hq, H, D, observe)
 
 
+@pytest.mark.parametrize("B,S,Hq,H,D,observe", [
+    (32, 2100, 32, 8, 128, 64),  # two tiles of two heads
+    (32, 2049, 16, 8, 64, 64),   # one
+    (32, 2176, 16, 8, 128, 120), # two
+])
+def test_key_weights_of_shared_queries_over_many_items(B, S, Hq, H, D, observe):
+    """The queries that a run's blocks shared make room for the next item's while
+    the last products are under way, and the run ends with one key tile."""
+    check_weights_of_many_items(B, S, Hq, H, D, observe)
+
+
 @pytest.mark.parametrize("causal,window,sink,observe", [(False, 0, 0, 64), (False, 3000, 9, 128),
                                                         (True, 0, 0, 4000), (False, 0, 0, 1)])
 def test_key_weights_of_runs_match_the_cuda_core_kernel(causal, window, sink, observe):
