@@ -119,12 +119,13 @@ struct WeightParams {
 
 template <int D>
 struct WSmem {
-  // A ring entry is written for tile x once the products of tile x - kSlots
-  // are done. With one key tile per item the scores four tiles before that
-  // have then been taken out, so entries up to x - kSlots - kSBufs - 2 are not
-  // used any more (the group that took tile x - kSlots - kSBufs is past its
-  // previous one).
-  static_assert(kRing >= kSlots + kSBufs + 2, "a statistics entry is free");
+  // A ring entry is written for tile x once both MMA warps have released tile
+  // y = x - kSlots (or later) in the last block of its item. One that multiplied it
+  // there had its two buffers emptied of all but the tile before, which is y - 1 or
+  // of y's item; one without keys there has waited until both were empty. So the
+  // softmax groups use no entry before y's item, nor, in an item of one block,
+  // before y - 1; and an item of several blocks has at most kSlots tiles.
+  static_assert(kRing > 2 * kSlots, "a statistics entry is free");
   static constexpr int kHalves = D / 64;
   static constexpr int kHalf = kTile * 128;             // 64 channels of a K or Q tile
   static constexpr int kTileBytes = kHalf * kHalves;
@@ -592,6 +593,16 @@ key_weights_tc_kernel(const WeightParams W, const __grid_constant__ CUtensorMap 
           if (ok && lane == 0) mbar_arrive(bar(L::kKFree + ks));
         };
         if (a > 0) pass_tile(0);
+        // A warp without keys in this block releases the queries as fast as they
+        // come, and the statistics ring with them: its groups first take out what
+        // they were given before.
+        if (ok && a >= ktiles) {
+          if (used0 > 0)
+            ok = mbar_wait(bar(L::kSFree + a), (used0 - 1) & 1, abort_flag, status);
+          if (ok && used1 > 0)
+            ok = mbar_wait(bar(L::kSFree + a + kKT), (used1 - 1) & 1, abort_flag, status);
+          ok = __all_sync(0xffffffffu, ok);
+        }
         for (int j = 0; j < count && ok; ++j) {
           ok = mbar_wait(bar(L::kQFull + slot), phase, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;

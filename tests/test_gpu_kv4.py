@@ -613,6 +613,18 @@ def test_key_weights_of_shared_queries_over_many_items(B, S, Hq, H, D, observe):
     check_weights_of_many_items(B, S, Hq, H, D, observe)
 
 
+@pytest.mark.parametrize("B,S,Hq,H,D,observe", [
+    (16, 2100, 8, 8, 64, 0),     # nine blocks, the last of one tile
+    (40, 1100, 8, 8, 128, 0),
+    (64, 900, 16, 8, 64, 0),
+    (160, 300, 24, 8, 128, 0),
+])
+def test_key_weights_of_all_queries_over_many_items(B, S, Hq, H, D, observe):
+    """Many query tiles per block: the ring of their statistics goes round while one
+    key tile's groups are behind and the other's block has begun."""
+    check_weights_of_many_items(B, S, Hq, H, D, observe)
+
+
 @pytest.mark.parametrize("causal,window,sink,observe", [(False, 0, 0, 64), (False, 3000, 9, 128),
                                                         (True, 0, 0, 4000), (False, 0, 0, 1)])
 def test_key_weights_of_runs_match_the_cuda_core_kernel(causal, window, sink, observe):
