@@ -110,6 +110,7 @@ struct Params {
   float2* scores;   // accumulate: [B][H][Rs / 2][C] log2-scaled scores of two rows
   int Tq, Hq, G, R, Rs, nrb;  // R = G Tq rows per KV head, nrb blocks of them
   int grid;
+  int slots;                  // of partials
   float score_mul;            // softmax scale * log2(e) * k_descale
   float v_descale;
   int causal, window, sink;
@@ -782,6 +783,14 @@ constexpr int kMergeThreads = 256;
 constexpr int kWeightKeys = 4;
 constexpr int kMaxWeightRows = 64;  // (m, 1 / l) kept at a time
 
+// A unit's first and last slot. Where a wait of the kernel before gave up (which
+// usp_device_status reports), they may never have been written: whatever stands
+// there, only slots that exist are read.
+__device__ __forceinline__ int2 span_of(const Params& P, int unit) {
+  const int2 s = P.span[unit];
+  return make_int2(max(s.x, 0), min(s.y, P.slots - 1));
+}
+
 // Block x < units * 8 NT: a row of a unit, whose partials (consecutive slots)
 // are merged in key order by D threads per part of them. Blocks behind those
 // (accumulate): a piece of the keys of a (sequence, KV head):
@@ -805,7 +814,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kv4_kernel(const Params P
     int2 span = make_int2(0, -1);  // no steps, no partials
     const bool some = seq_steps(P, seq_len(P, b)).n > 0;
     grid_dependency_wait();
-    if (some) span = P.span[unit];
+    if (some) span = span_of(P, unit);
     const int part = threadIdx.x / D, d = threadIdx.x - part * D;
     float M = -INFINITY, ls = 0.f, os = 0.f;
     #pragma unroll 2
@@ -870,7 +879,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kv4_kernel(const Params P
         __syncthreads();
         for (int r = warp; r < n; r += kMergeThreads / 32) {  // a warp per row
           const int rb = (r0 + r) / kRows, rr = r0 + r - rb * kRows;
-          const int2 span = P.span[b * per_seq + h * P.nrb + rb];
+          const int2 span = span_of(P, b * per_seq + h * P.nrb + rb);
           float M = -INFINITY, l = 0.f;
           for (long long i = span.x + lane; i <= span.y; i += 32)
             M = fmaxf(M, P.ml_part[i * kRows + rr].x);
@@ -1015,6 +1024,7 @@ usp_status_t launch_decode_kv4(const DecodeKv4Args& a, void* workspace, cudaStre
   const int nt = tiles_for(P.R);
   P.nrb = (P.R + 8 * nt - 1) / (8 * nt);
   P.grid = nt == 1 ? kGridMax : kGridMax / 2;
+  P.slots = P.c.B * P.c.H * P.nrb + kGridMax;  // as layout() has them
   P.score_mul = a.scale * kLog2e * a.k_descale;
   P.v_descale = a.v_descale * 16.f;  // the kernel's V is 2^-4 of the cache's
   P.causal = a.causal;
