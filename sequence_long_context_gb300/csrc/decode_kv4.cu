@@ -64,6 +64,7 @@
 #include <cuda_fp16.h>
 
 #include <cfloat>
+#include <cmath>
 
 #include "internal.h"
 #include "kv4.cuh"
@@ -111,7 +112,8 @@ struct Params {
   int Tq, Hq, G, R, Rs, nrb;  // R = G Tq rows per KV head, nrb blocks of them
   int grid;
   int slots;                  // of partials
-  float score_mul;            // softmax scale * log2(e) * k_descale
+  float score_mul;            // times 2^score_exp: softmax scale * log2(e) * k_descale
+  int score_exp;
   float v_descale;
   int causal, window, sink;
 };
@@ -444,7 +446,7 @@ decode_kv4_kernel(const Params P) {
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
       // 2^ex times a largest element in [1, 2) is brought to [64, 128)
-      const int ex = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100), 127);
+      const int ex = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -120), 127);
       const float up = __uint_as_float(static_cast<uint32_t>(127 + 6 - ex) << 23);
       float sum = 0.f;
 #pragma unroll
@@ -472,8 +474,10 @@ decode_kv4_kernel(const Params P) {
       const __half mid = __float2half_rn(rest);
       qb[nt][0] = half2_bits(__halves2half2(hi, mid));
       qb[nt][1] = half2_bits(__floats2half2_rn(rest - __half2float(mid), 0.f));
-      // 16 for the scale's 2^-4; not 0, which a masked key's -inf would make NaN
-      const float row_mul = fmaxf(ldexpf(P.score_mul * 16.f, ex - 6), FLT_MIN);
+      // 2^4 for the scale's 2^-4; not 0 or infinite, which a masked key's -inf or a
+      // score of 0 would make NaN
+      const float row_mul =
+          fminf(fmaxf(ldexpf(P.score_mul, P.score_exp + ex - 6 + 4), FLT_MIN), FLT_MAX);
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         mul[nt][e] = __shfl_sync(0xffffffffu, row_mul, 4 * (2 * t + e));
@@ -848,7 +852,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kv4_kernel(const Params P
     const float inv = none ? 0.f : 1.f / lt;
     const int i = d >> 4, half = (d >> 3) & 1, g = d & 7;
     const int ch = g * (D / 8) + 8 * (i >> 2) + (i & 3) + 4 * half;
-    P.out[o_row * D + ch] = __float2bfloat16_rn(none ? 0.f : ot * inv * P.v_descale);
+    // (the kernel's V is 2^-4 of the cache's)
+    P.out[o_row * D + ch] = __float2bfloat16_rn(none ? 0.f : ot * inv * 16.f * P.v_descale);
     if (d == 0) P.lse[o_row] = none ? -INFINITY : (Mt + log2f(lt)) * kLn2;
     return;
   }
@@ -1025,8 +1030,9 @@ usp_status_t launch_decode_kv4(const DecodeKv4Args& a, void* workspace, cudaStre
   P.nrb = (P.R + 8 * nt - 1) / (8 * nt);
   P.grid = nt == 1 ? kGridMax : kGridMax / 2;
   P.slots = P.c.B * P.c.H * P.nrb + kGridMax;  // as layout() has them
-  P.score_mul = a.scale * kLog2e * a.k_descale;
-  P.v_descale = a.v_descale * 16.f;  // the kernel's V is 2^-4 of the cache's
+  // (the product alone may be beyond fp32)
+  P.score_mul = (float)std::frexp((double)a.scale * kLog2e * a.k_descale, &P.score_exp);
+  P.v_descale = a.v_descale;
   P.causal = a.causal;
   P.window = a.window;
   P.sink = a.sink;

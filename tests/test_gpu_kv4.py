@@ -421,6 +421,21 @@ def test_decode_keys_far_below_the_dominant_ones(D, G, sink_scale):
     assert float((lse.double() - np.log(8 / p + n)).abs().max()) <= L * U + 20 * 4 * U + 2.0 ** -20
 
 
+@pytest.mark.parametrize("D,Tq", [(64, 1), (128, 3)])
+@pytest.mark.parametrize("which,descale", [("v", 3e37), ("v", 3.4e38), ("k", 3e37), ("k", 3.4e38)])
+def test_decode_with_the_largest_descales(which, descale, D, Tq):
+    """The smallest scales under descales up to fp32's largest number: the values
+    and the scores are ordinary numbers (k: under queries near 2^-121)."""
+    dev = device()
+    c = random_cache(dev, 2, 112, 2, D, [100, 57], seed=15)._replace(**{which + "_descale": descale})
+    for b, n in enumerate((100, 57)):
+        getattr(c, which + "_scale")[b, :, :n] = 1  # 2^-9
+    q = torch.randn(2, Tq, 8, D, generator=gen(16)) * (2.0 ** -121 if which == "k" else 1.0)
+    q = q.to(torch.bfloat16)
+    out, lse = usp.attn_decode_kv4(q.to(dev), c)
+    check_decode(c, q, out, lse, None, None, [100, 57], True, 0, 0)
+
+
 def test_decode_long_cache_offsets_pass_32_bits():
     """Codes of the last head start behind 4 GiB; only its rows are filled."""
     dev = device()
