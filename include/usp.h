@@ -565,7 +565,8 @@ size_t usp_attn_decode_kv4_workspace_size(int B, int Tq, int capacity, int Hq, i
  *                       heads h of KV head g of exp(s_ij - LSE_i),
  * the column sums of the attention matrix ("Long Context Attention" notes,
  * "Motivation": LSE is what is kept of the forward). `observe` <= 0 observes
- * every query; observe = n the last n of each sequence.
+ * every query; observe = n the last n of each sequence. Tokens before
+ * cu_seqlens[0] and from cu_seqlens[B] on (padding) add nothing and get 0.
  * weight [B, Hkv, S] fp32 (packed [Hkv, S]), rank-major, written; 16-byte
  *      aligned like the others. lse: a query with LSE = -inf adds nothing.
  * flags: USP_FLAG_FORCE_SIMT or none (else USP_ERR_UNSUPPORTED).

@@ -190,7 +190,8 @@ __device__ __forceinline__ ItemPos item_pos(const WeightParams& W, int item) {
   return r;
 }
 
-// The queries that see the key at natural position j, as positions [lo, hi].
+// The queries that see the key at natural position j, as positions [lo, hi]; none
+// where a packed batch has no sequence there.
 struct Seen {
   int lo, hi;
 };
@@ -200,6 +201,7 @@ __device__ __forceinline__ Seen seen_by(const AttnParams& P, int j) {
     const int n = seg_of(P.cu, P.nseq, j);
     s = __ldg(P.cu + n);
     e = __ldg(P.cu + n + 1);
+    if (j < s || j >= e) return Seen{1, 0};
   }
   Seen r;
   r.lo = P.causal ? j : s;
@@ -252,6 +254,7 @@ struct KeyBlock {
   PosRange k;     // natural positions of the keys
   PosRange q;     // of the queries that may see one of them
   int seg0, seg1; // packed sequences of the first and last key
+  int begin, end; // of them
 };
 __device__ __forceinline__ KeyBlock key_block(const AttnParams& P, int key0, int blocks) {
   KeyBlock b;
@@ -264,6 +267,8 @@ __device__ __forceinline__ KeyBlock key_block(const AttnParams& P, int key0, int
     s0 = __ldg(P.cu + b.seg0);
     e1 = __ldg(P.cu + b.seg1 + 1);
   }
+  b.begin = s0;
+  b.end = e1;
   const bool sinks = P.sink > 0 && (b.seg0 != b.seg1 || b.k.lo < s0 + P.sink);
   b.q.lo = P.causal ? b.k.lo : s0;
   b.q.hi = (P.window > 0 && !sinks) ? min(e1 - 1, b.k.hi + P.window - 1) : e1 - 1;
@@ -292,6 +297,8 @@ __device__ __forceinline__ int classify_tile(const WeightParams& W, int qt, cons
   if (P.cu != nullptr) {
     const int s0 = seg_of(P.cu, P.nseq, q.lo), s1 = seg_of(P.cu, P.nseq, q.hi);
     if (s0 != s1 || b.seg0 != b.seg1 || s0 != b.seg0) return kClsMasked;
+    // (rows outside the boundaries count as the first or last sequence's)
+    if (min(q.lo, b.k.lo) < b.begin || max(q.hi, b.k.hi) >= b.end) return kClsMasked;
   }
   if (P.causal && b.k.hi > q.lo) all = false;
   if (P.window > 0 && q.hi - b.k.lo >= P.window) all = false;

@@ -766,6 +766,38 @@ def test_key_weights_of_the_largest_window_and_sinks(cut, flags):
         assert torch.allclose(got, want, rtol=700 * 2 * U)
 
 
+@pytest.mark.parametrize("causal,window,observe", [(True, 0, 0), (False, 0, 0), (True, 90, 0),
+                                                   (False, 0, 25)])
+@pytest.mark.parametrize("path", ["bf16", "simt", "fp32"])
+def test_key_weights_of_a_padded_batch(path, causal, window, observe):
+    """Tokens before the first boundary and behind the last, whatever they hold, get
+    0 and add nothing: the sequences' weights are those of the batch without them."""
+    dev = device()
+    dt = torch.float32 if path == "fp32" else torch.bfloat16
+    cut, S, H = [30, 500, 500, 1101], 1400, 2
+    g = gen(17)
+    q = torch.randn(S, 4, 64, generator=g).to(dt).to(dev)
+    k = torch.randn(S, H, 64, generator=g).to(dt).to(dev)
+    kw = dict(causal=causal, window=window)
+    flags = usp.FLAG_FORCE_SIMT if path == "simt" else 0
+    mid = slice(cut[0], cut[-1])
+    cu = torch.tensor(cut, dtype=torch.int32, device=dev)
+    qm, km = q[mid].contiguous(), k[mid].contiguous()
+    _, lm = usp.attn_forward(qm, km, km, cu_seqlens=cu - cut[0], **kw)
+    want = usp.attn_key_weights(qm, km, lm, cu_seqlens=cu - cut[0], observe=observe, flags=flags, **kw)
+    for junk in (0.5, float("nan")):
+        lse = torch.full((4, S), junk, device=dev)
+        lse[:, mid] = lm
+        for t in (q, k):
+            t[:cut[0]] = junk
+            t[cut[-1]:] = junk
+        got = usp.attn_key_weights(q, k, lse, cu_seqlens=cu, observe=observe, flags=flags, **kw)
+        assert (got[:, :cut[0]] == 0).all() and (got[:, cut[-1]:] == 0).all()
+        # the sums run over other tiles: n u in each, on up to 2 S positive terms
+        assert torch.allclose(got[:, mid], want, rtol=2 * 2 * S * U, atol=0)
+    usp.usp_device_status()
+
+
 # ------------------------------------------------------------------------- evict
 
 EVICT = [
