@@ -494,8 +494,10 @@ typedef struct {
  * Token t of sequence b goes to row seq_lens[b] + t of the sequence's rows;
  *      tokens that find no room are dropped.
  * new_weight  NULL, or the new keys' attention weights so far, fp32
- *      [B, Hkv, T] (packed [Hkv, T]), as usp_attn_key_weights gives them.
- *      Where the cache has a key_weight, the new rows get these, or 0.
+ *      [B, Hkv, T] (packed [Hkv, T]), in natural order like k and v.
+ *      usp_attn_key_weights gives them in rank-major order: the same for the
+ *      contiguous layout, else USP_PERMUTE_RESTORE of B*Hkv sequences of T
+ *      4-byte rows brings them into this one. Where the cache has a key_weight, the new rows get these, or 0.
  * seq_lens_out  [B] int32 or NULL: min(capacity, seq_lens[b] + the sequence's
  *      new tokens) is written. May be the cache's seq_lens itself.
  * Two appends to one cache must not overlap on the GPU.
@@ -567,7 +569,8 @@ size_t usp_attn_decode_kv4_workspace_size(int B, int Tq, int capacity, int Hq, i
  * "Motivation": LSE is what is kept of the forward). `observe` <= 0 observes
  * every query; observe = n the last n of each sequence. Tokens before
  * cu_seqlens[0] and from cu_seqlens[B] on (padding) add nothing and get 0.
- * weight [B, Hkv, S] fp32 (packed [Hkv, S]), rank-major, written; 16-byte
+ * weight [B, Hkv, S] fp32 (packed [Hkv, S]), rank-major (usp_permute brings it
+ *      into natural order, as usp_kv4_append takes it), written; 16-byte
  *      aligned like the others. lse: a query with LSE = -inf adds nothing.
  * flags: USP_FLAG_FORCE_SIMT or none (else USP_ERR_UNSUPPORTED).
  * workspace: at least usp_attn_key_weights_workspace_size(...) bytes (B: the
@@ -629,7 +632,9 @@ usp_status_t usp_kv4_evict(const usp_kv4_cache_t *src, const usp_kv4_cache_t *ds
  *     dst[u][b][p][h][d] = src[b][p][u*H/ud + h][d].
  * ULYSSES_HEAD2SEQ is its inverse (dst [B,S,H,D], src [ud,B,S,H/ud,D]).
  * elem_bytes 1 (E4M3 codes), 2 or 4. H*D*elem_bytes (Ulysses: H/ud*D*elem_bytes) must be a
- * multiple of 16. S divisible as for usp_attn_fwd. src and dst must not
+ * multiple of 16; EXTRACT and RESTORE also take rows of 4 bytes in all, one number per
+ * token: an LSE ([B, Hq, S] as B*Hq sequences of S, H = D = 1, elem_bytes 4) or the
+ * weights of usp_attn_key_weights. S divisible as for usp_attn_fwd. src and dst must not
  * overlap. Errors: USP_ERR_INVALID_ARG, USP_ERR_ALIGNMENT, USP_ERR_CUDA.
  */
 usp_status_t usp_permute(const void *src, void *dst, usp_permute_kind_t kind,

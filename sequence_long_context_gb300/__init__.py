@@ -436,7 +436,8 @@ def attn_forward_fp8(q8, k8, v8, q_descale, k_descale, v_descale, *, causal=True
 def permute(x: torch.Tensor, kind: str, layout: str = "contiguous", cp: int = 1,
             ud: int = 1, stream=None) -> torch.Tensor:
     """Layout extract/restore of [B,S,H,D] (packed: [T,H,D]) or the Ulysses
-    exchange ([B,S,H,D] <-> [ud,B,S,H/ud,D])."""
+    exchange ([B,S,H,D] <-> [ud,B,S,H/ud,D]). One 4-byte number per token, such as
+    the key weights w [B,Hkv,S]: permute(w.view(B * Hkv, S, 1, 1), ...).view_as(w)."""
     if kind in ("extract", "restore"):
         xb = x if x.dim() == 4 else x.unsqueeze(0)
         B, S, H, D = xb.shape
@@ -581,7 +582,8 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, *, key_weight=
     """Store new tokens' keys and values (bf16 or fp32, natural order) behind
     each sequence's cached ones: k, v [B,T,Hkv,D], or packed [T,Hkv,D] with
     cu_seqlens. key_weight: their attention weights so far ([B,Hkv,T], packed
-    [Hkv,T]; attn_key_weights), else 0. Returns the new lengths, written to
+    [Hkv,T], natural order: attn_key_weights, restored by permute if the layout is
+    not contiguous), else 0. Returns the new lengths, written to
     seq_lens_out (default: the cache's own seq_lens, in place). Tokens that
     find no room are dropped."""
     s, at, B, H, _, D = _kv4_struct(cache)
@@ -666,7 +668,7 @@ def attn_key_weights(q, k, lse, *, causal=True, window=0, sink_tokens=0, cu_seql
     """[B,Hkv,S] fp32 (packed [Hkv,T]): the attention weight that each key
     collected from the observed queries (observe = n: the last n of each
     sequence; 0: all) and the query heads sharing its KV head, from the
-    forward's q, k (rank-major) and lse."""
+    forward's q, k (rank-major) and lse; rank-major too (permute restores it)."""
     if stream is not None:
         with _on(stream, q.device):
             return attn_key_weights(q, k, lse, causal=causal, window=window,

@@ -835,7 +835,9 @@ usp_status_t usp_permute(const void* src, void* dst, usp_permute_kind_t kind,
   switch (kind) {
     case USP_PERMUTE_EXTRACT:
     case USP_PERMUTE_RESTORE:
-      if (row % 16 != 0) return USP_ERR_INVALID_ARG;
+      // (a row of one 4-byte number: an LSE, key weights)
+      if (row % 16 != 0 && row != 4) return USP_ERR_INVALID_ARG;
+      if ((long long)B * S > 0x7fffffffLL) return USP_ERR_UNSUPPORTED;
       return launch_permute_layout(src, dst, B, S, (int)row, layout, cp_size,
                                    kind == USP_PERMUTE_RESTORE, st);
     case USP_PERMUTE_ULYSSES_SEQ2HEAD:

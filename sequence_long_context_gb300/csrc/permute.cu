@@ -1,7 +1,7 @@
 // Layout permutes and the Ulysses all-to-all, emulated in device memory.
 //
 // Both are pure data movement, so they are HBM-bound: each token row
-// (H*D*elem bytes, a multiple of 16) is moved with 16-byte vector loads and
+// (H*D*elem bytes, a multiple of 16, or one 4-byte number) is moved with 16-byte vector loads and
 // stores, several vectors in flight per thread, over a grid sized to the SM
 // count. Results are bit-exact copies.
 //
@@ -68,6 +68,22 @@ permute_layout_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst,
   }
 }
 
+// The same for rows of one 4-byte number (an LSE, key weights): a thread per row.
+// The rank-major side is read or written in order; the other side is runs of it
+// (stripe: strides that L2 gathers).
+__global__ void __launch_bounds__(kThreads)
+permute_layout_word_kernel(const uint32_t* __restrict__ src, uint32_t* __restrict__ dst,
+                           unsigned rows, unsigned S, int layout, int cp, int shard, int chunk,
+                           int restore) {
+  const unsigned step = gridDim.x * kThreads;
+  for (unsigned r = blockIdx.x * kThreads + threadIdx.x; r < rows; r += step) {
+    const unsigned b = r / S, p = r - b * S;
+    const unsigned other = b * S + (unsigned)nat_pos((int)p, layout, cp, shard, chunk);
+    if (restore) dst[other] = __ldg(src + r);
+    else dst[r] = __ldg(src + other);
+  }
+}
+
 // Ulysses exchange: src [B*S][ud][rvu] <-> dst [ud][B*S][rvu] (16-byte
 // vectors); one warp per (group, token row). With layout >= 0 the flat side
 // is in natural sequence order and the grouped side in rank-major order:
@@ -109,9 +125,19 @@ usp_status_t launch_permute_layout(const void* src, void* dst, int B, int S,
                                    int restore, cudaStream_t st) {
   unsigned rv = (unsigned)(row_bytes / 16);
   unsigned rows = (unsigned)B * (unsigned)S;
-  if ((long long)rows * rv == 0) return USP_OK;
+  if (rows == 0) return USP_OK;
   int shard = S / cp;
   int chunk = layout == kZigzag ? S / (2 * cp) : shard;
+  if (row_bytes == 4) {
+    {
+      ProfScope ps(st, "permute_layout");
+      permute_layout_word_kernel<<<grid_for((rows + 31ll) / 32), kThreads, 0, st>>>(
+          static_cast<const uint32_t*>(src), static_cast<uint32_t*>(dst), rows, (unsigned)S,
+          layout, cp, shard, chunk, restore);
+    }
+    note_launch();
+    return check_launch();
+  }
   {
     ProfScope ps(st, "permute_layout");
     permute_layout_kernel<<<grid_for(rows), kThreads, 0, st>>>(

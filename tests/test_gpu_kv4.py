@@ -938,6 +938,40 @@ def test_prompt_eviction_and_decoding_together():
     usp.usp_device_status()
 
 
+@pytest.mark.parametrize("layout,cp,packed", [("zigzag", 4, False), ("stripe", 2, False),
+                                              ("zigzag", 2, True)])
+def test_ring_prompt_into_the_cache_with_its_weights(layout, cp, packed):
+    """The weights of a ring's prompt are restored to natural order like its keys,
+    and are then those of the same prompt in natural order (sums over other tiles:
+    n u in each); the cache's rows and weights belong together."""
+    dev = device()
+    g = gen(22)
+    S, Hq, H, D = 776, 4, 2, 64
+    lead = () if packed else (2,)
+    q = torch.randn(*lead, S, Hq, D, generator=g).to(torch.bfloat16).to(dev)
+    k, v = (torch.randn(*lead, S, H, D, generator=g).to(torch.bfloat16).to(dev) for _ in "kv")
+    kw = dict(cu_seqlens=torch.tensor([0, 300, S], dtype=torch.int32, device=dev)) if packed else {}
+    _, lse = usp.attn_forward(q, k, v, **kw)
+    want = usp.attn_key_weights(q, k, lse, **kw)
+    qp, kp, vp = (usp.permute(t, "extract", layout, cp) for t in (q, k, v))
+    _, lp = usp.attn_forward(qp, kp, vp, cp=cp, layout=layout, **kw)
+    w = usp.attn_key_weights(qp, kp, lp, cp=cp, layout=layout, **kw)
+    nat = usp.permute(w.view(-1, S, 1, 1), "restore", layout, cp).view_as(w)
+    back = usp.permute(nat.view(-1, S, 1, 1), "extract", layout, cp).view_as(w)
+    assert torch.equal(back, w)
+    index = layouts.restore(np.arange(S), layout, cp, axis=0)
+    assert torch.equal(nat, w[..., torch.from_numpy(index).to(dev)])
+    # the LSEs, rounded sums of up to S terms near 10, may differ too
+    assert torch.allclose(nat, want, rtol=4 * S * U + 2 * 10 * U)
+    c = usp.kv4_cache(2, S, H, D, device=dev, key_weight=True)
+    usp.kv4_append(c, usp.permute(kp, "restore", layout, cp), usp.permute(vp, "restore", layout, cp),
+                   key_weight=nat, **kw)
+    for b, (at, n) in enumerate([(0, 300), (300, S - 300)] if packed else [(0, S)] * 2):
+        one = nat[:, at:at + n] if packed else nat[b]
+        assert torch.equal(c.key_weight[b, :, :n], one)
+    usp.usp_device_status()
+
+
 def test_evict_in_place_captured_and_twice():
     """An eviction in place, captured: each replay evicts what the cache holds
     then; a second one right behind it finds nothing to do."""

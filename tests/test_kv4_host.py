@@ -230,3 +230,14 @@ def test_helpers_refuse_what_does_not_fit():
         with pytest.raises((ValueError, KeyError)):
             f()
             pytest.fail(f"case {i} was accepted")
+
+
+def test_permute_of_one_number_per_token_refuses(lib):
+    def f(kind, B, S, H, D, eb, dst=FAR):
+        return lib.usp_permute(FAKE, dst, kind, 1, B, S, H, D, 4, 1, eb, None)
+    assert f(1, 2, 128, 1, 2, 4) == 1             # 8 bytes
+    assert f(1, 2, 124, 1, 1, 4) == 1             # S % (2 cp)
+    assert f(2, 2, 128, 1, 1, 4) == 1             # the Ulysses exchange moves whole heads
+    assert f(1, 2, 128, 1, 1, 4, FAR + 4) == 3
+    assert f(0, 65536, 1 << 15, 1, 1, 4) == 2     # 2^31 rows
+    assert f(1, 0, 128, 1, 1, 4) == 0             # nothing to do
