@@ -467,7 +467,8 @@ size_t usp_attn_decode_workspace_size(int B, int Tq, int S, int Hq, int Hkv,
  *                         capacity as capacity.
  * The struct is host memory, read during the call. Requirements, checked by
  * every call: B >= 0, Hkv >= 1 (both at most 65535), D 64 or 128
- * (USP_ERR_UNSUPPORTED), capacity >= 0 and a multiple of 16, descales finite,
+ * (USP_ERR_UNSUPPORTED), capacity >= 0 and a multiple of 16, at most
+ * 2^31 - 2^20 (USP_ERR_UNSUPPORTED), descales finite,
  * > 0 and with a finite reciprocal, the code, scale and weight arrays 16-byte
  * aligned, seq_lens 4-byte aligned. Rows behind a sequence's length are never
  * read as keys, and are left as they were.

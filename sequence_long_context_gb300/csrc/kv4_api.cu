@@ -12,11 +12,15 @@ bool aligned(const void* p, unsigned n) {
   return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
 }
 
+constexpr int kMaxCapacity = 0x7fffffff - (1 << 20) + 1;
+
 // The checks every call makes of a cache (usp.h, "The 4-bit KV cache").
 usp_status_t check_cache(const usp_kv4_cache_t* c) {
   if (!c || c->B < 0 || c->Hkv < 1 || c->capacity < 0 || c->capacity % kv4::kRowAlign != 0)
     return USP_ERR_INVALID_ARG;
   if (c->B > 65535 || c->Hkv > 65535) return USP_ERR_UNSUPPORTED;
+  // the kernels count rows in 32 bits, and step past the last by less than 2^20
+  if (c->capacity > kMaxCapacity) return USP_ERR_UNSUPPORTED;
   if (c->D != 64 && c->D != 128) return USP_ERR_UNSUPPORTED;
   const float d[] = {c->k_descale, c->v_descale};
   for (float x : d)

@@ -232,6 +232,14 @@ def test_helpers_refuse_what_does_not_fit():
             pytest.fail(f"case {i} was accepted")
 
 
+def test_capacities_whose_counts_would_pass_31_bits_are_refused(lib):
+    """Such a cache (one sequence, one head of 64: 146 GB) fits the GPU."""
+    for capacity in (2 ** 31 - 16, 2 ** 31 - 2 ** 20 + 16):
+        c = cache(B=1, Hkv=1, D=64, capacity=capacity)
+        assert append(lib, c) == read(lib, c) == 2
+        assert decode(lib, c, Hq=1) == decode(lib, c, Hq=1, acc=1) == evict(lib, c, c) == 2
+
+
 def test_permute_of_one_number_per_token_refuses(lib):
     def f(kind, B, S, H, D, eb, dst=FAR):
         return lib.usp_permute(FAKE, dst, kind, 1, B, S, H, D, 4, 1, eb, None)
