@@ -41,6 +41,12 @@ kv4::Cache view(const usp_kv4_cache_t* c) {
           c->key_weight, c->seq_lens, c->B, c->capacity, c->Hkv};
 }
 
+// 32-bit row and unit counts in the decode's kernels
+bool too_many_rows(int B, int Tq, int Hq, int Hkv) {
+  const long long rows = (long long)(Hq / Hkv) * Tq;
+  return rows > (1 << 20) || (long long)B * Hkv * ((rows + 7) / 8) > 0x3fffffffLL;
+}
+
 bool valid_dtype(usp_dtype_t t) { return t == USP_BF16 || t == USP_FP32; }
 
 // [a, a + na) and [b, b + nb) share a byte
@@ -89,7 +95,14 @@ usp_status_t usp_kv4_read(const usp_kv4_cache_t* cache, const int32_t* start, in
 
 size_t usp_attn_decode_kv4_workspace_size(int B, int Tq, int capacity, int Hq, int Hkv, int D,
                                           int accumulate) {
-  if (B < 0 || Tq < 1 || capacity < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || D < 1) return 0;
+  usp_kv4_cache_t c{};
+  c.capacity = capacity;
+  c.Hkv = Hkv;
+  c.D = D;
+  c.k_descale = c.v_descale = 1.f;
+  if (check_cache(&c) != USP_OK || B < 0 || B > 65535 || Tq < 1 || Hq < 1 || Hq % Hkv != 0 ||
+      too_many_rows(B, Tq, Hq, Hkv))
+    return 0;
   return decode_kv4_workspace(B, Tq, capacity, Hq, Hkv, D, accumulate);
 }
 
@@ -107,10 +120,7 @@ usp_status_t usp_attn_decode_kv4(const usp_kv4_cache_t* cache, const void* q, vo
     return USP_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 16)) return USP_ERR_ALIGNMENT;
   if (!aligned(workspace, 256)) return USP_ERR_ALIGNMENT;
-  // 32-bit row and unit counts in the kernels
-  const long long rows = (long long)(Hq / cache->Hkv) * Tq;
-  if (rows > (1 << 20) || (long long)cache->B * cache->Hkv * ((rows + 7) / 8) > 0x3fffffffLL)
-    return USP_ERR_UNSUPPORTED;
+  if (too_many_rows(cache->B, Tq, Hq, cache->Hkv)) return USP_ERR_UNSUPPORTED;
   if (cache->B == 0) return USP_OK;
   if (!workspace || workspace_bytes < decode_kv4_workspace(cache->B, Tq, cache->capacity, Hq,
                                                            cache->Hkv, cache->D, accumulate))

@@ -240,6 +240,15 @@ def test_capacities_whose_counts_would_pass_31_bits_are_refused(lib):
         assert decode(lib, c, Hq=1) == decode(lib, c, Hq=1, acc=1) == evict(lib, c, c) == 2
 
 
+def test_workspace_size_is_0_for_what_the_decode_refuses(lib):
+    f = usp.usp_attn_decode_kv4_workspace_size
+    ok = dict(B=2, Tq=1, capacity=64, Hq=8, Hkv=2, D=128, accumulate=1)
+    assert f(**ok) > 0 and f(**{**ok, "B": 0}) >= 0
+    for bad in (dict(D=96), dict(capacity=72), dict(capacity=2 ** 31 - 16), dict(B=70000),
+                dict(Hkv=70000, Hq=70000), dict(Tq=1 << 20), dict(B=65535, Hkv=65535, Hq=65535)):
+        assert f(**{**ok, **bad}) == 0, bad
+
+
 def test_permute_of_one_number_per_token_refuses(lib):
     def f(kind, B, S, H, D, eb, dst=FAR):
         return lib.usp_permute(FAKE, dst, kind, 1, B, S, H, D, 4, 1, eb, None)
