@@ -572,9 +572,12 @@ def _kv4_struct(cache: KV4Cache):
         _need(lens, "cache.seq_lens", _I32, (B,), k.device)
         if w is not None:
             _need(w, "cache.key_weight", _F32, (B, H, C), k.device)
-    return _pack_kv4(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(),
-                     0 if w is None else w.data_ptr(), lens.data_ptr(), B, C, H, 2 * half,
-                     kd, vd), at, B, H, C, 2 * half
+    try:
+        s = _pack_kv4(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(),
+                      0 if w is None else w.data_ptr(), lens.data_ptr(), B, C, H, 2 * half, kd, vd)
+    except struct.error as e:
+        raise ValueError(f"the sizes must fit 32 bits and the descales be numbers, got {kd} and {vd}") from e
+    return s, at, B, H, C, 2 * half
 
 
 def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, *, key_weight=None,
@@ -591,6 +594,8 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, *, key_weight=
     dt = k.dtype
     if dt not in DTYPE:
         raise ValueError("keys and values must be bf16 or fp32")
+    if k.dim() != (3 if packed else 4):
+        raise ValueError("k must be [B, T, Hkv, D], packed [T, Hkv, D]")
     T = k.shape[0] if packed else k.shape[1]
     shape = (T, H, D) if packed else (B, T, H, D)
     _require(k, "k", dt, shape, at, cache.k)

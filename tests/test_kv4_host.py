@@ -249,6 +249,24 @@ def test_workspace_size_is_0_for_what_the_decode_refuses(lib):
         assert f(**{**ok, **bad}) == 0, bad
 
 
+@pytest.mark.parametrize("over", [dict(v_descale="1"), dict(k_descale=None)])
+def test_helpers_refuse_descales_that_are_no_numbers(over):
+    c = usp.kv4_cache(2, 48, 2, 128, device="cpu", key_weight=True)._replace(**over)
+    x = torch.zeros(2, 1, 2, 128, dtype=torch.bfloat16)
+    for f in (lambda: usp.kv4_append(c, x, x), lambda: usp.kv4_read(c, 1),
+              lambda: usp.attn_decode_kv4(x, c), lambda: usp.kv4_evict(c, 4)):
+        with pytest.raises(ValueError, match="descale"):
+            f()
+
+
+@pytest.mark.parametrize("shape", [(3,), (2, 3), (2, 3, 2)])
+def test_append_refuses_other_ranks(shape):
+    c = usp.kv4_cache(2, 48, 2, 128, device="cpu")
+    x = torch.zeros(shape, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        usp.kv4_append(c, x, x)
+
+
 def test_permute_of_one_number_per_token_refuses(lib):
     def f(kind, B, S, H, D, eb, dst=FAR):
         return lib.usp_permute(FAKE, dst, kind, 1, B, S, H, D, 4, 1, eb, None)
