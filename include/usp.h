@@ -472,6 +472,9 @@ size_t usp_attn_decode_workspace_size(int B, int Tq, int S, int Hq, int Hkv,
  * > 0 and with a finite reciprocal, the code, scale and weight arrays 16-byte
  * aligned, seq_lens 4-byte aligned. Rows behind a sequence's length are never
  * read as keys, and are left as they were.
+ * A call that writes a cache (usp_kv4_append, usp_attn_decode_kv4 with
+ * accumulate, usp_kv4_evict into it) must not overlap on the GPU with another
+ * call on the same cache.
  */
 typedef struct {
   void *k_codes;
@@ -501,7 +504,6 @@ typedef struct {
  *      4-byte rows brings them into this one. Where the cache has a key_weight, the new rows get these, or 0.
  * seq_lens_out  [B] int32 or NULL: min(capacity, seq_lens[b] + the sequence's
  *      new tokens) is written. May be the cache's seq_lens itself.
- * Two appends to one cache must not overlap on the GPU.
  * Errors: USP_ERR_INVALID_ARG, USP_ERR_UNSUPPORTED, USP_ERR_ALIGNMENT,
  *      USP_ERR_CUDA.
  */
@@ -533,11 +535,14 @@ usp_status_t usp_kv4_read(const usp_kv4_cache_t *cache, const int32_t *start, in
  * token with i < 0, or that sees no key, gets O = 0 and LSE = -inf.
  *
  * q    [B, Tq, Hq, D] bf16; out likewise, written; lse [B, Tq, Hq] fp32,
- *      written (natural log of the scaled scores' sum; with it the partial of
- *      this cache can be merged with others by usp_merge_partials).
+ *      written (natural log of the scaled scores' sum). usp_merge_partials
+ *      merges the results of several caches by it, but takes fp32 partials: out
+ *      is converted, and stays rounded to bf16 once per cache.
  * accumulate  != 0: the attention weight that every cached key gets from this
  *      step, summed over the Tq tokens and the query heads that share its KV
- *      head, is added to the cache's key_weight (which must not be NULL).
+ *      head, is added to the cache's key_weight (which must not be NULL). The
+ *      weights are probabilities among this cache's keys: of a sequence whose
+ *      keys lie in several caches, they are not those of the whole.
  * The work is divided on the device by the lengths that it finds there: every
  * CTA takes an equal run of 32-key steps, over the ends of heads and
  * sequences, and the partials of a head are merged in key order. The result

@@ -642,7 +642,7 @@ def attn_decode_kv4(q: torch.Tensor, cache: KV4Cache, *, causal=True, window=0, 
                     ) -> Tuple[torch.Tensor, torch.Tensor]:
     """(out [B,Tq,Hq,D], lse [B,Tq,Hq]) of the newest Tq tokens q [B,Tq,Hq,D]
     (already in the cache) against the cached keys; accumulate adds each key's
-    attention weight of this step to cache.key_weight."""
+    attention weight of this step, among this cache's keys, to cache.key_weight."""
     if stream is not None:
         with _on(stream, q.device):
             return attn_decode_kv4(q, cache, causal=causal, window=window,
