@@ -915,6 +915,9 @@ bool make_map(CUtensorMap* m, const void* base, int Bt, int S, int H, int D, int
 // 34, 38 with 16, 8, 4; 2K tokens: 27, 20, 19; a zigzag ring of 4 over 4K: 32, 39,
 // 43; and 3 to 4 us for the sum of the segments, where there are any).
 constexpr int kMinTiles = 16;
+// Pairs of a query tile and a head in an item, at most: a pair takes 1.2 us, and
+// roles wait for up to an item's time, so 0.3 s where a wait gives up after 2.
+constexpr long long kMaxPairs = 1 << 18;
 // How the problem is cut (host side, from the shapes alone).
 struct Cut {
   int hpi, nseg, nkb, q0, ntiles, parts;
@@ -948,6 +951,8 @@ Cut cut_of(int B, int S, int Hq, int Hkv, int observe, bool tail, int nseq) {
       c.nseg = (int)n;
     }
   }
+  const long long cuts = ((long long)tiles * c.hpi + kMaxPairs - 1) / kMaxPairs;
+  if (c.nseg < cuts) c.nseg = (int)cuts;
   c.parts = (G / c.hpi) * c.nseg;
   return c;
 }

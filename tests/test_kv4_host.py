@@ -198,6 +198,17 @@ def test_key_weights_workspace(lib):
     assert weights(lib, S=0, q=None, k=None, lse=None, w=None) == 0
 
 
+def test_key_weights_of_very_long_prompts_are_cut(lib):
+    """An item's roles wait for one another for at most 2 s, and a pair of a query
+    tile and a head takes 1.2 us: items have 2^18 pairs at most, so the parts are
+    tiles x heads / 2^18 (each [B, Hkv, S] fp32)."""
+    f = usp.usp_attn_key_weights_workspace_size
+    assert f(1, 2 ** 20, 32, 1, 0, torch.bfloat16) == 0                    # 2^18 pairs
+    assert f(1, 2 ** 21, 128, 1, 0, torch.bfloat16) == 8 * 2 ** 21 * 4     # 2^21
+    assert f(1, 2 ** 22, 16, 1, 0, torch.bfloat16) == 2 * 2 ** 22 * 4      # 2^19
+    assert f(1, 2 ** 22, 16, 1, 4096, torch.bfloat16) == 0                 # few queries
+
+
 def test_helpers_refuse_what_does_not_fit():
     c = usp.kv4_cache(2, 40, 2, 128, device="cpu", key_weight=True)
     assert c.k.shape == (2, 2, 48, 64) and c.v_scale.shape == (2, 2, 48, 4)
