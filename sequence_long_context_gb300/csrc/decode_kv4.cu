@@ -8,8 +8,11 @@
 // 8 x 128K keys, 32 query heads over 8, D = 128: 236 us, 4.8 TB/s, 0.71 of the
 // measured copy rate; bound by instruction issue (64 % of all slots, 660
 // instructions of a warp per 32 keys, 16 warps per SM) more than by HBM. 16
-// windows of 1000 keys and 32 heads: 32 us, of which rounds of keys 15, the start
-// 4, the ends of units the rest. 3 new tokens (12 rows) over 4 x 32K: 61 us.
+// windows of 1000 keys and 32 heads: 30 us, of which rounds of keys 15, the start
+// 4, the ends of units the rest. 3 new tokens (12 rows) over 4 x 32K: 57 us. 16
+// and 32 rows per KV head over 8 x 128K: 357 and 702 us (a block of 16 rows reads
+// the keys anew); one row with its weights accumulated 318 (the scores, 134 MB,
+// are written and read once).
 //
 // Division of the work. A unit is one (sequence, KV head, block of up to 8 NT
 // query rows); a step is 32 of its keys. All steps of all units, in unit
@@ -58,9 +61,10 @@
 // the maximum keeps all 11 bits, and below that its error is at most 2^-32 of it
 // (against the maximum itself, keys below 2^-25 of a sink were 0 in O and still
 // counted in l). O's bias is taken off at the end of every step (32
-// multiply-adds of a thread's 700 instructions at D = 128; 240 us instead of 236
-// at 8 x 128K keys): taken off once at the end, the sums' roundings were 0.33 % of O at 128K keys per head and 3.3 % at 1M, where
-// bf16's own are 0.17 %.
+// multiply-adds of a thread's 700 instructions at D = 128; 8 x 128K keys took 241 us
+// with it and 243 without in one session): taken off once at the end, the sums'
+// roundings were 0.33 % of O at 128K keys per head and 3.3 % at 1M, where bf16's
+// own are 0.17 %.
 #include <cuda_fp16.h>
 
 #include <cfloat>
@@ -82,8 +86,9 @@ __device__ int g_decode_kv4_status = 0;
 constexpr int kStep = 32;                 // keys per step
 constexpr int kGridMax = 304;             // 152 SMs x 2 resident CTAs
 // Up to eight query rows: two CTAs of eight warps per SM at 128 registers;
-// sixteen: one CTA (with ten or twelve warps at 168 registers and Q^T in shared
-// memory it spills: 63 and 69 us instead of 51 for 4 x 32K keys and 12 rows).
+// sixteen: one CTA (at D = 128, with ten or twelve warps at 168 registers and Q^T in
+// shared memory, it spills: 63 and 69 us instead of 51 for 4 x 32K keys and 12 rows;
+// D = 64 has the same form, and was not tried with more warps).
 // Rows 9..16 as two blocks of eight read and decode every key twice: 76 us
 // instead of 61 for 4 x 32K keys, 459 instead of 352 for 8 x 128K (12.3 instead
 // of 14.7 for 2K keys of one sequence, which no rule is made for).

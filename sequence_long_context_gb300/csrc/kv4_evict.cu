@@ -15,9 +15,10 @@
 // Bound by latency: a cluster takes about 20 us to choose (of which the weights'
 // load 3.5, each pass 2, the barriers 1 each) and 9 to move 8192 rows, at HBM's
 // rate, and 36 clusters of eight fit the GPU at once. 64 heads of up to 128K
-// tokens, 8192 kept: 72 us, 2.3 TB/s (45 with 256 kept; 153 with clusters of four,
+// tokens, 8192 kept: 68 us, 2.5 TB/s (45 with 256 kept; 153 with clusters of four,
 // 232 of two: choosing is as long as a CTA's part). 64 heads of 1088, 1024 kept:
-// 19 us, of which launch and barriers are most. Rows only move towards the front,
+// 14 us replayed from a graph, of which launch and barriers are most. In place: 75
+// and 16 us. Rows only move towards the front,
 // so in place the copy goes in rounds: every row of a round is in registers
 // before a barrier, and written after it; later rounds read behind every row that
 // earlier ones write.
