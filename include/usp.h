@@ -622,6 +622,162 @@ usp_status_t usp_kv4_evict(const usp_kv4_cache_t *src, const usp_kv4_cache_t *ds
                            usp_stream_t stream);
 
 /*
+ * usp_rope - rotation of positions, and its gradient.
+ *
+ * The pages rotate nothing; but in rank-major order a token's index is not its
+ * position, so the rotation that a model applies to its queries and keys is the
+ * layout's business ("the functions reorder the input", YunChang README, "2.
+ * Usage"). With the natural position p of a token in its own sequence and R =
+ * rotary_dim, the pairs (a, b) of every head's first R channels, channels i and
+ * i + R/2 (interleaved: 2i and 2i + 1), become
+ *     a' = a c - b s,   b' = b c + a s,   c = table[p][i], s = table[p][R/2 + i]
+ * (inverse: with -s; as the rotation's matrix is orthogonal, that is the gradient
+ * with respect to x of a call without it). Products and sums are rounded to fp32
+ * one by one, the result once more to dtype. Channels from R on are copied.
+ *
+ * x, y  [B, S, H, D] (packed: [S, H, D] with cu_seqlens, B sequences), in the
+ *      rank-major order of (layout, cp_size), bf16 or fp32 (dtype). y may be x;
+ *      otherwise they share nothing. Tokens before cu_seqlens[0] and from
+ *      cu_seqlens[B] on (padding) are copied.
+ * table  [table_rows, R] fp32, 16-byte aligned: cos of R/2 angles, then sin.
+ *      S <= table_rows.
+ * R  a multiple of 16, 16 .. D. D 64 or 128 (USP_ERR_UNSUPPORTED). S divisible
+ *      as for usp_attn_fwd.
+ * Errors: USP_ERR_INVALID_ARG, USP_ERR_UNSUPPORTED, USP_ERR_ALIGNMENT,
+ *      USP_ERR_CUDA.
+ */
+usp_status_t usp_rope(const void *x, void *y, const float *table, int table_rows,
+                      int rotary_dim, int interleaved, int inverse, int B, int S, int H,
+                      int D, const int32_t *cu_seqlens, int cp_size, usp_layout_t layout,
+                      usp_dtype_t dtype, usp_stream_t stream);
+
+/*
+ * The paged 8-bit KV cache.
+ *
+ * A serving cache whose sequences take pages of page_size tokens from one pool,
+ * held as E4M3 codes with one power of two per 32 tokens of a head: 2 D + 2/32
+ * bytes per token and KV head, where bf16 takes 4 D. The pages of the reference
+ * have no counterpart; it stands beside the 4-bit cache, at twice its bytes and an
+ * eighth of its error.
+ *
+ * Values. Rows [32 n, 32 n + 32) of a sequence's KV head are a block, whose
+ * exponent e is the smallest in [-40, 40] with max |x| <= 448 * 2^e (40 if none
+ * is). A code is x * 2^-e rounded to the nearest E4M3 number, ties to even, +-448
+ * at most, a NaN taken as 0. An append that adds to a block which holds rows
+ * takes the larger of its exponent and the new rows'; if that raises it, the codes
+ * held are rounded once more (which changes those that become subnormal alone).
+ * An exponent outside [-40, 40] (never stored) reads as the nearest; a code 0x7F
+ * or 0xFF (never stored) as NaN.
+ *
+ *     k_codes, v_codes  [num_pages][Hkv][page_size][D]      bytes
+ *     k_exps, v_exps    [num_pages][Hkv][page_size / 32]    int8
+ *     page_table        [B][max_pages] int32: the page of rows [page_size n, ..) of
+ *                       each sequence. An entry outside [0, num_pages) names no
+ *                       page: rows there are not stored, and not visible as keys.
+ *     seq_lens          [B] int32, the cached tokens of every sequence; values
+ *                       below 0 count as 0, above max_pages * page_size as that.
+ * Table and lengths are on the device and read by no call on the host, so calls
+ * can be captured into graphs and replayed as the sequences grow. Sequences may
+ * share pages that no call writes; a page that a call writes rows of must stand
+ * in its table once (else its contents are unspecified).
+ * The struct is host memory, read during the call. Requirements, checked by every
+ * call: 0 <= B <= 65535, 1 <= Hkv <= 65535, D 64 or 128, page_size 32, 64 or 128,
+ * max_pages * page_size <= 2^30, num_pages * Hkv < 2^31 (USP_ERR_UNSUPPORTED), the
+ * code and exponent arrays 16-byte aligned, table and lengths 4-byte aligned.
+ * Rows behind a sequence's length are never read as keys, and are left as they
+ * were. usp_kv8_append must not overlap on the GPU with another call on the same
+ * cache.
+ */
+typedef struct {
+  void *k_codes;
+  int8_t *k_exps;
+  void *v_codes;
+  int8_t *v_exps;
+  const int32_t *page_table;
+  int32_t *seq_lens;
+  int B, max_pages, num_pages, page_size, Hkv, D;
+} usp_kv8_cache_t;
+
+/*
+ * usp_kv8_append - store new tokens' keys and values, rotated on the way.
+ *
+ * k, v  [B, T, Hkv, D] in natural order, bf16 or fp32 (dtype); with
+ *      cu_seqlens [B + 1] (int32, device, non-decreasing, trusted as in
+ *      usp_attn_fwd) a packed batch [T, Hkv, D] of T tokens in all. 0 <= T <= 2^30.
+ *      Tokens before cu_seqlens[0] and from cu_seqlens[B] on (padding) are not
+ *      stored.
+ * Token t of sequence b goes to row seq_lens[b] + t of the sequence; tokens that
+ *      find no room, or no page, are dropped.
+ * q, q_out  both NULL, or the same tokens' queries, [B, T, Hq, D] (packed
+ *      [T, Hq, D]), and where they are written rotated (padding: zeros). q_out may be
+ *      q; otherwise they share nothing, nor does q_out with k and v.
+ * table, table_rows, rotary_dim, interleaved  as in usp_rope, for k and q; table
+ *      NULL: no rotation. The position of a token is positions[b][t] (packed
+ *      positions[t]; int32, device), or with positions NULL its row in the cache,
+ *      and max_pages * page_size <= table_rows. Positions outside the table are
+ *      rotated as its nearest row. A rotated key is stored from fp32, with no
+ *      rounding in between.
+ * seq_lens_out  [B] int32 or NULL: min(max_pages * page_size, seq_lens[b] + the
+ *      sequence's new tokens) is written. May be the cache's seq_lens itself.
+ * Errors: USP_ERR_INVALID_ARG, USP_ERR_UNSUPPORTED, USP_ERR_ALIGNMENT,
+ *      USP_ERR_CUDA.
+ */
+usp_status_t usp_kv8_append(const usp_kv8_cache_t *cache, const void *k, const void *v,
+                            const void *q, void *q_out, int Hq, const float *table,
+                            int table_rows, int rotary_dim, int interleaved,
+                            const int32_t *positions, const int32_t *cu_seqlens, int T,
+                            usp_dtype_t dtype, int32_t *seq_lens_out, usp_stream_t stream);
+
+/*
+ * usp_kv8_read - the values the cache stands for.
+ *
+ * Writes rows start[b] .. start[b] + T - 1 (start NULL: 0 ..) of every
+ * sequence as k, v [B, T, Hkv, D] in dtype (exact in both). Rows before 0, behind
+ * the sequence's length or without a page are written as zeros. start: int32 [B],
+ * device, 4-byte aligned.
+ * Errors: USP_ERR_INVALID_ARG, USP_ERR_UNSUPPORTED, USP_ERR_ALIGNMENT,
+ *      USP_ERR_CUDA.
+ */
+usp_status_t usp_kv8_read(const usp_kv8_cache_t *cache, const int32_t *start, int T,
+                          void *k, void *v, usp_dtype_t dtype, usp_stream_t stream);
+
+/*
+ * usp_attn_kv8 - attention of the newest tokens to the paged 8-bit cache.
+ *
+ * A decoding step, or a whole chunk of a prompt: the newest n tokens of every
+ * sequence, the last n of its L = seq_lens[b] cached ones, attend to the cached
+ * keys. Token t sits at i = L - n + t and sees key j < L iff the library's mask
+ * says so (causal, window, sink_tokens, with the positions counted in the cache).
+ * A token with i < 0, or that sees no key, gets O = 0 and LSE = -inf.
+ *
+ * q    [B, T, Hq, D] bf16, n = T; with cu_seqlens [B + 1] (int32, device, trusted)
+ *      packed [T, Hq, D], n = cu_seqlens[b + 1] - cu_seqlens[b]; padding outside
+ *      the sequences gets O = 0 and LSE = -inf. T >= 1.
+ * max_new  packed: at least the largest n (rows of tokens t >= max_new are not
+ *      written), which chooses the kernel; outside [1, T]: T. Else ignored.
+ * out  as q, written; lse [B, T, Hq] fp32 (packed [T, Hq]), written (natural log of
+ *      the scaled scores' sum). usp_merge_partials merges results of several
+ *      caches by it.
+ * The result does not vary from run to run.
+ * Hq % Hkv == 0; any number of query rows per KV head. dtype USP_BF16.
+ * workspace: at least usp_attn_kv8_workspace_size(...) bytes, 256-byte aligned,
+ *      contents on entry irrelevant; calls that overlap on the GPU need one each.
+ * Errors: USP_ERR_INVALID_ARG, USP_ERR_UNSUPPORTED (D, page_size; dtype USP_FP32;
+ *      more than 2^26 rows per KV head, or 2^26 blocks of 8 of them in all),
+ *      USP_ERR_ALIGNMENT, USP_ERR_WORKSPACE, USP_ERR_CUDA.
+ */
+usp_status_t usp_attn_kv8(const usp_kv8_cache_t *cache, const void *q, void *out, float *lse,
+                          const int32_t *cu_seqlens, int T, int max_new, int Hq,
+                          float softmax_scale, int causal, int window, int sink_tokens,
+                          usp_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                          usp_stream_t stream);
+
+/* Bytes of scratch usp_attn_kv8 needs (T, max_new as there; packed: whether it
+ * gets cu_seqlens); 0 for invalid sizes. */
+size_t usp_attn_kv8_workspace_size(int B, int T, int max_new, int packed, int Hq, int Hkv,
+                                   int D);
+
+/*
  * usp_permute - sequence layouts and the Ulysses all-to-all, bit-exact.
  *
  * EXTRACT / RESTORE (the YunChang README's EXTRACT_FUNC_DICT /

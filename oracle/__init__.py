@@ -18,10 +18,12 @@ Modules
              attention of e4m3 q, k, v with per-tensor descales
   kv4        the 4-bit KV cache: its codes, a decode step over it, the
              attention weight of each key, eviction by that weight
+  kv8        rotation of positions; the paged 8-bit KV cache: its codes, an
+             append, reading back, attention of the newest tokens
 
 Every function is pinned by `-m "not gpu"` tests against something other than
 itself (brute force, a library routine, finite differences, closed forms and
 the worked examples printed on the pages). No function here is "parity
 unpinned".
 """
-from . import attention, decode, fp8, kv4, layouts, merge, ring  # noqa: F401
+from . import attention, decode, fp8, kv4, kv8, layouts, merge, ring  # noqa: F401

@@ -6,8 +6,9 @@ Every step of the computation runs in the CUDA library libusp.so; there is
 no Python or CPU fallback, and a missing library raises.
 
 The helpers below them (attn_forward, attn_backward, permute,
-merge_partials, the kv4_* calls of the 4-bit KV cache) allocate outputs and
-workspaces with PyTorch and call the same entry points.
+merge_partials, rope, the kv4_* calls of the 4-bit KV cache, the kv8_* calls of
+the paged 8-bit one) allocate outputs and workspaces with PyTorch and call the
+same entry points.
 """
 from __future__ import annotations
 
@@ -202,6 +203,40 @@ def usp_attn_key_weights_workspace_size(B, S, Hq, Hkv, observe, dtype, flags=0) 
 def usp_kv4_evict(src, dst, kept, keep, recent, sink_tokens, stream=None) -> None:
     _check(_lib.load().usp_kv4_evict(ctypes.addressof(src), ctypes.addressof(dst), _p(kept),
                                      int(keep), int(recent), int(sink_tokens), _stream(stream)))
+
+
+def usp_rope(x, y, table, table_rows, rotary_dim, interleaved, inverse, B, S, H, D, cu_seqlens,
+             cp_size, layout, dtype, stream=None) -> None:
+    _check(_lib.load().usp_rope(
+        _p(x), _p(y), _p(table), int(table_rows), int(rotary_dim), int(interleaved),
+        int(inverse), B, S, H, D, _p(cu_seqlens), cp_size, _enum(LAYOUT, layout),
+        _enum(DTYPE, dtype), _stream(stream)))
+
+
+def usp_kv8_append(cache, k, v, q, q_out, Hq, table, table_rows, rotary_dim, interleaved,
+                   positions, cu_seqlens, T, dtype, seq_lens_out, stream=None) -> None:
+    """cache: a _lib.Kv8CacheStruct (as in the other usp_kv8 calls)."""
+    _check(_lib.load().usp_kv8_append(
+        ctypes.addressof(cache), _p(k), _p(v), _p(q), _p(q_out), int(Hq), _p(table),
+        int(table_rows), int(rotary_dim), int(interleaved), _p(positions), _p(cu_seqlens),
+        int(T), _enum(DTYPE, dtype), _p(seq_lens_out), _stream(stream)))
+
+
+def usp_kv8_read(cache, start, T, k, v, dtype, stream=None) -> None:
+    _check(_lib.load().usp_kv8_read(ctypes.addressof(cache), _p(start), int(T), _p(k), _p(v),
+                                    _enum(DTYPE, dtype), _stream(stream)))
+
+
+def usp_attn_kv8(cache, q, out, lse, cu_seqlens, T, max_new, Hq, softmax_scale, causal, window,
+                 sink_tokens, dtype, workspace=None, workspace_bytes=0, stream=None) -> None:
+    _check(_lib.load().usp_attn_kv8(
+        ctypes.addressof(cache), _p(q), _p(out), _p(lse), _p(cu_seqlens), int(T), int(max_new),
+        Hq, float(softmax_scale), int(causal), int(window), int(sink_tokens),
+        _enum(DTYPE, dtype), _p(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def usp_attn_kv8_workspace_size(B, T, max_new, packed, Hq, Hkv, D) -> int:
+    return int(_lib.load().usp_attn_kv8_workspace_size(B, T, max_new, int(packed), Hq, Hkv, D))
 
 
 def usp_permute(src, dst, kind, layout, B, S, H, D, cp_size, ulysses_degree,
@@ -733,3 +768,236 @@ def kv4_evict(cache: KV4Cache, keep: int, *, recent=0, sink_tokens=0, out=None, 
     _call(_lib.load().usp_kv4_evict, at, None, s, d,
           kept.data_ptr(), keep, recent, sink_tokens)
     return dst, kept
+
+
+# --- rotation of positions ------------------------------------------------------
+
+def rope_table(positions: int, rotary_dim: int, *, base: float = 10000.0, scale: float = 1.0,
+               device="cuda") -> torch.Tensor:
+    """[positions, rotary_dim] fp32: cos, then sin, of position * scale *
+    base^(-2 i / rotary_dim), angles in 64 bits. A model with other frequencies, or a
+    factor on the rotated channels, makes its own."""
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+    a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * (
+        scale * base ** (-i / rotary_dim))
+    return torch.cat([a.cos(), a.sin()], -1).float()
+
+
+def _rope_args(table, like) -> Tuple[int, int, int]:
+    """(pointer, rows, rotary_dim) of a table."""
+    if table is None:
+        return 0, 0, 0
+    if table.dim() != 2:
+        raise ValueError("the table of a rotation must be [positions, rotary_dim]")
+    _require(table, "rope", _F32, table.shape, like.get_device(), like)
+    return table.data_ptr(), table.shape[0], table.shape[1]
+
+
+def rope(x: torch.Tensor, table: torch.Tensor, *, interleaved=False, inverse=False,
+         cu_seqlens=None, cp=1, layout="contiguous", out=None, stream=None) -> torch.Tensor:
+    """x (rank-major [B,S,H,D], or packed [T,H,D]; bf16 or fp32) rotated by its tokens'
+    positions; table: rope_table(...). The gradient of a rotation is the rotation of
+    the gradient with inverse=True. out may be x (in place)."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return rope(x, table, interleaved=interleaved, inverse=inverse,
+                        cu_seqlens=cu_seqlens, cp=cp, layout=layout, out=out)
+    dt, at = x.dtype, x.get_device()
+    if dt not in DTYPE:
+        raise ValueError("x must be bf16 or fp32")
+    packed = cu_seqlens is not None
+    if x.dim() != (3 if packed else 4):
+        raise ValueError("x must be [B, S, H, D], packed [T, H, D]")
+    _require(x, "x", dt, x.shape, at, x)
+    S, H, D = x.shape[-3:]
+    B = x.shape[0]
+    if packed:
+        B = cu_seqlens.numel() - 1
+        _require(cu_seqlens, "cu_seqlens", _I32, (B + 1,), at, x)
+    if table is None:
+        raise ValueError("a rotation needs a table")
+    ptr, rows, R = _rope_args(table, x)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _require(out, "out", dt, x.shape, at, x)
+    _call(_lib.load().usp_rope, at, None, _p(x), _p(out), ptr, rows, R, 1 if interleaved else 0,
+          1 if inverse else 0, B, S, H, D, cu_seqlens.data_ptr() if packed else None, cp,
+          _enum(LAYOUT, layout), DTYPE[dt])
+    return out
+
+
+# --- the paged 8-bit KV cache -----------------------------------------------------
+
+_I8 = torch.int8
+
+
+class KV8Cache(NamedTuple):
+    """A paged KV cache in 8 bits (usp_kv8_cache_t in include/usp.h, which gives the
+    number format): E4M3 codes uint8 [pages, Hkv, page size, D], exponents int8
+    [pages, Hkv, page size / 32], the sequences' pages int32 [B, max pages] (-1:
+    none), cached tokens int32 [B]. All on one device and contiguous; page size 32,
+    64 or 128."""
+    k: torch.Tensor
+    k_exp: torch.Tensor
+    v: torch.Tensor
+    v_exp: torch.Tensor
+    page_table: torch.Tensor
+    seq_lens: torch.Tensor
+
+
+def kv8_cache(B: int, capacity: int, Hkv: int, D: int, *, page_size: int = 64, num_pages=None,
+              device="cuda") -> KV8Cache:
+    """An empty cache for B sequences of up to `capacity` tokens (rounded up to whole
+    pages). num_pages None: every sequence has all its pages; else a pool of so many,
+    and a page_table of -1 that the caller fills as sequences grow."""
+    mp = -(-int(capacity) // page_size)
+    n = B * mp if num_pages is None else int(num_pages)
+    if num_pages is None:
+        table = torch.arange(n, dtype=torch.int32, device=device).view(B, mp)
+    else:
+        table = torch.full((B, mp), -1, dtype=torch.int32, device=device)
+    codes = dict(size=(n, Hkv, page_size, D), dtype=torch.uint8, device=device)
+    exps = dict(size=(n, Hkv, page_size // 32), dtype=torch.int8, device=device)
+    return KV8Cache(torch.zeros(**codes), torch.zeros(**exps), torch.zeros(**codes),
+                    torch.zeros(**exps), table, torch.zeros((B,), dtype=torch.int32, device=device))
+
+
+_pack_kv8 = struct.Struct("6Q6i").pack  # a _lib.Kv8CacheStruct's bytes
+
+
+def _kv8_struct(cache: KV8Cache):
+    """(C struct's bytes, device index, B, Hkv, capacity, D) of a cache whose
+    tensors fit together, else ValueError."""
+    k, ke, v, ve, table, lens = cache
+    shape, ts = k.shape, table.shape
+    if len(shape) != 4 or len(ts) != 2:
+        raise ValueError("cache.k must be [pages, Hkv, page size, D], page_table [B, max pages]")
+    n, H, ps, D = shape
+    B, mp = ts
+    at = k.get_device()
+    es = (n, H, ps // 32)
+    if not (_fits(k, _U8, shape, at) and _fits(ke, _I8, es, at) and _fits(v, _U8, shape, at)
+            and _fits(ve, _I8, es, at) and _fits(table, _I32, ts, at)
+            and _fits(lens, _I32, (B,), at)):
+        _need(k, "cache.k", _U8, shape, k.device)
+        _need(v, "cache.v", _U8, shape, k.device)
+        _need(ke, "cache.k_exp", _I8, es, k.device)
+        _need(ve, "cache.v_exp", _I8, es, k.device)
+        _need(table, "cache.page_table", _I32, ts, k.device)
+        _need(lens, "cache.seq_lens", _I32, (B,), k.device)
+    try:
+        s = _pack_kv8(k.data_ptr(), ke.data_ptr(), v.data_ptr(), ve.data_ptr(), table.data_ptr(),
+                      lens.data_ptr(), B, mp, n, ps, H, D)
+    except struct.error as e:
+        raise ValueError("the sizes must fit 32 bits") from e
+    return s, at, B, H, mp * ps, D
+
+
+def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, *, q=None, q_out=None, rope=None,
+               interleaved=False, positions=None, cu_seqlens=None, seq_lens_out=None, stream=None):
+    """Store new tokens' keys and values (bf16 or fp32, natural order) behind each
+    sequence's cached ones: k, v [B,T,Hkv,D], or packed [T,Hkv,D] with cu_seqlens.
+    rope: a table (rope_table) by which k, and q if given, are rotated on the way;
+    positions: int32 [B,T] (packed [T]), default the rows in the cache. Returns the
+    new lengths, written to seq_lens_out (default: the cache's own seq_lens, in
+    place); with q (lengths, q rotated), the latter written to q_out (default: a new
+    tensor; may be q). Tokens that find no room, or no page, are dropped."""
+    if stream is not None:
+        with _on(stream, cache.k.device):
+            return kv8_append(cache, k, v, q=q, q_out=q_out, rope=rope, interleaved=interleaved,
+                              positions=positions, cu_seqlens=cu_seqlens,
+                              seq_lens_out=seq_lens_out)
+    s, at, B, H, cap, D = _kv8_struct(cache)
+    packed = cu_seqlens is not None
+    dt = k.dtype
+    if dt not in DTYPE:
+        raise ValueError("keys and values must be bf16 or fp32")
+    if k.dim() != (3 if packed else 4):
+        raise ValueError("k must be [B, T, Hkv, D], packed [T, Hkv, D]")
+    lead = tuple(k.shape[:-2])
+    if not packed and lead[0] != B:
+        raise ValueError(f"k must have the cache's {B} sequences, got {lead[0]}")
+    T = lead[-1]
+    _require(k, "k", dt, lead + (H, D), at, cache.k)
+    _require(v, "v", dt, lead + (H, D), at, cache.k)
+    if packed:
+        _require(cu_seqlens, "cu_seqlens", _I32, (B + 1,), at, cache.k)
+    Hq = 0
+    if q is not None:
+        Hq = q.shape[-2]
+        _require(q, "q", dt, lead + (Hq, D), at, cache.k)
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        else:
+            _require(q_out, "q_out", dt, lead + (Hq, D), at, cache.k)
+    elif q_out is not None:
+        raise ValueError("q_out needs a q")
+    ptr, rows, R = _rope_args(rope, cache.k)
+    if rope is not None and positions is None and rows < cap:
+        raise ValueError(f"the table has {rows} positions, the cache {cap} rows")
+    if positions is not None:
+        _require(positions, "positions", _I32, lead, at, cache.k)
+    lens = cache.seq_lens
+    if seq_lens_out is not None:
+        lens = seq_lens_out
+        _require(lens, "seq_lens_out", _I32, (B,), at, cache.k)
+    _call(_lib.load().usp_kv8_append, at, None, s, _p(k), _p(v), _p(q), _p(q_out), Hq, ptr or None,
+          rows, R, 1 if interleaved else 0, _p(positions),
+          cu_seqlens.data_ptr() if packed else None, T, DTYPE[dt], lens.data_ptr())
+    return lens if q is None else (lens, q_out)
+
+
+def kv8_read(cache: KV8Cache, tokens: int, *, starts=None, dtype=torch.bfloat16, stream=None
+             ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(k, v) [B, tokens, Hkv, D]: the values of rows starts[b] (default 0) ..
+    of every sequence; zeros behind its length."""
+    if stream is not None:
+        with _on(stream, cache.k.device):
+            return kv8_read(cache, tokens, starts=starts, dtype=dtype)
+    s, at, B, H, _, D = _kv8_struct(cache)
+    if dtype not in DTYPE:
+        raise ValueError("keys and values are read as bf16 or fp32")
+    if starts is not None:
+        _require(starts, "starts", _I32, (B,), at, cache.k)
+    k = torch.empty((B, tokens, H, D), dtype=dtype, device=cache.k.device)
+    v = torch.empty_like(k)
+    _call(_lib.load().usp_kv8_read, at, None, s, None if starts is None else starts.data_ptr(),
+          tokens, k.data_ptr(), v.data_ptr(), DTYPE[dtype])
+    return k, v
+
+
+def attn_kv8(q: torch.Tensor, cache: KV8Cache, *, causal=True, window=0, sink_tokens=0,
+             cu_seqlens=None, max_new=0, softmax_scale=0.0, workspace=None, stream=None
+             ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(out, lse [B,T,Hq]) of the newest tokens q [B,T,Hq,D] (already in the cache, in
+    the end of each sequence) against the cached keys: a decoding step or a chunk of a
+    prompt. Packed: q [T,Hq,D] and lse [T,Hq] with cu_seqlens; max_new, if known, is
+    the most tokens that a sequence brings."""
+    if stream is not None:
+        with _on(stream, q.device):
+            return attn_kv8(q, cache, causal=causal, window=window, sink_tokens=sink_tokens,
+                            cu_seqlens=cu_seqlens, max_new=max_new, softmax_scale=softmax_scale,
+                            workspace=workspace)
+    s, at, B, Hkv, _, D = _kv8_struct(cache)
+    packed = cu_seqlens is not None
+    if q.dim() != (3 if packed else 4):
+        raise ValueError("q must be [B, T, Hq, D], packed [T, Hq, D]")
+    lead, Hq = tuple(q.shape[:-2]), q.shape[-2]
+    if not packed and lead[0] != B:
+        raise ValueError(f"q must have the cache's {B} sequences, got {lead[0]}")
+    T = lead[-1]
+    _require(q, "q", torch.bfloat16, lead + (Hq, D), at, cache.k)
+    if packed:
+        _require(cu_seqlens, "cu_seqlens", _I32, (B + 1,), at, cache.k)
+    lib = _lib.load()
+    dev = q.device
+    out = torch.empty_like(q)
+    lse = torch.empty(lead + (Hq,), dtype=_F32, device=dev)
+    need = lib.usp_attn_kv8_workspace_size(B, T, max_new, 1 if packed else 0, Hq, Hkv, D)
+    ws = torch.empty(need, dtype=_U8, device=dev) if workspace is None else \
+        _use_workspace(workspace, need, dev)[0]
+    _call(lib.usp_attn_kv8, at, None, s, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
+          cu_seqlens.data_ptr() if packed else None, T, max_new, Hq, softmax_scale,
+          1 if causal else 0, window, sink_tokens, 0, ws.data_ptr(), ws.numel())
+    return out, lse

@@ -44,6 +44,13 @@ SIGNATURES = {
                                   _i, _i, _i, _i, _u, _vp, _sz, _vp]),
     "usp_attn_key_weights_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _u]),
     "usp_kv4_evict": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp]),
+    "usp_rope": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _i, _i, _i, _vp]),
+    "usp_kv8_append": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _vp,
+                            _vp]),
+    "usp_kv8_read": (_i, [_vp, _vp, _i, _vp, _vp, _i, _vp]),
+    "usp_attn_kv8": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _i, _i, _i, _vp, _sz,
+                          _vp]),
+    "usp_attn_kv8_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "usp_permute": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
     "usp_status_string": (_c.c_char_p, [_i]),
     "usp_launch_count": (_u64, []),
@@ -65,6 +72,13 @@ class Kv4CacheStruct(ctypes.Structure):
     _fields_ = [("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp),
                 ("key_weight", _vp), ("seq_lens", _vp), ("B", _i), ("capacity", _i),
                 ("Hkv", _i), ("D", _i), ("k_descale", _f), ("v_descale", _f)]
+
+
+class Kv8CacheStruct(ctypes.Structure):
+    """usp_kv8_cache_t."""
+    _fields_ = [("k_codes", _vp), ("k_exps", _vp), ("v_codes", _vp), ("v_exps", _vp),
+                ("page_table", _vp), ("seq_lens", _vp), ("B", _i), ("max_pages", _i),
+                ("num_pages", _i), ("page_size", _i), ("Hkv", _i), ("D", _i)]
 
 
 _lib = None
