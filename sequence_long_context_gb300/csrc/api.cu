@@ -336,10 +336,11 @@ const char* usp_last_error_detail(void) { return g_detail; }
 
 usp_status_t usp_device_status(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return USP_ERR_CUDA;
-  const int words[8] = {read_clear_fwd_tc_status(), read_clear_bwd_tc_status(),
+  const int words[9] = {read_clear_fwd_tc_status(), read_clear_bwd_tc_status(),
                         read_clear_decode_status(), read_clear_selftest_status(),
                         read_clear_fwd_fp8_status(), read_clear_decode_kv4_status(),
-                        read_clear_key_weights_status(), read_clear_attn_kv8_status()};
+                        read_clear_key_weights_status(), read_clear_attn_kv8_status(),
+                        read_clear_attn_kv8_tc_status()};
   for (int w : words)
     if (w < 0) return USP_ERR_CUDA;
   for (int w : words)

@@ -39,15 +39,14 @@
 // (its rounding, 2^-12, is the only one of the products), and below that its error is at
 // most 2^-32 of it, so many small keys beside a sink still count.
 #include <cuda_fp16.h>
-#include <cudaTypedefs.h>
 
 #include <cfloat>
 #include <cmath>
-#include <cstdio>
 
 #include "internal.h"
 #include "kv4_host.h"
 #include "kv8.cuh"
+#include "kv8_attn.cuh"
 #include "kv8_host.h"
 #include "tc_ptx.cuh"
 
@@ -186,14 +185,6 @@ struct Smem {
   static_assert(kAlloc <= 227 * 1024, "one CTA per SM");
 };
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                            int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -207,14 +198,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   return d;
 }
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-
-// Byte offset of 16-byte chunk `chunk` of row `row` of a tile, as TMA's swizzle
-// (128 bytes for D = 128, 64 for D = 64) lays it out.
-template <int D>
-__device__ __forceinline__ int tile_at(int row, int chunk) {
-  return D == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4)
-                  : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
-}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -685,41 +668,8 @@ Ws layout(int B, int max_new, int Hq, int Hkv, int D) {
   return w;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
-
-// Codes [np][H][ps][D] as a 3-D map (D, ps, np H), a box one block of 32 tokens.
-bool make_map(CUtensorMap* m, const uint8_t* base, const Cache& c, int D) {
-  auto fn = encode_fn();
-  if (!fn) {
-    fail_cuda_msg("cuTensorMapEncodeTiled", "driver entry point not found");
-    return false;
-  }
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)c.ps, (cuuint64_t)c.np * c.H};
-  cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * c.ps};
-  cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)kBlock, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides,
-                  box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    char msg[64];
-    std::snprintf(msg, sizeof(msg), "CUresult %d", (int)r);
-    fail_cuda_msg("cuTensorMapEncodeTiled", msg);
-    return false;
-  }
-  return true;
-}
+// Rows per KV head from which the tcgen05 kernel takes over.
+bool many_rows(int Hq, int Hkv, int max_new) { return (long long)(Hq / Hkv) * max_new > 16; }
 
 template <int D, int NT>
 usp_status_t launch_t(const Params& P, cudaStream_t st) {
@@ -764,10 +714,12 @@ usp_status_t launch_t(const Params& P, cudaStream_t st) {
 }  // namespace
 
 size_t attn_kv8_workspace(int B, int T, int max_new, int packed, int Hq, int Hkv, int D) {
+  if (many_rows(Hq, Hkv, max_new)) return attn_kv8_tc_workspace(D);
   return layout(B, max_new, Hq, Hkv, D).total;
 }
 
 usp_status_t launch_attn_kv8(const AttnKv8Args& a, void* workspace, cudaStream_t st) {
+  if (many_rows(a.Hq, a.c.H, a.max_new)) return launch_attn_kv8_tc(a, workspace, st);
   const Ws w = layout(a.c.B, a.max_new, a.Hq, a.c.H, a.D);
   char* base = static_cast<char*>(workspace);
   Params P{};

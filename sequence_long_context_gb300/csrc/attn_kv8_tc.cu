@@ -1,0 +1,945 @@
+// Attention of the newest tokens to the paged 8-bit KV cache on the 5th-generation
+// tensor cores (tcgen05): chunks of a prompt, many query rows per KV head.
+//
+// A unit is 256 query rows of one (sequence, KV head), in two halves of 128; a step
+// is 128 of its keys. The rows of a KV head are its tokens' query heads, token by
+// token, so a half covers 128 / G neighbouring tokens and every K and V row that is
+// read serves all of them. All steps of all units are one line that the CTAs share
+// in equal runs (as in attn_kv8.cu), so ragged batches and causal triangles are
+// balanced; a unit that lies in one run is written at once, the others' partials
+// (m, l, O) go through the workspace to a second kernel.
+//
+// One persistent CTA per SM, 16 warps:
+//   warps 0-3, 4-7  softmax of half A and B, one query row per thread: scores from
+//                   tensor memory, p = 2^(score + e_v - m) back over them as fp16
+//   warps 8-11      converters: E4M3 codes to fp16 tiles in shared memory, once for
+//                   both halves (exact; the products need both operands of one type)
+//   warp 12         producer: pages and exponents of the tiles, TMA of the codes
+//   warp 13         MMA issuer (one thread), owner of the tensor memory
+// Tensor memory: S_A [0, 128), S_B [128, 256), O_A at 256, O_B at 256 + D. The
+// products of one half run while the softmax of the other works:
+//   P V (A, n), Q K (A, n + 1), P V (B, n), Q K (B, n + 1), ..
+// The numbers are attn_kv8.cu's: q scaled to fp16 by a power of two per row, K's
+// exponent a factor of the block's scores, V's added to them, p against a reference
+// 2^7 to 2^15 below the running maximum of score + e_v, the row's sum over p 2^-e_v.
+#include <cuda_fp16.h>
+
+#include <cfloat>
+
+#include "internal.h"
+#include "kv4_host.h"
+#include "kv8.cuh"
+#include "kv8_attn.cuh"
+#include "kv8_host.h"
+#include "tc_ptx.cuh"
+
+namespace usp {
+namespace {
+
+using namespace kv8;
+using namespace tc;
+
+__device__ int g_attn_kv8_tc_status = 0;
+
+constexpr int kBM = 128;                 // rows of a half
+constexpr int kUnitRows = 2 * kBM;
+constexpr int kBN = 128;                 // keys of a step
+constexpr int kBlocks = kBN / kBlock;    // exponents of a step
+constexpr int kGrid = 152;
+constexpr int kThreads = 512;
+constexpr int kConvWarp = 8, kConvWarps = 4, kProducerWarp = 12, kMmaWarp = 13;
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // 2 x 128 x (184 + 72) = 512 x 128
+// What a unit costs besides its steps, in steps (its queries, its end), and the
+// fewest steps that are worth a run of their own.
+constexpr int kUnitCost = 2;
+constexpr int kRunMin = 3;
+constexpr int kInfo = 8;                 // steps whose description is kept
+constexpr float kBelow = 7.f, kAbove = 15.f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// A step as the producer describes it.
+constexpr int kHasB = 1, kFirst = 2, kLast = 4, kEnd = 8;
+struct Info {
+  int key0;
+  int flags;        // k*; bits 8..: blocks that hold no key; bits 16..: keys below len
+  uint32_t ke, ve;  // exponents of the blocks, int8
+};
+
+struct TcParams {
+  Cache c;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* lse;
+  float* o_part;    // [2 kGrid][256][D]
+  float2* ml_part;  // [2 kGrid][256]
+  int4* rec;        // [2 kGrid]: 1 a partial, 3 its unit's last; b, rt, h
+  const int* cu;
+  int T, max_new, Hq, G;
+  float score_mul;
+  int causal, window, sink;
+};
+
+struct Seq {
+  int len, n, first, R, nt;
+};
+__device__ __forceinline__ Seq seq_of(const TcParams& P, int b) {
+  Seq q;
+  q.len = clamp_len(__ldg(P.c.lens + b), P.c.cap);
+  if (P.cu) {
+    q.first = min(max(__ldg(P.cu + b), 0), P.T);
+    q.n = min(max(__ldg(P.cu + b + 1), q.first), P.T) - q.first;
+  } else {
+    q.first = b * P.T;
+    q.n = P.T;
+  }
+  q.R = min(q.n, P.max_new) * P.G;
+  q.nt = (q.R + kUnitRows - 1) / kUnitRows;
+  return q;
+}
+// Steps of a unit: key tile s (s < sinks) or s + skip.
+struct Steps {
+  int n, sinks, skip;
+};
+__device__ __forceinline__ Steps steps_of(const TcParams& P, const Seq& q, int rt) {
+  Steps r{0, 0, 0};
+  const int t0 = rt * kUnitRows / P.G, t1 = (min(q.R, (rt + 1) * kUnitRows) - 1) / P.G;
+  const int i0 = max(0, q.len - q.n + t0), i1 = q.len - q.n + t1;
+  if (q.len <= 0 || i1 < 0) return r;
+  const int last = (P.causal ? min(i1, q.len - 1) : q.len - 1) / kBN;
+  int first = 0;
+  if (P.window > 0) {
+    first = max(0, i0 - P.window + 1) / kBN;
+    r.sinks = min((min(P.sink, q.len) + kBN - 1) / kBN, first);
+    r.skip = first - r.sinks;
+  }
+  r.n = last + 1 - r.skip;
+  return r;
+}
+__device__ __forceinline__ int line_len(int n) { return n + kUnitCost; }
+
+// A walk over the steps of a CTA's run: the current unit's steps [s, end).
+struct Walk {
+  int b, rt, h;
+  Seq q;
+  Steps st;
+  int s, end;
+  long long left;
+};
+__device__ __forceinline__ bool next_unit(const TcParams& P, Walk& w) {
+  if (w.left <= 0) return false;
+  if (++w.h == P.c.H) {
+    w.h = 0;
+    if (++w.rt >= w.q.nt) {
+      w.rt = 0;
+      do {
+        if (++w.b >= P.c.B) return false;
+        w.q = seq_of(P, w.b);
+      } while (w.q.nt == 0);
+    }
+    w.st = steps_of(P, w.q, w.rt);
+  }
+  w.s = 0;
+  w.end = (int)min((long long)w.st.n, w.left);
+  w.left -= line_len(w.st.n);
+  return true;
+}
+
+// Length on the line of a sequence's units of one head, by a warp.
+__device__ __forceinline__ long long seq_line(const TcParams& P, const Seq& q) {
+  long long x = 0;
+  for (int rt = threadIdx.x & 31; rt < q.nt; rt += 32) x += line_len(steps_of(P, q, rt).n);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ long long scan32(long long x) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if ((threadIdx.x & 31) >= o) x += y;
+  }
+  return x;
+}
+// The sequences [b0, b0 + 32) on the line, one per lane: where each ends.
+__device__ __forceinline__ long long line_ends(const TcParams& P, int b0) {
+  const int lane = threadIdx.x & 31, b = b0 + lane;
+  Seq q{};
+  if (b < P.c.B) q = seq_of(P, b);
+  long long x = 0;
+  if (!__any_sync(0xffffffffu, q.nt > 4)) {
+    for (int rt = 0; rt < q.nt; ++rt) x += line_len(steps_of(P, q, rt).n);
+  } else {
+    for (int i = 0; i < 32 && b0 + i < P.c.B; ++i) {
+      const long long y = seq_line(P, seq_of(P, b0 + i));
+      if (lane == i) x = y;
+    }
+  }
+  return scan32(x * P.c.H);
+}
+
+// This CTA's run, found by one warp. left == 0: none.
+__device__ __forceinline__ Walk find_run(const TcParams& P) {
+  Walk w{};
+  const int lane = threadIdx.x & 31;
+  long long ends = line_ends(P, 0);
+  long long T = __shfl_sync(0xffffffffu, ends, 31);
+  for (int b = 32; b < P.c.B; b += 32) T += __shfl_sync(0xffffffffu, line_ends(P, b), 31);
+  const long long N = min((T + kRunMin - 1) / kRunMin, (long long)gridDim.x);
+  if (blockIdx.x >= N) return w;
+  const long long first = T * blockIdx.x / N, count = T * (blockIdx.x + 1) / N - first;
+  int b0 = 0;
+  long long before = 0;
+  for (;;) {
+    const unsigned over = __ballot_sync(0xffffffffu, before + ends > first);
+    if (over) {
+      const int src = __ffs(over) - 1;
+      if (src > 0) before += __shfl_sync(0xffffffffu, ends, src - 1);
+      b0 += src;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, ends, 31);
+    b0 += 32;
+    if (b0 >= P.c.B) return w;  // not reached: first < T
+    ends = line_ends(P, b0);
+  }
+  w.b = b0;
+  w.q = seq_of(P, b0);
+  for (int rt0 = 0;; rt0 += 32) {
+    const int rt = rt0 + lane;
+    const long long x =
+        scan32(rt < w.q.nt ? (long long)line_len(steps_of(P, w.q, rt).n) * P.c.H : 0);
+    const unsigned over = __ballot_sync(0xffffffffu, before + x > first);
+    if (over) {
+      const int src = __ffs(over) - 1;
+      if (src > 0) before += __shfl_sync(0xffffffffu, x, src - 1);
+      w.rt = rt0 + src;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, x, 31);
+    if (rt0 >= w.q.nt) return w;  // not reached
+  }
+  w.st = steps_of(P, w.q, w.rt);
+  const int ln = line_len(w.st.n);
+  w.h = (int)((first - before) / ln);
+  const int at = (int)(first - before - (long long)w.h * ln);
+  w.s = at;
+  w.end = (int)min((long long)w.st.n, at + count);
+  w.left = count - (ln - at);
+  // the run may begin behind a unit's last step, and end there too: `end` is then no
+  // larger than `s`, and the unit (written by the run before) is passed over
+  if (at >= w.st.n && at > 0) {
+    w.end = 0;
+    if (!next_unit(P, w)) w.b = -1;
+  }
+  if (count == 0) w.b = -1;
+  return w;
+}
+
+template <int D>
+struct Smem {
+  static constexpr int kHalfBytes = kBN * 128;    // of an fp16 tile
+  static constexpr int kTile = kBN * D * 2;       // an fp16 tile
+  static constexpr int kCodes = kBN * D;
+  static constexpr int kQ = 0;                    // A, B
+  static constexpr int kK = kQ + 2 * kTile;       // two slots
+  static constexpr int kV = kK + 2 * kTile;
+  static constexpr int kKC = kV + 2 * kTile;      // codes, one slot each
+  static constexpr int kVC = kKC + kCodes;
+  static constexpr int kInfoAt = kVC + kCodes;
+  static constexpr int kBar = kInfoAt + kInfo * 16;
+  enum { kKcFull, kKcEmpty, kVcFull, kVcEmpty, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
+         kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kSFull = kQFull + 2, kPHalf = kSFull + 2,
+         kPFull = kPHalf + 2, kOFull = kPFull + 2, kInfoFull = kOFull + 2,
+         kMmaDone = kInfoFull + kInfo, kNumBars };
+  static constexpr int kWalk = (kBar + 8 * kNumBars + 15) / 16 * 16;
+  static constexpr int kMisc = kWalk + ((1 + kConvWarp) * sizeof(Walk) + 15) / 16 * 16;  // tmem base, abort
+  static constexpr int kBytes = kMisc + 16;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 227 * 1024, "one CTA per SM");
+};
+
+// Columns [lo, hi] (relative to a block's first key) as bits.
+__device__ __forceinline__ uint32_t col_bits(int lo, int hi) {
+  if (hi < 0 || lo > 31 || hi < lo) return 0;
+  const uint32_t a = lo <= 0 ? ~0u : ~0u << lo;
+  return hi >= 31 ? a : a & ((2u << hi) - 1);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_major) {
+  return idesc_bf16_f32(M, N, 0, b_mn_major) & ~((1u << 7) | (1u << 10));  // A, B format: f16
+}
+
+template <int kRegs>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(sm);
+  auto bar = [&](int i) { return sbase + L::kBar + 8 * i; };
+  volatile Info* infos = reinterpret_cast<volatile Info*>(sm + L::kInfoAt);
+  Walk* start = reinterpret_cast<Walk*>(sm + L::kWalk);  // the run's; the softmax warps'
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kMisc + 4);
+  int* status = &g_attn_kv8_tc_status;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == kProducerWarp && lane == 0) {
+    const int one[] = {L::kKcFull, L::kVcFull, L::kKEmpty, L::kKEmpty + 1, L::kVEmpty,
+                       L::kVEmpty + 1, L::kSFull, L::kSFull + 1, L::kOFull, L::kOFull + 1,
+                       L::kMmaDone};
+    for (int i : one) mbar_init(bar(i), 1);
+    const int conv[] = {L::kKcEmpty, L::kVcEmpty, L::kKFull, L::kKFull + 1, L::kVFull,
+                        L::kVFull + 1};
+    for (int i : conv) mbar_init(bar(i), kConvWarps);
+    const int soft[] = {L::kQFull, L::kQFull + 1, L::kPHalf, L::kPHalf + 1, L::kPFull,
+                        L::kPFull + 1};
+    for (int i : soft) mbar_init(bar(i), kBM / 32);
+    for (int i = 0; i < kInfo; ++i) mbar_init(bar(L::kInfoFull + i), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    if (P.c.np > 0) {
+      tma_prefetch(&tm_k);
+      tma_prefetch(&tm_v);
+    }
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(sbase + L::kMisc, 512);
+    tmem_relinquish();
+  }
+  if (warp == 0) {
+    const Walk w = find_run(P);
+    if (lane == 0) *start = w;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const bool any = start->b >= 0 && start->q.nt > 0;
+
+  if (warp >= kConvWarp) {
+    reg_dec<kOtherRegs>();
+    if (warp < kConvWarp + kConvWarps) {
+      // -------------------------------------------------------- converters
+      // lanes 0-7 take eight rows' same chunk: reads and writes then touch every
+      // bank once
+      const int cw = warp - kConvWarp, r8 = lane & 7, c4 = lane >> 3;
+      bool ok = any;
+      auto convert = [&](const uint8_t* src, uint8_t* dst, int valid, int none) {
+#pragma unroll
+        for (int i = 0; i < kBN / (8 * kConvWarps); ++i) {
+          const int row = 32 * cw + 8 * i + r8;
+          // rows that hold no key hold anything: 0, so that 0 * it is 0
+          const bool there = row < valid && !((none >> cw) & 1);
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            const int c = 4 * j + c4;
+            uint4 x = *reinterpret_cast<const uint4*>(src + tile_at<D>(row, c));
+            if (!there) x = make_uint4(0, 0, 0, 0);
+            uint8_t* d = dst + (c >> 2) * L::kHalfBytes + row * 128;
+            const int c8 = 2 * (c & 3);
+            *reinterpret_cast<uint4*>(d + ((c8 ^ r8) << 4)) =
+                make_uint4(e4m3x2_to_h2(x.x & 0xffffu), e4m3x2_to_h2(x.x >> 16),
+                           e4m3x2_to_h2(x.y & 0xffffu), e4m3x2_to_h2(x.y >> 16));
+            *reinterpret_cast<uint4*>(d + (((c8 + 1) ^ r8) << 4)) =
+                make_uint4(e4m3x2_to_h2(x.z & 0xffffu), e4m3x2_to_h2(x.z >> 16),
+                           e4m3x2_to_h2(x.w & 0xffffu), e4m3x2_to_h2(x.w >> 16));
+          }
+        }
+        fence_proxy_async_smem();  // read next by the tensor core
+        __syncwarp();
+      };
+      for (int n = 0; ok; ++n) {
+        const int sl = n & 1;
+        ok = mbar_wait(bar(L::kKcFull), n & 1, abort_flag, status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const int fl = infos[n % kInfo].flags;
+        if (fl & kEnd) break;
+        if (n >= 2) {
+          ok = mbar_wait(bar(L::kKEmpty + sl), ((n >> 1) + 1) & 1, abort_flag, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        }
+        convert(sm + L::kKC, sm + L::kK + sl * L::kTile, fl >> 16, (fl >> 8) & 15);
+        if (lane == 0) {
+          mbar_arrive(bar(L::kKFull + sl));
+          mbar_arrive(bar(L::kKcEmpty));
+        }
+        ok = mbar_wait(bar(L::kVcFull), n & 1, abort_flag, status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (n >= 2) {
+          ok = mbar_wait(bar(L::kVEmpty + sl), ((n >> 1) + 1) & 1, abort_flag, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        }
+        convert(sm + L::kVC, sm + L::kV + sl * L::kTile, fl >> 16, (fl >> 8) & 15);
+        if (lane == 0) {
+          mbar_arrive(bar(L::kVFull + sl));
+          mbar_arrive(bar(L::kVcEmpty));
+        }
+      }
+    } else if (warp == kProducerWarp && any) {
+      // ---------------------------------------------------------- producer
+      Walk w = *start;
+      int n = 0, nk = 0, nv = 0;  // steps described, K and V copies issued
+      bool ok = true, more = true, begins = true;
+      if (w.s >= w.end) {  // units without steps
+        do more = next_unit(P, w);
+        while (more && w.s >= w.end);
+      }
+      while (more && ok) {
+        // eight steps of the unit at a time: a lane per block
+        const int s8 = w.s + (lane >> 2);
+        int page = -1, ke = 0, ve = 0;
+        const int kt = s8 < w.st.sinks ? s8 : s8 + w.st.skip;
+        const int row = kt * kBN + (lane & 3) * kBlock;
+        if (s8 < w.end && row < w.q.len) {
+          page = page_of(P.c, w.b, row);
+          if (page >= 0) {
+            const long long blk = (head_rows(P.c, page, w.h) + (row & (P.c.ps - 1))) / kBlock;
+            ke = clamp_exp(P.c.ke[blk]);
+            ve = clamp_exp(P.c.ve[blk]);
+          }
+        }
+        const unsigned none = __ballot_sync(0xffffffffu, page < 0);
+        // four lanes' exponents as bytes
+        uint32_t ke4 = (ke & 0xff) << (8 * (lane & 3)), ve4 = (ve & 0xff) << (8 * (lane & 3));
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          ke4 |= __shfl_xor_sync(0xffffffffu, ke4, o);
+          ve4 |= __shfl_xor_sync(0xffffffffu, ve4, o);
+        }
+        const int cnt = min(8, w.end - w.s);
+        const bool has_b = w.q.R - w.rt * kUnitRows > kBM;
+        for (int i = 0; i < cnt; ++i, ++n) {
+          const int src = 4 * i;
+          const uint32_t k4 = __shfl_sync(0xffffffffu, ke4, src);
+          const uint32_t v4 = __shfl_sync(0xffffffffu, ve4, src);
+          const int key0 = (w.s + i < w.st.sinks ? w.s + i : w.s + i + w.st.skip) * kBN;
+          const int none4 = (none >> src) & 15;
+          const uint32_t bytes = (kBlocks - __popc(none4)) * kBlock * D;
+          const bool mine = (lane >> 2) == i && page >= 0;
+          const int at = (lane & 3) * kBlock;
+          ok = n < 1 || mbar_wait(bar(L::kKcEmpty), (n - 1) & 1, abort_flag, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (lane == 0) {
+            volatile Info* x = infos + n % kInfo;
+            x->key0 = key0;
+            x->flags = (has_b ? kHasB : 0) | (i == 0 && begins ? kFirst : 0) |
+                       (w.s + i + 1 == w.end ? kLast : 0) | none4 << 8 |
+                       min(kBN, w.q.len - key0) << 16;
+            x->ke = k4;
+            x->ve = v4;
+            mbar_arrive(bar(L::kInfoFull + n % kInfo));
+            if (bytes) mbar_expect_tx(bar(L::kKcFull), bytes);
+            else mbar_arrive(bar(L::kKcFull));
+          }
+          __syncwarp();
+          const int hp = page * P.c.H + w.h;
+          if (mine)
+            tma_load_3d(sbase + L::kKC + at * D, &tm_k, bar(L::kKcFull), 0,
+                        (key0 + at) & (P.c.ps - 1), hp);
+          ++nk;
+          ok = n < 1 || mbar_wait(bar(L::kVcEmpty), (n - 1) & 1, abort_flag, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (lane == 0) {
+            if (bytes) mbar_expect_tx(bar(L::kVcFull), bytes);
+            else mbar_arrive(bar(L::kVcFull));
+          }
+          __syncwarp();
+          if (mine)
+            tma_load_3d(sbase + L::kVC + at * D, &tm_v, bar(L::kVcFull), 0,
+                        (key0 + at) & (P.c.ps - 1), hp);
+          ++nv;
+        }
+        w.s += cnt;
+        begins = w.s >= w.end;
+        while (more && w.s >= w.end) more = next_unit(P, w);
+      }
+      if (ok && n >= 1) ok = mbar_wait(bar(L::kKcEmpty), (n - 1) & 1, abort_flag, status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (lane == 0) {
+        if (ok) {
+          infos[n % kInfo].flags = kEnd;
+          mbar_arrive(bar(L::kInfoFull + n % kInfo));
+          mbar_arrive(bar(L::kKcFull));
+        } else {
+          // aborted: the copies in flight land before the CTA ends
+          if (nk > 0) mbar_wait_drain(bar(L::kKcFull), (nk - 1) & 1);
+          if (nv > 0) mbar_wait_drain(bar(L::kVcFull), (nv - 1) & 1);
+        }
+      }
+    } else if (warp == kMmaWarp && any) {
+      // --------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t kIdQK = idesc_f16_f32(kBM, kBN, 0);
+        constexpr uint32_t kIdPV = idesc_f16_f32(kBM, D, 1);
+        const uint64_t dq0 = sdesc_sw128(sbase + L::kQ, 16, 1024);
+        const uint64_t dk0 = sdesc_sw128(sbase + L::kK, 16, 1024);
+        const uint64_t dv0 = sdesc_sw128(sbase + L::kV, L::kHalfBytes, 1024);
+        auto qk = [&](int hf, int n) {
+          const uint64_t dq = sdesc_add(dq0, hf * L::kTile), dk = sdesc_add(dk0, (n & 1) * L::kTile);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * L::kHalfBytes + (kk & 3) * 32;
+            mma_ss(tmem + hf * kBN, sdesc_add(dq, off), sdesc_add(dk, off), kIdQK, kk > 0);
+          }
+          mma_commit(bar(L::kSFull + hf));
+        };
+        auto wait = [&](int b, unsigned parity) {
+          return mbar_wait(bar(b), parity & 1, abort_flag, status);
+        };
+        int n = 0;                       // steps of the run
+        unsigned th[2] = {0, 0}, uh[2] = {0, 0};  // each half's steps and units
+        bool ok = wait(L::kInfoFull, 0);
+        while (ok) {  // a unit
+          int fl = infos[n % kInfo].flags;
+          if (fl & kEnd) break;
+          const int halves = fl & kHasB ? 2 : 1;
+          if (!(ok = wait(L::kKFull + (n & 1), n >> 1))) break;
+          for (int hf = 0; ok && hf < halves; ++hf) {
+            if (!(ok = wait(L::kQFull + hf, uh[hf]++))) break;
+            tc_fence_after();
+            qk(hf, n);
+          }
+          if (!ok) break;
+          mma_commit(bar(L::kKEmpty + (n & 1)));
+          for (;;) {  // its steps: P V of this one, Q K of the next
+            const bool last = fl & kLast;
+            const uint64_t dv = sdesc_add(dv0, (n & 1) * L::kTile);
+            for (int hf = 0; hf < halves; ++hf) {
+              const uint32_t s_tm = tmem + hf * kBN, o_tm = tmem + 2 * kBN + hf * D;
+              const bool begun = !(fl & kFirst);
+              if (hf == 0 && !(ok = wait(L::kVFull + (n & 1), n >> 1))) break;
+              // the first 64 keys' P as soon as the softmax has written them
+              if (!(ok = wait(L::kPHalf + hf, th[hf]))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < kBN / 32; ++kk)
+                mma_ts(o_tm, s_tm + kk * 8, sdesc_add(dv, kk * 2048), kIdPV, begun || kk > 0);
+              if (!(ok = wait(L::kPFull + hf, th[hf]))) break;
+              ++th[hf];
+              tc_fence_after();
+#pragma unroll
+              for (int kk = kBN / 32; kk < kBN / 16; ++kk)
+                mma_ts(o_tm, s_tm + kk * 8, sdesc_add(dv, kk * 2048), kIdPV, 1u);
+              if (hf == halves - 1) mma_commit(bar(L::kVEmpty + (n & 1)));
+              if (last) {
+                mma_commit(bar(L::kOFull + hf));
+              } else {
+                if (hf == 0 && !(ok = wait(L::kKFull + ((n + 1) & 1), (n + 1) >> 1))) break;
+                tc_fence_after();
+                qk(hf, n + 1);
+              }
+            }
+            if (!ok) break;
+            ++n;
+            if (!last) mma_commit(bar(L::kKEmpty + (n & 1)));
+            if (!(ok = wait(L::kInfoFull + n % kInfo, n / kInfo))) break;
+            fl = infos[n % kInfo].flags;
+            if (last) break;
+          }
+        }
+        // nothing of ours may still run on the tensor core when TMEM is freed
+        mma_commit(bar(L::kMmaDone));
+        mbar_wait_drain(bar(L::kMmaDone), 0);
+      }
+    }
+  } else {
+    // --------------------------------------------------------------- softmax
+    reg_inc<kSoftmaxRegs>();
+    // the walk stands in shared memory: no room for it in registers
+    Walk& w = start[1 + warp];
+    if (lane == 0) w = start[0];
+    __syncwarp();
+    const int hf = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // row of the half = lane of the tensor memory
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_tm = tmem + lane_off + hf * kBN, o_tm = tmem + lane_off + 2 * kBN + hf * D;
+    if (threadIdx.x == 0)
+      P.rec[2 * blockIdx.x] = P.rec[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+    int n = 0;              // steps of the run
+    unsigned th = 0, uh = 0;  // this half's steps and units
+    bool ok = any, more = any;
+    while (more) {  // a unit
+      const int steps = max(0, w.end - w.s);
+      const int row0 = w.rt * kUnitRows + hf * kBM, row = row0 + r;
+      const bool whole = w.s == 0 && w.end == w.st.n;
+      const int part = 2 * blockIdx.x + (w.s == 0 ? 1 : 0);
+      if (!whole && threadIdx.x == 0)
+        P.rec[part] = make_int4(w.end == w.st.n ? 3 : 1, w.b, w.rt, w.h);
+      if (row0 < w.q.R) {
+        const bool there = row < w.q.R;
+        const int tok = row / P.G, hh = row - tok * P.G;
+        const long long o_row = (long long)(w.q.first + tok) * P.Hq + w.h * P.G + hh;
+        const int i = w.q.len - w.q.n + tok;  // position
+        float m_run = -INFINITY, l_run = 0.f;
+        if (steps > 0) {
+          // ------------------------------------------------------ queries
+          // (every product with the rows that stood here has completed: its scores
+          // have been read)
+          float row_mul;
+          {
+            const uint4* src = reinterpret_cast<const uint4*>(P.q + o_row * D);
+            uint4 x[D / 8];
+            float big = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              x[c] = there ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+              const uint32_t e[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                big = fmaxf(big, fmaxf(fabsf(__uint_as_float(e[j] << 16)),
+                                       fabsf(__uint_as_float(e[j] & 0xffff0000u))));
+            }
+            // 2^ex times a largest element in [1, 2) is brought to [64, 128)
+            const int ex = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -120), 127);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 6 - ex) << 23);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              const uint32_t e[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+              uint32_t f[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                f[j] = pack_f16(__uint_as_float(e[j] << 16) * up,
+                                __uint_as_float(e[j] & 0xffff0000u) * up);
+              *reinterpret_cast<uint4*>(sm + L::kQ + hf * L::kTile + (c >> 3) * L::kHalfBytes +
+                                        r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(f[0], f[1], f[2], f[3]);
+            }
+            // not 0 or infinite, with a block's exponent too, which a masked key's -inf
+            // or a score of 0 would make NaN
+            row_mul = fminf(fmaxf(ldexpf(P.score_mul, ex - 6), FLT_MIN * 0x1p41f),
+                            FLT_MAX * 0x1p-41f);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kQFull + hf));
+          }
+          // the half's positions
+          const int i_lo = w.q.len - w.q.n + row0 / P.G;
+          const int i_hi = w.q.len - w.q.n + (min(w.q.R, row0 + kBM) - 1) / P.G;
+          const int hi = i < 0 ? -1 : P.causal ? min(i, w.q.len - 1) : w.q.len - 1;
+          const int lo = P.window > 0 ? i - P.window + 1 : 0;
+          const int sink_hi = P.window > 0 ? min(P.sink - 1, hi) : -1;
+          for (int s = 0; s < steps; ++s) {
+            const int ns = n + s;
+            // The scores first: a half that had no part in the units before may be more
+            // than kInfo steps ahead, where the description's barrier is still two phases
+            // back and would pass at once. Once the scores are there, so is it.
+            ok = mbar_wait(bar(L::kSFull + hf), th & 1, abort_flag, status) &&
+                 mbar_wait(bar(L::kInfoFull + ns % kInfo), (ns / kInfo) & 1, abort_flag, status);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            ++th;
+            tc_fence_after();
+            const int key0 = infos[ns % kInfo].key0, fl = infos[ns % kInfo].flags;
+            const uint32_t ke4 = infos[ns % kInfo].ke, ve4 = infos[ns % kInfo].ve;
+            const int none = (fl >> 8) & 15;
+            const bool masked = none || (fl >> 16) < kBN || i_lo < 0 ||
+                                (P.causal && key0 + kBN - 1 > i_lo) ||
+                                (P.window > 0 && i_hi - key0 >= P.window);
+            uint32_t sr[kBlocks][32];
+#pragma unroll
+            for (int c = 0; c < kBlocks; ++c) tmem_ld32(s_tm + 32 * c, sr[c]);
+            tmem_wait_ld();
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < kBlocks; ++c) {
+                const int k = key0 + 32 * c;
+                uint32_t vis = col_bits(lo - k, hi - k) | col_bits(-k, sink_hi - k);
+                if ((none >> c) & 1) vis = 0;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!((vis >> j) & 1u)) sr[c][j] = __float_as_uint(-INFINITY);
+              }
+            }
+            float mul[kBlocks], ve[kBlocks], mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kBlocks; ++c) {
+              mul[c] = row_mul * exp2i(static_cast<int8_t>(ke4 >> (8 * c)));
+              ve[c] = static_cast<float>(static_cast<int8_t>(ve4 >> (8 * c)));
+              float a[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) a[j] = __uint_as_float(sr[c][j]);
+#pragma unroll
+              for (int j = 4; j < 32; ++j) a[j & 3] = fmaxf(a[j & 3], __uint_as_float(sr[c][j]));
+              mx = fmaxf(mx, fmaf(mul[c], fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), ve[c]));
+            }
+            // the reference moves when p would leave fp16's range
+            const bool need = mx > m_run + kAbove;
+            float alpha = 1.f;
+            if (need) {
+              const float x = mx - kBelow;
+              alpha = m_run == -INFINITY ? 0.f : ex2(m_run - x);
+              m_run = x;
+              l_run *= alpha;
+            }
+            const float msub = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll
+            for (int hp = 0; hp < 2; ++hp) {  // P in two parts of 64 keys
+#pragma unroll
+              for (int cc = 0; cc < 2; ++cc) {
+                uint32_t pk[16];
+                const int c = 2 * hp + cc;
+                const uint64_t mul2 = f2_pack(mul[c], mul[c]);
+                const uint64_t add2 = f2_pack(ve[c] - msub, ve[c] - msub);
+                uint64_t ls[2] = {0, 0};
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  float x0, x1;
+                  f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c][2 * j]),
+                                           __uint_as_float(sr[c][2 * j + 1])), mul2, add2), x0, x1);
+                  const float p0 = ex2(x0), p1 = ex2(x1);
+                  ls[j & 1] = f2_add(ls[j & 1], f2_pack(p0, p1));
+                  pk[j] = pack_f16(p0, p1);
+                }
+                float a0, a1, b0, b1;
+                f2_unpack(ls[0], a0, a1);
+                f2_unpack(ls[1], b0, b1);
+                l_run = fmaf((a0 + a1) + (b0 + b1),
+                             exp2i(-static_cast<int8_t>(ve4 >> (8 * c))), l_run);
+                tmem_st16(s_tm + 16 * c, pk);
+              }
+              // O holds the steps before (complete: these scores' commit tracks every
+              // earlier product); it follows the reference before P V adds to it
+              if (hp == 0 && __any_sync(0xffffffffu, need && s > 0)) {
+#pragma unroll
+                for (int oc = 0; oc < D / 32; ++oc) {
+                  uint32_t o[32];
+                  tmem_ld32(o_tm + 32 * oc, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                  tmem_st32(o_tm + 32 * oc, o);
+                }
+              }
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar((hp == 0 ? L::kPHalf : L::kPFull) + hf));
+            }
+          }
+          if (!ok) break;
+          ok = mbar_wait(bar(L::kOFull + hf), uh & 1, abort_flag, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          ++uh;
+          tc_fence_after();
+        }
+        // ----------------------------------------------------------- the end
+        const bool none = l_run == 0.f;  // no visible key (a NaN score makes it NaN)
+        const float inv = none ? 0.f : 1.f / l_run;
+#pragma unroll
+        for (int oc = 0; oc < D / 32; ++oc) {
+          uint32_t o[32];
+          if (steps > 0) {
+            tmem_ld32(o_tm + 32 * oc, o);
+            tmem_wait_ld();
+          }
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              o[j] = none ? 0u : __float_as_uint(__uint_as_float(o[j]) * inv);
+            if (there) {
+              uint4* dst = reinterpret_cast<uint4*>(P.out + o_row * D + 32 * oc);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  f[e] = pack_bf16(__uint_as_float(o[8 * j + 2 * e]),
+                                   __uint_as_float(o[8 * j + 2 * e + 1]));
+                dst[j] = make_uint4(f[0], f[1], f[2], f[3]);
+              }
+            }
+          } else if (there) {
+            uint4* dst = reinterpret_cast<uint4*>(
+                P.o_part + ((long long)part * kUnitRows + hf * kBM + r) * D + 32 * oc);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+        }
+        if (there) {
+          if (whole)
+            P.lse[o_row] = none ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+          else
+            P.ml_part[(long long)part * kUnitRows + hf * kBM + r] = make_float2(m_run, l_run);
+        }
+      }
+      n += steps;
+      __syncwarp();
+      if (lane == 0) more = next_unit(P, w);
+      more = __shfl_sync(0xffffffffu, more, 0);
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+constexpr int kMergeThreads = 128, kMergeRows = 16;  // rows of a block
+constexpr int kPads = 64;
+
+// Block (j, y): rows [16 y, ..) of the unit whose first steps were run j's last, and
+// which run j did not end; its other partials are the first of the runs behind. Blocks
+// behind those (packed): zeros for the tokens outside the sequences.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) attn_kv8_tc_merge_kernel(const TcParams P) {
+  constexpr int kLanes = D / 4, kAtOnce = kMergeThreads / kLanes;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x >= kGrid - 1) {
+    const int i0 = (blockIdx.x - (kGrid - 1)) * gridDim.y + blockIdx.y;
+    const int step = (gridDim.x - (kGrid - 1)) * gridDim.y;
+    const int e0 = min(max(__ldg(P.cu), 0), P.T), e1 = max(e0, min(max(__ldg(P.cu + P.c.B), 0), P.T));
+    for (int i = i0; i < e0 + P.T - e1; i += step) {
+      const long long tok = i < e0 ? i : e1 + (i - e0);
+      uint2* r = reinterpret_cast<uint2*>(P.out + tok * P.Hq * D);
+      for (int u = threadIdx.x; u < P.Hq * D / 4; u += kMergeThreads) r[u] = make_uint2(0, 0);
+      for (int u = threadIdx.x; u < P.Hq; u += kMergeThreads) P.lse[tok * P.Hq + u] = -INFINITY;
+    }
+    return;
+  }
+  const int j = blockIdx.x;
+  const int4 rec = P.rec[2 * j + 1];
+  if (rec.x != 1) return;
+  const Seq q = seq_of(P, rec.y);
+  int last = j + 1;  // the run with the unit's last steps
+  while (last < kGrid - 1 && P.rec[2 * last].x == 1) ++last;
+  const int d = threadIdx.x % kLanes;
+  for (int rr = blockIdx.y * kMergeRows + threadIdx.x / kLanes; rr < (int)(blockIdx.y + 1) * kMergeRows;
+       rr += kAtOnce) {
+    const int row = rec.z * kUnitRows + rr;
+    if (row >= q.R) break;
+    float M = -INFINITY, ls = 0.f;
+    float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = j; k <= last; ++k) {
+      const long long at = (long long)(k == j ? 2 * j + 1 : 2 * k) * kUnitRows + rr;
+      const float2 a = P.ml_part[at];
+      const float4 x = reinterpret_cast<const float4*>(P.o_part + at * D)[d];
+      const float Mn = fmaxf(M, a.x);
+      const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn);
+      const float f1 = a.x == -INFINITY ? 0.f : ex2(a.x - Mn);
+      os.x = os.x * f0 + x.x * f1;
+      os.y = os.y * f0 + x.y * f1;
+      os.z = os.z * f0 + x.z * f1;
+      os.w = os.w * f0 + x.w * f1;
+      ls = ls * f0 + a.y * f1;
+      M = Mn;
+    }
+    const int tok = row / P.G, hh = row - tok * P.G;
+    const long long o_row = (long long)(q.first + tok) * P.Hq + rec.w * P.G + hh;
+    const bool none = ls == 0.f;
+    const float inv = none ? 0.f : 1.f / ls;
+    if (none) os = make_float4(0.f, 0.f, 0.f, 0.f);
+    reinterpret_cast<uint2*>(P.out + o_row * D)[d] =
+        make_uint2(pack_bf16(os.x * inv, os.y * inv), pack_bf16(os.z * inv, os.w * inv));
+    if (d == 0) P.lse[o_row] = none ? -INFINITY : (M + log2f(ls)) * kLn2;
+  }
+}
+
+// ------------------------------------------------------------------- host
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Ws {
+  size_t ml, rec, total;
+};
+Ws layout(int D) {
+  Ws w{};
+  w.ml = up256((size_t)2 * kGrid * kUnitRows * D * 4);
+  w.rec = w.ml + up256((size_t)2 * kGrid * kUnitRows * 8);
+  w.total = w.rec + up256((size_t)2 * kGrid * 16);
+  return w;
+}
+
+template <int D>
+usp_status_t launch_t(const TcParams& P, cudaStream_t st) {
+  CUtensorMap mk{}, mv{};  // (without pages, nothing is loaded through them)
+  if (P.c.np > 0 && (!make_map(&mk, P.c.kc, P.c, D) || !make_map(&mv, P.c.vc, P.c, D)))
+    return USP_ERR_CUDA;
+  const int smem = Smem<D>::kAlloc;
+  static SmemAttr attr;
+  cudaError_t e = attr.set(attn_kv8_tc_kernel<D>, smem);
+  if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
+  {
+    ProfScope ps(st, "attn_kv8_tc");
+    attn_kv8_tc_kernel<D><<<kGrid, kThreads, smem, st>>>(P, mk, mv);
+  }
+  note_launch();
+  usp_status_t r = check_launch();
+  if (r != USP_OK) return r;
+  // the merge's launch and set-up overlap the end of the kernel before it
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kGrid - 1 + (P.cu ? kPads / (kUnitRows / kMergeRows) : 0),
+                     kUnitRows / kMergeRows);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  {
+    ProfScope ps(st, "attn_kv8_tc_merge");
+    e = cudaLaunchKernelEx(&cfg, attn_kv8_tc_merge_kernel<D>, P);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail_cuda("kernel launch", e);
+  }
+  note_launch();
+  return USP_OK;
+}
+
+}  // namespace
+
+size_t attn_kv8_tc_workspace(int D) { return layout(D).total; }
+
+usp_status_t launch_attn_kv8_tc(const AttnKv8Args& a, void* workspace, cudaStream_t st) {
+  const Ws w = layout(a.D);
+  char* base = static_cast<char*>(workspace);
+  TcParams P{};
+  P.c = a.c;
+  P.q = static_cast<const __nv_bfloat16*>(a.q);
+  P.out = static_cast<__nv_bfloat16*>(a.out);
+  P.lse = a.lse;
+  P.o_part = reinterpret_cast<float*>(base);
+  P.ml_part = reinterpret_cast<float2*>(base + w.ml);
+  P.rec = reinterpret_cast<int4*>(base + w.rec);
+  P.cu = a.cu;
+  P.T = a.T;
+  P.max_new = a.max_new;
+  P.Hq = a.Hq;
+  P.G = a.Hq / a.c.H;
+  P.score_mul = a.scale * 1.4426950408889634f;
+  P.causal = a.causal;
+  P.window = a.window;
+  P.sink = a.sink;
+  return a.D == 128 ? launch_t<128>(P, st) : launch_t<64>(P, st);
+}
+
+int read_clear_attn_kv8_tc_status() {
+  int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_attn_kv8_tc_status, sizeof(int)) != cudaSuccess) return -1;
+  if (v != 0) cudaMemcpyToSymbol(g_attn_kv8_tc_status, &z, sizeof(int));
+  return v;
+}
+
+}  // namespace usp

@@ -87,6 +87,7 @@ int decode_keys_per_tile();
 
 int read_clear_decode_kv4_status();  // decode_kv4.cu; -1 on a CUDA error
 int read_clear_attn_kv8_status();    // attn_kv8.cu; -1 on a CUDA error
+int read_clear_attn_kv8_tc_status();  // attn_kv8_tc.cu; -1 on a CUDA error
 
 // key_weights.cu. P: the problem (q, k, lse and the masks); weight [Bt][Hkv][S]
 // fp32; observe 0: every query, else the last `observe` of each sequence. The

@@ -46,4 +46,9 @@ size_t attn_kv8_workspace(int B, int T, int max_new, int packed, int Hq, int Hkv
 usp_status_t launch_attn_kv8(const AttnKv8Args& a, void* workspace, cudaStream_t st);
 int read_clear_attn_kv8_status();  // -1 on a CUDA error
 
+// attn_kv8_tc.cu (many query rows per KV head), from launch_attn_kv8
+size_t attn_kv8_tc_workspace(int D);
+usp_status_t launch_attn_kv8_tc(const AttnKv8Args& a, void* workspace, cudaStream_t st);
+int read_clear_attn_kv8_tc_status();  // -1 on a CUDA error
+
 }  // namespace usp

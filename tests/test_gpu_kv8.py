@@ -364,6 +364,9 @@ ATTN = [
     (1, 257, 1024, 1, 8, 128, 128, [1000], True, 200, 200),
     (2, 65, 300, 2, 4, 64, 32, [0, 299], False, 37, 5),
     (1, 600, 2048, 2, 4, 128, 64, [2048], True, 0, 0),
+    # more units than the GPU takes at once
+    (5, 150, 768, 16, 4, 64, 64, [160, 700, 0, 333, 150], True, 0, 0),
+    (70, 9, 384, 8, 3, 128, 128, [(37 * b) % 385 for b in range(70)], True, 0, 0),
 ]
 
 
@@ -387,12 +390,17 @@ def test_attention_is_the_oracles(B, T, cap, H, G, D, page, lens, causal, window
     ([2, 3, 4, 140, 141, 300], [70, 0, 250, 129, 300], dict(window=0)),
     ([0, 40, 41, 41, 90, 91], [200, 33, 10, 49, 320], dict(window=40, sink_tokens=2)),
     ([1, 2, 3, 4, 5, 6], [320, 1, 0, 63, 64], dict(causal=False)),
+    ([0, 1, 2, 3, 200, 500], [320, 1, 150, 197, 320], dict(window=0, heads=12)),
+    # units of few rows and many steps, in which half of the tensor core's rows have no
+    # part, before units in which they have
+    ([0, 1, 2, 3, 200, 500], [8000, 5000, 3000, 2500, 1800], dict(window=0, heads=8, cap=8192)),
 ])
 @pytest.mark.parametrize("hint", [False, True])
 def test_packed_attention_is_the_oracles(cut, lens, kw, hint):
     dev = device()
-    B, H, G, D = 5, 2, 4, 128
-    c = random_cache(dev, B, 320, H, D, 32, lens, seed=cut[-1])
+    kw = dict(kw)
+    B, H, G, D = 5, kw.pop("heads", 2), 4, 128
+    c = random_cache(dev, B, kw.pop("cap", 320), H, D, 32, lens, seed=cut[-1])
     T = cut[-1] + 3
     q = torch.randn(T, H * G, D, generator=gen(T)).to(BF).to(dev)
     out, lse = usp.attn_kv8(q, c, cu_seqlens=i32(cut, dev),
