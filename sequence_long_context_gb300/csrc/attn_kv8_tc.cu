@@ -15,10 +15,10 @@
 //   warps 8-11      converters: E4M3 codes to fp16 tiles in shared memory, once for
 //                   both halves (exact; the products need both operands of one type)
 //   warp 12         producer: pages and exponents of the tiles, TMA of the codes
-//   warp 13         MMA issuer (one thread), owner of the tensor memory
-// Tensor memory: S_A [0, 128), S_B [128, 256), O_A at 256, O_B at 256 + D. The
-// products of one half run while the softmax of the other works:
-//   P V (A, n), Q K (A, n + 1), P V (B, n), Q K (B, n + 1), ..
+//   warps 13, 14    MMA issuers of half A and B (one thread each); 13 owns the tensor memory
+// Tensor memory: S_A [0, 128), S_B [128, 256) (P over them as fp16), O_A at 256, O_B at
+// 256 + D. The halves share the tiles and nothing else, and the products of one run
+// while the softmax of the other works.
 // The numbers are attn_kv8.cu's: q scaled to fp16 by a power of two per row, K's
 // exponent a factor of the block's scores, V's added to them, p against a reference
 // 2^7 to 2^15 below the running maximum of score + e_v, the row's sum over p 2^-e_v.
@@ -45,6 +45,7 @@ constexpr int kBM = 128;                 // rows of a half
 constexpr int kUnitRows = 2 * kBM;
 constexpr int kBN = 128;                 // keys of a step
 constexpr int kBlocks = kBN / kBlock;    // exponents of a step
+constexpr int kSub = 64;                 // keys whose scores are made at once
 constexpr int kGrid = 152;
 constexpr int kThreads = 512;
 constexpr int kConvWarp = 8, kConvWarps = 4, kProducerWarp = 12, kMmaWarp = 13;
@@ -248,9 +249,8 @@ struct Smem {
   static constexpr int kInfoAt = kVC + kCodes;
   static constexpr int kBar = kInfoAt + kInfo * 16;
   enum { kKcFull, kKcEmpty, kVcFull, kVcEmpty, kKFull, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
-         kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kSFull = kQFull + 2, kPHalf = kSFull + 2,
-         kPFull = kPHalf + 2, kOFull = kPFull + 2, kInfoFull = kOFull + 2,
-         kMmaDone = kInfoFull + kInfo, kNumBars };
+         kVEmpty = kVFull + 2, kQFull = kVEmpty + 2, kSFull = kQFull + 2, kPFull = kSFull + 4, kOFull = kPFull + 4,
+         kODone = kOFull + 2, kInfoFull = kODone + 2, kMmaDone = kInfoFull + kInfo, kNumBars = kMmaDone + 2 };
   static constexpr int kWalk = (kBar + 8 * kNumBars + 15) / 16 * 16;
   static constexpr int kMisc = kWalk + ((1 + kConvWarp) * sizeof(Walk) + 15) / 16 * 16;  // tmem base, abort
   static constexpr int kBytes = kMisc + 16;
@@ -301,15 +301,17 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == kProducerWarp && lane == 0) {
-    const int one[] = {L::kKcFull, L::kVcFull, L::kKEmpty, L::kKEmpty + 1, L::kVEmpty,
-                       L::kVEmpty + 1, L::kSFull, L::kSFull + 1, L::kOFull, L::kOFull + 1,
-                       L::kMmaDone};
+    const int one[] = {L::kKcFull, L::kVcFull, L::kSFull, L::kSFull + 1, L::kSFull + 2,
+                       L::kSFull + 3, L::kOFull, L::kOFull + 1, L::kODone,
+                       L::kODone + 1, L::kMmaDone, L::kMmaDone + 1};
     for (int i : one) mbar_init(bar(i), 1);
+    const int two[] = {L::kKEmpty, L::kKEmpty + 1, L::kVEmpty, L::kVEmpty + 1};
+    for (int i : two) mbar_init(bar(i), 2);  // both halves
     const int conv[] = {L::kKcEmpty, L::kVcEmpty, L::kKFull, L::kKFull + 1, L::kVFull,
                         L::kVFull + 1};
     for (int i : conv) mbar_init(bar(i), kConvWarps);
-    const int soft[] = {L::kQFull, L::kQFull + 1, L::kPHalf, L::kPHalf + 1, L::kPFull,
-                        L::kPFull + 1};
+    const int soft[] = {L::kQFull, L::kQFull + 1, L::kPFull, L::kPFull + 1, L::kPFull + 2,
+                        L::kPFull + 3};
     for (int i : soft) mbar_init(bar(i), kBM / 32);
     for (int i = 0; i < kInfo; ++i) mbar_init(bar(L::kInfoFull + i), 1);
     *abort_flag = 0;
@@ -483,80 +485,82 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
           if (nv > 0) mbar_wait_drain(bar(L::kVcFull), (nv - 1) & 1);
         }
       }
-    } else if (warp == kMmaWarp && any) {
-      // --------------------------------------------------------- MMA issuer
+    } else if ((warp == kMmaWarp || warp == kMmaWarp + 1) && any) {
+      // -------------------------------------------------- MMA issuer of a half
       if (lane == 0) {
-        constexpr uint32_t kIdQK = idesc_f16_f32(kBM, kBN, 0);
+        const int hf = warp - kMmaWarp;
+        constexpr uint32_t kIdQK = idesc_f16_f32(kBM, kSub, 0);
         constexpr uint32_t kIdPV = idesc_f16_f32(kBM, D, 1);
-        const uint64_t dq0 = sdesc_sw128(sbase + L::kQ, 16, 1024);
+        const uint32_t s_tm = tmem + hf * kBN, o_tm = tmem + 2 * kBN + hf * D;
+        const uint64_t dq0 = sdesc_sw128(sbase + L::kQ + hf * L::kTile, 16, 1024);
         const uint64_t dk0 = sdesc_sw128(sbase + L::kK, 16, 1024);
         const uint64_t dv0 = sdesc_sw128(sbase + L::kV, L::kHalfBytes, 1024);
-        auto qk = [&](int hf, int n) {
-          const uint64_t dq = sdesc_add(dq0, hf * L::kTile), dk = sdesc_add(dk0, (n & 1) * L::kTile);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * L::kHalfBytes + (kk & 3) * 32;
-            mma_ss(tmem + hf * kBN, sdesc_add(dq, off), sdesc_add(dk, off), kIdQK, kk > 0);
-          }
-          mma_commit(bar(L::kSFull + hf));
-        };
         auto wait = [&](int b, unsigned parity) {
           return mbar_wait(bar(b), parity & 1, abort_flag, status);
         };
-        int n = 0;                       // steps of the run
-        unsigned th[2] = {0, 0}, uh[2] = {0, 0};  // each half's steps and units
+        unsigned th = 0, uh = 0;  // steps and units of this half
+        // scores of 64 keys of step n into one of two places
+        auto qk = [&](int n, int sub) {
+          const uint64_t dk = sdesc_add(dk0, (n & 1) * L::kTile + sub * (kSub * 128));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * L::kHalfBytes + (kk & 3) * 32;
+            mma_ss(s_tm + sub * kSub, sdesc_add(dq0, off), sdesc_add(dk, off), kIdQK, kk > 0);
+          }
+          mma_commit(bar(L::kSFull + 2 * hf + sub));
+          if (sub == 1) mma_commit(bar(L::kKEmpty + (n & 1)));
+        };
+        int n = 0;  // steps of the run
         bool ok = wait(L::kInfoFull, 0);
-        while (ok) {  // a unit
+        while (ok) {
           int fl = infos[n % kInfo].flags;
           if (fl & kEnd) break;
-          const int halves = fl & kHasB ? 2 : 1;
           if (!(ok = wait(L::kKFull + (n & 1), n >> 1))) break;
-          for (int hf = 0; ok && hf < halves; ++hf) {
-            if (!(ok = wait(L::kQFull + hf, uh[hf]++))) break;
-            tc_fence_after();
-            qk(hf, n);
+          if (hf == 1 && !(fl & kHasB)) {  // no rows in this half
+            mbar_arrive(bar(L::kKEmpty + (n & 1)));
+            if (!(ok = wait(L::kVFull + (n & 1), n >> 1))) break;
+            mbar_arrive(bar(L::kVEmpty + (n & 1)));
+            ++n;
+            ok = wait(L::kInfoFull + n % kInfo, n / kInfo);
+            continue;
           }
-          if (!ok) break;
-          mma_commit(bar(L::kKEmpty + (n & 1)));
-          for (;;) {  // its steps: P V of this one, Q K of the next
-            const bool last = fl & kLast;
+          if (!(ok = wait(L::kQFull + hf, uh++))) break;
+          tc_fence_after();
+          qk(n, 0);
+          qk(n, 1);
+          for (;;) {  // a unit's steps
             const uint64_t dv = sdesc_add(dv0, (n & 1) * L::kTile);
-            for (int hf = 0; hf < halves; ++hf) {
-              const uint32_t s_tm = tmem + hf * kBN, o_tm = tmem + 2 * kBN + hf * D;
-              const bool begun = !(fl & kFirst);
-              if (hf == 0 && !(ok = wait(L::kVFull + (n & 1), n >> 1))) break;
-              // the first 64 keys' P as soon as the softmax has written them
-              if (!(ok = wait(L::kPHalf + hf, th[hf]))) break;
+            const bool last = fl & kLast;
+            if (!(ok = wait(L::kVFull + (n & 1), n >> 1))) break;
+#pragma unroll 1
+            for (int sub = 0; sub < 2; ++sub) {
+              if (!(ok = wait(L::kPFull + 2 * hf + sub, th))) break;
               tc_fence_after();
 #pragma unroll
-              for (int kk = 0; kk < kBN / 32; ++kk)
-                mma_ts(o_tm, s_tm + kk * 8, sdesc_add(dv, kk * 2048), kIdPV, begun || kk > 0);
-              if (!(ok = wait(L::kPFull + hf, th[hf]))) break;
-              ++th[hf];
-              tc_fence_after();
-#pragma unroll
-              for (int kk = kBN / 32; kk < kBN / 16; ++kk)
-                mma_ts(o_tm, s_tm + kk * 8, sdesc_add(dv, kk * 2048), kIdPV, 1u);
-              if (hf == halves - 1) mma_commit(bar(L::kVEmpty + (n & 1)));
-              if (last) {
-                mma_commit(bar(L::kOFull + hf));
-              } else {
-                if (hf == 0 && !(ok = wait(L::kKFull + ((n + 1) & 1), (n + 1) >> 1))) break;
+              for (int kk = 0; kk < kSub / 16; ++kk)
+                mma_ts(o_tm, s_tm + sub * kSub + kk * 8,
+                       sdesc_add(dv, sub * (kSub * 128) + kk * 2048), kIdPV,
+                       !(fl & kFirst) || sub > 0 || kk > 0);
+              mma_commit(bar(L::kOFull + hf));
+              if (sub == 1) mma_commit(bar(L::kVEmpty + (n & 1)));
+              if (sub == 1 && last) mma_commit(bar(L::kODone + hf));
+              if (!last) {
+                if (sub == 0 && !(ok = wait(L::kKFull + ((n + 1) & 1), (n + 1) >> 1))) break;
                 tc_fence_after();
-                qk(hf, n + 1);
+                qk(n + 1, sub);
               }
             }
             if (!ok) break;
+            ++th;
             ++n;
-            if (!last) mma_commit(bar(L::kKEmpty + (n & 1)));
             if (!(ok = wait(L::kInfoFull + n % kInfo, n / kInfo))) break;
-            fl = infos[n % kInfo].flags;
             if (last) break;
+            fl = infos[n % kInfo].flags;
           }
         }
         // nothing of ours may still run on the tensor core when TMEM is freed
-        mma_commit(bar(L::kMmaDone));
-        mbar_wait_drain(bar(L::kMmaDone), 0);
+        mma_commit(bar(L::kMmaDone + hf));
+        mbar_wait_drain(bar(L::kMmaDone + hf), 0);
       }
     }
   } else {
@@ -573,7 +577,7 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
     if (threadIdx.x == 0)
       P.rec[2 * blockIdx.x] = P.rec[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
     int n = 0;              // steps of the run
-    unsigned th = 0, uh = 0;  // this half's steps and units
+    unsigned th = 0, to = 0, uh = 0;  // this half's steps, parts of them, units
     bool ok = any, more = any;
     while (more) {  // a unit
       const int steps = max(0, w.end - w.s);
@@ -637,66 +641,83 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
           const int sink_hi = P.window > 0 ? min(P.sink - 1, hi) : -1;
           for (int s = 0; s < steps; ++s) {
             const int ns = n + s;
-            // The scores first: a half that had no part in the units before may be more
-            // than kInfo steps ahead, where the description's barrier is still two phases
-            // back and would pass at once. Once the scores are there, so is it.
-            ok = mbar_wait(bar(L::kSFull + hf), th & 1, abort_flag, status) &&
-                 mbar_wait(bar(L::kInfoFull + ns % kInfo), (ns / kInfo) & 1, abort_flag, status);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            ++th;
-            tc_fence_after();
-            const int key0 = infos[ns % kInfo].key0, fl = infos[ns % kInfo].flags;
-            const uint32_t ke4 = infos[ns % kInfo].ke, ve4 = infos[ns % kInfo].ve;
-            const int none = (fl >> 8) & 15;
-            const bool masked = none || (fl >> 16) < kBN || i_lo < 0 ||
-                                (P.causal && key0 + kBN - 1 > i_lo) ||
-                                (P.window > 0 && i_hi - key0 >= P.window);
-            uint32_t sr[kBlocks][32];
-#pragma unroll
-            for (int c = 0; c < kBlocks; ++c) tmem_ld32(s_tm + 32 * c, sr[c]);
-            tmem_wait_ld();
-            if (masked) {
-#pragma unroll
-              for (int c = 0; c < kBlocks; ++c) {
-                const int k = key0 + 32 * c;
-                uint32_t vis = col_bits(lo - k, hi - k) | col_bits(-k, sink_hi - k);
-                if ((none >> c) & 1) vis = 0;
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!((vis >> j) & 1u)) sr[c][j] = __float_as_uint(-INFINITY);
+            Info inf{};
+            bool masked = false;
+#pragma unroll 1
+            for (int sub = 0; sub < 2; ++sub, ++to) {
+              // The scores first: a half that had no part in the units before may be more
+              // than kInfo steps ahead, where the description's barrier is still two phases
+              // back and would pass at once. Once the scores are there, so is it.
+              ok = mbar_wait(bar(L::kSFull + 2 * hf + sub), th & 1, abort_flag, status) &&
+                   (sub == 1 || mbar_wait(bar(L::kInfoFull + ns % kInfo), (ns / kInfo) & 1,
+                                          abort_flag, status));
+              if (!(ok = __all_sync(0xffffffffu, ok))) break;
+              tc_fence_after();
+              uint32_t sr[2][32];
+              tmem_ld32(s_tm + sub * kSub, sr[0]);
+              tmem_ld32(s_tm + sub * kSub + 32, sr[1]);
+              if (sub == 0) {
+                const volatile Info* x = infos + ns % kInfo;
+                inf.key0 = x->key0;
+                inf.flags = x->flags;
+                inf.ke = x->ke;
+                inf.ve = x->ve;
+                masked = (inf.flags & 0xf00) || (inf.flags >> 16) < kBN || i_lo < 0 ||
+                         (P.causal && inf.key0 + kBN - 1 > i_lo) ||
+                         (P.window > 0 && i_hi - inf.key0 >= P.window);
+              } else {
+                inf.ke >>= 16;
+                inf.ve >>= 16;
               }
-            }
-            float mul[kBlocks], ve[kBlocks], mx = -INFINITY;
+              float mul[2], ev[2], mx = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < kBlocks; ++c) {
-              mul[c] = row_mul * exp2i(static_cast<int8_t>(ke4 >> (8 * c)));
-              ve[c] = static_cast<float>(static_cast<int8_t>(ve4 >> (8 * c)));
-              float a[4];
+              for (int c = 0; c < 2; ++c) {
+                mul[c] = row_mul * exp2i(static_cast<int8_t>(inf.ke >> (8 * c)));
+                ev[c] = static_cast<float>(static_cast<int8_t>(inf.ve >> (8 * c)));
+              }
+              tmem_wait_ld();
+              if (masked) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) a[j] = __uint_as_float(sr[c][j]);
+                for (int c = 0; c < 2; ++c) {
+                  const int k = inf.key0 + sub * kSub + 32 * c;
+                  uint32_t vis = col_bits(lo - k, hi - k) | col_bits(-k, sink_hi - k);
+                  if ((inf.flags >> (8 + 2 * sub + c)) & 1) vis = 0;
 #pragma unroll
-              for (int j = 4; j < 32; ++j) a[j & 3] = fmaxf(a[j & 3], __uint_as_float(sr[c][j]));
-              mx = fmaxf(mx, fmaf(mul[c], fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), ve[c]));
-            }
-            // the reference moves when p would leave fp16's range
-            const bool need = mx > m_run + kAbove;
-            float alpha = 1.f;
-            if (need) {
-              const float x = mx - kBelow;
-              alpha = m_run == -INFINITY ? 0.f : ex2(m_run - x);
-              m_run = x;
-              l_run *= alpha;
-            }
-            const float msub = m_run == -INFINITY ? 0.f : m_run;
+                  for (int j = 0; j < 32; ++j)
+                    if (!((vis >> j) & 1u)) sr[c][j] = __float_as_uint(-INFINITY);
+                }
+              }
 #pragma unroll
-            for (int hp = 0; hp < 2; ++hp) {  // P in two parts of 64 keys
+              for (int c = 0; c < 2; ++c) {
+                float a[4];
 #pragma unroll
-              for (int cc = 0; cc < 2; ++cc) {
-                uint32_t pk[16];
-                const int c = 2 * hp + cc;
-                const uint64_t mul2 = f2_pack(mul[c], mul[c]);
-                const uint64_t add2 = f2_pack(ve[c] - msub, ve[c] - msub);
+                for (int j = 0; j < 4; ++j) a[j] = __uint_as_float(sr[c][j]);
+#pragma unroll
+                for (int j = 4; j < 28; j += 8)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    a[e] = fmaxf(fmaxf(a[e], __uint_as_float(sr[c][j + e])),
+                                 __uint_as_float(sr[c][j + 4 + e]));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[e] = fmaxf(a[e], __uint_as_float(sr[c][28 + e]));
+                mx = fmaxf(mx, fmaf(mul[c], fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), ev[c]));
+              }
+              // the reference moves when p would leave fp16's range
+              const bool need = mx > m_run + kAbove;
+              float alpha = 1.f;
+              if (need) {
+                const float x = mx - kBelow;
+                alpha = m_run == -INFINITY ? 0.f : ex2(m_run - x);
+                m_run = x;
+                l_run *= alpha;
+              }
+              const float msub = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float a = ev[c] - msub;
+                const uint64_t mul2 = f2_pack(mul[c], mul[c]), add2 = f2_pack(a, a);
                 uint64_t ls[2] = {0, 0};
+                uint32_t pk[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                   float x0, x1;
@@ -710,13 +731,17 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
                 f2_unpack(ls[0], a0, a1);
                 f2_unpack(ls[1], b0, b1);
                 l_run = fmaf((a0 + a1) + (b0 + b1),
-                             exp2i(-static_cast<int8_t>(ve4 >> (8 * c))), l_run);
-                tmem_st16(s_tm + 16 * c, pk);
+                             exp2i(-static_cast<int8_t>(inf.ve >> (8 * c))), l_run);
+                tmem_st16(s_tm + sub * kSub + 16 * c, pk);
               }
-              // O holds the steps before (complete: these scores' commit tracks every
-              // earlier product); it follows the reference before P V adds to it
-              if (hp == 0 && __any_sync(0xffffffffu, need && s > 0)) {
-#pragma unroll
+              // O holds the keys before; it follows the reference before P V adds to it.
+              // (The P V before the last one has completed, as these scores came behind it:
+              // the phase waited for is the next to end.)
+              if (__any_sync(0xffffffffu, need && (s > 0 || sub > 0))) {
+                ok = mbar_wait(bar(L::kOFull + hf), (to - 1) & 1, abort_flag, status);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+#pragma unroll 1
                 for (int oc = 0; oc < D / 32; ++oc) {
                   uint32_t o[32];
                   tmem_ld32(o_tm + 32 * oc, o);
@@ -730,11 +755,13 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(bar((hp == 0 ? L::kPHalf : L::kPFull) + hf));
+              if (lane == 0) mbar_arrive(bar(L::kPFull + 2 * hf + sub));
             }
+            if (!ok) break;
+            ++th;
           }
           if (!ok) break;
-          ok = mbar_wait(bar(L::kOFull + hf), uh & 1, abort_flag, status);
+          ok = mbar_wait(bar(L::kODone + hf), uh & 1, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           ++uh;
           tc_fence_after();
@@ -742,7 +769,7 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
         // ----------------------------------------------------------- the end
         const bool none = l_run == 0.f;  // no visible key (a NaN score makes it NaN)
         const float inv = none ? 0.f : 1.f / l_run;
-#pragma unroll
+#pragma unroll 1
         for (int oc = 0; oc < D / 32; ++oc) {
           uint32_t o[32];
           if (steps > 0) {
