@@ -785,12 +785,11 @@ def rope_table(positions: int, rotary_dim: int, *, base: float = 10000.0, scale:
 
 def _rope_args(table, like) -> Tuple[int, int, int]:
     """(pointer, rows, rotary_dim) of a table."""
-    if table is None:
-        return 0, 0, 0
-    if table.dim() != 2:
+    shape = table.shape
+    if len(shape) != 2:
         raise ValueError("the table of a rotation must be [positions, rotary_dim]")
-    _require(table, "rope", _F32, table.shape, like.get_device(), like)
-    return table.data_ptr(), table.shape[0], table.shape[1]
+    _require(table, "rope", _F32, shape, like.get_device(), like)
+    return table.data_ptr(), *shape
 
 
 def rope(x: torch.Tensor, table: torch.Tensor, *, interleaved=False, inverse=False,
@@ -870,16 +869,21 @@ def _kv8_struct(cache: KV8Cache):
     """(C struct's bytes, device index, B, Hkv, capacity, D) of a cache whose
     tensors fit together, else ValueError."""
     k, ke, v, ve, table, lens = cache
-    shape, ts = k.shape, table.shape
-    if len(shape) != 4 or len(ts) != 2:
-        raise ValueError("cache.k must be [pages, Hkv, page size, D], page_table [B, max pages]")
-    n, H, ps, D = shape
-    B, mp = ts
-    at = k.get_device()
+    shape, ts, at = k.shape, table.shape, k.get_device()
+    try:
+        (n, H, ps, D), (B, mp) = shape, ts
+    except ValueError:
+        raise ValueError("cache.k must be [pages, Hkv, page size, D], page_table [B, max pages]") \
+            from None
     es = (n, H, ps // 32)
-    if not (_fits(k, _U8, shape, at) and _fits(ke, _I8, es, at) and _fits(v, _U8, shape, at)
-            and _fits(ve, _I8, es, at) and _fits(table, _I32, ts, at)
-            and _fits(lens, _I32, (B,), at)):
+    # (_fits of each, spelled out: a decoding step's helpers run for microseconds)
+    if not (k.dtype is _U8 and v.dtype is _U8 and ke.dtype is _I8 and ve.dtype is _I8
+            and table.dtype is _I32 and lens.dtype is _I32 and v.shape == shape
+            and ke.shape == es and ve.shape == es and lens.shape == (B,)
+            and at == v.get_device() == ke.get_device() == ve.get_device() == table.get_device()
+            == lens.get_device() and k.is_contiguous() and v.is_contiguous()
+            and ke.is_contiguous() and ve.is_contiguous() and table.is_contiguous()
+            and lens.is_contiguous()):
         _need(k, "cache.k", _U8, shape, k.device)
         _need(v, "cache.v", _U8, shape, k.device)
         _need(ke, "cache.k_exp", _I8, es, k.device)
@@ -909,42 +913,49 @@ def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, *, q=None, q_o
                               positions=positions, cu_seqlens=cu_seqlens,
                               seq_lens_out=seq_lens_out)
     s, at, B, H, cap, D = _kv8_struct(cache)
-    packed = cu_seqlens is not None
-    dt = k.dtype
-    if dt not in DTYPE:
+    dt, shape = k.dtype, k.shape
+    code = DTYPE.get(dt)
+    if code is None:
         raise ValueError("keys and values must be bf16 or fp32")
-    if k.dim() != (3 if packed else 4):
-        raise ValueError("k must be [B, T, Hkv, D], packed [T, Hkv, D]")
-    lead = tuple(k.shape[:-2])
-    if not packed and lead[0] != B:
-        raise ValueError(f"k must have the cache's {B} sequences, got {lead[0]}")
-    T = lead[-1]
-    _require(k, "k", dt, lead + (H, D), at, cache.k)
-    _require(v, "v", dt, lead + (H, D), at, cache.k)
-    if packed:
+    cu = None
+    if cu_seqlens is not None:
+        if len(shape) != 3:
+            raise ValueError("k must be packed [T, Hkv, D]")
+        T, lead = shape[0], shape[:1]
         _require(cu_seqlens, "cu_seqlens", _I32, (B + 1,), at, cache.k)
-    Hq = 0
+        cu = cu_seqlens.data_ptr()
+    else:
+        if len(shape) != 4 or shape[0] != B:
+            raise ValueError(f"k must be [{B}, T, Hkv, D] (the cache has {B} sequences)")
+        T, lead = shape[1], shape[:2]
+    _require(k, "k", dt, (*lead, H, D), at, cache.k)
+    _require(v, "v", dt, shape, at, cache.k)
+    Hq, qp, qo = 0, None, None
     if q is not None:
         Hq = q.shape[-2]
-        _require(q, "q", dt, lead + (Hq, D), at, cache.k)
+        _require(q, "q", dt, (*lead, Hq, D), at, cache.k)
         if q_out is None:
             q_out = torch.empty_like(q)
-        else:
-            _require(q_out, "q_out", dt, lead + (Hq, D), at, cache.k)
+        elif q_out is not q:
+            _require(q_out, "q_out", dt, (*lead, Hq, D), at, cache.k)
+        if T:
+            qp, qo = q.data_ptr() or None, q_out.data_ptr() or None
     elif q_out is not None:
         raise ValueError("q_out needs a q")
-    ptr, rows, R = _rope_args(rope, cache.k)
-    if rope is not None and positions is None and rows < cap:
-        raise ValueError(f"the table has {rows} positions, the cache {cap} rows")
+    ptr, rows, R = None, 0, 0
+    if rope is not None:
+        ptr, rows, R = _rope_args(rope, cache.k)
+        if positions is None and rows < cap:
+            raise ValueError(f"the table has {rows} positions, the cache {cap} rows")
     if positions is not None:
         _require(positions, "positions", _I32, lead, at, cache.k)
+        positions = positions.data_ptr()
     lens = cache.seq_lens
     if seq_lens_out is not None:
         lens = seq_lens_out
         _require(lens, "seq_lens_out", _I32, (B,), at, cache.k)
-    _call(_lib.load().usp_kv8_append, at, None, s, _p(k), _p(v), _p(q), _p(q_out), Hq, ptr or None,
-          rows, R, 1 if interleaved else 0, _p(positions),
-          cu_seqlens.data_ptr() if packed else None, T, DTYPE[dt], lens.data_ptr())
+    _call(_lib.load().usp_kv8_append, at, None, s, k.data_ptr(), v.data_ptr(), qp, qo, Hq, ptr,
+          rows, R, 1 if interleaved else 0, positions, cu, T, code, lens.data_ptr())
     return lens if q is None else (lens, q_out)
 
 
@@ -980,24 +991,29 @@ def attn_kv8(q: torch.Tensor, cache: KV8Cache, *, causal=True, window=0, sink_to
                             cu_seqlens=cu_seqlens, max_new=max_new, softmax_scale=softmax_scale,
                             workspace=workspace)
     s, at, B, Hkv, _, D = _kv8_struct(cache)
-    packed = cu_seqlens is not None
-    if q.dim() != (3 if packed else 4):
-        raise ValueError("q must be [B, T, Hq, D], packed [T, Hq, D]")
-    lead, Hq = tuple(q.shape[:-2]), q.shape[-2]
-    if not packed and lead[0] != B:
-        raise ValueError(f"q must have the cache's {B} sequences, got {lead[0]}")
-    T = lead[-1]
-    _require(q, "q", torch.bfloat16, lead + (Hq, D), at, cache.k)
-    if packed:
+    shape = q.shape
+    cu, packed = None, 0
+    if cu_seqlens is not None:
+        if len(shape) != 3:
+            raise ValueError("q must be packed [T, Hq, D]")
+        T, Hq, _ = shape
         _require(cu_seqlens, "cu_seqlens", _I32, (B + 1,), at, cache.k)
+        cu, packed = cu_seqlens.data_ptr(), 1
+        want, rows = (T, Hq, D), (T, Hq)
+    else:
+        if len(shape) != 4 or shape[0] != B:
+            raise ValueError(f"q must be [{B}, T, Hq, D] (the cache has {B} sequences)")
+        _, T, Hq, _ = shape
+        want, rows = (B, T, Hq, D), (B, T, Hq)
+    _require(q, "q", torch.bfloat16, want, at, cache.k)
     lib = _lib.load()
     dev = q.device
     out = torch.empty_like(q)
-    lse = torch.empty(lead + (Hq,), dtype=_F32, device=dev)
-    need = lib.usp_attn_kv8_workspace_size(B, T, max_new, 1 if packed else 0, Hq, Hkv, D)
+    lse = torch.empty(rows, dtype=_F32, device=dev)
+    need = lib.usp_attn_kv8_workspace_size(B, T, max_new, packed, Hq, Hkv, D)
     ws = torch.empty(need, dtype=_U8, device=dev) if workspace is None else \
         _use_workspace(workspace, need, dev)[0]
-    _call(lib.usp_attn_kv8, at, None, s, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
-          cu_seqlens.data_ptr() if packed else None, T, max_new, Hq, softmax_scale,
-          1 if causal else 0, window, sink_tokens, 0, ws.data_ptr(), ws.numel())
+    _call(lib.usp_attn_kv8, at, None, s, q.data_ptr(), out.data_ptr(), lse.data_ptr(), cu, T,
+          max_new, Hq, softmax_scale, 1 if causal else 0, window, sink_tokens, 0, ws.data_ptr(),
+          need if workspace is None else ws.numel())
     return out, lse
