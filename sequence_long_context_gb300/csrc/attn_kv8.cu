@@ -63,7 +63,9 @@ constexpr int kSms = 152;
 constexpr int kWarps = 8;       // of a CTA, one CTA per SM
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRuns = kSms * kWarps;
-constexpr int kUnitCost = 3;    // of a unit's end, in steps
+// Of a unit's end, in steps (4 x 32K keys and 12 rows: 41.7 us with 1, 40.2 with 3, 38.8
+// with 5, 39.5 with 8; 512 units of 33 steps: 30.9, 30.0, 30.0, 30.7).
+constexpr int kUnitCost = 5;
 constexpr float kBelow = 7.f, kAbove = 15.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -232,6 +234,7 @@ attn_kv8_kernel(const Params P, const __grid_constant__ CUtensorMap tm_k,
     }
   }
   __syncthreads();  // the only one: no warp waits for another from here on
+  grid_dependency_wait();  // (this kernel's launch overlaps the end of what came before it)
 
   // ------------------------------------------------------- this warp's run
   const unsigned run = warp * kSms + blockIdx.x;
@@ -277,25 +280,40 @@ attn_kv8_kernel(const Params P, const __grid_constant__ CUtensorMap tm_k,
   // ------------------------------------------------- copies, kStages ahead
   Walk pre = cur;
   bool more = true;
-  unsigned issued = 0, known = 0, used = 0;  // steps: copied, with page and exponents, taken
+  unsigned issued = 0, known = 0, used = 0;  // steps: copied, with a page, taken
   const uint32_t ring = sbase + warp * L::kWarpBytes;
+  // Exponents of the steps whose pages came last, on their way: nothing needs them before
+  // the keys are there, so the copies do not wait for them.
+  unsigned exps_at = 0;
+  bool exps_due = false;
+  int ke = 0, ve = 0;
+  auto put_exps = [&]() {
+    meta[(exps_at + lane) & (kMeta - 1)].y = (clamp_exp(ke) & 0xffff) | (clamp_exp(ve) << 16);
+    __syncwarp();
+    exps_due = false;
+  };
   auto issue = [&]() {
     if (issued == known) {
+      if (exps_due) put_exps();
       // pages and exponents of the unit's next 32 steps, one per lane
       const int s = pre.s + lane;
-      const int h = pre.hr / pre.q.nrb;
-      int2 x = make_int2(-1, 0);
+      int page = -1;
+      ke = ve = 0;
       if (s < pre.end) {
         const int row = (s < pre.q.sinks ? s : s + pre.q.skip) * kStep;
-        const int page = page_of(P.c, pre.b, row);
+        page = page_of(P.c, pre.b, row);
         if (page >= 0) {
-          const long long blk = (head_rows(P.c, page, h) + (row & (P.c.ps - 1))) / kBlock;
-          x = make_int2(page, (clamp_exp(P.c.ke[blk]) & 0xffff) | (clamp_exp(P.c.ve[blk]) << 16));
+          const long long blk =
+              (head_rows(P.c, page, pre.hr / pre.q.nrb) + (row & (P.c.ps - 1))) / kBlock;
+          ke = P.c.ke[blk];
+          ve = P.c.ve[blk];
         }
       }
       // (the entries of the last kStages steps and of these 32 are in use: kMeta has room)
-      meta[(known + lane) & (kMeta - 1)] = x;
+      meta[(known + lane) & (kMeta - 1)].x = page;
       __syncwarp();
+      exps_at = known;
+      exps_due = true;
       known += min(32, pre.end - pre.s);
     }
     if (lane == 0) {
@@ -382,6 +400,7 @@ attn_kv8_kernel(const Params P, const __grid_constant__ CUtensorMap tm_k,
     }
     for (int s = cur.s; s < cur.end; ++s) {
       const int st = used % kStages;
+      if (exps_due) put_exps();
       ok = mbar_wait(full(st), (used / kStages) & 1, abort_flag, &g_attn_kv8_status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const int2 mt = meta[used & (kMeta - 1)];
@@ -573,20 +592,22 @@ __device__ __forceinline__ int2 span_of(const Params& P, int unit) {
   return make_int2(max(s.x, 0), min(s.y, P.slots - 1));
 }
 
-// Block x < units * 8 NT: a row of a unit, whose partials (consecutive slots) are
-// merged by D / 4 threads for every kParts-th. Blocks behind those (packed): zeros
-// for the tokens outside the sequences. Launched while the kernel above still
-// runs; nothing it writes is read before the wait.
-template <int D, int NT>
+// D / 4 threads take every kParts-th partial of a row (they stand in consecutive slots);
+// a block kMaxParts / kParts rows. Blocks behind the rows (packed): zeros for the
+// tokens outside the sequences. Launched while the kernel above still runs; nothing it
+// writes is read before the wait.
+template <int D>
+constexpr int kMaxParts = kMergeThreads / (D / 4);
+template <int D, int NT, int kParts>
 __global__ void __launch_bounds__(kMergeThreads) attn_kv8_merge_kernel(const Params P, int pads) {
-  constexpr int kRows = 8 * NT, kLanes = D / 4, kParts = kMergeThreads / kLanes;
-  __shared__ float4 s_o[kParts][kLanes];
+  constexpr int kRows = 8 * NT, kLanes = D / 4, kPer = kMaxParts<D> / kParts;
+  __shared__ float4 s_o[kParts > 1 ? kParts : 1][kLanes];
   __shared__ float2 s_ml[kParts];
-  const int units = P.c.B * P.c.H * P.nrb;
-  if ((int)blockIdx.x >= units * kRows) {
+  const int rows = P.c.B * P.c.H * P.nrb * kRows, blocks = (rows + kPer - 1) / kPer;
+  if ((int)blockIdx.x >= blocks) {
     const int e0 = min(max(__ldg(P.cu), 0), P.T), e1 = max(e0, min(max(__ldg(P.cu + P.c.B), 0), P.T));
     grid_dependency_wait();
-    for (int i = blockIdx.x - units * kRows; i < e0 + P.T - e1; i += pads) {
+    for (int i = blockIdx.x - blocks; i < e0 + P.T - e1; i += pads) {
       const long long tok = i < e0 ? i : e1 + (i - e0);
       uint2* r = reinterpret_cast<uint2*>(P.out + tok * P.Hq * D);
       for (int u = threadIdx.x; u < P.Hq * D / 4; u += kMergeThreads) r[u] = make_uint2(0, 0);
@@ -594,7 +615,10 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv8_merge_kernel(const Par
     }
     return;
   }
-  const int unit = blockIdx.x / kRows, r = blockIdx.x % kRows;  // r: row within the block
+  const int group = threadIdx.x / kLanes, d = threadIdx.x - group * kLanes;
+  const int part = group % kParts, x = blockIdx.x * kPer + group / kParts;
+  if (x >= rows) return;  // (kParts > 1: all of a block's threads, kPer being 1)
+  const int unit = x / kRows, r = x % kRows;  // r: row within the block
   const int bh = unit / P.nrb, rb = unit - bh * P.nrb;
   const int b = bh / P.c.H, h = bh - b * P.c.H;
   const int row = rb * kRows + r;
@@ -603,49 +627,50 @@ __global__ void __launch_bounds__(kMergeThreads) attn_kv8_merge_kernel(const Par
   int2 span = make_int2(0, -1);  // no steps, no partials
   grid_dependency_wait();
   if (q.steps > 0) span = span_of(P, unit);
-  const int part = threadIdx.x / kLanes, d = threadIdx.x - part * kLanes;
   float M = -INFINITY, ls = 0.f;
   float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (long long s = span.x + part; s <= span.y; s += kParts) {
     const float2 a = P.ml_part[s * kRows + r];
-    const float4 x = reinterpret_cast<const float4*>(P.o_part + (s * kRows + r) * D)[d];
+    const float4 y = reinterpret_cast<const float4*>(P.o_part + (s * kRows + r) * D)[d];
     const float Mn = fmaxf(M, a.x);
     const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn);
     const float f1 = a.x == -INFINITY ? 0.f : ex2(a.x - Mn);
-    os.x = os.x * f0 + x.x * f1;
-    os.y = os.y * f0 + x.y * f1;
-    os.z = os.z * f0 + x.z * f1;
-    os.w = os.w * f0 + x.w * f1;
+    os.x = os.x * f0 + y.x * f1;
+    os.y = os.y * f0 + y.y * f1;
+    os.z = os.z * f0 + y.z * f1;
+    os.w = os.w * f0 + y.w * f1;
     ls = ls * f0 + a.y * f1;
     M = Mn;
   }
-  s_o[part][d] = os;
-  if (d == 0) s_ml[part] = make_float2(M, ls);
-  __syncthreads();
-  if (part != 0) return;
-  float Mt = -INFINITY;
+  if constexpr (kParts > 1) {
+    s_o[part][d] = os;
+    if (d == 0) s_ml[part] = make_float2(M, ls);
+    __syncthreads();
+    if (part != 0) return;
+    M = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kParts; ++i) Mt = fmaxf(Mt, s_ml[i].x);
-  float lt = 0.f;
-  float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < kParts; ++i) M = fmaxf(M, s_ml[i].x);
+    ls = 0.f;
+    os = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < kParts; ++i) {
-    const float f = s_ml[i].x == -INFINITY ? 0.f : ex2(s_ml[i].x - Mt);
-    lt += s_ml[i].y * f;
-    ot.x += s_o[i][d].x * f;
-    ot.y += s_o[i][d].y * f;
-    ot.z += s_o[i][d].z * f;
-    ot.w += s_o[i][d].w * f;
+    for (int i = 0; i < kParts; ++i) {
+      const float f = s_ml[i].x == -INFINITY ? 0.f : ex2(s_ml[i].x - M);
+      ls += s_ml[i].y * f;
+      os.x += s_o[i][d].x * f;
+      os.y += s_o[i][d].y * f;
+      os.z += s_o[i][d].z * f;
+      os.w += s_o[i][d].w * f;
+    }
   }
   const int tok = row / P.G, hh = row - tok * P.G;
   const long long o_row = (long long)(q.first + tok) * P.Hq + h * P.G + hh;
-  const bool none = lt == 0.f;  // no visible key (a NaN score makes lt NaN)
-  const float inv = none ? 0.f : 1.f / lt;
-  if (none) ot = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool none = ls == 0.f;  // no visible key (a NaN score makes ls NaN)
+  const float inv = none ? 0.f : 1.f / ls;
+  if (none) os = make_float4(0.f, 0.f, 0.f, 0.f);
   reinterpret_cast<uint2*>(P.out + o_row * D)[d] =
-      make_uint2(pack_bf16(ot.x * inv, ot.y * inv), pack_bf16(ot.z * inv, ot.w * inv));
-  if (d == 0) P.lse[o_row] = none ? -INFINITY : (Mt + log2f(lt)) * kLn2;
+      make_uint2(pack_bf16(os.x * inv, os.y * inv), pack_bf16(os.z * inv, os.w * inv));
+  if (d == 0) P.lse[o_row] = none ? -INFINITY : (M + log2f(ls)) * kLn2;
 }
 
 // ------------------------------------------------------------------- host
@@ -679,29 +704,37 @@ usp_status_t launch_t(const Params& P, cudaStream_t st) {
   static SmemAttr attr;
   cudaError_t e = attr.set(attn_kv8_kernel<D, NT>, smem);
   if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
+  // A row's partials are merged by a block where a unit has many, else by a few threads:
+  // of units spread over kRuns warps, each has about kRuns / units + 1.
+  const long long units = (long long)P.c.B * P.c.H * P.nrb, rows = units * 8 * NT;
+  const bool one = units * 4 > kRuns;
+  const int per = one ? kMaxParts<D> : 1;
   const int pads = P.cu ? 64 : 0;
-  const long long blocks = (long long)P.c.B * P.c.H * P.nrb * 8 * NT + pads;
+  const long long blocks = (rows + per - 1) / per + pads;
   if (blocks > 0x7fffffffLL) return USP_ERR_UNSUPPORTED;
-  {
-    ProfScope ps(st, "attn_kv8");
-    attn_kv8_kernel<D, NT><<<kSms, kThreads, smem, st>>>(P, mk, mv);
-  }
-  note_launch();
-  usp_status_t r = check_launch();
-  if (r != USP_OK) return r;
-  // the merge's launch and set-up overlap the end of the kernel before it
+  // each kernel's launch and set-up overlap the end of the one before it
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
+  cfg.gridDim = dim3(kSms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   {
+    ProfScope ps(st, "attn_kv8");
+    e = cudaLaunchKernelEx(&cfg, attn_kv8_kernel<D, NT>, P, mk, mv);
+  }
+  if (e == cudaSuccess) {
+    note_launch();
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = 0;
     ProfScope ps(st, "attn_kv8_merge");
-    e = cudaLaunchKernelEx(&cfg, attn_kv8_merge_kernel<D, NT>, P, pads);
+    e = one ? cudaLaunchKernelEx(&cfg, attn_kv8_merge_kernel<D, NT, 1>, P, pads)
+            : cudaLaunchKernelEx(&cfg, attn_kv8_merge_kernel<D, NT, kMaxParts<D>>, P, pads);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();

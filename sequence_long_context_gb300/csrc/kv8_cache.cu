@@ -5,9 +5,11 @@
 // maximum is known before its first code is written. A CTA of four warps takes
 // one block of a sequence: each warp eight rows, each lane one item (two vectors
 // of 16 bytes of the input) of a row, in kPass passes. Cos and sin of a lane's
-// rows stay in registers while the CTA passes over the heads of K, V and Q, and
-// the next head's rows are loaded before the present one's are used. A prompt's
-// blocks are shared out among CTAs by heads too where there are few.
+// rows stay in registers while the CTA passes over the heads of K and V, and the next
+// head's rows are loaded before the present one's are used. A prompt's blocks are
+// shared out among CTAs by heads too where there are few. Queries are a copy with a
+// rotation: warps of other CTAs of the same launch take a token each, eight rows in
+// flight (with the keys' and values' blocks they were 134 us for 32K tokens).
 //
 // Rows that the block held before the call keep their codes unless the exponent
 // rises; then they are rounded once more. Every block belongs to one CTA for a
@@ -31,6 +33,7 @@ struct AppendParams {
   int splits;     // CTAs that share a block's heads
   int slots;      // blocks per sequence (dense), or in all (packed)
   int seq_form;   // a cluster of `splits` CTAs takes a whole sequence
+  int kv_blocks;  // CTAs behind these rotate queries (other form)
 };
 
 // Tokens of sequence b: the first and how many. Boundaries are trusted, but no
@@ -106,56 +109,38 @@ __device__ __forceinline__ void append_block(const AppendParams& P, int b, int b
     if (fresh[p] && it.f >= 0)
       load_turn(A.rope, it, A.positions ? __ldg(A.positions + token[p]) : base + row[p], c[p], s[p]);
   }
-  const int H = A.c.H, n_kv = page >= 0 ? 2 * H : 0;
-  // jobs: K heads, V heads, Q heads; this CTA takes every splits-th
-  const int jobs = 2 * H + (A.q ? A.Hq : 0);
-  auto next_job = [&](int j) {
-    j += P.splits;
-    return j < 2 * H && n_kv == 0 ? j + (2 * H - j + P.splits - 1) / P.splits * P.splits : j;
-  };
+  const int H = A.c.H;
+  if (page < 0) return;
   uint4 xa[kPass], xb[kPass];
-  auto load = [&](int j) {
-    const bool isq = j >= 2 * H;
-    const T* src = static_cast<const T*>(isq ? A.q : j < H ? A.k : A.v);
-    const int heads = isq ? A.Hq : H, h = isq ? j - 2 * H : j < H ? j : j - H;
+  auto load = [&](int j) {  // K heads, then V heads
+    const T* src = static_cast<const T*>(j < H ? A.k : A.v);
+    const int h = j < H ? j : j - H;
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
       xa[p] = xb[p] = make_uint4(0, 0, 0, 0);
       if (fresh[p]) {
-        const T* r = src + (token[p] * heads + h) * D;
+        const T* r = src + (token[p] * H + h) * D;
         // V is not rotated: its items are the two vectors of a rotated one all the same
         xa[p] = *reinterpret_cast<const uint4*>(r + it.a);
         xb[p] = *reinterpret_cast<const uint4*>(r + it.b);
       }
     }
   };
-  int j = next_job(split - P.splits);
-  if (j < jobs) load(j);
-  for (; j < jobs; j = next_job(j)) {
-    const bool isq = j >= 2 * H, isk = j < H;
+  int j = split;
+  if (j < 2 * H) load(j);
+  for (; j < 2 * H; j += P.splits) {
+    const bool isk = j < H;
     float fa[kPass][V], fb[kPass][V];
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
       unpack(xa[p], fa[p]);
       unpack(xb[p], fb[p]);
     }
-    const int after = next_job(j);
-    // (q may be q_out: the rows loaded ahead are another head's)
-    if (after < jobs) load(after);
-    if (isq || isk) {
+    if (j + P.splits < 2 * H) load(j + P.splits);
+    if (isk) {
 #pragma unroll
       for (int p = 0; p < kPass; ++p)
         if (fresh[p]) rotate(it, A.rope.inter != 0, c[p], s[p], fa[p], fb[p]);
-    }
-    if (isq) {
-#pragma unroll
-      for (int p = 0; p < kPass; ++p)
-        if (fresh[p]) {
-          T* r = static_cast<T*>(A.q_out) + (token[p] * A.Hq + (j - 2 * H)) * D;
-          *reinterpret_cast<uint4*>(r + it.a) = pack(fa[p]);
-          *reinterpret_cast<uint4*>(r + it.b) = pack(fb[p]);
-        }
-      continue;
     }
     const int h = isk ? j : j - H;
     int8_t* ex = (isk ? A.c.ke : A.c.ve) +
@@ -202,6 +187,43 @@ __device__ __forceinline__ void append_block(const AppendParams& P, int b, int b
   }
 }
 
+// Rotates `chunk` heads of a token from head h0 on, by a warp.
+template <typename T, int D>
+__device__ __forceinline__ void rotate_q(const Kv8AppendArgs& A, long long token, int pos, int h0,
+                                         int chunk) {
+  constexpr int V = kVec<T>, kItems = D / (2 * V), kHeads = 32 / kItems, kFlight = 8;
+  const int lane = threadIdx.x & 31;
+  const Item<V> it = item_of<V>(A.rope, lane % kItems);
+  float c[V], s[V];
+  load_turn(A.rope, it, pos, c, s);
+  const T* x = static_cast<const T*>(A.q) + token * A.Hq * D;
+  T* y = static_cast<T*>(A.q_out) + token * A.Hq * D;
+  const int end = min(h0 + chunk, A.Hq);
+  for (int h = h0 + lane / kItems; h < end; h += kFlight * kHeads) {
+    uint4 a[kFlight], b[kFlight];
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i)
+      if (h + i * kHeads < end) {
+        a[i] = *reinterpret_cast<const uint4*>(x + (h + i * kHeads) * D + it.a);
+        b[i] = *reinterpret_cast<const uint4*>(x + (h + i * kHeads) * D + it.b);
+      }
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i)
+      if (h + i * kHeads < end) {
+        if (it.f >= 0) {
+          float fa[V], fb[V];
+          unpack(a[i], fa);
+          unpack(b[i], fb);
+          rotate(it, A.rope.inter != 0, c, s, fa, fb);
+          a[i] = pack(fa);
+          b[i] = pack(fb);
+        }
+        *reinterpret_cast<uint4*>(y + (h + i * kHeads) * D + it.a) = a[i];
+        *reinterpret_cast<uint4*>(y + (h + i * kHeads) * D + it.b) = b[i];
+      }
+  }
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                ::: "memory");
@@ -213,11 +235,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) 
   const Kv8AppendArgs& A = P.a;
   int turn_no = 0;
   const int split = blockIdx.x % P.splits, x = blockIdx.x / P.splits;
-  if (A.cu && A.q) {  // q of padding tokens: zeros
+  const int warp = threadIdx.x >> 5;
+  if (A.cu && A.q && (P.seq_form || (int)blockIdx.x >= P.kv_blocks)) {  // q of padding: zeros
+    const int i0 = P.seq_form ? 0 : P.kv_blocks;
     const int e0 = min(max(__ldg(A.cu), 0), A.T), e1 = min(max(__ldg(A.cu + A.c.B), 0), A.T);
     const int pad = e0 + A.T - max(e0, e1);
     const int vecs = A.Hq * D / kVec<T>;
-    for (int i = blockIdx.x; i < pad; i += gridDim.x) {
+    for (int i = blockIdx.x - i0; i < pad; i += gridDim.x - i0) {
       const long long t = i < e0 ? i : (long long)max(e0, e1) + (i - e0);
       uint4* r = reinterpret_cast<uint4*>(static_cast<T*>(A.q_out) + t * A.Hq * D);
       for (int u = threadIdx.x; u < vecs; u += kThreads) r[u] = make_uint4(0, 0, 0, 0);
@@ -232,10 +256,33 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams P) 
       for (int blk = start / kBlock; blk <= last; ++blk)
         append_block<T, D>(P, b, blk, start, tok, split, s_max, turn_no);
     }
+    if (A.q) {  // few heads of a token per warp
+      constexpr int kChunk = 32 / (D / (2 * kVec<T>));
+      const int slices = (A.Hq + kChunk - 1) / kChunk;
+      for (int i = split * kWarps + warp; i < tok.n * slices; i += P.splits * kWarps) {
+        const int t = i / slices;
+        rotate_q<T, D>(A, tok.first + t,
+                       A.positions ? __ldg(A.positions + tok.first + t) : start + t,
+                       (i - t * slices) * kChunk, kChunk);
+      }
+    }
     if (A.lens_out) {
       cluster_sync();  // every CTA of the sequence has read its length
       if (split == 0 && threadIdx.x == 0)
         A.lens_out[b] = (int)min((long long)A.c.cap, (long long)start + tok.n);
+    }
+    return;
+  }
+  if ((int)blockIdx.x >= P.kv_blocks) {  // queries: a token per warp
+    const long long tokens = A.cu ? A.T : (long long)A.c.B * A.T;
+    const long long step = (long long)(gridDim.x - P.kv_blocks) * kWarps;
+    for (long long t = (long long)(blockIdx.x - P.kv_blocks) * kWarps + warp; t < tokens; t += step) {
+      const int b = A.cu ? seg_of(A.cu, A.c.B, (int)t) : (int)(t / A.T);
+      const Tokens tok = tokens_of(A.cu, A.T, b);
+      if (t < tok.first || t >= tok.first + tok.n) continue;
+      const int pos = A.positions ? __ldg(A.positions + t)
+                                  : clamp_len(A.c.lens[b], A.c.cap) + (int)(t - tok.first);
+      rotate_q<T, D>(A, t, pos, 0, A.Hq);
     }
     return;
   }
@@ -275,7 +322,7 @@ __global__ void append_lens_kernel(const AppendParams P) {
 template <typename T, int D>
 usp_status_t launch_append(AppendParams& P, cudaStream_t st) {
   const Kv8AppendArgs& A = P.a;
-  const int jobs = 2 * A.c.H + (A.q ? A.Hq : 0);
+  const int jobs = 2 * A.c.H;
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
@@ -286,7 +333,7 @@ usp_status_t launch_append(AppendParams& P, cudaStream_t st) {
   if (P.seq_form) {
     P.splits = 1;
     while (P.splits < 8 && P.splits < jobs) P.splits *= 2;
-    blocks = A.c.B;
+    blocks = (long long)A.c.B * P.splits;
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = P.splits;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
@@ -297,8 +344,15 @@ usp_status_t launch_append(AppendParams& P, cudaStream_t st) {
     const long long want = 5LL * sm_count();  // resident CTAs
     long long n = (want + blocks - 1) / blocks;
     P.splits = (int)(n < 1 ? 1 : n > jobs ? jobs : n);
+    blocks *= P.splits;
+    if (blocks > 0x7fffffffLL) return USP_ERR_UNSUPPORTED;
+    P.kv_blocks = (int)blocks;
+    if (A.q) {
+      const long long warps = A.cu ? A.T : (long long)A.c.B * A.T;
+      const long long need = (warps + kWarps - 1) / kWarps, most = 16LL * sm_count();
+      blocks += need < most ? need : most;
+    }
   }
-  blocks *= P.splits;
   if (blocks > 0x7fffffffLL) return USP_ERR_UNSUPPORTED;
   cfg.gridDim = dim3((unsigned)blocks);
   cudaError_t e;
@@ -338,61 +392,67 @@ struct ReadParams {
 };
 constexpr int kReadThreads = 256;
 
-// A thread takes 16 channels of one row of K and of V at a time: 16 bytes of codes
-// in, 32 (64) bytes of values out, in the order of the output.
+// A thread takes as many channels of a row of K and of V as make 16 bytes of output, so
+// that a warp's loads and stores are each one run. It steps over the rows of one
+// sequence (blockIdx.y) without a division.
 template <typename T, int D>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadParams P) {
-  constexpr int kPer = D / 16;
-  const long long n = (long long)P.c.B * P.T * P.c.H * kPer;
-  const long long step = (long long)gridDim.x * kReadThreads;
-  for (long long i = (long long)blockIdx.x * kReadThreads + threadIdx.x; i < n; i += step) {
-    const int part = (int)(i % kPer);
-    const long long bth = i / kPer, bt = bth / P.c.H;
-    const int h = (int)(bth - bt * P.c.H);
-    const int b = (int)(bt / P.T), t = (int)(bt - (long long)b * P.T);
-    const long long row = (long long)(P.start ? __ldg(P.start + b) : 0) + t;
-    uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    float s[2] = {0.f, 0.f};
-    if (row >= 0 && row < clamp_len(__ldg(P.c.lens + b), P.c.cap)) {
+  constexpr int V = kVec<T>, kPer = D / V;
+  const int b = blockIdx.y;
+  const unsigned per_row = P.c.H * kPer;  // of all heads
+  const unsigned step = gridDim.x * kReadThreads, step_t = step / per_row, step_x = step % per_row;
+  const unsigned i0 = blockIdx.x * kReadThreads + threadIdx.x;
+  unsigned t = i0 / per_row, x = i0 % per_row;
+  const int first = P.start ? __ldg(P.start + b) : 0;
+  const int len = clamp_len(__ldg(P.c.lens + b), P.c.cap);
+  T* k = static_cast<T*>(P.k) + (long long)b * P.T * P.c.H * D;
+  T* v = static_cast<T*>(P.v) + (long long)b * P.T * P.c.H * D;
+  for (; t < (unsigned)P.T; t += step_t, x += step_x) {
+    if (x >= per_row) {
+      x -= per_row;
+      if (++t >= (unsigned)P.T) break;
+    }
+    const long long row = (long long)first + t;
+    uint32_t kw[V / 4], vw[V / 4];
+    float ks = 0.f, vs = 0.f;
+#pragma unroll
+    for (int e = 0; e < V / 4; ++e) kw[e] = vw[e] = 0;
+    if (row >= 0 && row < len) {
       const int page = page_of(P.c, b, (int)row);
       if (page >= 0) {
-        const long long at = head_rows(P.c, page, h) + ((int)row & (P.c.ps - 1));
-        x[0] = *reinterpret_cast<const uint4*>(P.c.kc + at * D + part * 16);
-        x[1] = *reinterpret_cast<const uint4*>(P.c.vc + at * D + part * 16);
-        s[0] = exp2i(clamp_exp(P.c.ke[at / kBlock]));
-        s[1] = exp2i(clamp_exp(P.c.ve[at / kBlock]));
+        const long long at = head_rows(P.c, page, x / kPer) + ((int)row & (P.c.ps - 1));
+        load_codes(P.c.kc + at * D + (x % kPer) * V, kw);
+        load_codes(P.c.vc + at * D + (x % kPer) * V, vw);
+        ks = exp2i(clamp_exp(P.c.ke[at / kBlock]));
+        vs = exp2i(clamp_exp(P.c.ve[at / kBlock]));
       }
     }
+    float kf[V], vf[V];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float f[16];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 y = e4m3x2_to_float2(e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu);
-        f[2 * e] = y.x * s[u];
-        f[2 * e + 1] = y.y * s[u];
-      }
-      constexpr int V = kVec<T>;
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(u ? P.v : P.k) + bth * D + part * 16);
-#pragma unroll
-      for (int e = 0; e < 16 / V; ++e) {
-        float g[V];
-#pragma unroll
-        for (int m = 0; m < V; ++m) g[m] = f[e * V + m];
-        dst[e] = pack(g);
-      }
+    for (int e = 0; e < V / 2; ++e) {
+      const float2 a = e4m3x2_to_float2(e & 1 ? kw[e / 2] >> 16 : kw[e / 2] & 0xffffu);
+      const float2 c = e4m3x2_to_float2(e & 1 ? vw[e / 2] >> 16 : vw[e / 2] & 0xffffu);
+      kf[2 * e] = a.x * ks;
+      kf[2 * e + 1] = a.y * ks;
+      vf[2 * e] = c.x * vs;
+      vf[2 * e + 1] = c.y * vs;
     }
+    const long long at = ((long long)t * per_row + x) * V;
+    *reinterpret_cast<uint4*>(k + at) = pack(kf);
+    *reinterpret_cast<uint4*>(v + at) = pack(vf);
   }
 }
 
 template <typename T, int D>
 usp_status_t launch_read(const ReadParams& P, cudaStream_t st) {
-  const long long n = (long long)P.c.B * P.T * P.c.H * (D / 16);
-  const long long need = (n + kReadThreads - 1) / kReadThreads, cap = 8LL * sm_count();
+  const long long n = (long long)P.T * P.c.H * (D / kVec<T>);  // of a sequence
+  long long cap = (16LL * sm_count() + P.c.B - 1) / P.c.B;
+  // (a thread's first row and column in 32 bits)
+  if (cap > 0x7fffffff / kReadThreads / 2) cap = 0x7fffffff / kReadThreads / 2;
+  const long long need = (n + kReadThreads - 1) / kReadThreads;
   {
     ProfScope ps(st, "kv8_read");
-    read_kernel<T, D><<<(unsigned)(need < cap ? need : cap), kReadThreads, 0, st>>>(P);
+    read_kernel<T, D><<<dim3((unsigned)(need < cap ? need : cap), P.c.B), kReadThreads, 0, st>>>(P);
   }
   note_launch();
   return check_launch();
