@@ -693,8 +693,16 @@ Ws layout(int B, int max_new, int Hq, int Hkv, int D) {
   return w;
 }
 
-// Rows per KV head from which the tcgen05 kernel takes over.
-bool many_rows(int Hq, int Hkv, int max_new) { return (long long)(Hq / Hkv) * max_new > 16; }
+// Which kernel: this one reads the keys once per 16 rows, the tcgen05 kernel (its 128
+// rows cost the same however many there are) once per 128 or 256. 4 x 64K keys, 8 KV heads:
+// 32 rows 166 us here and 215 there, 48 rows 243 and 217. Where the keys are few the
+// ends count: 16 x 1024 keys, 32 rows 29 us and 39, 64 rows 35 and 41, 128 rows 45
+// and 44; 8192 keys of one sequence, 64 rows 26 and 43. `rows` of a KV head; `keys` of all
+// heads and sequences that the cache has room for.
+constexpr long long kRowsHere = 32, kRowsFewKeys = 64, kFewKeys = 1 << 18;
+bool many_rows(long long rows, long long keys) {
+  return rows > (keys <= kFewKeys ? kRowsFewKeys : kRowsHere);
+}
 
 template <int D, int NT>
 usp_status_t launch_t(const Params& P, cudaStream_t st) {
@@ -746,13 +754,17 @@ usp_status_t launch_t(const Params& P, cudaStream_t st) {
 
 }  // namespace
 
-size_t attn_kv8_workspace(int B, int T, int max_new, int packed, int Hq, int Hkv, int D) {
-  if (many_rows(Hq, Hkv, max_new)) return attn_kv8_tc_workspace(D);
-  return layout(B, max_new, Hq, Hkv, D).total;
+size_t attn_kv8_workspace(int B, int max_new, int Hq, int Hkv, int D) {
+  // (the caller need not know the capacity: where it decides, what either kernel needs)
+  const long long rows = (long long)(Hq / Hkv) * max_new;
+  const size_t here = rows <= kRowsFewKeys ? layout(B, max_new, Hq, Hkv, D).total : 0;
+  const size_t there = rows > kRowsHere ? attn_kv8_tc_workspace(D) : 0;
+  return here > there ? here : there;
 }
 
 usp_status_t launch_attn_kv8(const AttnKv8Args& a, void* workspace, cudaStream_t st) {
-  if (many_rows(a.Hq, a.c.H, a.max_new)) return launch_attn_kv8_tc(a, workspace, st);
+  if (many_rows((long long)(a.Hq / a.c.H) * a.max_new, (long long)a.c.B * a.c.H * a.c.cap))
+    return launch_attn_kv8_tc(a, workspace, st);
   const Ws w = layout(a.c.B, a.max_new, a.Hq, a.c.H, a.D);
   char* base = static_cast<char*>(workspace);
   Params P{};

@@ -174,7 +174,7 @@ size_t usp_attn_kv8_workspace_size(int B, int T, int max_new, int packed, int Hq
     return 0;
   if (!packed || max_new < 1 || max_new > T) max_new = T;
   if (too_many_rows(B, max_new, Hq, Hkv)) return 0;
-  return attn_kv8_workspace(B, T, max_new, packed ? 1 : 0, Hq, Hkv, D);
+  return attn_kv8_workspace(B, max_new, Hq, Hkv, D);
 }
 
 usp_status_t usp_attn_kv8(const usp_kv8_cache_t* cache, const void* q, void* out, float* lse,
@@ -196,8 +196,8 @@ usp_status_t usp_attn_kv8(const usp_kv8_cache_t* cache, const void* q, void* out
       too_many_rows(cache->B, max_new, Hq, cache->Hkv))
     return USP_ERR_UNSUPPORTED;
   if (cache->B == 0) return USP_OK;
-  if (!workspace || workspace_bytes < attn_kv8_workspace(cache->B, T, max_new, cu_seqlens ? 1 : 0,
-                                                         Hq, cache->Hkv, cache->D))
+  if (!workspace ||
+      workspace_bytes < attn_kv8_workspace(cache->B, max_new, Hq, cache->Hkv, cache->D))
     return USP_ERR_WORKSPACE;
   AttnKv8Args a{};
   a.c = view(cache);

@@ -435,7 +435,7 @@ def test_blocks_of_very_different_exponents(T, exps):
     check_attn(q, c, out, lse)
 
 
-@pytest.mark.parametrize("T", [1, 33])
+@pytest.mark.parametrize("T", [1, 33, 130])
 def test_many_small_keys_beside_a_sink_count(T):
     """A first key that takes nearly all the attention, with a value of next to nothing,
     and 8191 keys of 2^-24 of its weight: O is theirs."""
@@ -495,7 +495,7 @@ def test_offsets_beyond_32_bits():
     k, v = (torch.randn(2, 900, H, D, generator=gen(s)).to(BF).to(dev) for s in (1, 2))
     for x in (c, small):
         usp.kv8_append(x, k, v)
-    for T in (1, 50):
+    for T in (1, 50, 130):
         q = torch.randn(2, T, H, D, generator=gen(T)).to(BF).to(dev)
         a, b = usp.attn_kv8(q, c), usp.attn_kv8(q, small)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
