@@ -16,9 +16,22 @@
 //                   both halves (exact; the products need both operands of one type)
 //   warp 12         producer: pages and exponents of the tiles, TMA of the codes
 //   warps 13, 14    MMA issuers of half A and B (one thread each); 13 owns the tensor memory
-// Tensor memory: S_A [0, 128), S_B [128, 256) (P over them as fp16), O_A at 256, O_B at
-// 256 + D. The halves share the tiles and nothing else, and the products of one run
-// while the softmax of the other works.
+// Tensor memory, for each half: scores of 64 keys in two places of 64 columns (P over
+// them as fp16), and O. So the products of one place, P V of its keys and then Q K of the
+// next step's, run while the softmax works on the other; the halves share the tiles
+// and nothing else.
+//
+// 4096 tokens at the end of 16K keys, 32 query heads over 8, D = 128 (0.96 TFLOP): 822 us,
+// 0.62 of the measured bf16 rate; 512 tokens at 32K: 247 us; a packed batch of single
+// tokens and chunks: 143 us. What bounds it is the chain from one role to the next more
+// than any unit: of a step's 4200 clocks the tensor core is busy 2560 (its products of 64
+// keys with both operands in shared memory take 48 clocks for 32 of arithmetic); without the
+// conversions it takes 4 % less, without the exponentials and the maximum 2 %, without
+// most of the products 6 %. Also measured for the first of these calls: scores of 128 keys
+// in one place 983 us; one place for both halves 1062; P apart from the scores, which then
+// come a part ahead, 977; one half per CTA with 128 keys in two places and K's codes
+// as they are (q as the sum of two E4M3 numbers) 1010; two such CTAs per SM with one
+// place 1032.
 // The numbers are attn_kv8.cu's: q scaled to fp16 by a power of two per row, K's
 // exponent a factor of the block's scores, V's added to them, p against a reference
 // 2^7 to 2^15 below the running maximum of score + e_v, the row's sum over p 2^-e_v.
@@ -50,9 +63,10 @@ constexpr int kGrid = 152;
 constexpr int kThreads = 512;
 constexpr int kConvWarp = 8, kConvWarps = 4, kProducerWarp = 12, kMmaWarp = 13;
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // 2 x 128 x (184 + 72) = 512 x 128
-// What a unit costs besides its steps, in steps (its queries, its end), and the
-// fewest steps that are worth a run of their own.
-constexpr int kUnitCost = 2;
+// What a unit costs besides its steps, in steps (its queries, its end; the packed batch
+// takes 168 us with 1, 158 with 2, 149 with 4 and 6, 151 with 8), and the fewest steps that
+// are worth a run of their own.
+constexpr int kUnitCost = 6;
 constexpr int kRunMin = 3;
 constexpr int kInfo = 8;                 // steps whose description is kept
 constexpr float kBelow = 7.f, kAbove = 15.f;
@@ -71,7 +85,7 @@ struct TcParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
   float* lse;
-  float* o_part;    // [2 kGrid][256][D]
+  float* o_part;    // [2 kGrid][D / 4][256] of four channels
   float2* ml_part;  // [2 kGrid][256]
   int4* rec;        // [2 kGrid]: 1 a partial, 3 its unit's last; b, rt, h
   const int* cu;
@@ -325,6 +339,7 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
     tmem_alloc(sbase + L::kMisc, 512);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (the launch overlaps what came before)
   if (warp == 0) {
     const Walk w = find_run(P);
     if (lane == 0) *start = w;
@@ -369,7 +384,8 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
       };
       for (int n = 0; ok; ++n) {
         const int sl = n & 1;
-        ok = mbar_wait(bar(L::kKcFull), n & 1, abort_flag, status);
+        ok = mbar_wait(bar(L::kInfoFull + n % kInfo), (n / kInfo) & 1, abort_flag, status) &&
+             mbar_wait(bar(L::kKcFull), n & 1, abort_flag, status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         const int fl = infos[n % kInfo].flags;
         if (fl & kEnd) break;
@@ -413,31 +429,43 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
           page = page_of(P.c, w.b, row);
           if (page >= 0) {
             const long long blk = (head_rows(P.c, page, w.h) + (row & (P.c.ps - 1))) / kBlock;
-            ke = clamp_exp(P.c.ke[blk]);
-            ve = clamp_exp(P.c.ve[blk]);
+            ke = P.c.ke[blk];  // (in flight: the copies do not wait for them)
+            ve = P.c.ve[blk];
           }
         }
         const unsigned none = __ballot_sync(0xffffffffu, page < 0);
-        // four lanes' exponents as bytes
-        uint32_t ke4 = (ke & 0xff) << (8 * (lane & 3)), ve4 = (ve & 0xff) << (8 * (lane & 3));
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          ke4 |= __shfl_xor_sync(0xffffffffu, ke4, o);
-          ve4 |= __shfl_xor_sync(0xffffffffu, ve4, o);
-        }
         const int cnt = min(8, w.end - w.s);
         const bool has_b = w.q.R - w.rt * kUnitRows > kBM;
+        uint32_t ke4 = 0, ve4 = 0;
         for (int i = 0; i < cnt; ++i, ++n) {
           const int src = 4 * i;
-          const uint32_t k4 = __shfl_sync(0xffffffffu, ke4, src);
-          const uint32_t v4 = __shfl_sync(0xffffffffu, ve4, src);
           const int key0 = (w.s + i < w.st.sinks ? w.s + i : w.s + i + w.st.skip) * kBN;
           const int none4 = (none >> src) & 15;
           const uint32_t bytes = (kBlocks - __popc(none4)) * kBlock * D;
           const bool mine = (lane >> 2) == i && page >= 0;
-          const int at = (lane & 3) * kBlock;
+          const int at = (lane & 3) * kBlock, hp = page * P.c.H + w.h;
           ok = n < 1 || mbar_wait(bar(L::kKcEmpty), (n - 1) & 1, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (lane == 0) {
+            if (bytes) mbar_expect_tx(bar(L::kKcFull), bytes);
+            else mbar_arrive(bar(L::kKcFull));
+          }
+          __syncwarp();
+          if (mine)
+            tma_load_3d(sbase + L::kKC + at * D, &tm_k, bar(L::kKcFull), 0,
+                        (key0 + at) & (P.c.ps - 1), hp);
+          ++nk;
+          if (i == 0) {  // four lanes' exponents as bytes (the first copy is on its way)
+            ke4 = (clamp_exp(ke) & 0xff) << (8 * (lane & 3));
+            ve4 = (clamp_exp(ve) & 0xff) << (8 * (lane & 3));
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+              ke4 |= __shfl_xor_sync(0xffffffffu, ke4, o);
+              ve4 |= __shfl_xor_sync(0xffffffffu, ve4, o);
+            }
+          }
+          const uint32_t k4 = __shfl_sync(0xffffffffu, ke4, src);
+          const uint32_t v4 = __shfl_sync(0xffffffffu, ve4, src);
           if (lane == 0) {
             volatile Info* x = infos + n % kInfo;
             x->key0 = key0;
@@ -447,15 +475,7 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
             x->ke = k4;
             x->ve = v4;
             mbar_arrive(bar(L::kInfoFull + n % kInfo));
-            if (bytes) mbar_expect_tx(bar(L::kKcFull), bytes);
-            else mbar_arrive(bar(L::kKcFull));
           }
-          __syncwarp();
-          const int hp = page * P.c.H + w.h;
-          if (mine)
-            tma_load_3d(sbase + L::kKC + at * D, &tm_k, bar(L::kKcFull), 0,
-                        (key0 + at) & (P.c.ps - 1), hp);
-          ++nk;
           ok = n < 1 || mbar_wait(bar(L::kVcEmpty), (n - 1) & 1, abort_flag, status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           if (lane == 0) {
@@ -579,31 +599,36 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
     int n = 0;              // steps of the run
     unsigned th = 0, to = 0, uh = 0;  // this half's steps, parts of them, units
     bool ok = any, more = any;
+    // This thread's query row of the unit in w, or null. The next unit's is asked for
+    // before the end of the one before it.
+    auto q_row = [&]() -> const uint4* {
+      const int row = w.rt * kUnitRows + hf * kBM + r, tok = row / P.G;
+      if (w.end <= w.s || row >= w.q.R) return nullptr;
+      return reinterpret_cast<const uint4*>(
+          P.q + ((long long)(w.q.first + tok) * P.Hq + w.h * P.G + row - tok * P.G) * D);
+    };
     while (more) {  // a unit
-      const int steps = max(0, w.end - w.s);
+      const int steps = max(0, w.end - w.s), R = w.q.R, first = w.q.first, h = w.h;
       const int row0 = w.rt * kUnitRows + hf * kBM, row = row0 + r;
       const bool whole = w.s == 0 && w.end == w.st.n;
       const int part = 2 * blockIdx.x + (w.s == 0 ? 1 : 0);
       if (!whole && threadIdx.x == 0)
         P.rec[part] = make_int4(w.end == w.st.n ? 3 : 1, w.b, w.rt, w.h);
-      if (row0 < w.q.R) {
-        const bool there = row < w.q.R;
-        const int tok = row / P.G, hh = row - tok * P.G;
-        const long long o_row = (long long)(w.q.first + tok) * P.Hq + w.h * P.G + hh;
-        const int i = w.q.len - w.q.n + tok;  // position
-        float m_run = -INFINITY, l_run = 0.f;
+      float m_run = -INFINITY, l_run = 0.f;
+      if (row0 < R) {
+        const int i = w.q.len - w.q.n + row / P.G;  // position
         if (steps > 0) {
           // ------------------------------------------------------ queries
           // (every product with the rows that stood here has completed: its scores
           // have been read)
           float row_mul;
           {
-            const uint4* src = reinterpret_cast<const uint4*>(P.q + o_row * D);
+            const uint4* src = q_row();
             uint4 x[D / 8];
             float big = 0.f;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
-              x[c] = there ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+              x[c] = src ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
               const uint32_t e[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
               for (int j = 0; j < 4; ++j)
@@ -761,50 +786,6 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
             ++th;
           }
           if (!ok) break;
-          ok = mbar_wait(bar(L::kODone + hf), uh & 1, abort_flag, status);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          ++uh;
-          tc_fence_after();
-        }
-        // ----------------------------------------------------------- the end
-        const bool none = l_run == 0.f;  // no visible key (a NaN score makes it NaN)
-        const float inv = none ? 0.f : 1.f / l_run;
-#pragma unroll 1
-        for (int oc = 0; oc < D / 32; ++oc) {
-          uint32_t o[32];
-          if (steps > 0) {
-            tmem_ld32(o_tm + 32 * oc, o);
-            tmem_wait_ld();
-          }
-          if (whole) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              o[j] = none ? 0u : __float_as_uint(__uint_as_float(o[j]) * inv);
-            if (there) {
-              uint4* dst = reinterpret_cast<uint4*>(P.out + o_row * D + 32 * oc);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t f[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  f[e] = pack_bf16(__uint_as_float(o[8 * j + 2 * e]),
-                                   __uint_as_float(o[8 * j + 2 * e + 1]));
-                dst[j] = make_uint4(f[0], f[1], f[2], f[3]);
-              }
-            }
-          } else if (there) {
-            uint4* dst = reinterpret_cast<uint4*>(
-                P.o_part + ((long long)part * kUnitRows + hf * kBM + r) * D + 32 * oc);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          }
-        }
-        if (there) {
-          if (whole)
-            P.lse[o_row] = none ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
-          else
-            P.ml_part[(long long)part * kUnitRows + hf * kBM + r] = make_float2(m_run, l_run);
         }
       }
       n += steps;
@@ -812,6 +793,73 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
       if (lane == 0) more = next_unit(P, w);
       more = __shfl_sync(0xffffffffu, more, 0);
       __syncwarp();
+      if (const uint4* src = more ? q_row() : nullptr) {
+#pragma unroll
+        for (int l = 0; l < D / 64; ++l)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 8 * l));
+      }
+      // ------------------------------------------------------------- the end
+      if (row0 >= R) continue;
+      if (steps > 0) {
+        ok = mbar_wait(bar(L::kODone + hf), uh & 1, abort_flag, status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        ++uh;
+        tc_fence_after();
+      }
+      const bool none = l_run == 0.f;  // no visible key (a NaN score makes it NaN)
+      const float inv = none ? 0.f : 1.f / l_run;
+      // Rows of O go out through the queries' places (free: every product with them has
+      // completed), a warp's own 32, so that neighbouring lanes write neighbouring bytes.
+      uint8_t* stage = sm + L::kQ + hf * L::kTile;
+      auto place = [&](int row, int c) {  // of 8 channels of a row of the half
+        return reinterpret_cast<uint4*>(stage + (c >> 3) * L::kHalfBytes + row * 128 +
+                                        (((c & 7) ^ (row & 7)) << 4));
+      };
+#pragma unroll 1
+      for (int oc = 0; oc < D / 32; ++oc) {
+        uint32_t o[32];
+        if (steps > 0) {
+          tmem_ld32(o_tm + 32 * oc, o);
+          tmem_wait_ld();
+        }
+        if (whole) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            o[j] = none ? 0u : __float_as_uint(__uint_as_float(o[j]) * inv);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              f[e] = pack_bf16(__uint_as_float(o[8 * j + 2 * e]),
+                               __uint_as_float(o[8 * j + 2 * e + 1]));
+            *place(r, 4 * oc + j) = make_uint4(f[0], f[1], f[2], f[3]);
+          }
+        } else if (row < R) {  // (four channels of all rows stand together)
+          uint4* dst = reinterpret_cast<uint4*>(P.o_part) +
+                       ((long long)part * (D / 4) + 8 * oc) * kUnitRows + hf * kBM + r;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            dst[j * kUnitRows] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+      }
+      auto o_row = [&](int row) {
+        const int tok = row / P.G;
+        return (long long)(first + tok) * P.Hq + h * P.G + row - tok * P.G;
+      };
+      if (whole) {
+        __syncwarp();
+#pragma unroll 4
+        for (int e = lane; e < 32 * (D / 8); e += 32) {
+          const int rr = quarter * 32 + e / (D / 8), c = e % (D / 8);
+          if (row0 + rr < R)
+            reinterpret_cast<uint4*>(P.out + o_row(row0 + rr) * D)[c] = *place(rr, c);
+        }
+        __syncwarp();  // (before the next queries)
+        if (row < R) P.lse[o_row(row)] = none ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+      } else if (row < R) {
+        P.ml_part[(long long)part * kUnitRows + hf * kBM + r] = make_float2(m_run, l_run);
+      }
     }
   }
 
@@ -821,65 +869,92 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-constexpr int kMergeThreads = 128, kMergeRows = 16;  // rows of a block
-constexpr int kPads = 64;
-
-// Block (j, y): rows [16 y, ..) of the unit whose first steps were run j's last, and
-// which run j did not end; its other partials are the first of the runs behind. Blocks
-// behind those (packed): zeros for the tokens outside the sequences.
+constexpr int kPads = 64;           // blocks that clear padding
+constexpr int kMergeRows = 32;      // of a block: a row per lane, 8 channels per warp
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) attn_kv8_tc_merge_kernel(const TcParams P) {
-  constexpr int kLanes = D / 4, kAtOnce = kMergeThreads / kLanes;
+constexpr int kMergeThreads = 32 * (D / 8);
+
+// Block (x, y): rows [32 y, ..) of the x-th unit that lies in several runs. Its
+// first partial stands behind the run j that it begins in, the others before the runs
+// behind j. Blocks x >= heads (packed): zeros for the tokens outside the sequences.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads<D>)
+attn_kv8_tc_merge_kernel(const TcParams P, int heads) {
+  __shared__ int s_run[2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.x >= kGrid - 1) {
-    const int i0 = (blockIdx.x - (kGrid - 1)) * gridDim.y + blockIdx.y;
-    const int step = (gridDim.x - (kGrid - 1)) * gridDim.y;
+  if ((int)blockIdx.x >= heads) {
+    const int i0 = (blockIdx.x - heads) * gridDim.y + blockIdx.y;
+    const int step = (gridDim.x - heads) * gridDim.y;
     const int e0 = min(max(__ldg(P.cu), 0), P.T), e1 = max(e0, min(max(__ldg(P.cu + P.c.B), 0), P.T));
     for (int i = i0; i < e0 + P.T - e1; i += step) {
       const long long tok = i < e0 ? i : e1 + (i - e0);
       uint2* r = reinterpret_cast<uint2*>(P.out + tok * P.Hq * D);
-      for (int u = threadIdx.x; u < P.Hq * D / 4; u += kMergeThreads) r[u] = make_uint2(0, 0);
-      for (int u = threadIdx.x; u < P.Hq; u += kMergeThreads) P.lse[tok * P.Hq + u] = -INFINITY;
+      for (int u = threadIdx.x; u < P.Hq * D / 4; u += kMergeThreads<D>) r[u] = make_uint2(0, 0);
+      for (int u = threadIdx.x; u < P.Hq; u += kMergeThreads<D>) P.lse[tok * P.Hq + u] = -INFINITY;
     }
     return;
   }
-  const int j = blockIdx.x;
-  const int4 rec = P.rec[2 * j + 1];
-  if (rec.x != 1) return;
-  const Seq q = seq_of(P, rec.y);
-  int last = j + 1;  // the run with the unit's last steps
-  while (last < kGrid - 1 && P.rec[2 * last].x == 1) ++last;
-  const int d = threadIdx.x % kLanes;
-  for (int rr = blockIdx.y * kMergeRows + threadIdx.x / kLanes; rr < (int)(blockIdx.y + 1) * kMergeRows;
-       rr += kAtOnce) {
-    const int row = rec.z * kUnitRows + rr;
-    if (row >= q.R) break;
-    float M = -INFINITY, ls = 0.f;
-    float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = j; k <= last; ++k) {
-      const long long at = (long long)(k == j ? 2 * j + 1 : 2 * k) * kUnitRows + rr;
-      const float2 a = P.ml_part[at];
-      const float4 x = reinterpret_cast<const float4*>(P.o_part + at * D)[d];
-      const float Mn = fmaxf(M, a.x);
-      const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn);
-      const float f1 = a.x == -INFINITY ? 0.f : ex2(a.x - Mn);
-      os.x = os.x * f0 + x.x * f1;
-      os.y = os.y * f0 + x.y * f1;
-      os.z = os.z * f0 + x.z * f1;
-      os.w = os.w * f0 + x.w * f1;
-      ls = ls * f0 + a.y * f1;
-      M = Mn;
+  if (threadIdx.x < 32) {  // run j, and the one with the unit's last steps
+    int left = blockIdx.x, j = -1, last = -1;
+    for (int j0 = 0; j0 < kGrid && last < 0; j0 += 32) {
+      const int k = j0 + (threadIdx.x & 31);
+      const int tail = k < kGrid ? P.rec[2 * k].x : 0, head = k < kGrid ? P.rec[2 * k + 1].x : 0;
+      // the ends of units behind run j (their first parts' runs come before them)
+      unsigned ends = __ballot_sync(0xffffffffu, tail == 3);
+      unsigned begins = __ballot_sync(0xffffffffu, head == 1);
+      if (j < 0) {
+        const int here = __popc(begins);
+        if (left >= here) {
+          left -= here;
+          continue;
+        }
+        for (; left > 0; --left) begins &= begins - 1;
+        const int at = __ffs(begins) - 1;
+        j = j0 + at;
+        ends &= at == 31 ? 0u : ~0u << (at + 1);
+      }
+      if (ends) last = j0 + __ffs(ends) - 1;
     }
-    const int tok = row / P.G, hh = row - tok * P.G;
-    const long long o_row = (long long)(q.first + tok) * P.Hq + rec.w * P.G + hh;
-    const bool none = ls == 0.f;
-    const float inv = none ? 0.f : 1.f / ls;
-    if (none) os = make_float4(0.f, 0.f, 0.f, 0.f);
-    reinterpret_cast<uint2*>(P.out + o_row * D)[d] =
-        make_uint2(pack_bf16(os.x * inv, os.y * inv), pack_bf16(os.z * inv, os.w * inv));
-    if (d == 0) P.lse[o_row] = none ? -INFINITY : (M + log2f(ls)) * kLn2;
+    if (threadIdx.x == 0) {
+      s_run[0] = last < 0 ? -1 : j;
+      s_run[1] = last;
+    }
   }
+  __syncthreads();
+  const int j = s_run[0], last = s_run[1];
+  if (j < 0) return;  // fewer such units
+  const int4 rec = P.rec[2 * j + 1];
+  const Seq q = seq_of(P, rec.y);
+  const int c8 = threadIdx.x >> 5, rr = blockIdx.y * kMergeRows + (threadIdx.x & 31);
+  const int row = rec.z * kUnitRows + rr;
+  if (row >= q.R) return;
+  float M = -INFINITY, ls = 0.f, os[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = j; k <= last; ++k) {
+    const long long slot = k == j ? 2 * j + 1 : 2 * k;
+    const float2 a = P.ml_part[slot * kUnitRows + rr];
+    const float4* o = reinterpret_cast<const float4*>(P.o_part) +
+                      (slot * (D / 4) + 2 * c8) * kUnitRows + rr;
+    const float4 x = o[0], y = o[kUnitRows];
+    const float Mn = fmaxf(M, a.x);
+    const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn);
+    const float f1 = a.x == -INFINITY ? 0.f : ex2(a.x - Mn);
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) os[e] = os[e] * f0 + v[e] * f1;
+    ls = ls * f0 + a.y * f1;
+    M = Mn;
+  }
+  const int tok = row / P.G, hh = row - tok * P.G;
+  const long long o_row = (long long)(q.first + tok) * P.Hq + rec.w * P.G + hh;
+  const bool none = ls == 0.f;
+  const float inv = none ? 0.f : 1.f / ls;
+  uint32_t f[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    f[e] = none ? 0u : pack_bf16(os[2 * e] * inv, os[2 * e + 1] * inv);
+  reinterpret_cast<uint4*>(P.out + o_row * D)[c8] = make_uint4(f[0], f[1], f[2], f[3]);
+  if (c8 == 0) P.lse[o_row] = none ? -INFINITY : (M + log2f(ls)) * kLn2;
 }
 
 // ------------------------------------------------------------------- host
@@ -905,27 +980,33 @@ usp_status_t launch_t(const TcParams& P, cudaStream_t st) {
   static SmemAttr attr;
   cudaError_t e = attr.set(attn_kv8_tc_kernel<D>, smem);
   if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
-  {
-    ProfScope ps(st, "attn_kv8_tc");
-    attn_kv8_tc_kernel<D><<<kGrid, kThreads, smem, st>>>(P, mk, mv);
-  }
-  note_launch();
-  usp_status_t r = check_launch();
-  if (r != USP_OK) return r;
-  // the merge's launch and set-up overlap the end of the kernel before it
+  // each kernel's launch and set-up overlap the end of the one before it
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kGrid - 1 + (P.cu ? kPads / (kUnitRows / kMergeRows) : 0),
-                     kUnitRows / kMergeRows);
-  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
+  cfg.gridDim = dim3(kGrid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   {
+    ProfScope ps(st, "attn_kv8_tc");
+    e = cudaLaunchKernelEx(&cfg, attn_kv8_tc_kernel<D>, P, mk, mv);
+  }
+  if (e == cudaSuccess) {
+    note_launch();
+    // at most one unit in several runs per run's end, and no more than there are units
+    const long long tiles = ((long long)P.max_new * P.G + kUnitRows - 1) / kUnitRows;
+    const long long units = (long long)P.c.B * P.c.H * tiles;
+    const int heads = units < kGrid - 1 ? (int)units : kGrid - 1;
+    const int slices = kUnitRows / kMergeRows;
+    cfg.gridDim = dim3(heads + (P.cu ? kPads / slices : 0), slices);
+    cfg.blockDim = dim3(kMergeThreads<D>);
+    cfg.dynamicSmemBytes = 0;
     ProfScope ps(st, "attn_kv8_tc_merge");
-    e = cudaLaunchKernelEx(&cfg, attn_kv8_tc_merge_kernel<D>, P);
+    e = cudaLaunchKernelEx(&cfg, attn_kv8_tc_merge_kernel<D>, P, heads);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
