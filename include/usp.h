@@ -761,7 +761,8 @@ usp_status_t usp_kv8_read(const usp_kv8_cache_t *cache, const int32_t *start, in
  * The result does not vary from run to run.
  * Hq % Hkv == 0; any number of query rows per KV head. dtype USP_BF16.
  * workspace: at least usp_attn_kv8_workspace_size(...) bytes, 256-byte aligned,
- *      contents on entry irrelevant; calls that overlap on the GPU need one each.
+ *      may be NULL when that is 0; contents on entry irrelevant; calls that overlap on
+ *      the GPU need one each.
  * Errors: USP_ERR_INVALID_ARG, USP_ERR_UNSUPPORTED (D, page_size; dtype USP_FP32;
  *      more than 2^26 rows per KV head, or 2^26 blocks of 8 of them in all),
  *      USP_ERR_ALIGNMENT, USP_ERR_WORKSPACE, USP_ERR_CUDA.
@@ -773,9 +774,10 @@ usp_status_t usp_attn_kv8(const usp_kv8_cache_t *cache, const void *q, void *out
                           usp_stream_t stream);
 
 /* Bytes of scratch usp_attn_kv8 needs (T, max_new as there; packed: whether it
- * gets cu_seqlens); 0 for invalid sizes. */
-size_t usp_attn_kv8_workspace_size(int B, int T, int max_new, int packed, int Hq, int Hkv,
-                                   int D);
+ * gets cu_seqlens; capacity = max_pages * page_size). 0 where it needs none (few rows
+ * and few keys) and for invalid sizes. */
+size_t usp_attn_kv8_workspace_size(int B, int T, int max_new, int packed, int capacity,
+                                   int Hq, int Hkv, int D);
 
 /*
  * usp_permute - sequence layouts and the Ulysses all-to-all, bit-exact.

@@ -13,6 +13,7 @@ same entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 from typing import NamedTuple, Optional, Tuple
 
@@ -235,8 +236,10 @@ def usp_attn_kv8(cache, q, out, lse, cu_seqlens, T, max_new, Hq, softmax_scale, 
         _enum(DTYPE, dtype), _p(workspace), int(workspace_bytes), _stream(stream)))
 
 
-def usp_attn_kv8_workspace_size(B, T, max_new, packed, Hq, Hkv, D) -> int:
-    return int(_lib.load().usp_attn_kv8_workspace_size(B, T, max_new, int(packed), Hq, Hkv, D))
+@functools.lru_cache(maxsize=1024)
+def usp_attn_kv8_workspace_size(B, T, max_new, packed, capacity, Hq, Hkv, D) -> int:
+    return int(_lib.load().usp_attn_kv8_workspace_size(B, T, max_new, int(packed), capacity, Hq,
+                                                       Hkv, D))
 
 
 def usp_permute(src, dst, kind, layout, B, S, H, D, cp_size, ulysses_degree,
@@ -990,7 +993,7 @@ def attn_kv8(q: torch.Tensor, cache: KV8Cache, *, causal=True, window=0, sink_to
             return attn_kv8(q, cache, causal=causal, window=window, sink_tokens=sink_tokens,
                             cu_seqlens=cu_seqlens, max_new=max_new, softmax_scale=softmax_scale,
                             workspace=workspace)
-    s, at, B, Hkv, _, D = _kv8_struct(cache)
+    s, at, B, Hkv, cap, D = _kv8_struct(cache)
     shape = q.shape
     cu, packed = None, 0
     if cu_seqlens is not None:
@@ -1010,10 +1013,13 @@ def attn_kv8(q: torch.Tensor, cache: KV8Cache, *, causal=True, window=0, sink_to
     dev = q.device
     out = torch.empty_like(q)
     lse = torch.empty(rows, dtype=_F32, device=dev)
-    need = lib.usp_attn_kv8_workspace_size(B, T, max_new, packed, Hq, Hkv, D)
-    ws = torch.empty(need, dtype=_U8, device=dev) if workspace is None else \
-        _use_workspace(workspace, need, dev)[0]
+    need = usp_attn_kv8_workspace_size(B, T, max_new, packed, cap, Hq, Hkv, D)
+    ws = workspace
+    if ws is not None:
+        ws = _use_workspace(ws, need, dev)[0]
+    elif need:
+        ws = torch.empty(need, dtype=_U8, device=dev)
     _call(lib.usp_attn_kv8, at, None, s, q.data_ptr(), out.data_ptr(), lse.data_ptr(), cu, T,
-          max_new, Hq, softmax_scale, 1 if causal else 0, window, sink_tokens, 0, ws.data_ptr(),
-          need if workspace is None else ws.numel())
+          max_new, Hq, softmax_scale, 1 if causal else 0, window, sink_tokens, 0,
+          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return out, lse

@@ -50,7 +50,7 @@ SIGNATURES = {
     "usp_kv8_read": (_i, [_vp, _vp, _i, _vp, _vp, _i, _vp]),
     "usp_attn_kv8": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _i, _i, _i, _vp, _sz,
                           _vp]),
-    "usp_attn_kv8_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "usp_attn_kv8_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
     "usp_permute": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]),
     "usp_status_string": (_c.c_char_p, [_i]),
     "usp_launch_count": (_u64, []),

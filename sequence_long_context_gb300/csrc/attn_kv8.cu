@@ -14,7 +14,8 @@
 // unit of which it has steps, in slot c + unit (between two consecutive partials
 // either c or the unit grows), and the second kernel merges a unit's partials,
 // which are consecutive, in order. Neighbouring runs go to different SMs, so that
-// a short problem uses all of them.
+// a short problem uses all of them. Where few units have few keys (own_cluster below) a
+// cluster of CTAs takes each instead, and that is the only kernel.
 //
 // One warp. It is on its own: its own ring of stages (32 keys and values each,
 // 4 D / 128 KB, brought in by TMA with the swizzle that makes its reads free of bank
@@ -201,9 +202,25 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-template <int D, int NT>
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // (aligned: the warp is together)
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+  return x;
+}
+
+// kOwn: a cluster of `cl` CTAs has a unit to itself; its warps take equal parts of the
+// steps, and their partials are joined in order over (distributed) shared memory: no
+// workspace, no second kernel.
+template <int D, int NT, bool kOwn>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_kv8_kernel(const Params P, const __grid_constant__ CUtensorMap tm_k,
+attn_kv8_kernel(const Params P, int cl, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v) {
   using L = Smem<D>;
   constexpr int kStages = L::kStages;
@@ -233,13 +250,39 @@ attn_kv8_kernel(const Params P, const __grid_constant__ CUtensorMap tm_k,
       }
     }
   }
-  __syncthreads();  // the only one: no warp waits for another from here on
+  __syncthreads();  // no warp waits for another from here to the end of its steps
   grid_dependency_wait();  // (this kernel's launch overlaps the end of what came before it)
 
   // ------------------------------------------------------- this warp's run
   const unsigned run = warp * kSms + blockIdx.x;
+  const unsigned rank = kOwn ? blockIdx.x % cl : 0;
   Walk cur;
-  {
+  bool more = true;
+  if constexpr (kOwn) {
+    if (P.cu) {  // zeros for the tokens outside the sequences, by all clusters
+      const int e0 = min(max(__ldg(P.cu), 0), P.T), e1 = max(e0, min(max(__ldg(P.cu + P.c.B), 0), P.T));
+      for (int i = blockIdx.x; i < e0 + P.T - e1; i += gridDim.x) {
+        const long long tok = i < e0 ? i : e1 + (i - e0);
+        uint2* r = reinterpret_cast<uint2*>(P.out + tok * P.Hq * D);
+        for (int u = threadIdx.x; u < P.Hq * D / 4; u += kThreads) r[u] = make_uint2(0, 0);
+        for (int u = threadIdx.x; u < P.Hq; u += kThreads) P.lse[tok * P.Hq + u] = -INFINITY;
+      }
+    }
+    const int unit = blockIdx.x / cl, bh = unit / P.nrb, rb = unit - bh * P.nrb;
+    if (bh >= P.c.B * P.c.H) return;  // a cluster for such tokens alone
+    cur.b = bh / P.c.H;
+    cur.q = seq_of<NT>(P, cur.b);
+    const int n = rb < cur.q.nrb ? cur.q.steps : 0;
+    cur.q.nrb = max(cur.q.nrb, 1);
+    cur.hr = (bh - cur.b * P.c.H) * cur.q.nrb + (rb < cur.q.nrb ? rb : 0);
+    // equal parts of the steps; neighbouring ones to different CTAs (no products that pass
+    // 32 bits: a unit has kOwnSteps * W steps at most)
+    const int w = warp * cl + rank, W = kWarps * cl;
+    cur.s = n * w / W;
+    cur.end = n * (w + 1) / W;
+    cur.left = 0;
+    more = cur.end > cur.s;
+  } else {
     long long ends = line_ends<NT>(P, 0);
     long long T = __shfl_sync(0xffffffffu, ends, 31);
     for (int b = 32; b < P.c.B; b += 32)
@@ -279,7 +322,6 @@ attn_kv8_kernel(const Params P, const __grid_constant__ CUtensorMap tm_k,
 
   // ------------------------------------------------- copies, kStages ahead
   Walk pre = cur;
-  bool more = true;
   unsigned issued = 0, known = 0, used = 0;  // steps: copied, with a page, taken
   const uint32_t ring = sbase + warp * L::kWarpBytes;
   // Exponents of the steps whose pages came last, on their way: nothing needs them before
@@ -341,7 +383,7 @@ attn_kv8_kernel(const Params P, const __grid_constant__ CUtensorMap tm_k,
   for (;;) {
     // ---------------------------------------------------------------- a unit
     const Seq sq = cur.q;
-    const int h = cur.hr / sq.nrb, rb = cur.hr - h * sq.nrb;
+    const int h = cur.hr / sq.nrb, rb = kOwn ? (int)(blockIdx.x / cl) % P.nrb : cur.hr - h * sq.nrb;
     const int len = sq.len, i_first = len - sq.n;
     // Q^T fragments: product kk = 4 j + w takes channels 4 w .. 4 w + 3 of chunk j of
     // the thread's run of D/4
@@ -551,6 +593,76 @@ attn_kv8_kernel(const Params P, const __grid_constant__ CUtensorMap tm_k,
       __syncwarp();  // the stage has been read
       if (more) issue();
     }
+    if constexpr (kOwn) {
+      // the warp's partial where its tiles stood, then the CTA's, then the cluster's
+      if (!ok)  // (aborted: the copies in flight land first)
+        for (; used < issued; ++used) mbar_wait_drain(full(used % kStages), (used / kStages) & 1);
+      __syncwarp();
+      float* mine = reinterpret_cast<float*>(sm + warp * L::kWarpBytes);  // [rows][D], then m, l
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = l[nt][e];
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+          const int r = nt * 8 + 2 * t + e;
+          if (g == 0) {
+            mine[kRows * D + 2 * r] = m[nt][e];
+            mine[kRows * D + 2 * r + 1] = x;
+          }
+          float4* dst = reinterpret_cast<float4*>(mine + r * D + g * (D / 8));
+#pragma unroll
+          for (int i = 0; i < kMT; i += 2)
+            dst[i / 2] =
+                make_float4(o[nt][i][e], o[nt][i][e + 2], o[nt][i + 1][e], o[nt][i + 1][e + 2]);
+        }
+      __syncthreads();
+      const int rows = min(kRows, sq.R - rb * kRows);  // that exist
+      constexpr int kPart = L::kWarpBytes / 4;         // floats from one warp's to the next's
+      const float* parts = reinterpret_cast<const float*>(sm);
+      float* cta = reinterpret_cast<float*>(sm) + kRows * D + 2 * kRows;  // the CTA's, behind warp 0's
+      static_assert(2 * (kRows * D + 2 * kRows) <= kPart, "a warp's tiles hold two partials");
+      for (int x = threadIdx.x; x < rows * D; x += kThreads) {
+        const int r = x / D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, parts[w * kPart + kRows * D + 2 * r]);
+        float os = 0.f, ls = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = parts[w * kPart + kRows * D + 2 * r];
+          const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
+          ls += parts[w * kPart + kRows * D + 2 * r + 1] * f;
+          os += parts[w * kPart + x] * f;
+        }
+        cta[x] = os;
+        if (x == r * D) {
+          cta[kRows * D + 2 * r] = M;
+          cta[kRows * D + 2 * r + 1] = ls;
+        }
+      }
+      cluster_sync();
+      const uint32_t at = smem_u32(cta);
+      for (int x = rank * kThreads + threadIdx.x; x < rows * D; x += cl * kThreads) {
+        const int r = x / D, row = rb * kRows + r;
+        float M = -INFINITY, os = 0.f, ls = 0.f;
+        for (int c = 0; c < cl; ++c) M = fmaxf(M, ld_cluster(at + 4 * (kRows * D + 2 * r), c));
+        for (int c = 0; c < cl; ++c) {
+          const float mc = ld_cluster(at + 4 * (kRows * D + 2 * r), c);
+          const float f = mc == -INFINITY ? 0.f : ex2(mc - M);
+          ls += ld_cluster(at + 4 * (kRows * D + 2 * r + 1), c) * f;
+          os += ld_cluster(at + 4 * x, c) * f;
+        }
+        const int tok = row / P.G, hh = row - tok * P.G;
+        const long long o_row = (long long)(sq.first + tok) * P.Hq + h * P.G + hh;
+        const bool none = ls == 0.f;  // no visible key (a NaN score makes ls NaN)
+        P.out[o_row * D + x - r * D] = __float2bfloat16_rn(none ? 0.f : os * (1.f / ls));
+        if (x == r * D) P.lse[o_row] = none ? -INFINITY : (M + log2f(ls)) * kLn2;
+      }
+      cluster_sync();  // (no CTA ends while another reads its memory)
+      return;
+    }
     if (!ok) break;
     // ------------------------------------------------- the unit's partial
     const int unit = (cur.b * P.c.H + h) * P.nrb + rb;
@@ -704,13 +816,66 @@ bool many_rows(long long rows, long long keys) {
   return rows > (keys <= kFewKeys ? kRowsFewKeys : kRowsHere);
 }
 
+// The CTAs of a unit's cluster, where units have clusters of their own; else 0. One launch
+// and no workspace, 4.5 us less for the host of a call (23.6 -> 19), and on the GPU (8 KV
+// heads, 4 heads each, sequences of one length): 1 x 4096 keys 10.2 us on one line and 8.3
+// in clusters, 4 x 1024 8.0 and 7.0, 4 x 8192 18.3 and 17.4, 16 x 2048 19.3 and 17.6; 1 x
+// 32768 21.6 and 24.4. But a short sequence's cluster does not help with a long one's
+// keys, so it stays below kOwnSteps steps of a warp, where the host's time is the longer
+// even then. The sizes are those of which a GB300 holds as many at once as there are units
+// (15 clusters of 8, 23 of 6, 46 of 3, 76 of 2, with one CTA per SM: 2 x 8 units in
+// clusters of 8, of which one waits for the others' end, took 15.6 us instead of 10.8).
+constexpr int kOwnSteps = 8;  // of a warp at most
+int own_cluster(long long units, long long cap) {
+  if (units < 1 || units > kSms) return 0;
+  const int u = (int)units;
+  const int cl = u <= 15 ? 8 : u <= 46 ? min(6, 138 / u) : u <= 76 ? 2 : 1;
+  return (cap + kStep - 1) / kStep <= (long long)kOwnSteps * kWarps * cl ? cl : 0;
+}
+
+template <int D, int NT>
+usp_status_t launch_own(const Params& P, int cl, cudaStream_t st) {
+  CUtensorMap mk{}, mv{};
+  if (P.c.np > 0 && (!make_map(&mk, P.c.kc, P.c, D) || !make_map(&mv, P.c.vc, P.c, D)))
+    return USP_ERR_CUDA;
+  const int smem = Smem<D>::kAlloc;
+  static SmemAttr attr;
+  cudaError_t e = attr.set(attn_kv8_kernel<D, NT, true>, smem);
+  if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
+  int clusters = P.c.B * P.c.H * P.nrb;
+  if (P.cu && P.T > kSms) clusters = max(clusters, kSms / cl);  // many tokens to clear, perhaps
+  cfg.gridDim = dim3((unsigned)(clusters * cl));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = cl;
+  a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 2;
+  {
+    ProfScope ps(st, "attn_kv8");
+    e = cudaLaunchKernelEx(&cfg, attn_kv8_kernel<D, NT, true>, P, cl, mk, mv);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail_cuda("kernel launch", e);
+  }
+  note_launch();
+  return USP_OK;
+}
+
 template <int D, int NT>
 usp_status_t launch_t(const Params& P, cudaStream_t st) {
   CUtensorMap mk{}, mv{};  // (without pages, nothing is loaded through them)
   if (P.c.np > 0 && (!make_map(&mk, P.c.kc, P.c, D) || !make_map(&mv, P.c.vc, P.c, D))) return USP_ERR_CUDA;
   const int smem = Smem<D>::kAlloc;
   static SmemAttr attr;
-  cudaError_t e = attr.set(attn_kv8_kernel<D, NT>, smem);
+  cudaError_t e = attr.set(attn_kv8_kernel<D, NT, false>, smem);
   if (e != cudaSuccess) return fail_cuda("cudaFuncSetAttribute(smem)", e);
   // A row's partials are merged by a block where a unit has many, else by a few threads:
   // of units spread over kRuns warps, each has about kRuns / units + 1.
@@ -733,7 +898,7 @@ usp_status_t launch_t(const Params& P, cudaStream_t st) {
   cfg.dynamicSmemBytes = smem;
   {
     ProfScope ps(st, "attn_kv8");
-    e = cudaLaunchKernelEx(&cfg, attn_kv8_kernel<D, NT>, P, mk, mv);
+    e = cudaLaunchKernelEx(&cfg, attn_kv8_kernel<D, NT, false>, P, 1, mk, mv);
   }
   if (e == cudaSuccess) {
     note_launch();
@@ -754,12 +919,11 @@ usp_status_t launch_t(const Params& P, cudaStream_t st) {
 
 }  // namespace
 
-size_t attn_kv8_workspace(int B, int max_new, int Hq, int Hkv, int D) {
-  // (the caller need not know the capacity: where it decides, what either kernel needs)
+size_t attn_kv8_workspace(int B, int max_new, long long cap, int Hq, int Hkv, int D) {
   const long long rows = (long long)(Hq / Hkv) * max_new;
-  const size_t here = rows <= kRowsFewKeys ? layout(B, max_new, Hq, Hkv, D).total : 0;
-  const size_t there = rows > kRowsHere ? attn_kv8_tc_workspace(D) : 0;
-  return here > there ? here : there;
+  if (many_rows(rows, (long long)B * Hkv * cap)) return attn_kv8_tc_workspace(D);
+  const Ws w = layout(B, max_new, Hq, Hkv, D);
+  return own_cluster((long long)B * Hkv * w.nrb, cap) ? 0 : w.total;
 }
 
 usp_status_t launch_attn_kv8(const AttnKv8Args& a, void* workspace, cudaStream_t st) {
@@ -786,6 +950,11 @@ usp_status_t launch_attn_kv8(const AttnKv8Args& a, void* workspace, cudaStream_t
   P.causal = a.causal;
   P.window = a.window;
   P.sink = a.sink;
+  if (const int cl = own_cluster((long long)a.c.B * a.c.H * w.nrb, a.c.cap)) {
+    if (a.D == 128)
+      return w.rows == 8 ? launch_own<128, 1>(P, cl, st) : launch_own<128, 2>(P, cl, st);
+    return w.rows == 8 ? launch_own<64, 1>(P, cl, st) : launch_own<64, 2>(P, cl, st);
+  }
   if (a.D == 128) return w.rows == 8 ? launch_t<128, 1>(P, st) : launch_t<128, 2>(P, st);
   return w.rows == 8 ? launch_t<64, 1>(P, st) : launch_t<64, 2>(P, st);
 }

@@ -168,13 +168,14 @@ usp_status_t usp_kv8_read(const usp_kv8_cache_t* cache, const int32_t* start, in
                          reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t usp_attn_kv8_workspace_size(int B, int T, int max_new, int packed, int Hq, int Hkv, int D) {
-  if (B < 0 || B > 65535 || T < 1 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv != 0 ||
-      (D != 64 && D != 128))
+size_t usp_attn_kv8_workspace_size(int B, int T, int max_new, int packed, int capacity, int Hq,
+                                   int Hkv, int D) {
+  if (B < 0 || B > 65535 || T < 1 || capacity < 0 || capacity > kMaxRows || Hq < 1 || Hkv < 1 ||
+      Hkv > 65535 || Hq % Hkv != 0 || (D != 64 && D != 128))
     return 0;
   if (!packed || max_new < 1 || max_new > T) max_new = T;
   if (too_many_rows(B, max_new, Hq, Hkv)) return 0;
-  return attn_kv8_workspace(B, max_new, Hq, Hkv, D);
+  return attn_kv8_workspace(B, max_new, capacity, Hq, Hkv, D);
 }
 
 usp_status_t usp_attn_kv8(const usp_kv8_cache_t* cache, const void* q, void* out, float* lse,
@@ -196,9 +197,10 @@ usp_status_t usp_attn_kv8(const usp_kv8_cache_t* cache, const void* q, void* out
       too_many_rows(cache->B, max_new, Hq, cache->Hkv))
     return USP_ERR_UNSUPPORTED;
   if (cache->B == 0) return USP_OK;
-  if (!workspace ||
-      workspace_bytes < attn_kv8_workspace(cache->B, max_new, Hq, cache->Hkv, cache->D))
-    return USP_ERR_WORKSPACE;
+  const size_t need =
+      attn_kv8_workspace(cache->B, max_new, (long long)cache->max_pages * cache->page_size, Hq,
+                         cache->Hkv, cache->D);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return USP_ERR_WORKSPACE;
   AttnKv8Args a{};
   a.c = view(cache);
   a.q = q;

@@ -42,7 +42,7 @@ struct AttnKv8Args {
   float scale;
   int causal, window, sink;
 };
-size_t attn_kv8_workspace(int B, int max_new, int Hq, int Hkv, int D);
+size_t attn_kv8_workspace(int B, int max_new, long long cap, int Hq, int Hkv, int D);
 usp_status_t launch_attn_kv8(const AttnKv8Args& a, void* workspace, cudaStream_t st);
 int read_clear_attn_kv8_status();  // -1 on a CUDA error
 

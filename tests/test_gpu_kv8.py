@@ -355,6 +355,21 @@ ATTN = [
     (1, 5, 512, 2, 2, 128, 64, [512], False, 64, 1),
     (40, 1, 96, 2, 2, 64, 32, [(7 * b) % 97 for b in range(40)], True, 0, 0),
     (1, 1, 32768, 2, 4, 128, 128, [32700], True, 0, 0),
+    # room for more keys than a cluster of CTAs takes per unit: units on one line
+    (3, 1, 20480, 2, 4, 128, 64, [500, 33, 0], True, 0, 0),
+    (2, 3, 32768, 2, 5, 64, 32, [20000, 2], True, 0, 0),
+    (2, 2, 65536, 3, 8, 64, 128, [1000, 97], False, 0, 0),
+    (2, 1, 20480, 1, 5, 128, 128, [2047, 1024], True, 100, 4),
+    (2, 4, 33024, 2, 3, 128, 64, [639, 64], True, 33, 70),
+    (40, 1, 4096, 4, 2, 64, 32, [(7 * b) % 97 for b in range(40)], True, 0, 0),
+    (40, 5, 96, 4, 4, 64, 32, [(7 * b) % 97 for b in range(40)], True, 0, 0),
+    # clusters of 6, 5, 4, 3, 2 CTAs
+    (2, 1, 12288, 8, 4, 64, 64, [12288, 31], True, 0, 0),
+    (3, 1, 1024, 8, 4, 128, 128, [1024, 0, 97], True, 0, 0),
+    (3, 2, 8192, 10, 4, 64, 64, [8191, 700, 1], True, 0, 0),
+    (9, 4, 256, 4, 4, 128, 32, [(31 * b) % 257 for b in range(9)], True, 50, 3),
+    (5, 3, 320, 4, 5, 64, 32, [64, 320, 0, 289, 5], False, 0, 0),
+    (5, 1, 2048, 10, 2, 128, 64, [2048, 1, 65, 1999, 512], True, 0, 0),
     # whole chunks
     (1, 33, 64, 1, 4, 128, 32, [33], True, 0, 0),
     (2, 100, 384, 2, 2, 128, 64, [380, 100], True, 0, 0),
@@ -407,6 +422,18 @@ def test_packed_attention_is_the_oracles(cut, lens, kw, hint):
                             max_new=max(b - a for a, b in zip(cut, cut[1:])) if hint else 0, **kw)
     check_attn(q, c, out, lse, kw.get("causal", True), kw.get("window", 0), kw.get("sink_tokens", 0), cut=cut)
     for s in (slice(0, cut[0]), slice(cut[-1], T)):  # padding
+        assert not out[s].any() and torch.isneginf(lse[s]).all()
+
+
+@pytest.mark.parametrize("first,T", [(0, 700), (100, 400), (695, 700)])
+def test_padding_around_single_tokens(first, T):
+    dev = device()
+    cut = [first + i for i in range(6)]
+    c = random_cache(dev, 5, 320, 2, 128, 32, [320, 1, 0, 63, 64])
+    q = torch.randn(T, 8, 128, generator=gen(T)).to(BF).to(dev)
+    out, lse = usp.attn_kv8(q, c, cu_seqlens=i32(cut, dev), max_new=1)
+    check_attn(q, c, out, lse, True, 0, 0, cut=cut)
+    for s in (slice(0, cut[0]), slice(cut[-1], T)):
         assert not out[s].any() and torch.isneginf(lse[s]).all()
 
 
@@ -570,7 +597,7 @@ def test_captured_step_replays_as_the_cache_grows():
     q = torch.randn(B, 6, Hq, D, generator=g).to(BF).to(dev)
     caches = [random_cache(dev, B, 256, H, D, 64, [30, 64, 0], seed=2) for _ in "ab"]
     kb, vb, qb = k[:, :1].clone(), v[:, :1].clone(), q[:, :1].clone()
-    ws = torch.empty(usp.usp_attn_kv8_workspace_size(B, 1, 0, False, Hq, H, D), dtype=torch.uint8, device=dev)
+    ws = torch.empty(max(1, usp.usp_attn_kv8_workspace_size(B, 1, 0, False, 256, Hq, H, D)), dtype=torch.uint8, device=dev)
 
     def step(c):
         _, qr = usp.kv8_append(c, kb, vb, q=qb, rope=table)
@@ -620,7 +647,7 @@ def test_other_streams(T):
 
 def test_a_small_workspace_is_refused():
     dev = device()
-    c = random_cache(dev, 2, 128, 2, 64, 64, [100, 50])
+    c = random_cache(dev, 2, 65536, 2, 64, 64, [100, 50])
     q = torch.zeros(2, 1, 4, 64, dtype=BF, device=dev)
     with pytest.raises(ValueError):
         usp.attn_kv8(q, c, workspace=torch.empty(128, dtype=torch.uint8, device=dev))

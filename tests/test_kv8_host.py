@@ -118,20 +118,27 @@ def test_read_refuses(lib, over, code):
     (dict(q=FAKE + 8), 3), (dict(out=FAKE + 8), 3), (dict(lse=FAKE + 8), 3), (dict(cu=FAKE + 1), 3),
     (dict(ws=FAKE + 16), 3), (dict(ws=None), 4), (dict(wsb=1024), 4), (dict(T=1 << 25), 2)])
 def test_attn_refuses(lib, over, code):
-    assert attn(lib, cache(), **over) == code
+    assert attn(lib, cache(max_pages=4096), **over) == code
 
 
 def test_attn_workspace_sizes(lib):
     f = usp.usp_attn_kv8_workspace_size
-    for T, cu in ((1, None), (3, None), (300, None), (300, FAKE)):
-        for max_new in (0, 2):
-            need = f(2, T, max_new, cu is not None, 8, 2, 128)
-            assert need > 0
-            assert attn(lib, cache(), T=T, max_new=max_new, cu=cu, wsb=need - 1) == 4
-    assert f(2, 0, 0, False, 8, 2, 128) == 0 and f(2, 1, 0, False, 7, 2, 128) == 0
-    assert f(2, 1, 0, False, 8, 2, 96) == 0 and f(2, 1 << 25, 0, False, 8, 2, 128) == 0
+    for mp, few in ((4, True), (4096, False)):  # 256 and 262144 rows of each sequence
+        c = cache(max_pages=mp)
+        for T, cu in ((1, None), (3, None), (300, None), (300, FAKE)):
+            for max_new in (0, 2):
+                need = f(2, T, max_new, cu is not None, mp * 64, 8, 2, 128)
+                if few and (T < 300 or (cu and max_new)):
+                    assert need == 0  # few rows, few keys
+                    continue
+                assert need > 0
+                assert attn(lib, c, T=T, max_new=max_new, cu=cu, wsb=need - 1) == 4
+                assert attn(lib, c, T=T, max_new=max_new, cu=cu, ws=None) == 4
+    assert f(2, 0, 0, False, 256, 8, 2, 128) == 0 and f(2, 1, 0, False, 1 << 20, 7, 2, 128) == 0
+    assert f(2, 1, 0, False, 1 << 20, 8, 2, 96) == 0 and f(2, 1 << 25, 0, False, 256, 8, 2, 128) == 0
+    assert f(2, 1, 0, False, -1, 8, 2, 128) == 0 and f(2, 1, 0, False, (1 << 30) + 1, 8, 2, 128) == 0
     # dense calls do not look at max_new
-    assert f(2, 300, 2, False, 8, 2, 128) == f(2, 300, 0, False, 8, 2, 128)
+    assert f(2, 300, 2, False, 256, 8, 2, 128) == f(2, 300, 0, False, 256, 8, 2, 128)
 
 
 @pytest.mark.parametrize("over,code", [
