@@ -66,6 +66,12 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two_bytes) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // (aligned: the warp is together)
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+
 // ------------------------------------------------------------------ rotation
 struct Rope {
   const float* table;  // [rows][R]: cos of R/2 frequencies, sin of them; or nullptr
