@@ -21,23 +21,28 @@
 // next step's, run while the softmax works on the other; the halves share the tiles
 // and nothing else.
 //
-// 4096 tokens at the end of 16K keys, 32 query heads over 8, D = 128 (0.96 TFLOP): 822 us,
-// 0.62 of the measured bf16 rate; 512 tokens at 32K: 247 us; a packed batch of single
-// tokens and chunks: 143 us. What bounds it is the chain from one role to the next more
-// than any unit: of a step's 4200 clocks the tensor core is busy 2560 (its products of 64
-// keys with both operands in shared memory take 48 clocks for 32 of arithmetic); without the
-// conversions it takes 4 % less, without the exponentials and the maximum 2 %, without
-// most of the products 6 %. Also measured for the first of these calls: scores of 128 keys
+// 4096 tokens at the end of 16K keys, 32 query heads over 8, D = 128 (0.96 TFLOP): 805 us,
+// 0.64 of the measured bf16 rate; 512 tokens at 32K: 244 us; a packed batch of single
+// tokens and chunks: 141 us. What bounds it is the chain from one role to the next more
+// than any unit: of a step's 4100 clocks the tensor core is busy 2560 (its products of 64
+// keys with both operands in shared memory take 48 clocks for 32 of arithmetic), shared
+// memory about 3000, a tile's conversion 1000 for K and 1000 for V, each hand-over 200 to
+// 300. At 822 us the conversions left out saved 4 %, the exponentials and the maximum 2 %,
+// most of the products 6 %. Copies of the next step but one into L2 gave 1 %, a path
+// without the test of rows for whole tiles 1 %. Also measured, at 822 us: scores of 128 keys
 // in one place 983 us; one place for both halves 1062; P apart from the scores, which then
 // come a part ahead, 977; one half per CTA with 128 keys in two places and K's codes
 // as they are (q as the sum of two E4M3 numbers) 1010; two such CTAs per SM with one
-// place 1032.
+// place 1032. Units of at most 128 rows with both halves on the same rows and every other
+// tile each: no faster (4 x 64K keys, 128 rows 214 us; the converters' chain of hand-overs
+// bounds them), and 10 % slower for the others by spills.
 // The numbers are attn_kv8.cu's: q scaled to fp16 by a power of two per row, K's
 // exponent a factor of the block's scores, V's added to them, p against a reference
 // 2^7 to 2^15 below the running maximum of score + e_v, the row's sum over p 2^-e_v.
 #include <cuda_fp16.h>
 
 #include <cfloat>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv4_host.h"
@@ -358,17 +363,15 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
       // bank once
       const int cw = warp - kConvWarp, r8 = lane & 7, c4 = lane >> 3;
       bool ok = any;
-      auto convert = [&](const uint8_t* src, uint8_t* dst, int valid, int none) {
+      auto rows_of = [&](const uint8_t* src, uint8_t* dst, int valid, auto all) {
 #pragma unroll
         for (int i = 0; i < kBN / (8 * kConvWarps); ++i) {
           const int row = 32 * cw + 8 * i + r8;
-          // rows that hold no key hold anything: 0, so that 0 * it is 0
-          const bool there = row < valid && !((none >> cw) & 1);
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) {
             const int c = 4 * j + c4;
             uint4 x = *reinterpret_cast<const uint4*>(src + tile_at<D>(row, c));
-            if (!there) x = make_uint4(0, 0, 0, 0);
+            if (!all && row >= valid) x = make_uint4(0, 0, 0, 0);
             uint8_t* d = dst + (c >> 2) * L::kHalfBytes + row * 128;
             const int c8 = 2 * (c & 3);
             *reinterpret_cast<uint4*>(d + ((c8 ^ r8) << 4)) =
@@ -379,6 +382,12 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
                            e4m3x2_to_h2(x.w & 0xffffu), e4m3x2_to_h2(x.w >> 16));
           }
         }
+      };
+      // rows that hold no key hold anything: 0, so that 0 * it is 0
+      auto convert = [&](const uint8_t* src, uint8_t* dst, int valid, int none) {
+        if ((none >> cw) & 1) valid = 0;
+        if (valid >= kBN) rows_of(src, dst, valid, std::true_type{});
+        else rows_of(src, dst, valid, std::false_type{});
         fence_proxy_async_smem();  // read next by the tensor core
         __syncwarp();
       };
@@ -487,6 +496,11 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
             tma_load_3d(sbase + L::kVC + at * D, &tm_v, bar(L::kVcFull), 0,
                         (key0 + at) & (P.c.ps - 1), hp);
           ++nv;
+          // the next copies but one come from L2
+          if ((lane >> 2) == i + 2 && page >= 0) {
+            tma_prefetch_3d(&tm_k, 0, row & (P.c.ps - 1), hp);
+            tma_prefetch_3d(&tm_v, 0, row & (P.c.ps - 1), hp);
+          }
         }
         w.s += cnt;
         begins = w.s >= w.end;
