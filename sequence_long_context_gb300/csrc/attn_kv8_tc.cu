@@ -277,13 +277,6 @@ struct Smem {
   static_assert(kAlloc <= 227 * 1024, "one CTA per SM");
 };
 
-// Columns [lo, hi] (relative to a block's first key) as bits.
-__device__ __forceinline__ uint32_t col_bits(int lo, int hi) {
-  if (hi < 0 || lo > 31 || hi < lo) return 0;
-  const uint32_t a = lo <= 0 ? ~0u : ~0u << lo;
-  return hi >= 31 ? a : a & ((2u << hi) - 1);
-}
-
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -675,9 +668,7 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
           // the half's positions
           const int i_lo = w.q.len - w.q.n + row0 / P.G;
           const int i_hi = w.q.len - w.q.n + (min(w.q.R, row0 + kBM) - 1) / P.G;
-          const int hi = i < 0 ? -1 : P.causal ? min(i, w.q.len - 1) : w.q.len - 1;
-          const int lo = P.window > 0 ? i - P.window + 1 : 0;
-          const int sink_hi = P.window > 0 ? min(P.sink - 1, hi) : -1;
+          const RowKeys seen = row_keys(i, w.q.len, P.causal, P.window, P.sink);
           for (int s = 0; s < steps; ++s) {
             const int ns = n + s;
             Info inf{};
@@ -718,8 +709,7 @@ attn_kv8_tc_kernel(const TcParams P, const __grid_constant__ CUtensorMap tm_k,
               if (masked) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                  const int k = inf.key0 + sub * kSub + 32 * c;
-                  uint32_t vis = col_bits(lo - k, hi - k) | col_bits(-k, sink_hi - k);
+                  uint32_t vis = key_bits(seen, inf.key0 + sub * kSub + 32 * c);
                   if ((inf.flags >> (8 + 2 * sub + c)) & 1) vis = 0;
 #pragma unroll
                   for (int j = 0; j < 32; ++j)

@@ -5,6 +5,7 @@
 
 #include "internal.h"
 #include "kv8_host.h"
+#include "kv8_mask.h"
 
 namespace usp {
 namespace {
@@ -14,9 +15,7 @@ bool aligned(const void* p, unsigned n) {
 }
 bool valid_dtype(usp_dtype_t t) { return t == USP_BF16 || t == USP_FP32; }
 
-// rows of a sequence, and tokens of a call: the kernels count rows in 32 bits and
-// add the two
-constexpr long long kMaxRows = 1LL << 30;
+using kv8::kMaxRows;
 
 // The checks every call makes of a cache (usp.h, "The paged 8-bit KV cache").
 usp_status_t check_cache(const usp_kv8_cache_t* c) {
@@ -213,7 +212,7 @@ usp_status_t usp_attn_kv8(const usp_kv8_cache_t* cache, const void* q, void* out
   a.D = cache->D;
   a.scale = softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)cache->D);
   a.causal = causal ? 1 : 0;
-  a.window = window > 0 ? window : 0;
+  a.window = kv8::window_of(window);  // (the kernels subtract it from positions)
   a.sink = sink_tokens;
   return launch_attn_kv8(a, workspace, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -9,6 +9,7 @@
 
 #include "internal.h"
 #include "kv8.cuh"
+#include "kv8_mask.h"
 
 namespace usp {
 namespace kv8 {
