@@ -154,8 +154,9 @@ AttnParams make_params(const Shape& s, float scale, int causal, int window,
   P.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)s.D);
   P.scale_log2 = P.scale * 1.4426950408889634f;
   P.causal = causal ? 1 : 0;
-  P.window = window > 0 ? window : 0;
-  P.sink = sink;
+  // a window or sinks of S reach every key; the kernels add them to positions
+  P.window = window > 0 ? std::min(window, s.S) : 0;
+  P.sink = std::min(sink, s.S);
   P.cu = cu;
   P.nseq = cu ? s.B : 0;
   P.cp = s.cp;
@@ -787,9 +788,7 @@ usp_status_t usp_attn_key_weights(const void* q, const void* k, const float* lse
   const size_t need =
       usp_attn_key_weights_workspace_size(s.B_eff(), S, Hq, Hkv, observe, dtype, flags);
   if (need > 0 && (!workspace || workspace_bytes < need)) return USP_ERR_WORKSPACE;
-  // a window or sinks of S reach every key; the kernels add them to positions
-  AttnParams P = make_params(s, softmax_scale, causal, std::min(window, S),
-                             std::min(sink_tokens, S), cu_seqlens);
+  AttnParams P = make_params(s, softmax_scale, causal, window, sink_tokens, cu_seqlens);
   P.q = q;
   P.k = k;
   P.lse = const_cast<float*>(lse);
