@@ -98,9 +98,12 @@ def draw(rng):
         if cp > 1:
             S = max(1, S // (2 * cp)) * 2 * cp
         packed = rng.choice([0, 0, 3, 7]) if S >= 16 else 0
-        return dict(op=op, B=1 if packed else rng.randint(1, 3), S=S, H=Hq, D=D, R=R, inter=inter,
-                    inverse=rng.random() < 0.5, dtype=dtype, cp=cp,
-                    layout=rng.choice(["contiguous", "zigzag", "stripe"]), packed=packed)
+        c = dict(op=op, B=1 if packed else rng.randint(1, 3), S=S, H=Hq, D=D, R=R, inter=inter,
+                 inverse=rng.random() < 0.5, dtype=dtype, cp=cp,
+                 layout=rng.choice(["contiguous", "zigzag", "stripe"]), packed=packed)
+        if c["layout"] == "zigzag":  # two chunks per rank
+            c["S"] -= S % (2 * cp)
+        return c
     window = rng.choice([0, 0, _log(rng, 1, 4000)])
     sink = rng.choice([0, 1, 4]) if window else 0
     if op == "decode":
