@@ -757,7 +757,7 @@ usp_status_t usp_kv8_read(const usp_kv8_cache_t *cache, const int32_t *start, in
  *      written), which chooses the kernel; outside [1, T]: T. Else ignored.
  * out  as q, written; lse [B, T, Hq] fp32 (packed [T, Hq]), written (natural log of
  *      the scaled scores' sum). usp_merge_partials merges results of several
- *      caches by it.
+ *      caches by it (it takes O in fp32).
  * The result does not vary from run to run.
  * Hq % Hkv == 0; any number of query rows per KV head. dtype USP_BF16.
  * workspace: at least usp_attn_kv8_workspace_size(...) bytes, 256-byte aligned,

@@ -3,10 +3,10 @@
 //
 // A code is an E4M3 number; a block of 32 tokens of a head has one exponent e
 // (int8, [-40, 40]) and stands for code * 2^e. A power of two costs E4M3 nothing:
-// the largest element of a block keeps 4 significant bits at any scale, so does
-// every element down to 2^-15 of it, and a block whose exponent rises keeps its
-// older values but for those that become subnormal. Codes are exact in fp16, and
-// their products with 2^e in bf16.
+// while e is not clamped, the largest element of a block becomes a code of more than
+// 224, and every element down to 2^-13 of it keeps 4 significant bits (codes below 2^-6
+// are subnormal); a block whose exponent rises keeps its older values but for those that
+// become subnormal. Codes are exact in fp16, and their products with 2^e in bf16.
 #pragma once
 
 #include <cuda_bf16.h>

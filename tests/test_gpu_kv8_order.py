@@ -94,3 +94,36 @@ def test_the_line_in_a_captured_step():
         want = step(b)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), i
     assert a.seq_lens.tolist() == b.seq_lens.tolist() == [70, 70]
+
+
+def test_a_captured_chunk_grows_the_cache():
+    """An append of more than 64 tokens, whose lengths a second, dependent kernel writes in
+    place, and the chunk's attention, captured and replayed."""
+    dev = device()
+    B, T = 2, 100
+    a, b = (give_pages(empty(dev, B)) for _ in "ab")
+    q, k, v = tokens(dev, (B, T), 1)
+    table = usp.rope_table(CAP, D, device=dev)
+
+    def step(c):
+        _, qr = usp.kv8_append(c, k, v, q=q, rope=table)
+        return usp.attn_kv8(qr, c)
+
+    s = torch.cuda.Stream(device=dev)
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(give_pages(empty(dev, B)))
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = step(a)
+    for i in range(5):
+        for x, y in zip((q, k, v), tokens(dev, (B, T), i + 2)):
+            x.copy_(y)
+        graph.replay()
+        got = out.clone(), lse.clone()
+        want = step(b)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), i
+    assert a.seq_lens.tolist() == b.seq_lens.tolist() == [500, 500]
+    for x, y in zip(a[:4], b[:4]):
+        assert torch.equal(x, y)
