@@ -714,7 +714,7 @@ typedef struct {
  * table, table_rows, rotary_dim, interleaved  as in usp_rope, for k and q; table
  *      NULL: no rotation. The position of a token is positions[b][t] (packed
  *      positions[t]; int32, device), or with positions NULL its row in the cache,
- *      and max_pages * page_size <= table_rows. Positions outside the table are
+ *      and max_pages * page_size <= table_rows (if T > 0). Positions outside the table are
  *      rotated as its nearest row. A rotated key is stored from fp32, with no
  *      rounding in between.
  * seq_lens_out  [B] int32 or NULL: min(max_pages * page_size, seq_lens[b] + the

@@ -120,8 +120,9 @@ usp_status_t usp_kv8_append(const usp_kv8_cache_t* cache, const void* k, const v
   if (T > kMaxRows) return USP_ERR_UNSUPPORTED;
   r = check_rope(table, table_rows, rotary_dim, cache->D);
   if (r != USP_OK) return r;
-  // the positions of the cache's rows, all of them in the table
-  if (table && !positions && (long long)cache->max_pages * cache->page_size > table_rows)
+  // the positions of the cache's rows, all of them in the table (without tokens there are none,
+  // and an empty tensor of positions is a null pointer)
+  if (T > 0 && table && !positions && (long long)cache->max_pages * cache->page_size > table_rows)
     return USP_ERR_INVALID_ARG;
   if (cu_seqlens && cache->B < 1) return USP_ERR_INVALID_ARG;
   if (cache->B > 0 && T > 0 && (!k || !v)) return USP_ERR_INVALID_ARG;

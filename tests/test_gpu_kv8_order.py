@@ -127,3 +127,17 @@ def test_a_captured_chunk_grows_the_cache():
     assert a.seq_lens.tolist() == b.seq_lens.tolist() == [500, 500]
     for x, y in zip(a[:4], b[:4]):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_an_empty_chunk_at_given_positions(packed):
+    """No tokens: lengths stay, with a table of fewer positions than the cache has rows."""
+    dev = device()
+    c = give_pages(empty(dev, 2))
+    c.seq_lens.copy_(torch.tensor([5, 0]))
+    lead = (0,) if packed else (2, 0)
+    q, k, v = tokens(dev, lead, 1)
+    lens, qr = usp.kv8_append(c, k, v, q=q, rope=usp.rope_table(8, D, device=dev),
+                              positions=torch.empty(lead, dtype=torch.int32, device=dev),
+                              cu_seqlens=torch.zeros(3, dtype=torch.int32, device=dev) if packed else None)
+    assert lens.tolist() == [5, 0] and qr.shape == q.shape
